@@ -15,6 +15,7 @@
 #include <type_traits>
 
 #include "../../include/mp3d.h"
+#include "api_common.hpp"
 #include "dtype.hpp"
 #include "idxsrc.hpp"
 #include "kernels.hpp"
@@ -28,13 +29,10 @@ thread_local char g_msg[256] = "";
 // mp3d_time_next_call: events armed for the next call on this thread
 thread_local LaunchTiming g_timing = {nullptr, nullptr};
 
-// Disarms the kernel-time events when a C-ABI call returns, whether or not
-// it launched anything.
-struct TimingScope {
-    ~TimingScope() { g_timing = {nullptr, nullptr}; }
-};
+}  // namespace
 
-int fail(int code, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
+TimingScope::~TimingScope() { g_timing = {nullptr, nullptr}; }
+
 int fail(int code, const char *fmt, ...)
 {
     va_list ap;
@@ -43,6 +41,24 @@ int fail(int code, const char *fmt, ...)
     va_end(ap);
     return code;
 }
+
+int hip_status(hipError_t e, const char *what)
+{
+    if (e == hipSuccess) return MP3D_OK;
+    return fail(MP3D_EHIP, "%s: %s (hipError %d)", what, hipGetErrorString(e), (int)e);
+}
+
+bool log_enabled()
+{
+    static int on = -1;
+    if (on < 0) {
+        const char *v = getenv("MP3D_LOG");
+        on = (v && *v && strcmp(v, "0") != 0) ? 1 : 0;
+    }
+    return on == 1;
+}
+
+namespace {
 
 // MP3D_SMALL=0 turns the small-tensor kernels off, so that the general
 // kernels can be exercised on small inputs (read on every call).
@@ -59,18 +75,6 @@ bool two_pass_forced()
     const char *v = getenv("MP3D_TWO_PASS");
     return v && strcmp(v, "1") == 0;
 }
-
-bool log_enabled()
-{
-    static int on = -1;
-    if (on < 0) {
-        const char *v = getenv("MP3D_LOG");
-        on = (v && *v && strcmp(v, "0") != 0) ? 1 : 0;
-    }
-    return on == 1;
-}
-
-constexpr int64_t kInt32Max = 2147483647;
 
 // Shared checks of shapes and pointers; fills the per-plane sizes of g.
 int check_common(int dtype, int64_t N, int64_t C, int64_t D, int64_t H, int64_t W)
@@ -170,12 +174,6 @@ int finish_geom(Geom *g, int64_t N, int64_t C)
     if (g->planes > 0 && g->planes > ((int64_t)1 << 62) / out)
         return fail(MP3D_EOVERFLOW, "N*C*OD*OH*OW exceeds 2^62 elements");
     return MP3D_OK;
-}
-
-int hip_status(hipError_t e, const char *what)
-{
-    if (e == hipSuccess) return MP3D_OK;
-    return fail(MP3D_EHIP, "%s: %s (hipError %d)", what, hipGetErrorString(e), (int)e);
 }
 
 template <typename T, typename IT>
