@@ -22,6 +22,16 @@ PyTorch fallback: if the library is missing every call raises ImportError.
 x, y, gy and gx are float32, float16, bfloat16 or float64; idx is int32 (int64 on
 request: index_dtype=torch.int64), flat within each D*H*W plane.
 
+Operators over a pooled volume's tokens (bwd_max_pool3d_amd/tokens.py):
+  mp3d_rope_forward / mp3d_rope_backward(q, k, inv_freq, pairs, positions or grid)
+      rotary positions over the volume's axes
+  mp3d_attention_forward(q, k, v, ...) -> (out, lse)
+  mp3d_attention_backward(dout, q, k, v, out, lse, ...) -> (dq, dk, dv)
+      capped scores, bias by distance, document, causal and prefix masks
+  mp3d_gated_norm_forward(x, h, ...) -> (y, z, stats)
+  mp3d_gated_norm_backward(dy, dz, x, h, stats, ...) -> (dx, dh, dgate, dpost, dpre)
+      norm after a block, gate, residual sum, norm before the next block
+
 The names of the three-call sketch are kept as aliases:
   max_pool3d(x, kernel, stride) = mp3d_forward,
   adaptive_max_pool3d(x, out_size) = amp3d_forward,
@@ -41,7 +51,11 @@ __all__ = ["mp3d_forward", "amp3d_forward", "mp3d_backward", "mp3d_out_size",
            "mp3d_forward_ex", "mp3d_backward_ex", "mp3d_out_size_ex",
            "mp3d_backward_recompute", "recompute_workspace_size",
            "mp3d_backward_workspace_bytes", "mp3d_time_next_call", "Mp3dError",
-           "max_pool3d", "adaptive_max_pool3d", "max_pool3d_backward"]
+           "max_pool3d", "adaptive_max_pool3d", "max_pool3d_backward",
+           "mp3d_rope_forward", "mp3d_rope_backward", "mp3d_attention_forward",
+           "mp3d_attention_backward", "mp3d_attention_workspace_bytes",
+           "mp3d_gated_norm_forward", "mp3d_gated_norm_backward",
+           "mp3d_gated_norm_workspace_bytes"]
 
 _IDX = {torch.int32: _lib.MP3D_IDX_I32, torch.int64: _lib.MP3D_IDX_I64}
 
@@ -363,3 +377,9 @@ def max_pool3d_backward(gy: torch.Tensor, idx: torch.Tensor, in_shape, kernel=No
     """Alias of mp3d_backward under the sketch's name; ``overlap`` None,
     False or True (or the C ABI's integer codes)."""
     return mp3d_backward(gy, idx, in_shape, kernel, stride, overlap=overlap_code(overlap), out=out)
+
+
+from .tokens import (mp3d_attention_backward, mp3d_attention_forward,  # noqa: E402
+                     mp3d_attention_workspace_bytes, mp3d_gated_norm_backward,
+                     mp3d_gated_norm_forward, mp3d_gated_norm_workspace_bytes, mp3d_rope_backward,
+                     mp3d_rope_forward)

@@ -21,10 +21,26 @@ EXPORTS = ("mp3d_forward", "amp3d_forward", "mp3d_backward", "mp3d_out_size",
            "mp3d_out_size_ex", "mp3d_forward_ex", "mp3d_backward_ex", "mp3d_backward_recompute",
            "mp3d_recompute_workspace_size", "mp3d_backward_recompute_ws",
            "mp3d_backward_workspace_bytes", "mp3d_time_next_call",
-           "mp3d_backward_recompute_static", "mp3d_strerror", "mp3d_last_error")
+           "mp3d_backward_recompute_static", "mp3d_strerror", "mp3d_last_error",
+           "mp3d_rope_forward", "mp3d_rope_backward", "mp3d_attention_workspace_bytes",
+           "mp3d_attention_forward", "mp3d_attention_backward", "mp3d_gated_norm_forward",
+           "mp3d_gated_norm_workspace_bytes", "mp3d_gated_norm_backward")
+
+MP3D_NORM_RMS, MP3D_NORM_LAYER = 0, 1
+MP3D_NORM_POST, MP3D_NORM_PRE = 1, 2
 
 _i32, _i64, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
 _lib = None
+
+
+class Attention(ctypes.Structure):
+    """struct mp3d_attention (include/mp3d.h)."""
+    _fields_ = [("dtype", ctypes.c_int), ("B", _i64), ("Tq", _i64), ("Tk", _i64), ("Hq", _i32),
+                ("Hk", _i32), ("D", _i32), ("q_stride", _i64 * 3), ("k_stride", _i64 * 3),
+                ("v_stride", _i64 * 3), ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("causal", ctypes.c_int), ("kv_len", _vp), ("doc_offsets", _vp),
+                ("n_docs", _i32), ("prefix", _vp), ("axes", _i32), ("slopes", _vp),
+                ("pos_q", _vp), ("pos_k", _vp)]
 
 
 class Mp3dError(RuntimeError):
@@ -74,6 +90,20 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.mp3d_backward_recompute_static.argtypes = ([_vp, _vp, _vp, _vp, ctypes.c_int]
                                                    + [_i64] * 5 + [_i32] * 3 + [_a3] * 4
                                                    + [ctypes.c_int, _vp])
+    _a3l, _f32, _int, _size = ctypes.POINTER(_i64), ctypes.c_float, ctypes.c_int, ctypes.c_size_t
+    for name in ("mp3d_rope_forward", "mp3d_rope_backward"):
+        getattr(lib, name).argtypes = ([_vp] * 4 + [_int] + [_i64] * 2 + [_i32] * 3 + [_a3l] * 4
+                                       + [_vp, _a3, _vp, _a3, _int, _vp])
+    _attn = ctypes.POINTER(Attention)
+    lib.mp3d_attention_workspace_bytes.argtypes = [_attn, _int, ctypes.POINTER(_size)]
+    lib.mp3d_attention_forward.argtypes = [_attn] + [_vp] * 6 + [_size, _vp]
+    lib.mp3d_attention_backward.argtypes = [_attn, _vp, _a3l] + [_vp] * 9 + [_size, _vp]
+    lib.mp3d_gated_norm_forward.argtypes = ([_vp] * 8 + [_int, _i64, _i32, _i64, _f32, _int, _int,
+                                                        _f32, _vp])
+    lib.mp3d_gated_norm_workspace_bytes.argtypes = [_int, _i64, _i32, _i64,
+                                                    ctypes.POINTER(_size)]
+    lib.mp3d_gated_norm_backward.argtypes = ([_vp] * 13 + [_int, _i64, _i32, _i64, _f32, _int,
+                                                          _int, _f32, _vp, _size, _vp])
     lib.mp3d_strerror.argtypes = [ctypes.c_int]
     lib.mp3d_strerror.restype = ctypes.c_char_p
     lib.mp3d_last_error.argtypes = []
@@ -82,7 +112,10 @@ def load(path: str | None = None) -> ctypes.CDLL:
                  "mp3d_out_size_ex", "mp3d_forward_ex", "mp3d_backward_ex",
                  "mp3d_backward_recompute", "mp3d_recompute_workspace_size",
                  "mp3d_backward_recompute_ws", "mp3d_backward_workspace_bytes",
-                 "mp3d_time_next_call", "mp3d_backward_recompute_static"):
+                 "mp3d_time_next_call", "mp3d_backward_recompute_static", "mp3d_rope_forward",
+                 "mp3d_rope_backward", "mp3d_attention_workspace_bytes",
+                 "mp3d_attention_forward", "mp3d_attention_backward", "mp3d_gated_norm_forward",
+                 "mp3d_gated_norm_workspace_bytes", "mp3d_gated_norm_backward"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib

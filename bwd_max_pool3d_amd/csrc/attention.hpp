@@ -1,0 +1,359 @@
+// attention.hpp -- what the attention kernels share: their arguments, the
+// keys a query sees, tiles in LDS and the matrix fragments read from them.
+//
+// Fragments.  All products run on 32x32 matrix instructions, 16 deep.  A
+// fragment is 8 elements of one lane; lane l holds row (or column) l % 32
+// and the half l / 32 of the depth.  The 32x32 result lies with column
+// l % 32 in lane l and rows 8 (r / 4) + 4 (l / 32) + r % 4 in its registers
+// r = 0 .. 15.  So the scores are formed transposed to what they feed: a
+// result's registers 8c .. 8c + 7, rounded to the storage type, are the
+// second operand of the next product over the rows 16c .. 16c + 15, taken
+// in the order {0-3, 8-11} (lower half) and {4-7, 12-15} (upper half), with
+// no exchange between lanes.  The first operand of that product is read
+// from LDS in the same order: for 16-bit types by the transposing LDS read,
+// which hands each of 16 lanes one column of a 4 x 16 block.
+#pragma once
+
+#include "dtype.hpp"
+#include "tokens.hpp"
+
+namespace mp3d {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNegInf = -__builtin_huge_valf();
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+// 8 elements of a lane: 16 bytes, or 32 for float32
+template <typename T>
+struct Frag {
+    static constexpr int NV = sizeof(typename T::raw) * 8 / 16;
+    u32x4 w[NV];
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) w[i] = u32x4{0u, 0u, 0u, 0u};
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ f32x16 mma(const Frag<T> &a, const Frag<T> &b, f32x16 c)
+{
+    if constexpr (T::code == BF16::code) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a.w[0]),
+                                                       __builtin_bit_cast(bf16x8, b.w[0]), c, 0, 0,
+                                                       0);
+    } else if constexpr (T::code == F16::code) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a.w[0]),
+                                                      __builtin_bit_cast(f16x8, b.w[0]), c, 0, 0,
+                                                      0);
+    } else {
+        // eight products 2 deep: the halves' elements i meet
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const u32x4 x = a.w[i / 4], y = b.w[i / 4];
+            const uint32_t xe[4] = {x.x, x.y, x.z, x.w}, ye[4] = {y.x, y.y, y.z, y.w};
+            c = __builtin_amdgcn_mfma_f32_32x32x2f32(__builtin_bit_cast(float, xe[i % 4]),
+                                                     __builtin_bit_cast(float, ye[i % 4]), c, 0, 0,
+                                                     0);
+        }
+        return c;
+    }
+}
+
+// Registers 8c .. 8c + 7 of a result as an operand.
+template <typename T>
+__device__ __forceinline__ Frag<T> pack8(const f32x16 &s, int c)
+{
+    struct alignas(16) {
+        typename T::raw e[8];
+    } o;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o.e[i] = T::narrow(s[8 * c + i]);
+    return __builtin_bit_cast(Frag<T>, o);
+}
+
+// Row of a result's register r (see above).
+__device__ __forceinline__ constexpr int acc_row(int r, int half)
+{
+    return 8 * (r / 4) + 4 * half + r % 4;
+}
+
+// Channels d of a result's column (one row of a tensor in memory, rows
+// starting at multiples of 16 bytes times the row's number), times f.
+template <typename T, int ND>
+__device__ __forceinline__ void store_cols(typename T::raw *out, const f32x16 *o, float f, int D,
+                                           int half)
+{
+    using R = typename T::raw;
+    const bool wide = D % 4 == 0;          // rows then start at multiples of 4 elements
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+            const int e = d * 32 + acc_row(r, half);
+            struct alignas(4 * sizeof(R)) {
+                R v[4];
+            } w;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) w.v[x] = T::narrow(o[d][r + x] * f);
+            if (wide) {
+                if (e < D) *(decltype(w) *)(out + e) = w;
+            } else {
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    if (e + x < D) out[e + x] = w.v[x];
+            }
+        }
+}
+
+// The other half's value.
+__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
+
+// --- tiles in LDS: rows of DP elements in chunks of 8, the chunks of a row
+// swapped by the row's number so that neither the row fragments (the same
+// chunk of 32 rows) nor the column fragments (4 rows by 16 columns) meet on
+// a bank.
+__device__ __forceinline__ int tile_swap(int row) { return ((row & 3) << 1) | ((row >> 2) & 1); }
+
+template <int DP>
+__device__ __forceinline__ int tile_at(int row, int chunk)
+{
+    return row * DP + ((chunk ^ tile_swap(row)) << 3);
+}
+
+// Elements d0 .. d0 + 7 (d0 a multiple of 8) of a row.
+template <typename T, int DP>
+__device__ __forceinline__ Frag<T> row_frag(const typename T::raw *tile, int row, int d0)
+{
+    const u32x4 *p = (const u32x4 *)(tile + tile_at<DP>(row, d0 >> 3));
+    Frag<T> f;
+#pragma unroll
+    for (int i = 0; i < Frag<T>::NV; ++i) f.w[i] = p[i];
+    return f;
+}
+
+// Column l % 32 of the 32 columns from d0, rows 16c .. 16c + 15 in the
+// operand order above.
+template <typename T, int DP>
+__device__ __forceinline__ Frag<T> col_frag(const typename T::raw *tile, int c, int d0, int l)
+{
+    const int half = l >> 5;
+    Frag<T> f;
+    if constexpr (sizeof(typename T::raw) == 2) {
+        const int col = d0 + (l & 16) + (l & 3) * 4;
+        const int row = 16 * c + 4 * half + ((l & 15) >> 2);
+        typedef __attribute__((address_space(3))) s16x4 lds_t;
+        struct alignas(16) {
+            s16x4 v[2];
+        } o;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const typename T::raw *p =
+                tile + tile_at<DP>(row + 8 * k, col >> 3) + (col & 7);
+            o.v[k] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t *)p);
+        }
+        f = __builtin_bit_cast(Frag<T>, o);
+    } else {
+        const int col = d0 + (l & 31);
+        struct alignas(16) {
+            float e[8];
+        } o;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = 16 * c + 4 * half + (i < 4 ? i : i + 4);
+            o.e[i] = tile[tile_at<DP>(row, col >> 3) + (col & 7)];
+        }
+        f = __builtin_bit_cast(Frag<T>, o);
+    }
+    return f;
+}
+
+// Infinities and NaN set to 0; true if there was one.
+template <typename T>
+__device__ __forceinline__ bool drop_nonfinite(Frag<T> &f)
+{
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < Frag<T>::NV; ++i) {
+        uint32_t w[4] = {f.w[i].x, f.w[i].y, f.w[i].z, f.w[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (T::code == F32::code) {
+                if ((w[j] & 0x7f800000u) == 0x7f800000u) {
+                    bad = true;
+                    w[j] = 0;
+                }
+            } else {
+                constexpr uint32_t e = T::code == F16::code ? 0x7c00u : 0x7f80u;
+                if ((w[j] & e) == e) {
+                    bad = true;
+                    w[j] &= 0xffff0000u;
+                }
+                if ((w[j] & (e << 16)) == (e << 16)) {
+                    bad = true;
+                    w[j] &= 0xffffu;
+                }
+            }
+        }
+        f.w[i] = u32x4{w[0], w[1], w[2], w[3]};
+    }
+    return bad;
+}
+
+// Elements d0 .. d0 + 7 of a row of D in memory, zero past D.  vec: rows
+// start at multiples of 16 bytes.
+template <typename T>
+__device__ __forceinline__ Frag<T> load8(const typename T::raw *p, int d0, int D, bool vec)
+{
+    Frag<T> f;
+    f.zero();
+    if (vec && d0 + 8 <= D) {
+#pragma unroll
+        for (int i = 0; i < Frag<T>::NV; ++i) f.w[i] = ((const u32x4 *)(p + d0))[i];
+    } else if (d0 < D) {
+        struct alignas(16) {
+            typename T::raw e[8];
+        } o = __builtin_bit_cast(decltype(o), f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (d0 + i < D) o.e[i] = p[d0 + i];
+        f = __builtin_bit_cast(Frag<T>, o);
+    }
+    return f;
+}
+
+// A tile of ROWS rows on its way from memory to LDS, spread over NT threads.
+template <typename T, int DP, int ROWS, int NT>
+struct TileRegs {
+    using R = typename T::raw;
+    static constexpr int N = ROWS * (DP / 8) / NT;
+    static_assert(N * NT == ROWS * (DP / 8), "whole chunks per thread");
+    Frag<T> f[N];
+
+    // rows r0 .. r0 + ROWS - 1 of base; rows outside [lo, hi) are zero and
+    // are not read
+    __device__ __forceinline__ void load(const R *base, int64_t stride, int r0, int lo, int hi,
+                                         int D, bool vec, int t)
+    {
+        if (vec && D == DP && lo <= r0 && r0 + ROWS <= hi) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const int id = t + NT * j;
+                const R *p = base + (int64_t)(r0 + id / (DP / 8)) * stride + (id % (DP / 8)) * 8;
+#pragma unroll
+                for (int i = 0; i < Frag<T>::NV; ++i) f[j].w[i] = ((const u32x4 *)p)[i];
+            }
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int id = t + NT * j, row = r0 + id / (DP / 8);
+            if (row >= lo && row < hi)
+                f[j] = load8<T>(base + (int64_t)row * stride, (id % (DP / 8)) * 8, D, vec);
+            else
+                f[j].zero();
+        }
+    }
+    __device__ __forceinline__ void store(R *tile, int t) const
+    {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int id = t + NT * j;
+            u32x4 *p = (u32x4 *)(tile + tile_at<DP>(id / (DP / 8), id % (DP / 8)));
+#pragma unroll
+            for (int i = 0; i < Frag<T>::NV; ++i) p[i] = f[j].w[i];
+        }
+    }
+    __device__ __forceinline__ bool nonfinite() const
+    {
+        bool bad = false;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            Frag<T> x = f[j];
+            bad |= drop_nonfinite<T>(x);
+        }
+        return bad;
+    }
+    __device__ __forceinline__ bool drop()
+    {
+        bool bad = false;
+#pragma unroll
+        for (int j = 0; j < N; ++j) bad |= drop_nonfinite<T>(f[j]);
+        return bad;
+    }
+};
+
+// --- infinities and NaN in masked places
+//
+// 0 * inf is NaN, so a masked weight of 0 does not keep a key's value out of
+// a matrix product.  Keys that no query of the workgroup sees are staged as
+// zeros.  Where some see a key and others do not, its infinities and NaN are
+// staged as zeros too, and added afterwards to the results of those who do
+// see it: a positive weight times such a value is that value, so the weight
+// itself is not needed.
+//
+// --- the keys a query sees
+struct Span {
+    int lo, hi;                            // [lo, hi) within [0, Tk); {0, 0}: none
+};
+
+__device__ __forceinline__ Span row_span(const AttnArgs &a, int b, int i)
+{
+    int L = a.Tk;
+    if (a.kv_len) L = min(max(a.kv_len[b], 0), a.Tk);
+    const int p = i + L - a.Tq;
+    int lo = 0, hi = L, pre = 0;
+    if (a.docs) {
+        const int32_t *o = a.docs + (int64_t)b * (a.ndocs + 1);
+        if (p < o[0] || p >= o[a.ndocs]) return {0, 0};
+        int d = 0, e = a.ndocs;            // o[d] <= p < o[e]
+        while (e - d > 1) {
+            const int m = (d + e) >> 1;
+            if (o[m] <= p) d = m;
+            else e = m;
+        }
+        lo = max(o[d], 0);
+        hi = min(o[d + 1], L);
+        if (a.prefix) pre = a.prefix[(int64_t)b * a.ndocs + d];
+    } else if (a.prefix) {
+        pre = a.prefix[b];
+    }
+    if (a.causal) hi = min(hi, max(p + 1, min(lo, a.Tk) + min(max(pre, 0), a.Tk)));
+    return hi > lo ? Span{lo, hi} : Span{0, 0};
+}
+
+// --- scores: from the accumulated products to the exponents' domain.
+// Without a cap or a bias the scores stay as they are and c1 (scale times
+// log2 e) is applied inside the exponent's multiply-add.
+struct ScoreMul {
+    float mul;                             // exponent = score * mul - row maximum
+    bool transform;
+};
+
+__device__ __forceinline__ ScoreMul score_mul(const AttnArgs &a)
+{
+    const bool tr = a.cap > 0.f || a.axes > 0 || !(a.scale > 0.f);
+    return {tr ? 1.f : a.scale * kLog2e, tr};
+}
+
+// tanh: 1 - 2 / (1 + e^2x) is within 2e-7 of the truth, which as an
+// exponent's error is below a 16-bit weight's rounding; float32 results
+// need the relative accuracy near 0 that the library's tanhf has
+template <typename T>
+__device__ __forceinline__ float cap_tanh(float x)
+{
+    if constexpr (T::code == F32::code) {
+        return tanhf(x);
+    } else {
+        const float e = __builtin_amdgcn_exp2f(x * (2.f * kLog2e));
+        return 1.f - 2.f * __builtin_amdgcn_rcpf(1.f + e);
+    }
+}
+
+}  // namespace mp3d

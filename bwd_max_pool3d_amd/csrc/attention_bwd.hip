@@ -1,0 +1,615 @@
+// attention_bwd.hip -- attention backward.
+//
+// With the weights p_ij = exp(s_ij - lse_i) formed again from the forward's
+// log-sum-exp, and delta_i = sum_j p_ij (do_i . v_j) = do_i . out_i:
+//   dv_j = sum_i p_ij do_i
+//   e_ij = p_ij (do_i . v_j - delta_i) (1 - tanh^2(scale q_i . k_j / cap))
+//   dq_i = scale sum_j e_ij k_j        dk_j = scale sum_i e_ij q_i
+// (the last factor of e only with a cap; the bias has no gradient).
+//
+// Three launches: the rows' constants (delta, the spans of keys, and their
+// unions over 32 queries); dk and dv, a workgroup of four waves per 128
+// keys of one key head, walking the queries of the heads that share it; dq,
+// a workgroup per 128 queries, walking their keys.  Scores and do . v are
+// formed in both (7 products where 5 would do), and in exchange every sum
+// is kept by one wave in registers and written once: no atomics, the same
+// bits on every run.  Where one pass over a key head's query heads would
+// leave the card idle they are dealt to several workgroups, whose binary32
+// sums a fourth launch adds in a fixed order.
+//
+// p and e are rounded to the storage type for the second products, as the
+// forward's weights are.
+#include "attention.hpp"
+
+namespace mp3d {
+
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kStep = 32;                  // keys (dq) or queries (dk, dv) per step
+constexpr float kInf = __builtin_huge_valf();
+
+// ------------------------------------------------------------ constants
+
+// One workgroup per 32 queries of one head: 8 threads per row.
+template <typename T>
+__global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a)
+{
+    using R = typename T::raw;
+    const int nt = (a.Tq + 31) / 32;
+    const int qt = blockIdx.x % nt;
+    const int64_t bh = blockIdx.x / nt;
+    const int b = (int)(bh / a.Hq), h = (int)(bh - (int64_t)b * a.Hq);
+    const int row = threadIdx.x >> 3, sub = threadIdx.x & 7, i = qt * 32 + row;
+    float s = 0.f;
+    if (i < a.Tq) {
+        const R *o = (const R *)a.out + (((int64_t)b * a.Tq + i) * a.Hq + h) * a.D;
+        const R *g = (const R *)a.dout + b * a.gs[0] + (int64_t)i * a.gs[1] + h * a.gs[2];
+        const bool ovec = (int64_t)a.D * sizeof(R) % 16 == 0;
+#pragma unroll
+        for (int d = sub * 8; d < kAttnMaxD; d += 64) {
+            struct alignas(16) {
+                R e[8];
+            } x = __builtin_bit_cast(decltype(x), load8<T>(o, d, a.D, ovec)),
+              y = __builtin_bit_cast(decltype(y), load8<T>(g, d, a.D, a.vec));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s = fmaf(T::widen(x.e[k]), T::widen(y.e[k]), s);
+        }
+    }
+#pragma unroll
+    for (int m = 4; m; m >>= 1) s += __shfl_xor(s, m);
+    if (sub == 0 && i < a.Tq) {
+        const int64_t at = bh * a.Tq + i;
+        const float l = a.lse[at];
+        // a row without weights: its exponents become -inf
+        *(float2 *)(a.rowd + 2 * at) = make_float2(l == kNegInf ? kInf : l * kLog2e, s);
+    }
+    if (h == 0 && threadIdx.x < 64) {
+        const int j = qt * 32 + (threadIdx.x & 31);
+        Span sp = {0, 0};                  // (past the last query: none)
+        if (j < a.Tq) sp = row_span(a, b, j);
+        if (threadIdx.x < 32 && j < a.Tq)
+            *(int2 *)(a.spans + 2 * ((int64_t)b * a.Tq + j)) = make_int2(sp.lo, sp.hi);
+        int lo = sp.hi > sp.lo ? sp.lo : 0x7fffffff, hi = sp.hi, alo = sp.lo, ahi = sp.hi;
+#pragma unroll
+        for (int m = 16; m; m >>= 1) {
+            lo = min(lo, __shfl_xor(lo, m));
+            hi = max(hi, __shfl_xor(hi, m));
+            alo = max(alo, __shfl_xor(alo, m));
+            ahi = min(ahi, __shfl_xor(ahi, m));
+        }
+        if (threadIdx.x == 0)
+            *(int4 *)(a.tiles + 4 * ((int64_t)b * nt + qt)) = make_int4(lo, hi, alo, ahi);
+    }
+}
+
+// From a step's products to the weights p and to e / (dp - delta) = p times
+// the cap's slope: s holds q.k on entry and p on return; slope is written
+// (and 1 without a cap).
+struct Shape {
+    float capin, c2, mul;
+    bool cap, transform;
+};
+
+__device__ __forceinline__ Shape score_shape(const AttnArgs &a)
+{
+    const ScoreMul sm = score_mul(a);
+    return {a.cap > 0.f ? a.scale / a.cap : 0.f, (a.cap > 0.f ? a.cap : a.scale) * kLog2e, sm.mul,
+            a.cap > 0.f, sm.transform};
+}
+
+// ------------------------------------------------------------------- dq
+
+template <typename T, int DP>
+constexpr int bwd_occupancy() { return sizeof(typename T::raw) * DP > 256 ? 1 : 2; }
+
+template <typename T, int DP>
+__global__ __launch_bounds__(64 * kWaves, (bwd_occupancy<T, DP>())) void attn_dq_kernel(AttnArgs a)
+{
+    using R = typename T::raw;
+    constexpr int NT = 64 * kWaves, KB = kStep, NC = DP / 16, ND = DP / 32;
+    extern __shared__ __align__(16) unsigned char smem[];
+    R *const kt = (R *)smem;                               // [2][KB * DP]
+    R *const vt = kt + 2 * KB * DP;                        // [2][KB * DP]
+    float *const pk = (float *)(vt + 2 * KB * DP);         // [2][3][KB]
+    int *const flag = (int *)(pk + 2 * 3 * KB);            // [3] a tile holds an inf or a NaN
+    int *const ends = flag + 3;                            // [2][kWaves]
+
+    const int nq = (a.Tq + 32 * kWaves - 1) / (32 * kWaves);
+    const int heads = a.B * a.Hq;
+    int bh, qt;
+    if (heads % 8 == 0) {
+        const int per = heads / 8, j = blockIdx.x / 8;
+        bh = (blockIdx.x % 8) * per + j % per;
+        qt = nq - 1 - j / per;
+    } else {
+        bh = blockIdx.x % heads;
+        qt = nq - 1 - blockIdx.x / heads;
+    }
+    const int b = bh / a.Hq, h = bh - b * a.Hq, hk = h / a.G;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, col = lane & 31,
+              half = lane >> 5;
+    const int q0 = qt * 32 * kWaves, i = q0 + wave * 32 + col;
+    const int ic = min(i, a.Tq - 1);
+    const int2 sp = *(const int2 *)(a.spans + 2 * ((int64_t)b * a.Tq + ic));
+    const int nt = (a.Tq + 31) / 32, wt = min(qt * kWaves + wave, nt - 1);
+    const int4 wu = *(const int4 *)(a.tiles + 4 * ((int64_t)b * nt + wt));
+    const int wlo = __builtin_amdgcn_readfirstlane(wu.x), whi = __builtin_amdgcn_readfirstlane(wu.y);
+    const int alo = __builtin_amdgcn_readfirstlane(wu.z), ahi = __builtin_amdgcn_readfirstlane(wu.w);
+    if (lane == 0) {
+        ends[wave] = wlo;
+        ends[kWaves + wave] = whi;
+    }
+    if (tid < 3) flag[tid] = 0;
+    __syncthreads();
+    int glo = ends[0], ghi = ends[kWaves];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) {
+        glo = min(glo, ends[w]);
+        ghi = max(ghi, ends[kWaves + w]);
+    }
+
+    const R *kp = (const R *)a.k + b * a.ks[0] + hk * a.ks[2];
+    const R *vp = (const R *)a.v + b * a.vs[0] + hk * a.vs[2];
+    const R *qp = (const R *)a.q + b * a.qs[0] + h * a.qs[2] + (int64_t)ic * a.qs[1];
+    const R *gp = (const R *)a.dout + b * a.gs[0] + h * a.gs[2] + (int64_t)ic * a.gs[1];
+    Frag<T> qf[NC], gf[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        qf[c] = load8<T>(qp, c * 16 + half * 8, a.D, a.vec);
+        gf[c] = load8<T>(gp, c * 16 + half * 8, a.D, a.vec);
+    }
+    const float2 rd = *(const float2 *)(a.rowd + 2 * ((int64_t)bh * a.Tq + ic));
+    float pq[3], sl[3];
+    int64_t base[3];
+#pragma unroll
+    for (int x = 0; x < 3; ++x) {
+        if (x >= a.axes) break;
+        const int32_t *p = a.pos_q + ((int64_t)x * a.B + b) * a.Tq;
+        base[x] = p[q0];
+        pq[x] = (float)(p[ic] - base[x]);
+        sl[x] = a.slopes[h * a.axes + x] * kLog2e;
+    }
+    const Shape sh = score_shape(a);
+
+    f32x16 o[ND];
+#pragma unroll
+    for (int d = 0; d < ND; ++d) o[d] = f32x16(0.f);
+
+    const int kbeg = ghi > 0 ? glo / KB * KB : 0, kend = ghi;
+    TileRegs<T, DP, KB, NT> kr, vr;
+    float pr[3];
+    auto fetch = [&](int k0) {
+        kr.load(kp, a.ks[1], k0, glo, ghi, a.D, a.vec, tid);
+        vr.load(vp, a.vs[1], k0, glo, ghi, a.D, a.vec, tid);
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+            if (x < a.axes && tid < KB)
+                pr[x] = (float)(a.pos_k[((int64_t)x * a.B + b) * a.Tk + min(k0 + tid, a.Tk - 1)] -
+                                base[x]);
+    };
+    auto place = [&](int buf, int n) {
+        kr.store(kt + buf * KB * DP, tid);
+        vr.store(vt + buf * KB * DP, tid);
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+            if (x < a.axes && tid < KB) pk[(buf * 3 + x) * KB + tid] = pr[x];
+        if (kr.nonfinite()) flag[n % 3] = 1;
+    };
+    if (kbeg < kend) {
+        fetch(kbeg);
+        place(0, 0);
+    }
+    __syncthreads();
+    int n = 0;
+    for (int k0 = kbeg; k0 < kend; k0 += KB, ++n) {
+        const int buf = n & 1;
+        const bool more = k0 + KB < kend;
+        if (more) fetch(k0 + KB);
+        if (tid == 0) flag[(n + 2) % 3] = 0;               // read last in step n - 1
+        if (k0 < whi && k0 + KB > wlo) {
+            const R *kb = kt + buf * KB * DP, *vb = vt + buf * KB * DP;
+            f32x16 s = f32x16(0.f), dp = f32x16(0.f);
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                s = mma<T>(row_frag<T, DP>(kb, col, c * 16 + half * 8), qf[c], s);
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                dp = mma<T>(row_frag<T, DP>(vb, col, c * 16 + half * 8), gf[c], dp);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) dp[r] -= rd.y;
+            if (sh.transform) {
+                if (sh.cap) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const float th = cap_tanh<T>(s[r] * sh.capin);
+                        s[r] = sh.c2 * th;
+                        dp[r] *= 1.f - th * th;
+                    }
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) s[r] *= sh.c2;
+                }
+#pragma unroll
+                for (int x = 0; x < 3; ++x) {
+                    if (x >= a.axes) break;
+                    const float *p = pk + (buf * 3 + x) * KB + 4 * half;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        s[r] = fmaf(-sl[x], fabsf(p[8 * (r / 4) + r % 4] - pq[x]), s[r]);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], sh.mul, -rd.x)) * dp[r];
+            const bool part = !(alo <= k0 && k0 + KB <= ahi);
+            if (part) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int key = k0 + acc_row(r, half);
+                    if (key < sp.x || key >= sp.y) s[r] = 0.f;
+                }
+            }
+            const Frag<T> e0 = pack8<T>(s, 0), e1 = pack8<T>(s, 1);
+            if (!(part && flag[n % 3])) {
+#pragma unroll
+                for (int d = 0; d < ND; ++d) {
+                    o[d] = mma<T>(col_frag<T, DP>(kb, 0, d * 32, lane), e0, o[d]);
+                    o[d] = mma<T>(col_frag<T, DP>(kb, 1, d * 32, lane), e1, o[d]);
+                }
+            } else {
+                // (a key that is seen and not finite has made e NaN already)
+#pragma unroll
+                for (int d = 0; d < ND; ++d) {
+                    Frag<T> f0 = col_frag<T, DP>(kb, 0, d * 32, lane);
+                    Frag<T> f1 = col_frag<T, DP>(kb, 1, d * 32, lane);
+                    drop_nonfinite<T>(f0);
+                    drop_nonfinite<T>(f1);
+                    o[d] = mma<T>(f0, e0, o[d]);
+                    o[d] = mma<T>(f1, e1, o[d]);
+                }
+            }
+        }
+        if (more) place(buf ^ 1, n + 1);
+        __syncthreads();
+    }
+    if (i >= a.Tq) return;
+    store_cols<T, ND>((R *)a.dq + (((int64_t)b * a.Tq + i) * a.Hq + h) * a.D, o, a.scale, a.D, half);
+}
+
+// -------------------------------------------------------------- dk and dv
+
+template <typename T, int DP>
+constexpr int dkv_occupancy() { return sizeof(typename T::raw) * DP > 128 ? 1 : 2; }
+
+template <typename T, int DP>
+__global__ __launch_bounds__(64 * kWaves, (dkv_occupancy<T, DP>())) void attn_dkv_kernel(AttnArgs a)
+{
+    using R = typename T::raw;
+    constexpr int NT = 64 * kWaves, QB = kStep, NC = DP / 16, ND = DP / 32;
+    extern __shared__ __align__(16) unsigned char smem[];
+    R *const qt = (R *)smem;                               // [2][QB * DP]
+    R *const gt = qt + 2 * QB * DP;                        // [2][QB * DP]
+    float *const pq = (float *)(gt + 2 * QB * DP);         // [2][3][QB] positions
+    float *const rl = pq + 2 * 3 * QB;                     // [2][QB] lse * log2 e
+    float *const rd = rl + 2 * QB;                         // [2][QB] delta
+    int *const slo = (int *)(rd + 2 * QB);                 // [2][QB] spans
+    int *const shi = slo + 2 * QB;
+    int *const flag = shi + 2 * QB;                        // [3]
+    int *const ends = flag + 3;                            // [2] first and last tile
+
+    // parts of one key head, and the key blocks of one sequence, on one XCD
+    const int nk = (a.Tk + 32 * kWaves - 1) / (32 * kWaves);
+    const uint32_t id = xcd_local_block(blockIdx.x, gridDim.x);
+    const int kb = id % nk;
+    int64_t rest = id / nk;
+    const int gpart = (int)(rest % a.gsplit);
+    rest /= a.gsplit;
+    const int hk = (int)(rest % a.Hk), b = (int)(rest / a.Hk);
+    const int g0 = (int)((int64_t)a.G * gpart / a.gsplit);
+    const int g1 = (int)((int64_t)a.G * (gpart + 1) / a.gsplit);
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, col = lane & 31,
+              half = lane >> 5;
+    const int k0 = kb * 32 * kWaves, kw = k0 + wave * 32, key = kw + col;
+    const int kc = min(key, a.Tk - 1);
+    const int nt = (a.Tq + QB - 1) / QB;
+    const int32_t *tiles = a.tiles + 4 * (int64_t)b * nt;
+
+    // the tiles of queries that see a key of this block
+    if (tid < 3) flag[tid] = 0;
+    if (tid < 2) ends[tid] = tid ? -1 : nt;
+    __syncthreads();
+    {
+        int first = nt, last = -1;
+        for (int t = tid; t < nt; t += NT) {
+            const int4 u = *(const int4 *)(tiles + 4 * (int64_t)t);
+            if (u.x < k0 + 32 * kWaves && u.y > k0) {
+                first = min(first, t);
+                last = t;
+            }
+        }
+        if (last >= 0) {
+            atomicMin(ends, first);
+            atomicMax(ends + 1, last);
+        }
+    }
+    __syncthreads();
+    const int first = ends[0], last = ends[1], span = last - first + 1;
+    const int steps = span > 0 ? span * (g1 - g0) : 0;
+
+    const R *kp = (const R *)a.k + b * a.ks[0] + hk * a.ks[2] + (int64_t)kc * a.ks[1];
+    const R *vp = (const R *)a.v + b * a.vs[0] + hk * a.vs[2] + (int64_t)kc * a.vs[1];
+    Frag<T> kf[NC], vf[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        kf[c] = load8<T>(kp, c * 16 + half * 8, a.D, a.vec);
+        vf[c] = load8<T>(vp, c * 16 + half * 8, a.D, a.vec);
+    }
+    float pk[3];
+    int64_t base[3];
+#pragma unroll
+    for (int x = 0; x < 3; ++x) {
+        if (x >= a.axes) break;
+        const int32_t *p = a.pos_k + ((int64_t)x * a.B + b) * a.Tk;
+        base[x] = p[k0];
+        pk[x] = (float)(p[kc] - base[x]);
+    }
+    const Shape sh = score_shape(a);
+    f32x16 dk[ND], dv[ND];
+#pragma unroll
+    for (int d = 0; d < ND; ++d) dk[d] = dv[d] = f32x16(0.f);
+
+    TileRegs<T, DP, QB, NT> qr, gr;
+    float prq[3];
+    float2 prd = make_float2(0.f, 0.f);
+    int2 psp = make_int2(0, 0);
+    // step n: head hk * G + g0 + n / span, tile first + n % span
+    auto fetch = [&](int n) {
+        const int h = hk * a.G + g0 + n / span, q0 = (first + n % span) * QB;
+        qr.load((const R *)a.q + b * a.qs[0] + h * a.qs[2], a.qs[1], q0, 0, a.Tq, a.D, a.vec, tid);
+        gr.load((const R *)a.dout + b * a.gs[0] + h * a.gs[2], a.gs[1], q0, 0, a.Tq, a.D, a.vec,
+                tid);
+        if (tid < QB) {
+            const int i = min(q0 + tid, a.Tq - 1);
+            prd = *(const float2 *)(a.rowd + 2 * (((int64_t)b * a.Hq + h) * a.Tq + i));
+            psp = *(const int2 *)(a.spans + 2 * ((int64_t)b * a.Tq + i));
+            if (q0 + tid >= a.Tq) {                // no query, no weight
+                prd = make_float2(kInf, 0.f);
+                psp = make_int2(0, 0);
+            }
+#pragma unroll
+            for (int x = 0; x < 3; ++x)
+                if (x < a.axes)
+                    prq[x] = (float)(a.pos_q[((int64_t)x * a.B + b) * a.Tq + i] - base[x]);
+        }
+    };
+    auto place = [&](int buf, int n) {
+        qr.store(qt + buf * QB * DP, tid);
+        gr.store(gt + buf * QB * DP, tid);
+        if (tid < QB) {
+            rl[buf * QB + tid] = prd.x;
+            rd[buf * QB + tid] = prd.y;
+            slo[buf * QB + tid] = psp.x;
+            shi[buf * QB + tid] = psp.y;
+#pragma unroll
+            for (int x = 0; x < 3; ++x)
+                if (x < a.axes) pq[(buf * 3 + x) * QB + tid] = prq[x];
+        }
+        if (qr.nonfinite() || gr.nonfinite()) flag[n % 3] = 1;
+    };
+    // (the union of keys of tile n % span, whether all its queries see the wave's keys)
+    auto touched = [&](int n, bool *part) {
+        const int32_t *u = tiles + 4 * (int64_t)(first + n % span);
+        *part = !(u[2] <= kw && kw + 32 <= u[3]);
+        return u[0] < kw + 32 && u[1] > kw;
+    };
+    bool dropped = false;
+    if (steps > 0) {
+        fetch(0);
+        place(0, 0);
+    }
+    __syncthreads();
+    for (int n = 0; n < steps; ++n) {
+        const int buf = n & 1;
+        const bool more = n + 1 < steps;
+        if (more) fetch(n + 1);
+        if (tid == 0) flag[(n + 2) % 3] = 0;
+        bool part;
+        if (touched(n, &part)) {
+            const R *qb = qt + buf * QB * DP, *gb = gt + buf * QB * DP;
+            const int h = hk * a.G + g0 + n / span;
+            f32x16 s = f32x16(0.f), dp = f32x16(0.f);
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                s = mma<T>(row_frag<T, DP>(qb, col, c * 16 + half * 8), kf[c], s);
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                dp = mma<T>(row_frag<T, DP>(gb, col, c * 16 + half * 8), vf[c], dp);
+            const float *lr = rl + buf * QB + 4 * half, *dr = rd + buf * QB + 4 * half;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) dp[r] -= dr[8 * (r / 4) + r % 4];
+            if (sh.transform) {
+                if (sh.cap) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const float th = cap_tanh<T>(s[r] * sh.capin);
+                        s[r] = sh.c2 * th;
+                        dp[r] *= 1.f - th * th;
+                    }
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) s[r] *= sh.c2;
+                }
+#pragma unroll
+                for (int x = 0; x < 3; ++x) {
+                    if (x >= a.axes) break;
+                    const float sl = a.slopes[h * a.axes + x] * kLog2e;
+                    const float *p = pq + (buf * 3 + x) * QB + 4 * half;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        s[r] = fmaf(-sl, fabsf(p[8 * (r / 4) + r % 4] - pk[x]), s[r]);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], sh.mul, -lr[8 * (r / 4) + r % 4]));
+                dp[r] *= s[r];
+            }
+            if (part) {
+                const int *l4 = slo + buf * QB + 4 * half, *h4 = shi + buf * QB + 4 * half;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int e = 8 * (r / 4) + r % 4;
+                    if (key < l4[e] || key >= h4[e]) s[r] = dp[r] = 0.f;
+                }
+            }
+            const Frag<T> p0 = pack8<T>(s, 0), p1 = pack8<T>(s, 1);
+            const Frag<T> e0 = pack8<T>(dp, 0), e1 = pack8<T>(dp, 1);
+            if (!(part && flag[n % 3])) {
+#pragma unroll
+                for (int d = 0; d < ND; ++d) {
+                    dv[d] = mma<T>(col_frag<T, DP>(gb, 0, d * 32, lane), p0, dv[d]);
+                    dv[d] = mma<T>(col_frag<T, DP>(gb, 1, d * 32, lane), p1, dv[d]);
+                    dk[d] = mma<T>(col_frag<T, DP>(qb, 0, d * 32, lane), e0, dk[d]);
+                    dk[d] = mma<T>(col_frag<T, DP>(qb, 1, d * 32, lane), e1, dk[d]);
+                }
+            } else {
+                dropped = true;
+#pragma unroll
+                for (int d = 0; d < ND; ++d) {
+                    Frag<T> f[4] = {col_frag<T, DP>(gb, 0, d * 32, lane),
+                                    col_frag<T, DP>(gb, 1, d * 32, lane),
+                                    col_frag<T, DP>(qb, 0, d * 32, lane),
+                                    col_frag<T, DP>(qb, 1, d * 32, lane)};
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) drop_nonfinite<T>(f[x]);
+                    dv[d] = mma<T>(f[0], p0, dv[d]);
+                    dv[d] = mma<T>(f[1], p1, dv[d]);
+                    dk[d] = mma<T>(f[2], e0, dk[d]);
+                    dk[d] = mma<T>(f[3], e1, dk[d]);
+                }
+            }
+        }
+        if (more) place(buf ^ 1, n + 1);
+        __syncthreads();
+    }
+    if (dropped) {
+        // infinities and NaN of do that were dropped, for the keys they reach
+        // (in dk they are there already: e is NaN with them)
+        for (int n = 0; n < steps; ++n) {
+            bool part;
+            if (!touched(n, &part) || !part) continue;
+            const int h = hk * a.G + g0 + n / span, q0 = (first + n % span) * QB;
+            for (int i = q0; i < min(q0 + QB, a.Tq); ++i) {
+                const int2 sp = *(const int2 *)(a.spans + 2 * ((int64_t)b * a.Tq + i));
+                const R *g = (const R *)a.dout + b * a.gs[0] + (int64_t)i * a.gs[1] + h * a.gs[2];
+                if (key < sp.x || key >= sp.y) continue;
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const int e = d * 32 + acc_row(r, half);
+                        const float v = e < a.D ? T::widen(g[e]) : 0.f;
+                        if (!(fabsf(v) < kInf)) dv[d][r] += v;
+                    }
+            }
+        }
+    }
+    if (key >= a.Tk) return;
+    const int64_t at = (((int64_t)b * a.Tk + key) * a.Hk + hk) * a.D;
+    if (a.gsplit == 1) {
+        store_cols<T, ND>((R *)a.dk + at, dk, a.scale, a.D, half);
+        store_cols<T, ND>((R *)a.dv + at, dv, 1.f, a.D, half);
+    } else {
+        const int64_t all = (int64_t)a.B * a.Tk * a.Hk * a.D;
+        store_cols<F32, ND>(a.part_dk + gpart * all + at, dk, a.scale, a.D, half);
+        store_cols<F32, ND>(a.part_dv + gpart * all + at, dv, 1.f, a.D, half);
+    }
+}
+
+// Adds the parts of dk and dv (blockIdx.y) in order.
+template <typename T>
+__global__ __launch_bounds__(256) void attn_parts_kernel(AttnArgs a)
+{
+    using R = typename T::raw;
+    const int64_t all = (int64_t)a.B * a.Tk * a.Hk * a.D;
+    const float *p = blockIdx.y ? a.part_dv : a.part_dk;
+    R *out = (R *)(blockIdx.y ? a.dv : a.dk);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all;
+         i += (int64_t)gridDim.x * 256) {
+        float s = 0.f;
+        for (int g = 0; g < a.gsplit; ++g) s += p[g * all + i];
+        out[i] = T::narrow(s);
+    }
+}
+
+template <typename T, int DP>
+void run(const AttnArgs &a, hipStream_t s)
+{
+    constexpr uint32_t tiles = 4 * kStep * DP * sizeof(typename T::raw);
+    const int64_t nq = (a.Tq + 32 * kWaves - 1) / (32 * kWaves);
+    const int64_t nk = (a.Tk + 32 * kWaves - 1) / (32 * kWaves);
+    if (nk > 0)
+        launch_kernel((attn_dkv_kernel<T, DP>), dim3((uint32_t)(nk * a.B * a.Hk * a.gsplit)),
+                      dim3(64 * kWaves), tiles + (2 * 3 + 8) * kStep * 4 + 5 * 4, s, a);
+    if (nk > 0 && a.gsplit > 1) {
+        const int64_t need = ((int64_t)a.B * a.Tk * a.Hk * a.D + 255) / 256;
+        launch_kernel((attn_parts_kernel<T>),
+                      dim3((uint32_t)(need < kMaxTileGrid ? need : kMaxTileGrid), 2), dim3(256), 0,
+                      s, a);
+    }
+    if (nq > 0)
+        launch_kernel((attn_dq_kernel<T, DP>), dim3((uint32_t)(nq * a.B * a.Hq)),
+                      dim3(64 * kWaves), tiles + 2 * 3 * kStep * 4 + (3 + 2 * kWaves) * 4, s, a);
+}
+
+int64_t round16(int64_t bytes) { return (bytes + 15) & ~(int64_t)15; }
+
+}  // namespace
+
+// Workspace: tiles, spans, rowd, then the parts (each at a multiple of 16
+// bytes).
+size_t plan_attn_backward(AttnArgs *a)
+{
+    const int64_t blocks = (int64_t)((a->Tk + 127) / 128) * a->B * a->Hk;
+    const int64_t want = 2 * device_cus();
+    int64_t g = blocks > 0 ? (want + blocks - 1) / blocks : 1;
+    a->gsplit = (int32_t)(g < 1 ? 1 : g > a->G ? a->G : g);
+    const int64_t nt = (a->Tq + 31) / 32, rows = (int64_t)a->B * a->Tq;
+    int64_t n = round16(rows * a->Hq * 8) + round16(rows * 8) + (int64_t)a->B * nt * 16;
+    if (a->gsplit > 1)
+        n += 2 * round16((int64_t)a->gsplit * a->B * a->Tk * a->Hk * a->D * 4);
+    return (size_t)n;
+}
+
+void place_attn_backward(AttnArgs *a, void *workspace)
+{
+    const int64_t nt = (a->Tq + 31) / 32, rows = (int64_t)a->B * a->Tq;
+    char *p = (char *)workspace;
+    a->tiles = (int32_t *)p;
+    p += (int64_t)a->B * nt * 16;
+    a->spans = (int32_t *)p;
+    p += round16(rows * 8);
+    a->rowd = (float *)p;
+    p += round16(rows * a->Hq * 8);
+    a->part_dk = (float *)p;
+    p += round16((int64_t)a->gsplit * a->B * a->Tk * a->Hk * a->D * 4);
+    a->part_dv = (float *)p;
+}
+
+template <typename T>
+hipError_t launch_attn_backward(const AttnArgs &a, hipStream_t s)
+{
+    const int64_t nt = (a.Tq + 31) / 32;
+    if (nt > 0)
+        launch_kernel((attn_rows_kernel<T>), dim3((uint32_t)(nt * a.B * a.Hq)), dim3(256), 0, s, a);
+    if (a.D <= 64) run<T, 64>(a, s);
+    else run<T, 128>(a, s);
+    return hipGetLastError();
+}
+
+template hipError_t launch_attn_backward<F32>(const AttnArgs &, hipStream_t);
+template hipError_t launch_attn_backward<F16>(const AttnArgs &, hipStream_t);
+template hipError_t launch_attn_backward<BF16>(const AttnArgs &, hipStream_t);
+
+}  // namespace mp3d

@@ -1,0 +1,281 @@
+// attention_fwd.hip -- attention forward for many queries.
+//
+//   out_i = sum_j p_ij v_j,  p_ij = exp(s_ij - lse_i),  lse_i = log sum_j exp(s_ij)
+// over the keys j that query i sees, in one pass with a running maximum and
+// sum per query.  A workgroup of four waves takes 128 queries of one head,
+// each wave 32 of them, and walks the keys that any of its queries sees in
+// tiles of 64, read once into LDS for the four waves (attention.hpp has the
+// layout).  The scores are formed as (keys x queries), so a query's scores
+// lie in two lanes: its maximum and sum are sums over registers and one
+// exchange between the wave's halves, and the weights go into the second
+// product where they are.
+//
+// The running maximum is only raised when a score exceeds it by 2^8 (the
+// weights then stay under 2^8, and the sums' relative error is the same);
+// raising it costs a pass over the accumulators.  Weights are rounded to the
+// storage type for the second product (its matrix instruction takes no
+// other), their sum is not: the rounding errors are independent and as
+// small as that of the output itself.
+#include "attention.hpp"
+
+namespace mp3d {
+
+namespace {
+
+constexpr int kFwdWaves = 4;
+constexpr int kFwdKeys = 64;
+constexpr float kRaise = 8.f;
+
+// float32 tiles of 128 channels take twice the LDS and the registers: one
+// workgroup on a CU
+template <typename T, int DP>
+constexpr int fwd_occupancy() { return sizeof(typename T::raw) * DP > 256 ? 1 : 2; }
+
+template <typename T, int DP>
+__global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn_fwd_kernel(AttnArgs a)
+{
+    using R = typename T::raw;
+    constexpr int NT = 64 * kFwdWaves, KB = kFwdKeys, NC = DP / 16, ND = DP / 32;
+    extern __shared__ __align__(16) unsigned char smem[];
+    R *const kt = (R *)smem;                               // [2][KB * DP]
+    R *const vt = kt + 2 * KB * DP;                        // [2][KB * DP]
+    float *const pk = (float *)(vt + 2 * KB * DP);         // [2][3][KB] key positions
+    int *const flag = (int *)(pk + 2 * 3 * KB);            // an infinity or a NaN was dropped
+    int *const ends = flag + 1;                            // [4][kFwdWaves]
+
+    // The heads of one sequence that share keys run on one XCD, and the
+    // queries that see most keys (the last, if causal) come first.
+    const int nq = (a.Tq + 32 * kFwdWaves - 1) / (32 * kFwdWaves);
+    const int heads = a.B * a.Hq;
+    int bh, qt;
+    if (heads % 8 == 0) {
+        const int per = heads / 8, j = blockIdx.x / 8;
+        bh = (blockIdx.x % 8) * per + j % per;
+        qt = nq - 1 - j / per;
+    } else {
+        bh = blockIdx.x % heads;
+        qt = nq - 1 - blockIdx.x / heads;
+    }
+    const int b = bh / a.Hq, h = bh - b * a.Hq, hk = h / a.G;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, col = lane & 31, half = lane >> 5;
+    const int q0 = qt * 32 * kFwdWaves, i = q0 + wave * 32 + col;
+    const int ic = min(i, a.Tq - 1);
+    const Span sp = row_span(a, b, ic);
+
+    // the wave's and the workgroup's keys: union, and the part all rows see
+    int wlo = sp.hi > sp.lo ? sp.lo : 0x7fffffff, whi = sp.hi, alo = sp.lo, ahi = sp.hi;
+#pragma unroll
+    for (int m = 16; m; m >>= 1) {
+        wlo = min(wlo, __shfl_xor(wlo, m));
+        whi = max(whi, __shfl_xor(whi, m));
+        alo = max(alo, __shfl_xor(alo, m));
+        ahi = min(ahi, __shfl_xor(ahi, m));
+    }
+    wlo = __builtin_amdgcn_readfirstlane(wlo);
+    whi = __builtin_amdgcn_readfirstlane(whi);
+    alo = __builtin_amdgcn_readfirstlane(alo);
+    ahi = __builtin_amdgcn_readfirstlane(ahi);
+    if ((tid & 63) == 0) {
+        ends[wave] = wlo;
+        ends[kFwdWaves + wave] = whi;
+        ends[2 * kFwdWaves + wave] = alo;
+        ends[3 * kFwdWaves + wave] = ahi;
+    }
+    if (tid == 0) *flag = 0;
+    __syncthreads();
+    int glo = ends[0], ghi = ends[kFwdWaves], galo = ends[2 * kFwdWaves],
+        gahi = ends[3 * kFwdWaves];
+#pragma unroll
+    for (int w = 1; w < kFwdWaves; ++w) {
+        glo = min(glo, ends[w]);
+        ghi = max(ghi, ends[kFwdWaves + w]);
+        galo = max(galo, ends[2 * kFwdWaves + w]);
+        gahi = min(gahi, ends[3 * kFwdWaves + w]);
+    }
+
+    const R *kp = (const R *)a.k + b * a.ks[0] + hk * a.ks[2];
+    const R *vp = (const R *)a.v + b * a.vs[0] + hk * a.vs[2];
+    const R *qp = (const R *)a.q + b * a.qs[0] + h * a.qs[2] + (int64_t)ic * a.qs[1];
+    Frag<T> qf[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) qf[c] = load8<T>(qp, c * 16 + half * 8, a.D, a.vec);
+
+    // positions relative to the workgroup's first query: differences of
+    // tokens near each other stay exact in binary32
+    float pq[3], sl[3];
+    int64_t base[3];
+#pragma unroll
+    for (int x = 0; x < 3; ++x) {
+        if (x >= a.axes) break;
+        const int32_t *p = a.pos_q + ((int64_t)x * a.B + b) * a.Tq;
+        base[x] = p[q0];
+        pq[x] = (float)(p[ic] - base[x]);
+        sl[x] = a.slopes[h * a.axes + x] * kLog2e;
+    }
+    const ScoreMul sm = score_mul(a);
+    const float capin = a.cap > 0.f ? a.scale / a.cap : 0.f;
+    const float c2 = a.cap > 0.f ? a.cap * kLog2e : a.scale * kLog2e;
+
+    f32x16 o[ND];
+#pragma unroll
+    for (int d = 0; d < ND; ++d) o[d] = f32x16(0.f);
+    float m = kNegInf, l = 0.f;            // l: this half's sum
+
+    const int kbeg = ghi > 0 ? glo / KB * KB : 0, kend = ghi;
+    TileRegs<T, DP, KB, NT> kr, vr;
+    float pr[3];
+    auto fetch = [&](int k0) {
+        kr.load(kp, a.ks[1], k0, glo, ghi, a.D, a.vec, tid);
+        vr.load(vp, a.vs[1], k0, glo, ghi, a.D, a.vec, tid);
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+            if (x < a.axes && tid < KB)
+                pr[x] = (float)(a.pos_k[((int64_t)x * a.B + b) * a.Tk + min(k0 + tid, a.Tk - 1)] -
+                                base[x]);
+    };
+    auto place = [&](int k0, int buf) {
+        if (!(galo <= k0 && k0 + KB <= gahi) && vr.drop()) *flag = 1;
+        kr.store(kt + buf * KB * DP, tid);
+        vr.store(vt + buf * KB * DP, tid);
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+            if (x < a.axes && tid < KB) pk[(buf * 3 + x) * KB + tid] = pr[x];
+    };
+    if (kbeg < kend) {
+        fetch(kbeg);
+        place(kbeg, 0);
+    }
+    __syncthreads();
+    int n = 0;
+    for (int k0 = kbeg; k0 < kend; k0 += KB, ++n) {
+        const int buf = n & 1;
+        const bool more = k0 + KB < kend;
+        if (more) fetch(k0 + KB);
+        if (k0 < whi && k0 + KB > wlo) {
+            const R *kb = kt + buf * KB * DP, *vb = vt + buf * KB * DP;
+            f32x16 s[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                s[u] = f32x16(0.f);
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+                    s[u] = mma<T>(row_frag<T, DP>(kb, u * 32 + col, c * 16 + half * 8), qf[c],
+                                  s[u]);
+            }
+            if (sm.transform) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    if (a.cap > 0.f) {
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) s[u][r] = c2 * cap_tanh<T>(s[u][r] * capin);
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) s[u][r] *= c2;
+                    }
+#pragma unroll
+                    for (int x = 0; x < 3; ++x) {
+                        if (x >= a.axes) break;
+                        const float *p = pk + (buf * 3 + x) * KB + u * 32 + 4 * half;
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+                            s[u][r] = fmaf(-sl[x], fabsf(p[8 * (r / 4) + r % 4] - pq[x]), s[u][r]);
+                    }
+                }
+            }
+            const bool part = !(alo <= k0 && k0 + KB <= ahi);
+            if (part) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const int key = k0 + u * 32 + acc_row(r, half);
+                        if (key < sp.lo || key >= sp.hi) s[u][r] = kNegInf;
+                    }
+            }
+            float mx = s[0][0];
+#pragma unroll
+            for (int r = 1; r < 16; ++r) mx = fmaxf(mx, s[0][r]);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[1][r]);
+            mx = fmaxf(mx, other_half(mx)) * sm.mul;
+            if (__any(mx > m + kRaise)) {
+                // (each query by itself: its result does not depend on its neighbours)
+                const float mn = mx > m + kRaise ? mx : m;
+                const float al = __builtin_amdgcn_exp2f(m - (mn == kNegInf ? 0.f : mn));
+                l *= al;
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) o[d][r] *= al;
+                m = mn;
+            }
+            const float ms = m == kNegInf ? 0.f : m;
+            Frag<T> pf[4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    s[u][r] = __builtin_amdgcn_exp2f(fmaf(s[u][r], sm.mul, -ms));
+                    l += s[u][r];
+                }
+                pf[2 * u] = pack8<T>(s[u], 0);
+                pf[2 * u + 1] = pack8<T>(s[u], 1);
+            }
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    o[d] = mma<T>(col_frag<T, DP>(vb, c, d * 32, lane), pf[c], o[d]);
+        }
+        if (more) place(k0 + KB, buf ^ 1);
+        __syncthreads();
+    }
+
+    if (*flag) {                           // (the loop's last barrier is behind us)
+        for (int key = kbeg; key < kend; ++key) {
+            const int k0 = key / KB * KB;
+            if ((galo <= k0 && k0 + KB <= gahi) || key < sp.lo || key >= sp.hi) continue;
+            const R *p = vp + (int64_t)key * a.vs[1];
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int e = d * 32 + acc_row(r, half);
+                    const float v = e < a.D ? T::widen(p[e]) : 0.f;
+                    if (!(fabsf(v) < __builtin_huge_valf())) o[d][r] += v;
+                }
+        }
+    }
+
+    if (i >= a.Tq) return;
+    l += other_half(l);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (half == 0)
+        a.lse[((int64_t)b * a.Hq + h) * a.Tq + i] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
+    store_cols<T, ND>((R *)a.out + (((int64_t)b * a.Tq + i) * a.Hq + h) * a.D, o, inv, a.D, half);
+}
+
+template <typename T, int DP>
+hipError_t run(const AttnArgs &a, hipStream_t s)
+{
+    constexpr uint32_t lds = 4 * kFwdKeys * DP * sizeof(typename T::raw) +
+                             2 * 3 * kFwdKeys * sizeof(float) + (1 + 4 * kFwdWaves) * sizeof(int);
+    const int64_t nq = (a.Tq + 32 * kFwdWaves - 1) / (32 * kFwdWaves);
+    launch_kernel((attn_fwd_kernel<T, DP>), dim3((uint32_t)(nq * a.B * a.Hq)),
+                  dim3(64 * kFwdWaves), lds, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+template <typename T>
+hipError_t launch_attn_forward(const AttnArgs &a, hipStream_t s)
+{
+    return a.D <= 64 ? run<T, 64>(a, s) : run<T, 128>(a, s);
+}
+
+template hipError_t launch_attn_forward<F32>(const AttnArgs &, hipStream_t);
+template hipError_t launch_attn_forward<F16>(const AttnArgs &, hipStream_t);
+template hipError_t launch_attn_forward<BF16>(const AttnArgs &, hipStream_t);
+
+}  // namespace mp3d

@@ -1,6 +1,7 @@
 /*
  * mp3d.h -- C ABI of libmp3d: 3-D max pooling over NCDHW tensors on AMD
- * Instinct MI355X (gfx950).
+ * Instinct MI355X (gfx950), and operators over the pooled volumes' tokens
+ * (rotary positions, attention, gated norm; a section of their own below).
  *
  * Operations:
  *  - forward, fixed windows: "Struct Maxpool3dForward" (teenygrad API docs),
@@ -301,6 +302,151 @@ int mp3d_backward_workspace_bytes(int dtype, int idx_type, int64_t N, int64_t C,
  * launches nothing records neither event).  stop_event NULL disarms;
  * start_event without stop_event is MP3D_EINVAL. */
 int mp3d_time_next_call(void *start_event, void *stop_event);
+
+/* --- Operators over a pooled volume's tokens ---------------------------
+ *
+ * A pooled (N, C, D, H, W) volume is, cell by cell in d, h, w scan order, a
+ * sequence of T = D*H*W tokens (the order of idx).  These entry points are
+ * what a token model puts on such sequences: rotary positions over the
+ * volume's axes, attention, and the norm that joins a block's output to the
+ * residual stream, each with its backward.  They define their own
+ * mathematics (stated at each call); the pages above have no such
+ * operators.
+ *
+ * Storage types: MP3D_F32, MP3D_F16, MP3D_BF16 (MP3D_F64: MP3D_EDTYPE).
+ * Every sum, softmax statistic and norm is held in binary32 and rounded
+ * once on its way out.  Strides are in elements, for (batch, token, head),
+ * and >= 0; a head's channels are adjacent.  Accesses are 16 bytes wide
+ * where every row starts at a multiple of 16 bytes, and element-wise
+ * otherwise.  Streams, errors, MP3D_LOG and mp3d_time_next_call are as for
+ * the pooling calls; results are the same bits on every run (no atomics). */
+
+/* Rotary positions over three axes, for q (B, T, Hq, D) and k (B, T, Hk, D)
+ * in one launch (Hk or Hq may be 0: that tensor is absent).  Of a head's D
+ * channels the first 2P turn, P = pairs[0] + pairs[1] + pairs[2] <= D / 2:
+ * pair i is channels (i, P + i), or (2i, 2i + 1) when interleaved, and
+ * turns by the angle position[axis(i)] * inv_freq[i], where the first
+ * pairs[0] pairs go by the first axis, the next pairs[1] by the second, the
+ * last by the third:
+ *   (u, v) -> (u cos - v sin, u sin + v cos).
+ * The other channels are copied.  Positions: `positions` int32 (3, B, T) in
+ * device memory, or NULL and `grid` = {d, h, w} (host memory) with
+ * d*h*w == T: token t stands at cell t of the grid.  inv_freq: float32 (P)
+ * in device memory.  The angle is reduced in binary64, so it keeps its
+ * accuracy at any position.  An output may be its input with the same
+ * strides (in place); otherwise outputs overlap nothing. */
+int mp3d_rope_forward(const void *q, const void *k, void *q_out, void *k_out, int dtype,
+                      int64_t B, int64_t T, int32_t Hq, int32_t Hk, int32_t D,
+                      const int64_t *q_stride, const int64_t *k_stride,
+                      const int64_t *q_out_stride, const int64_t *k_out_stride,
+                      const float *inv_freq, const int32_t *pairs,
+                      const int32_t *positions, const int32_t *grid, int interleaved,
+                      void *stream);
+
+/* Gradients of the turned q and k to gradients of q and k: the turn by the
+ * negative angle.  Arguments as for mp3d_rope_forward. */
+int mp3d_rope_backward(const void *gq, const void *gk, void *gq_out, void *gk_out, int dtype,
+                       int64_t B, int64_t T, int32_t Hq, int32_t Hk, int32_t D,
+                       const int64_t *q_stride, const int64_t *k_stride,
+                       const int64_t *q_out_stride, const int64_t *k_out_stride,
+                       const float *inv_freq, const int32_t *pairs,
+                       const int32_t *positions, const int32_t *grid, int interleaved,
+                       void *stream);
+
+/* Attention of q (B, Tq, Hq, D) over k, v (B, Tk, Hk, D), D <= 128; Hq is a
+ * multiple of Hk, and Hq / Hk consecutive query heads share a key head.
+ *   s_ij = scale q_i . k_j
+ *   s_ij = softcap tanh(s_ij / softcap)                    (softcap > 0)
+ *   s_ij = s_ij - sum_a slopes[h, a] |pos_q[a, i] - pos_k[a, j]|   (axes > 0)
+ *   out_i = sum_j exp(s_ij - lse_i) v_j,  lse_i = log sum_j exp(s_ij)
+ * over the keys j that query i sees.  With L = kv_len[b] (Tk without
+ * kv_len; clamped to 0 .. Tk), query i stands at position p = i + L - Tq
+ * (the queries are the last Tq of L tokens).  It sees
+ *   - the keys [0, L); with documents, those of [doc_offsets[b, d],
+ *     doc_offsets[b, d + 1]) cut to [0, L), d the last document that starts at
+ *     or before p; a query in no document sees none.  doc_offsets is not
+ *     decreasing (a document may be empty);
+ *   - if causal, of these only the keys up to p, and the first
+ *     prefix[b, d] of its document (of the sequence without documents),
+ *     which are seen by all.
+ * A query that sees no key, or only scores of -infinity, gets out = 0 and
+ * lse = -infinity.  Infinities and NaN in keys and values reach the queries
+ * that see them and no others.  All pointers but the descriptor are device
+ * memory; pointers that are NULL switch their part off. */
+typedef struct mp3d_attention {
+    int dtype;
+    int64_t B, Tq, Tk;
+    int32_t Hq, Hk, D;
+    int64_t q_stride[3], k_stride[3], v_stride[3]; /* batch, token, head */
+    float scale, softcap;
+    int causal;
+    const int32_t *kv_len;       /* (B) */
+    const int32_t *doc_offsets;  /* (B, n_docs + 1) */
+    int32_t n_docs;
+    const int32_t *prefix;       /* (B, n_docs), or (B) without documents; needs causal */
+    int32_t axes;                /* 0: no bias by distance; at most 3 */
+    const float *slopes;         /* (Hq, axes); constants, not differentiated */
+    const int32_t *pos_q;        /* (axes, B, Tq) */
+    const int32_t *pos_k;        /* (axes, B, Tk) */
+} mp3d_attention;
+
+/* Device workspace, in bytes, that the forward (backward = 0) or the
+ * backward (1) of this descriptor takes (0: none).  16-byte aligned; its
+ * contents do not matter; the caller may reuse it once the stream has
+ * passed the call.  Depends on the current device's number of CUs. */
+int mp3d_attention_workspace_bytes(const mp3d_attention *a, int backward, size_t *bytes);
+
+/* Writes out (B, Tq, Hq, D), contiguous, 16-byte aligned, and lse
+ * (B, Hq, Tq) float32.  MP3D_EWORKSPACE if the workspace is short. */
+int mp3d_attention_forward(const mp3d_attention *a, const void *q, const void *k, const void *v,
+                           void *out, float *lse, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
+/* Gradients dq (B, Tq, Hq, D), dk and dv (B, Tk, Hk, D), contiguous and
+ * 16-byte aligned, from dout (B, Tq, Hq, D) of strides dout_stride and the
+ * forward's inputs, out and lse.  dk and dv are sums over the query heads
+ * that share a key head; keys that no query sees get 0. */
+int mp3d_attention_backward(const mp3d_attention *a, const void *dout, const int64_t *dout_stride,
+                            const void *q, const void *k, const void *v, const void *out,
+                            const float *lse, void *dq, void *dk, void *dv, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/* Norms of the gated norm, and which of its two are there. */
+enum mp3d_norm { MP3D_NORM_RMS = 0, MP3D_NORM_LAYER = 1 };
+enum mp3d_norm_parts { MP3D_NORM_POST = 1, MP3D_NORM_PRE = 2 };
+
+/* The norm after a block, its gate and residual scale, the residual sum,
+ * and the norm before the next block, on rows of C <= 16384 channels:
+ *   y = x + residual_scale * gate * post_weight * n(h)
+ *   z = pre_weight * n(y)
+ *   n(a) = (a - mean(a)) / sqrt(mean((a - mean(a))^2) + eps)
+ * with mean(a) = 0 for MP3D_NORM_RMS.  x is the residual stream, h the
+ * block's output, both (rows, C), contiguous.  Without MP3D_NORM_POST n(h) is
+ * h; without MP3D_NORM_PRE there is no z.  h NULL: no block, y = x is not
+ * written (z = pre_weight * n(x)).  gate: (gate_rows, C), each row for
+ * rows / gate_rows rows that follow each other, or NULL; weights (C) or
+ * NULL.  z is formed from y before its rounding.  stats: float32 (rows, 4),
+ * 16-byte aligned, for the backward, or NULL. */
+int mp3d_gated_norm_forward(const void *x, const void *h, const void *gate,
+                            const void *post_weight, const void *pre_weight, void *y, void *z,
+                            float *stats, int dtype, int64_t rows, int32_t C, int64_t gate_rows,
+                            float residual_scale, int kind, int parts, float eps, void *stream);
+
+/* Device workspace of the backward, in bytes (gate_rows 0: no gate). */
+int mp3d_gated_norm_workspace_bytes(int dtype, int64_t rows, int32_t C, int64_t gate_rows,
+                                    size_t *bytes);
+
+/* Gradients from those of y (dy, or NULL: 0) and z (dz): dx and dh in the
+ * storage type, dgate (gate_rows, C) and the weights' in float32, summed
+ * over the rows in a fixed order.  dgate goes with gate; a weight's
+ * gradient may be NULL (not wanted). */
+int mp3d_gated_norm_backward(const void *dy, const void *dz, const void *x, const void *h,
+                             const void *gate, const void *post_weight, const void *pre_weight,
+                             const float *stats, void *dx, void *dh, float *dgate,
+                             float *dpost_weight, float *dpre_weight, int dtype, int64_t rows,
+                             int32_t C, int64_t gate_rows, float residual_scale, int kind,
+                             int parts, float eps, void *workspace, size_t workspace_bytes,
+                             void *stream);
 
 /* Text for a status code (static storage). */
 const char *mp3d_strerror(int code);
