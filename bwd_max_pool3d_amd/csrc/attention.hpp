@@ -112,6 +112,22 @@ __device__ __forceinline__ void store_cols(typename T::raw *out, const f32x16 *o
         }
 }
 
+// The values of a result's rows from an array of 32 in LDS (16-byte aligned).
+template <typename E>
+__device__ __forceinline__ auto acc_rows(const E *v, int half)
+{
+    typedef E e4 __attribute__((ext_vector_type(4)));
+    typedef E e16 __attribute__((ext_vector_type(16)));
+    e16 o;
+#pragma unroll
+    for (int r = 0; r < 16; r += 4) {
+        const e4 x = *(const e4 *)(v + acc_row(r, half));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[r + i] = x[i];
+    }
+    return o;
+}
+
 // The other half's value.
 __device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
 
@@ -270,21 +286,23 @@ struct TileRegs {
             for (int i = 0; i < Frag<T>::NV; ++i) p[i] = f[j].w[i];
         }
     }
-    __device__ __forceinline__ bool nonfinite() const
-    {
-        bool bad = false;
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            Frag<T> x = f[j];
-            bad |= drop_nonfinite<T>(x);
-        }
-        return bad;
-    }
     __device__ __forceinline__ bool drop()
     {
         bool bad = false;
 #pragma unroll
         for (int j = 0; j < N; ++j) bad |= drop_nonfinite<T>(f[j]);
+        return bad;
+    }
+    // the same, with the rows that held one marked
+    __device__ __forceinline__ bool drop(int *row_mark, int mark, int t)
+    {
+        bool bad = false;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (drop_nonfinite<T>(f[j])) {
+                row_mark[(t + NT * j) / (DP / 8)] = mark;
+                bad = true;
+            }
         return bad;
     }
 };
@@ -296,7 +314,11 @@ struct TileRegs {
 // zeros.  Where some see a key and others do not, its infinities and NaN are
 // staged as zeros too, and added afterwards to the results of those who do
 // see it: a positive weight times such a value is that value, so the weight
-// itself is not needed.
+// itself is not needed.  In dq and dk nothing is added: there a weight's
+// gradient is NaN with it already.  (A key that is not finite gives a query
+// the score -infinity, and weight 0, or makes its lse NaN: dq sets the
+// score of such a key to -infinity, which gives both.  A query that is not
+// finite has no finite score, so its lse is NaN, or -infinity.)
 //
 // --- the keys a query sees
 struct Span {

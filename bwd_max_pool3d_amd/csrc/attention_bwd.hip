@@ -83,9 +83,7 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a)
     }
 }
 
-// From a step's products to the weights p and to e / (dp - delta) = p times
-// the cap's slope: s holds q.k on entry and p on return; slope is written
-// (and 1 without a cap).
+// How scores become exponents (see ScoreMul), and the cap's constants.
 struct Shape {
     float capin, c2, mul;
     bool cap, transform;
@@ -112,8 +110,9 @@ __global__ __launch_bounds__(64 * kWaves, (bwd_occupancy<T, DP>())) void attn_dq
     R *const kt = (R *)smem;                               // [2][KB * DP]
     R *const vt = kt + 2 * KB * DP;                        // [2][KB * DP]
     float *const pk = (float *)(vt + 2 * KB * DP);         // [2][3][KB]
-    int *const flag = (int *)(pk + 2 * 3 * KB);            // [3] a tile holds an inf or a NaN
-    int *const ends = flag + 3;                            // [2][kWaves]
+    int *const bad = (int *)(pk + 2 * 3 * KB);             // [2][KB] 1 + last step with a key's inf or NaN
+    int *const flag = bad + 2 * KB;                        // there was one
+    int *const ends = flag + 1;                            // [4][kWaves]
 
     const int nq = (a.Tq + 32 * kWaves - 1) / (32 * kWaves);
     const int heads = a.B * a.Hq;
@@ -139,14 +138,19 @@ __global__ __launch_bounds__(64 * kWaves, (bwd_occupancy<T, DP>())) void attn_dq
     if (lane == 0) {
         ends[wave] = wlo;
         ends[kWaves + wave] = whi;
+        ends[2 * kWaves + wave] = alo;
+        ends[3 * kWaves + wave] = ahi;
     }
-    if (tid < 3) flag[tid] = 0;
+    if (tid < 2 * KB) bad[tid] = 0;
+    if (tid == 0) *flag = 0;
     __syncthreads();
-    int glo = ends[0], ghi = ends[kWaves];
+    int glo = ends[0], ghi = ends[kWaves], galo = ends[2 * kWaves], gahi = ends[3 * kWaves];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) {
         glo = min(glo, ends[w]);
         ghi = max(ghi, ends[kWaves + w]);
+        galo = max(galo, ends[2 * kWaves + w]);
+        gahi = min(gahi, ends[3 * kWaves + w]);
     }
 
     const R *kp = (const R *)a.k + b * a.ks[0] + hk * a.ks[2];
@@ -177,28 +181,28 @@ __global__ __launch_bounds__(64 * kWaves, (bwd_occupancy<T, DP>())) void attn_dq
     for (int d = 0; d < ND; ++d) o[d] = f32x16(0.f);
 
     const int kbeg = ghi > 0 ? glo / KB * KB : 0, kend = ghi;
+    // (nothing in flight is touched before place: that would wait for it)
     TileRegs<T, DP, KB, NT> kr, vr;
-    float pr[3];
+    int32_t pr[3];
     auto fetch = [&](int k0) {
         kr.load(kp, a.ks[1], k0, glo, ghi, a.D, a.vec, tid);
         vr.load(vp, a.vs[1], k0, glo, ghi, a.D, a.vec, tid);
 #pragma unroll
         for (int x = 0; x < 3; ++x)
             if (x < a.axes && tid < KB)
-                pr[x] = (float)(a.pos_k[((int64_t)x * a.B + b) * a.Tk + min(k0 + tid, a.Tk - 1)] -
-                                base[x]);
+                pr[x] = a.pos_k[((int64_t)x * a.B + b) * a.Tk + min(k0 + tid, a.Tk - 1)];
     };
-    auto place = [&](int buf, int n) {
+    auto place = [&](int k0, int buf, int n) {
+        if (!(galo <= k0 && k0 + KB <= gahi) && kr.drop(bad + buf * KB, n + 1, tid)) *flag = 1;
         kr.store(kt + buf * KB * DP, tid);
         vr.store(vt + buf * KB * DP, tid);
 #pragma unroll
         for (int x = 0; x < 3; ++x)
-            if (x < a.axes && tid < KB) pk[(buf * 3 + x) * KB + tid] = pr[x];
-        if (kr.nonfinite()) flag[n % 3] = 1;
+            if (x < a.axes && tid < KB) pk[(buf * 3 + x) * KB + tid] = (float)(pr[x] - base[x]);
     };
     if (kbeg < kend) {
         fetch(kbeg);
-        place(0, 0);
+        place(kbeg, 0, 0);
     }
     __syncthreads();
     int n = 0;
@@ -206,7 +210,6 @@ __global__ __launch_bounds__(64 * kWaves, (bwd_occupancy<T, DP>())) void attn_dq
         const int buf = n & 1;
         const bool more = k0 + KB < kend;
         if (more) fetch(k0 + KB);
-        if (tid == 0) flag[(n + 2) % 3] = 0;               // read last in step n - 1
         if (k0 < whi && k0 + KB > wlo) {
             const R *kb = kt + buf * KB * DP, *vb = vt + buf * KB * DP;
             f32x16 s = f32x16(0.f), dp = f32x16(0.f);
@@ -233,44 +236,33 @@ __global__ __launch_bounds__(64 * kWaves, (bwd_occupancy<T, DP>())) void attn_dq
 #pragma unroll
                 for (int x = 0; x < 3; ++x) {
                     if (x >= a.axes) break;
-                    const float *p = pk + (buf * 3 + x) * KB + 4 * half;
+                    const f32x16 p = acc_rows(pk + (buf * 3 + x) * KB, half);
 #pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        s[r] = fmaf(-sl[x], fabsf(p[8 * (r / 4) + r % 4] - pq[x]), s[r]);
+                    for (int r = 0; r < 16; ++r) s[r] = fmaf(-sl[x], fabsf(p[r] - pq[x]), s[r]);
                 }
+            }
+            const bool part = !(alo <= k0 && k0 + KB <= ahi);
+            if (part && *flag) {
+                const auto x = acc_rows(bad + buf * KB, half);
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[r] = x[r] == n + 1 ? kNegInf : s[r];
             }
 #pragma unroll
             for (int r = 0; r < 16; ++r)
                 s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], sh.mul, -rd.x)) * dp[r];
-            const bool part = !(alo <= k0 && k0 + KB <= ahi);
             if (part) {
+                const uint32_t at = k0 + 4 * half - sp.x, len = sp.y - sp.x;
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int key = k0 + acc_row(r, half);
-                    if (key < sp.x || key >= sp.y) s[r] = 0.f;
-                }
+                for (int r = 0; r < 16; ++r) s[r] = at + acc_row(r, 0) < len ? s[r] : 0.f;
             }
             const Frag<T> e0 = pack8<T>(s, 0), e1 = pack8<T>(s, 1);
-            if (!(part && flag[n % 3])) {
 #pragma unroll
-                for (int d = 0; d < ND; ++d) {
-                    o[d] = mma<T>(col_frag<T, DP>(kb, 0, d * 32, lane), e0, o[d]);
-                    o[d] = mma<T>(col_frag<T, DP>(kb, 1, d * 32, lane), e1, o[d]);
-                }
-            } else {
-                // (a key that is seen and not finite has made e NaN already)
-#pragma unroll
-                for (int d = 0; d < ND; ++d) {
-                    Frag<T> f0 = col_frag<T, DP>(kb, 0, d * 32, lane);
-                    Frag<T> f1 = col_frag<T, DP>(kb, 1, d * 32, lane);
-                    drop_nonfinite<T>(f0);
-                    drop_nonfinite<T>(f1);
-                    o[d] = mma<T>(f0, e0, o[d]);
-                    o[d] = mma<T>(f1, e1, o[d]);
-                }
+            for (int d = 0; d < ND; ++d) {
+                o[d] = mma<T>(col_frag<T, DP>(kb, 0, d * 32, lane), e0, o[d]);
+                o[d] = mma<T>(col_frag<T, DP>(kb, 1, d * 32, lane), e1, o[d]);
             }
         }
-        if (more) place(buf ^ 1, n + 1);
+        if (more) place(k0 + KB, buf ^ 1, n + 1);
         __syncthreads();
     }
     if (i >= a.Tq) return;
@@ -293,10 +285,10 @@ __global__ __launch_bounds__(64 * kWaves, (dkv_occupancy<T, DP>())) void attn_dk
     float *const pq = (float *)(gt + 2 * QB * DP);         // [2][3][QB] positions
     float *const rl = pq + 2 * 3 * QB;                     // [2][QB] lse * log2 e
     float *const rd = rl + 2 * QB;                         // [2][QB] delta
-    int *const slo = (int *)(rd + 2 * QB);                 // [2][QB] spans
-    int *const shi = slo + 2 * QB;
-    int *const flag = shi + 2 * QB;                        // [3]
-    int *const ends = flag + 3;                            // [2] first and last tile
+    int *const slo = (int *)(rd + 2 * QB);                 // [2][QB] first key seen
+    int *const sln = slo + 2 * QB;                         // [2][QB] keys seen
+    int *const flag = sln + 2 * QB;                        // an infinity or a NaN was dropped
+    int *const ends = flag + 1;                            // [2] first and last tile
 
     // parts of one key head, and the key blocks of one sequence, on one XCD
     const int nk = (a.Tk + 32 * kWaves - 1) / (32 * kWaves);
@@ -316,7 +308,7 @@ __global__ __launch_bounds__(64 * kWaves, (dkv_occupancy<T, DP>())) void attn_dk
     const int32_t *tiles = a.tiles + 4 * (int64_t)b * nt;
 
     // the tiles of queries that see a key of this block
-    if (tid < 3) flag[tid] = 0;
+    if (tid == 0) *flag = 0;
     if (tid < 2) ends[tid] = tid ? -1 : nt;
     __syncthreads();
     {
@@ -359,65 +351,72 @@ __global__ __launch_bounds__(64 * kWaves, (dkv_occupancy<T, DP>())) void attn_dk
 #pragma unroll
     for (int d = 0; d < ND; ++d) dk[d] = dv[d] = f32x16(0.f);
 
+    // (nothing in flight is touched before place: that would wait for it)
     TileRegs<T, DP, QB, NT> qr, gr;
-    float prq[3];
+    int32_t prq[3];
+    int4 nu = make_int4(0, 0, 0, 0);       // the tile's keys (see AttnArgs::tiles)
+    float nsl[3] = {0.f, 0.f, 0.f}, sl[3];  // the head's slopes
     float2 prd = make_float2(0.f, 0.f);
     int2 psp = make_int2(0, 0);
-    // step n: head hk * G + g0 + n / span, tile first + n % span
-    auto fetch = [&](int n) {
-        const int h = hk * a.G + g0 + n / span, q0 = (first + n % span) * QB;
+    // the next step's head and tile of queries
+    int fh = hk * a.G + g0, ft = first;
+    bool past = false;
+    auto fetch = [&]() {
+        const int h = fh, q0 = ft * QB;
         qr.load((const R *)a.q + b * a.qs[0] + h * a.qs[2], a.qs[1], q0, 0, a.Tq, a.D, a.vec, tid);
         gr.load((const R *)a.dout + b * a.gs[0] + h * a.gs[2], a.gs[1], q0, 0, a.Tq, a.D, a.vec,
                 tid);
         if (tid < QB) {
             const int i = min(q0 + tid, a.Tq - 1);
+            past = q0 + tid >= a.Tq;
             prd = *(const float2 *)(a.rowd + 2 * (((int64_t)b * a.Hq + h) * a.Tq + i));
             psp = *(const int2 *)(a.spans + 2 * ((int64_t)b * a.Tq + i));
-            if (q0 + tid >= a.Tq) {                // no query, no weight
-                prd = make_float2(kInf, 0.f);
-                psp = make_int2(0, 0);
-            }
 #pragma unroll
             for (int x = 0; x < 3; ++x)
-                if (x < a.axes)
-                    prq[x] = (float)(a.pos_q[((int64_t)x * a.B + b) * a.Tq + i] - base[x]);
+                if (x < a.axes) prq[x] = a.pos_q[((int64_t)x * a.B + b) * a.Tq + i];
+        }
+        nu = *(const int4 *)(tiles + 4 * (int64_t)ft);
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+            if (x < a.axes) nsl[x] = a.slopes[h * a.axes + x];
+        if (++ft > last) {
+            ft = first;
+            ++fh;
         }
     };
-    auto place = [&](int buf, int n) {
+    auto place = [&](int buf) {
+        if (!(nu.z <= k0 && k0 + 32 * kWaves <= nu.w)) {
+            const bool x = qr.drop(), y = gr.drop();
+            if (x || y) *flag = 1;
+        }
         qr.store(qt + buf * QB * DP, tid);
         gr.store(gt + buf * QB * DP, tid);
         if (tid < QB) {
-            rl[buf * QB + tid] = prd.x;
-            rd[buf * QB + tid] = prd.y;
-            slo[buf * QB + tid] = psp.x;
-            shi[buf * QB + tid] = psp.y;
+            // past the last query: no weight
+            rl[buf * QB + tid] = past ? kInf : prd.x;
+            rd[buf * QB + tid] = past ? 0.f : prd.y;
+            slo[buf * QB + tid] = past ? 0 : psp.x;
+            sln[buf * QB + tid] = past ? 0 : psp.y - psp.x;
 #pragma unroll
             for (int x = 0; x < 3; ++x)
-                if (x < a.axes) pq[(buf * 3 + x) * QB + tid] = prq[x];
+                if (x < a.axes) pq[(buf * 3 + x) * QB + tid] = (float)(prq[x] - base[x]);
         }
-        if (qr.nonfinite() || gr.nonfinite()) flag[n % 3] = 1;
     };
-    // (the union of keys of tile n % span, whether all its queries see the wave's keys)
-    auto touched = [&](int n, bool *part) {
-        const int32_t *u = tiles + 4 * (int64_t)(first + n % span);
-        *part = !(u[2] <= kw && kw + 32 <= u[3]);
-        return u[0] < kw + 32 && u[1] > kw;
-    };
-    bool dropped = false;
     if (steps > 0) {
-        fetch(0);
-        place(0, 0);
+        fetch();
+        place(0);
     }
     __syncthreads();
     for (int n = 0; n < steps; ++n) {
         const int buf = n & 1;
         const bool more = n + 1 < steps;
-        if (more) fetch(n + 1);
-        if (tid == 0) flag[(n + 2) % 3] = 0;
-        bool part;
-        if (touched(n, &part)) {
+        const int4 u = nu;
+#pragma unroll
+        for (int x = 0; x < 3; ++x) sl[x] = nsl[x] * kLog2e;
+        if (more) fetch();
+        if (__builtin_amdgcn_readfirstlane(u.x < kw + 32 && u.y > kw)) {
             const R *qb = qt + buf * QB * DP, *gb = gt + buf * QB * DP;
-            const int h = hk * a.G + g0 + n / span;
+            const bool part = !__builtin_amdgcn_readfirstlane(u.z <= kw && kw + 32 <= u.w);
             f32x16 s = f32x16(0.f), dp = f32x16(0.f);
 #pragma unroll
             for (int c = 0; c < NC; ++c)
@@ -425,9 +424,9 @@ __global__ __launch_bounds__(64 * kWaves, (dkv_occupancy<T, DP>())) void attn_dk
 #pragma unroll
             for (int c = 0; c < NC; ++c)
                 dp = mma<T>(row_frag<T, DP>(gb, col, c * 16 + half * 8), vf[c], dp);
-            const float *lr = rl + buf * QB + 4 * half, *dr = rd + buf * QB + 4 * half;
+            const f32x16 lr = acc_rows(rl + buf * QB, half), dr = acc_rows(rd + buf * QB, half);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) dp[r] -= dr[8 * (r / 4) + r % 4];
+            for (int r = 0; r < 16; ++r) dp[r] -= dr[r];
             if (sh.transform) {
                 if (sh.cap) {
 #pragma unroll
@@ -443,62 +442,44 @@ __global__ __launch_bounds__(64 * kWaves, (dkv_occupancy<T, DP>())) void attn_dk
 #pragma unroll
                 for (int x = 0; x < 3; ++x) {
                     if (x >= a.axes) break;
-                    const float sl = a.slopes[h * a.axes + x] * kLog2e;
-                    const float *p = pq + (buf * 3 + x) * QB + 4 * half;
+                    const f32x16 p = acc_rows(pq + (buf * 3 + x) * QB, half);
 #pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        s[r] = fmaf(-sl, fabsf(p[8 * (r / 4) + r % 4] - pk[x]), s[r]);
+                    for (int r = 0; r < 16; ++r) s[r] = fmaf(-sl[x], fabsf(p[r] - pk[x]), s[r]);
                 }
             }
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], sh.mul, -lr[8 * (r / 4) + r % 4]));
+                s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], sh.mul, -lr[r]));
                 dp[r] *= s[r];
             }
             if (part) {
-                const int *l4 = slo + buf * QB + 4 * half, *h4 = shi + buf * QB + 4 * half;
+                const auto lo = acc_rows(slo + buf * QB, half), len = acc_rows(sln + buf * QB, half);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    const int e = 8 * (r / 4) + r % 4;
-                    if (key < l4[e] || key >= h4[e]) s[r] = dp[r] = 0.f;
+                    const bool see = (uint32_t)(key - lo[r]) < (uint32_t)len[r];
+                    s[r] = see ? s[r] : 0.f;
+                    dp[r] = see ? dp[r] : 0.f;
                 }
             }
             const Frag<T> p0 = pack8<T>(s, 0), p1 = pack8<T>(s, 1);
             const Frag<T> e0 = pack8<T>(dp, 0), e1 = pack8<T>(dp, 1);
-            if (!(part && flag[n % 3])) {
 #pragma unroll
-                for (int d = 0; d < ND; ++d) {
-                    dv[d] = mma<T>(col_frag<T, DP>(gb, 0, d * 32, lane), p0, dv[d]);
-                    dv[d] = mma<T>(col_frag<T, DP>(gb, 1, d * 32, lane), p1, dv[d]);
-                    dk[d] = mma<T>(col_frag<T, DP>(qb, 0, d * 32, lane), e0, dk[d]);
-                    dk[d] = mma<T>(col_frag<T, DP>(qb, 1, d * 32, lane), e1, dk[d]);
-                }
-            } else {
-                dropped = true;
-#pragma unroll
-                for (int d = 0; d < ND; ++d) {
-                    Frag<T> f[4] = {col_frag<T, DP>(gb, 0, d * 32, lane),
-                                    col_frag<T, DP>(gb, 1, d * 32, lane),
-                                    col_frag<T, DP>(qb, 0, d * 32, lane),
-                                    col_frag<T, DP>(qb, 1, d * 32, lane)};
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) drop_nonfinite<T>(f[x]);
-                    dv[d] = mma<T>(f[0], p0, dv[d]);
-                    dv[d] = mma<T>(f[1], p1, dv[d]);
-                    dk[d] = mma<T>(f[2], e0, dk[d]);
-                    dk[d] = mma<T>(f[3], e1, dk[d]);
-                }
+            for (int d = 0; d < ND; ++d) {
+                dv[d] = mma<T>(col_frag<T, DP>(gb, 0, d * 32, lane), p0, dv[d]);
+                dv[d] = mma<T>(col_frag<T, DP>(gb, 1, d * 32, lane), p1, dv[d]);
+                dk[d] = mma<T>(col_frag<T, DP>(qb, 0, d * 32, lane), e0, dk[d]);
+                dk[d] = mma<T>(col_frag<T, DP>(qb, 1, d * 32, lane), e1, dk[d]);
             }
         }
-        if (more) place(buf ^ 1, n + 1);
+        if (more) place(buf ^ 1);
         __syncthreads();
     }
-    if (dropped) {
+    if (*flag) {                           // (the loop's last barrier is behind us)
         // infinities and NaN of do that were dropped, for the keys they reach
         // (in dk they are there already: e is NaN with them)
         for (int n = 0; n < steps; ++n) {
-            bool part;
-            if (!touched(n, &part) || !part) continue;
+            const int32_t *u = tiles + 4 * (int64_t)(first + n % span);
+            if (u[2] <= k0 && k0 + 32 * kWaves <= u[3]) continue;
             const int h = hk * a.G + g0 + n / span, q0 = (first + n % span) * QB;
             for (int i = q0; i < min(q0 + QB, a.Tq); ++i) {
                 const int2 sp = *(const int2 *)(a.spans + 2 * ((int64_t)b * a.Tq + i));
@@ -551,7 +532,7 @@ void run(const AttnArgs &a, hipStream_t s)
     const int64_t nk = (a.Tk + 32 * kWaves - 1) / (32 * kWaves);
     if (nk > 0)
         launch_kernel((attn_dkv_kernel<T, DP>), dim3((uint32_t)(nk * a.B * a.Hk * a.gsplit)),
-                      dim3(64 * kWaves), tiles + (2 * 3 + 8) * kStep * 4 + 5 * 4, s, a);
+                      dim3(64 * kWaves), tiles + (2 * 3 + 8) * kStep * 4 + 3 * 4, s, a);
     if (nk > 0 && a.gsplit > 1) {
         const int64_t need = ((int64_t)a.B * a.Tk * a.Hk * a.D + 255) / 256;
         launch_kernel((attn_parts_kernel<T>),
@@ -560,7 +541,7 @@ void run(const AttnArgs &a, hipStream_t s)
     }
     if (nq > 0)
         launch_kernel((attn_dq_kernel<T, DP>), dim3((uint32_t)(nq * a.B * a.Hq)),
-                      dim3(64 * kWaves), tiles + 2 * 3 * kStep * 4 + (3 + 2 * kWaves) * 4, s, a);
+                      dim3(64 * kWaves), tiles + (2 * 3 + 2) * kStep * 4 + (1 + 4 * kWaves) * 4, s, a);
 }
 
 int64_t round16(int64_t bytes) { return (bytes + 15) & ~(int64_t)15; }

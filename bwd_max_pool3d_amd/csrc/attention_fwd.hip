@@ -123,15 +123,14 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
 
     const int kbeg = ghi > 0 ? glo / KB * KB : 0, kend = ghi;
     TileRegs<T, DP, KB, NT> kr, vr;
-    float pr[3];
+    int32_t pr[3];                         // (not touched before place: that would wait)
     auto fetch = [&](int k0) {
         kr.load(kp, a.ks[1], k0, glo, ghi, a.D, a.vec, tid);
         vr.load(vp, a.vs[1], k0, glo, ghi, a.D, a.vec, tid);
 #pragma unroll
         for (int x = 0; x < 3; ++x)
             if (x < a.axes && tid < KB)
-                pr[x] = (float)(a.pos_k[((int64_t)x * a.B + b) * a.Tk + min(k0 + tid, a.Tk - 1)] -
-                                base[x]);
+                pr[x] = a.pos_k[((int64_t)x * a.B + b) * a.Tk + min(k0 + tid, a.Tk - 1)];
     };
     auto place = [&](int k0, int buf) {
         if (!(galo <= k0 && k0 + KB <= gahi) && vr.drop()) *flag = 1;
@@ -139,7 +138,7 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
         vr.store(vt + buf * KB * DP, tid);
 #pragma unroll
         for (int x = 0; x < 3; ++x)
-            if (x < a.axes && tid < KB) pk[(buf * 3 + x) * KB + tid] = pr[x];
+            if (x < a.axes && tid < KB) pk[(buf * 3 + x) * KB + tid] = (float)(pr[x] - base[x]);
     };
     if (kbeg < kend) {
         fetch(kbeg);
@@ -175,22 +174,21 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
 #pragma unroll
                     for (int x = 0; x < 3; ++x) {
                         if (x >= a.axes) break;
-                        const float *p = pk + (buf * 3 + x) * KB + u * 32 + 4 * half;
+                        const f32x16 p = acc_rows(pk + (buf * 3 + x) * KB + u * 32, half);
 #pragma unroll
                         for (int r = 0; r < 16; ++r)
-                            s[u][r] = fmaf(-sl[x], fabsf(p[8 * (r / 4) + r % 4] - pq[x]), s[u][r]);
+                            s[u][r] = fmaf(-sl[x], fabsf(p[r] - pq[x]), s[u][r]);
                     }
                 }
             }
             const bool part = !(alo <= k0 && k0 + KB <= ahi);
             if (part) {
+                const uint32_t at = k0 + 4 * half - sp.lo, len = sp.hi - sp.lo;
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const int key = k0 + u * 32 + acc_row(r, half);
-                        if (key < sp.lo || key >= sp.hi) s[u][r] = kNegInf;
-                    }
+                    for (int r = 0; r < 16; ++r)
+                        s[u][r] = at + (u * 32 + acc_row(r, 0)) < len ? s[u][r] : kNegInf;
             }
             float mx = s[0][0];
 #pragma unroll

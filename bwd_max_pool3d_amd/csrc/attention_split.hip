@@ -96,15 +96,14 @@ void attn_split_kernel(AttnArgs a)
         const float capin = a.cap > 0.f ? a.scale / a.cap : 0.f;
         const float c2 = a.cap > 0.f ? a.cap * kLog2e : a.scale * kLog2e;
         TileRegs<T, DP, KB, 64> kr, vr;
-        float pr[3];
+        int32_t pr[3];
         auto fetch = [&](int k0) {
             kr.load(kp, a.ks[1], k0, glo, ghi, a.D, a.vec, lane);
             vr.load(vp, a.vs[1], k0, glo, ghi, a.D, a.vec, lane);
 #pragma unroll
             for (int x = 0; x < 3; ++x)
                 if (x < a.axes && lane < KB)
-                    pr[x] = (float)(a.pos_k[((int64_t)x * a.B + b) * a.Tk +
-                                            min(k0 + lane, a.Tk - 1)] - base[x]);
+                    pr[x] = a.pos_k[((int64_t)x * a.B + b) * a.Tk + min(k0 + lane, a.Tk - 1)];
         };
         const int kbeg = glo / KB * KB + wave * KB;
         if (kbeg < ghi) fetch(kbeg);
@@ -119,7 +118,7 @@ void attn_split_kernel(AttnArgs a)
             vr.store(vt, lane);
 #pragma unroll
             for (int x = 0; x < 3; ++x)
-                if (x < a.axes && lane < KB) pk[x * KB + lane] = pr[x];
+                if (x < a.axes && lane < KB) pk[x * KB + lane] = (float)(pr[x] - base[x]);
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
             if (k0 + NW * KB < ghi) fetch(k0 + NW * KB);
@@ -139,19 +138,16 @@ void attn_split_kernel(AttnArgs a)
 #pragma unroll
                 for (int x = 0; x < 3; ++x) {
                     if (x >= a.axes) break;
-                    const float *p = pk + x * KB + 4 * half;
+                    const f32x16 p = acc_rows(pk + x * KB, half);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        s[e] = fmaf(-sl[x], fabsf(p[8 * (e / 4) + e % 4] - pq[x]), s[e]);
+                    for (int e = 0; e < 16; ++e) s[e] = fmaf(-sl[x], fabsf(p[e] - pq[x]), s[e]);
                 }
             }
             // (a chunk's ends are multiples of the tile, or the ends of every span)
             if (part) {
+                const uint32_t at = k0 + 4 * half - sp.lo, len = sp.hi - sp.lo;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int key = k0 + acc_row(e, half);
-                    if (key < sp.lo || key >= sp.hi) s[e] = kNegInf;
-                }
+                for (int e = 0; e < 16; ++e) s[e] = at + acc_row(e, 0) < len ? s[e] : kNegInf;
             }
             float mx = s[0];
 #pragma unroll
