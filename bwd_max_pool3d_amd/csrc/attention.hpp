@@ -128,8 +128,21 @@ __device__ __forceinline__ auto acc_rows(const E *v, int half)
     return o;
 }
 
-// The other half's value.
-__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
+// The larger, and the sum, of the two halves' values.
+__device__ __forceinline__ float halves_max(float v)
+{
+    const auto x = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v),
+                                                    __builtin_bit_cast(uint32_t, v), false, false);
+    const uint32_t a = x[0], b = x[1];
+    return fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
+}
+__device__ __forceinline__ float halves_sum(float v)
+{
+    const auto x = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v),
+                                                    __builtin_bit_cast(uint32_t, v), false, false);
+    const uint32_t a = x[0], b = x[1];
+    return __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b);
+}
 
 // --- tiles in LDS: rows of DP elements in chunks of 8, the chunks of a row
 // swapped by the row's number so that neither the row fragments (the same
@@ -350,31 +363,56 @@ __device__ __forceinline__ Span row_span(const AttnArgs &a, int b, int i)
     return hi > lo ? Span{lo, hi} : Span{0, 0};
 }
 
-// --- scores: from the accumulated products to the exponents' domain.
-// Without a cap or a bias the scores stay as they are and c1 (scale times
-// log2 e) is applied inside the exponent's multiply-add.
-struct ScoreMul {
-    float mul;                             // exponent = score * mul - row maximum
-    bool transform;
+// --- scores: from the accumulated products q.k to exponents of 2.  The
+// last multiplication is left to the exponent's own multiply-add
+// (exponent = score * mul - maximum) where nothing comes after it and its
+// factor is positive, so that the largest score has the largest exponent.
+struct Scores {
+    float capin;                           // scale / cap; 0: no cap
+    float c2;                              // cap (or scale) * log2 e
+    float mul;
+    bool multiply;                         // by c2 before the bias; mul is 1 then
 };
 
-__device__ __forceinline__ ScoreMul score_mul(const AttnArgs &a)
+__device__ __forceinline__ Scores scores(const AttnArgs &a)
 {
-    const bool tr = a.cap > 0.f || a.axes > 0 || !(a.scale > 0.f);
-    return {tr ? 1.f : a.scale * kLog2e, tr};
+    const float c2 = (a.cap > 0.f ? a.cap : a.scale) * kLog2e;
+    const bool multiply = a.axes > 0 || !(c2 > 0.f);
+    return {a.cap > 0.f ? a.scale / a.cap : 0.f, c2, multiply ? 1.f : c2, multiply};
 }
 
-// tanh: 1 - 2 / (1 + e^2x) is within 2e-7 of the truth, which as an
-// exponent's error is below a 16-bit weight's rounding; float32 results
-// need the relative accuracy near 0 that the library's tanhf has
+// tanh of the 16 scores of a result times f.  float32: the library's tanhf,
+// for its relative accuracy near 0.  16-bit types, whose weights keep 2^-9
+// at best: 1 - 2 / (1 + e^2x), within 2e-7; and where no score of the wave
+// passes 0.35, as with a cap well above the scores, its odd Taylor
+// polynomial, within 1e-7, at half the cost (the exponential and the
+// reciprocal take four times an ordinary instruction each).
 template <typename T>
-__device__ __forceinline__ float cap_tanh(float x)
+__device__ __forceinline__ void cap_tanh(f32x16 &s, float f)
 {
     if constexpr (T::code == F32::code) {
-        return tanhf(x);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[r] = tanhf(s[r] * f);
+        return;
+    }
+    float big = fabsf(s[0]);
+#pragma unroll
+    for (int r = 1; r < 16; ++r) big = fmaxf(big, fabsf(s[r]));
+    // (written so that a NaN takes the other branch)
+    if (!__any(!(big * fabsf(f) < 0.35f))) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const float x = s[r] * f, y = x * x;
+            float t = fmaf(y, 62.f / 2835.f, -17.f / 315.f);
+            t = fmaf(t, y, 2.f / 15.f);
+            t = fmaf(t, y, -1.f / 3.f);
+            s[r] = fmaf(t * y, x, x);
+        }
     } else {
-        const float e = __builtin_amdgcn_exp2f(x * (2.f * kLog2e));
-        return 1.f - 2.f * __builtin_amdgcn_rcpf(1.f + e);
+        const float g = f * (2.f * kLog2e);
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            s[r] = fmaf(-2.f, __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(s[r] * g)), 1.f);
     }
 }
 

@@ -83,19 +83,6 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a)
     }
 }
 
-// How scores become exponents (see ScoreMul), and the cap's constants.
-struct Shape {
-    float capin, c2, mul;
-    bool cap, transform;
-};
-
-__device__ __forceinline__ Shape score_shape(const AttnArgs &a)
-{
-    const ScoreMul sm = score_mul(a);
-    return {a.cap > 0.f ? a.scale / a.cap : 0.f, (a.cap > 0.f ? a.cap : a.scale) * kLog2e, sm.mul,
-            a.cap > 0.f, sm.transform};
-}
-
 // ------------------------------------------------------------------- dq
 
 template <typename T, int DP>
@@ -174,7 +161,7 @@ __global__ __launch_bounds__(64 * kWaves, (bwd_occupancy<T, DP>())) void attn_dq
         pq[x] = (float)(p[ic] - base[x]);
         sl[x] = a.slopes[h * a.axes + x] * kLog2e;
     }
-    const Shape sh = score_shape(a);
+    const Scores sc = scores(a);
 
     f32x16 o[ND];
 #pragma unroll
@@ -221,18 +208,13 @@ __global__ __launch_bounds__(64 * kWaves, (bwd_occupancy<T, DP>())) void attn_dq
                 dp = mma<T>(row_frag<T, DP>(vb, col, c * 16 + half * 8), gf[c], dp);
 #pragma unroll
             for (int r = 0; r < 16; ++r) dp[r] -= rd.y;
-            if (sh.transform) {
-                if (sh.cap) {
+            if (a.cap > 0.f) {
+                cap_tanh<T>(s, sc.capin);
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const float th = cap_tanh<T>(s[r] * sh.capin);
-                        s[r] = sh.c2 * th;
-                        dp[r] *= 1.f - th * th;
-                    }
-                } else {
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) s[r] *= sh.c2;
-                }
+                for (int r = 0; r < 16; ++r) dp[r] *= fmaf(-s[r], s[r], 1.f);
+            }
+            if (sc.multiply) {
+                s *= sc.c2;
 #pragma unroll
                 for (int x = 0; x < 3; ++x) {
                     if (x >= a.axes) break;
@@ -249,7 +231,7 @@ __global__ __launch_bounds__(64 * kWaves, (bwd_occupancy<T, DP>())) void attn_dq
             }
 #pragma unroll
             for (int r = 0; r < 16; ++r)
-                s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], sh.mul, -rd.x)) * dp[r];
+                s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], sc.mul, -rd.x)) * dp[r];
             if (part) {
                 const uint32_t at = k0 + 4 * half - sp.x, len = sp.y - sp.x;
 #pragma unroll
@@ -346,7 +328,7 @@ __global__ __launch_bounds__(64 * kWaves, (dkv_occupancy<T, DP>())) void attn_dk
         base[x] = p[k0];
         pk[x] = (float)(p[kc] - base[x]);
     }
-    const Shape sh = score_shape(a);
+    const Scores sc = scores(a);
     f32x16 dk[ND], dv[ND];
 #pragma unroll
     for (int d = 0; d < ND; ++d) dk[d] = dv[d] = f32x16(0.f);
@@ -427,18 +409,13 @@ __global__ __launch_bounds__(64 * kWaves, (dkv_occupancy<T, DP>())) void attn_dk
             const f32x16 lr = acc_rows(rl + buf * QB, half), dr = acc_rows(rd + buf * QB, half);
 #pragma unroll
             for (int r = 0; r < 16; ++r) dp[r] -= dr[r];
-            if (sh.transform) {
-                if (sh.cap) {
+            if (a.cap > 0.f) {
+                cap_tanh<T>(s, sc.capin);
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const float th = cap_tanh<T>(s[r] * sh.capin);
-                        s[r] = sh.c2 * th;
-                        dp[r] *= 1.f - th * th;
-                    }
-                } else {
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) s[r] *= sh.c2;
-                }
+                for (int r = 0; r < 16; ++r) dp[r] *= fmaf(-s[r], s[r], 1.f);
+            }
+            if (sc.multiply) {
+                s *= sc.c2;
 #pragma unroll
                 for (int x = 0; x < 3; ++x) {
                     if (x >= a.axes) break;
@@ -449,7 +426,7 @@ __global__ __launch_bounds__(64 * kWaves, (dkv_occupancy<T, DP>())) void attn_dk
             }
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], sh.mul, -lr[r]));
+                s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], sc.mul, -lr[r]));
                 dp[r] *= s[r];
             }
             if (part) {

@@ -112,9 +112,7 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
         pq[x] = (float)(p[ic] - base[x]);
         sl[x] = a.slopes[h * a.axes + x] * kLog2e;
     }
-    const ScoreMul sm = score_mul(a);
-    const float capin = a.cap > 0.f ? a.scale / a.cap : 0.f;
-    const float c2 = a.cap > 0.f ? a.cap * kLog2e : a.scale * kLog2e;
+    const Scores sc = scores(a);
 
     f32x16 o[ND];
 #pragma unroll
@@ -161,16 +159,14 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
                     s[u] = mma<T>(row_frag<T, DP>(kb, u * 32 + col, c * 16 + half * 8), qf[c],
                                   s[u]);
             }
-            if (sm.transform) {
+            if (a.cap > 0.f) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) cap_tanh<T>(s[u], sc.capin);
+            }
+            if (sc.multiply) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    if (a.cap > 0.f) {
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) s[u][r] = c2 * cap_tanh<T>(s[u][r] * capin);
-                    } else {
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) s[u][r] *= c2;
-                    }
+                    s[u] *= sc.c2;
 #pragma unroll
                     for (int x = 0; x < 3; ++x) {
                         if (x >= a.axes) break;
@@ -195,7 +191,7 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
             for (int r = 1; r < 16; ++r) mx = fmaxf(mx, s[0][r]);
 #pragma unroll
             for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[1][r]);
-            mx = fmaxf(mx, other_half(mx)) * sm.mul;
+            mx = halves_max(mx) * sc.mul;
             if (__any(mx > m + kRaise)) {
                 // (each query by itself: its result does not depend on its neighbours)
                 const float mn = mx > m + kRaise ? mx : m;
@@ -213,7 +209,7 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
             for (int u = 0; u < 2; ++u) {
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    s[u][r] = __builtin_amdgcn_exp2f(fmaf(s[u][r], sm.mul, -ms));
+                    s[u][r] = __builtin_amdgcn_exp2f(fmaf(s[u][r], sc.mul, -ms));
                     l += s[u][r];
                 }
                 pf[2 * u] = pack8<T>(s[u], 0);
@@ -246,7 +242,7 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
     }
 
     if (i >= a.Tq) return;
-    l += other_half(l);
+    l = halves_sum(l);
     const float inv = l == 0.f ? 0.f : 1.f / l;
     if (half == 0)
         a.lse[((int64_t)b * a.Hq + h) * a.Tq + i] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;

@@ -92,9 +92,7 @@ void attn_split_kernel(AttnArgs a)
             pq[x] = (float)(p[t] - base[x]);
             sl[x] = a.slopes[h * a.axes + x] * kLog2e;
         }
-        const ScoreMul sm = score_mul(a);
-        const float capin = a.cap > 0.f ? a.scale / a.cap : 0.f;
-        const float c2 = a.cap > 0.f ? a.cap * kLog2e : a.scale * kLog2e;
+        const Scores sc = scores(a);
         TileRegs<T, DP, KB, 64> kr, vr;
         int32_t pr[3];
         auto fetch = [&](int k0) {
@@ -127,14 +125,9 @@ void attn_split_kernel(AttnArgs a)
 #pragma unroll
             for (int c = 0; c < NC; ++c)
                 s = mma<T>(row_frag<T, DP>(kt, col, c * 16 + half * 8), qf[c], s);
-            if (sm.transform) {
-                if (a.cap > 0.f) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) s[e] = c2 * cap_tanh<T>(s[e] * capin);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) s[e] *= c2;
-                }
+            if (a.cap > 0.f) cap_tanh<T>(s, sc.capin);
+            if (sc.multiply) {
+                s *= sc.c2;
 #pragma unroll
                 for (int x = 0; x < 3; ++x) {
                     if (x >= a.axes) break;
@@ -152,7 +145,7 @@ void attn_split_kernel(AttnArgs a)
             float mx = s[0];
 #pragma unroll
             for (int e = 1; e < 16; ++e) mx = fmaxf(mx, s[e]);
-            mx = fmaxf(mx, other_half(mx)) * sm.mul;
+            mx = halves_max(mx) * sc.mul;
             if (__any(mx > m + kRaise)) {
                 // (each query by itself: its result does not depend on its neighbours)
                 const float mn = mx > m + kRaise ? mx : m;
@@ -167,7 +160,7 @@ void attn_split_kernel(AttnArgs a)
             const float ms = m == kNegInf ? 0.f : m;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], sm.mul, -ms));
+                s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], sc.mul, -ms));
                 l += s[e];
             }
             const Frag<T> p0 = pack8<T>(s, 0), p1 = pack8<T>(s, 1);
@@ -195,7 +188,7 @@ void attn_split_kernel(AttnArgs a)
             }
         }
     }
-    l += other_half(l);
+    l = halves_sum(l);
 
     // join the four waves
     __syncthreads();
