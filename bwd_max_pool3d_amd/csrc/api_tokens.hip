@@ -455,7 +455,7 @@ int mp3d_attention_forward(const mp3d_attention *d, const void *q, const void *k
         if ((rc = check_workspace(workspace, workspace_bytes, plan_attn_split(&a)))) return rc;
         if ((rc = check_launch((int64_t)a.nrb * a.Hk * a.B * a.nsplit))) return rc;
         place_attn_split(&a, workspace);
-    } else if ((rc = check_launch((int64_t)((a.Tq + 127) / 128) * a.B * a.Hq))) {
+    } else if ((rc = check_launch((int64_t)((a.Tq + 63) / 64) * a.B * a.Hq))) {
         return rc;
     }
     if (log_enabled())
@@ -502,8 +502,8 @@ int mp3d_attention_backward(const mp3d_attention *d, const void *dout, const int
     a.vec = wide_rows(q, a.qs, es) && wide_rows(k, a.ks, es) && wide_rows(v, a.vs, es) &&
             wide_rows(dout, a.gs, es);
     if ((rc = check_workspace(workspace, workspace_bytes, plan_attn_backward(&a)))) return rc;
-    if ((rc = check_launch((int64_t)((a.Tq + 127) / 128) * a.B * a.Hq)) ||
-        (rc = check_launch((int64_t)((a.Tk + 127) / 128) * a.B * a.Hk * a.gsplit)))
+    if ((rc = check_launch((int64_t)((a.Tq + 63) / 64) * a.B * a.Hq)) ||
+        (rc = check_launch((int64_t)((a.Tk + 63) / 64) * a.B * a.Hk * a.gsplit)))
         return rc;
     place_attn_backward(&a, workspace);
     if (log_enabled())

@@ -320,6 +320,52 @@ struct TileRegs {
     }
 };
 
+// The same tile straight from memory to LDS, 16 bytes a lane, with nothing
+// in registers meanwhile: for tiles that need no second look (every row
+// there, nothing to drop).  A wave's lanes fill 1 KiB of LDS in order, so the
+// swap of the chunks is made on the memory side.  What is not so goes
+// through place(), which waits for its loads.
+template <typename T, int DP, int ROWS, int NT>
+struct TileDirect {
+    using R = typename T::raw;
+    static constexpr int PER = 16 / sizeof(R);             // elements of a lane's 16 bytes
+    static constexpr int UNITS = DP / PER;                 // of a row
+    static constexpr int STEP = NT / UNITS;                // rows of one round over the threads
+    static constexpr int N = ROWS / STEP;
+    static_assert(N * STEP == ROWS && STEP % 8 == 0, "every round swaps alike");
+    uint32_t off;                                          // bytes from the round's first row
+    bool on;                                               // the lane's channels are there
+
+    __device__ __forceinline__ void init(int t, int64_t stride, int D)
+    {
+        const int row = t / UNITS, u = t % UNITS, c = (u * PER / 8) ^ tile_swap(row);
+        const int e = c * 8 + (u * PER) % 8;
+        off = (uint32_t)(row * stride + e) * (uint32_t)sizeof(R);
+        on = e < D;
+    }
+    // The tile's first row at p (the same in every lane).  Every wave waits
+    // for its loads (wait_direct) before the barrier that hands the tile over.
+    __device__ __forceinline__ void load(const R *p, int64_t stride, R *tile, int wave) const
+    {
+        typedef const __attribute__((address_space(1))) void global_t;
+        typedef __attribute__((address_space(3))) void lds_t;
+        if (!on) return;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            __builtin_amdgcn_global_load_lds(
+                (global_t *)((const char *)(p + j * STEP * stride) + off),
+                (lds_t *)(tile + (j * NT + wave * 64) * PER), 16, 0, 0);
+    }
+    // Can tiles be loaded this way at all?  Whole chunks, a row's offset
+    // within 31 bits, and LDS addresses within the 16 bits the load has.
+    __device__ static __forceinline__ bool usable(bool vec, int64_t stride, int D)
+    {
+        return 4 * ROWS * DP * sizeof(R) <= 65536 && vec && D % 8 == 0 && stride < (1 << 24);
+    }
+};
+
+__device__ __forceinline__ void wait_direct() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
 // --- infinities and NaN in masked places
 //
 // 0 * inf is NaN, so a masked weight of 0 does not keep a key's value out of
@@ -363,22 +409,26 @@ __device__ __forceinline__ Span row_span(const AttnArgs &a, int b, int i)
     return hi > lo ? Span{lo, hi} : Span{0, 0};
 }
 
-// --- scores: from the accumulated products q.k to exponents of 2.  The
-// last multiplication is left to the exponent's own multiply-add
-// (exponent = score * mul - maximum) where nothing comes after it and its
-// factor is positive, so that the largest score has the largest exponent.
+// --- scores: from the accumulated products q.k to exponents of 2.  Their
+// factor (scale, or the cap) is left to the exponent's own multiply-add
+// (exponent = score * mul - maximum) and divided out of the bias' slopes,
+// unless it is not positive: the largest score would not have the largest
+// exponent.
 struct Scores {
     float capin;                           // scale / cap; 0: no cap
-    float c2;                              // cap (or scale) * log2 e
+    float scale;                           // the scores are multiplied by it first
     float mul;
-    bool multiply;                         // by c2 before the bias; mul is 1 then
+    float slope;                           // factor of the slopes
+    bool multiply;                         // scale is not 1
 };
 
 __device__ __forceinline__ Scores scores(const AttnArgs &a)
 {
-    const float c2 = (a.cap > 0.f ? a.cap : a.scale) * kLog2e;
-    const bool multiply = a.axes > 0 || !(c2 > 0.f);
-    return {a.cap > 0.f ? a.scale / a.cap : 0.f, c2, multiply ? 1.f : c2, multiply};
+    const float f = a.cap > 0.f ? a.cap : a.scale;
+    // (a factor whose reciprocal overflows is applied first, too)
+    const bool multiply = !(f > 1e-30f);
+    return {a.cap > 0.f ? a.scale / a.cap : 0.f, multiply ? f : 1.f,
+            multiply ? kLog2e : f * kLog2e, multiply ? 1.f : 1.f / f, multiply};
 }
 
 // tanh of the 16 scores of a result times f.  float32: the library's tanhf,

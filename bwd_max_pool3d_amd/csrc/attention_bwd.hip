@@ -8,9 +8,9 @@
 // (the last factor of e only with a cap; the bias has no gradient).
 //
 // Three launches: the rows' constants (delta, the spans of keys, and their
-// unions over 32 queries); dk and dv, a workgroup of four waves per 128
-// keys of one key head, walking the queries of the heads that share it; dq,
-// a workgroup per 128 queries, walking their keys.  Scores and do . v are
+// unions over 32 queries); dk and dv, a workgroup per 32 keys and wave
+// of one key head, walking the queries of the heads that share it; dq,
+// a workgroup per 32 queries and wave, walking their keys.  Scores and do . v are
 // formed in both (7 products where 5 would do), and in exchange every sum
 // is kept by one wave in registers and written once: no atomics, the same
 // bits on every run.  Where one pass over a key head's query heads would
@@ -25,7 +25,6 @@ namespace mp3d {
 
 namespace {
 
-constexpr int kWaves = 4;
 constexpr int kStep = 32;                  // keys (dq) or queries (dk, dv) per step
 constexpr float kInf = __builtin_huge_valf();
 
@@ -83,25 +82,32 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a)
     }
 }
 
+// Waves of a workgroup (see attention_fwd.hip)
+template <int DP>
+constexpr int bwd_waves() { return 4; }
+
 // ------------------------------------------------------------------- dq
 
 template <typename T, int DP>
-constexpr int bwd_occupancy() { return sizeof(typename T::raw) * DP > 256 ? 1 : 2; }
+constexpr int bwd_occupancy()
+{
+    return sizeof(typename T::raw) * DP > 256 ? 1 : sizeof(typename T::raw) * DP > 128 ? 2 : 3;
+}
 
 template <typename T, int DP>
-__global__ __launch_bounds__(64 * kWaves, (bwd_occupancy<T, DP>())) void attn_dq_kernel(AttnArgs a)
+__global__ __launch_bounds__(64 * bwd_waves<DP>(), (bwd_occupancy<T, DP>())) void attn_dq_kernel(AttnArgs a)
 {
     using R = typename T::raw;
-    constexpr int NT = 64 * kWaves, KB = kStep, NC = DP / 16, ND = DP / 32;
+    constexpr int NW = bwd_waves<DP>(), NT = 64 * NW, KB = kStep, NC = DP / 16, ND = DP / 32;
     extern __shared__ __align__(16) unsigned char smem[];
     R *const kt = (R *)smem;                               // [2][KB * DP]
     R *const vt = kt + 2 * KB * DP;                        // [2][KB * DP]
     float *const pk = (float *)(vt + 2 * KB * DP);         // [2][3][KB]
     int *const bad = (int *)(pk + 2 * 3 * KB);             // [2][KB] 1 + last step with a key's inf or NaN
     int *const flag = bad + 2 * KB;                        // there was one
-    int *const ends = flag + 1;                            // [4][kWaves]
+    int *const ends = flag + 1;                            // [4][NW]
 
-    const int nq = (a.Tq + 32 * kWaves - 1) / (32 * kWaves);
+    const int nq = (a.Tq + 32 * NW - 1) / (32 * NW);
     const int heads = a.B * a.Hq;
     int bh, qt;
     if (heads % 8 == 0) {
@@ -115,29 +121,29 @@ __global__ __launch_bounds__(64 * kWaves, (bwd_occupancy<T, DP>())) void attn_dq
     const int b = bh / a.Hq, h = bh - b * a.Hq, hk = h / a.G;
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, col = lane & 31,
               half = lane >> 5;
-    const int q0 = qt * 32 * kWaves, i = q0 + wave * 32 + col;
+    const int q0 = qt * 32 * NW, i = q0 + wave * 32 + col;
     const int ic = min(i, a.Tq - 1);
     const int2 sp = *(const int2 *)(a.spans + 2 * ((int64_t)b * a.Tq + ic));
-    const int nt = (a.Tq + 31) / 32, wt = min(qt * kWaves + wave, nt - 1);
+    const int nt = (a.Tq + 31) / 32, wt = min(qt * NW + wave, nt - 1);
     const int4 wu = *(const int4 *)(a.tiles + 4 * ((int64_t)b * nt + wt));
     const int wlo = __builtin_amdgcn_readfirstlane(wu.x), whi = __builtin_amdgcn_readfirstlane(wu.y);
     const int alo = __builtin_amdgcn_readfirstlane(wu.z), ahi = __builtin_amdgcn_readfirstlane(wu.w);
     if (lane == 0) {
         ends[wave] = wlo;
-        ends[kWaves + wave] = whi;
-        ends[2 * kWaves + wave] = alo;
-        ends[3 * kWaves + wave] = ahi;
+        ends[NW + wave] = whi;
+        ends[2 * NW + wave] = alo;
+        ends[3 * NW + wave] = ahi;
     }
     if (tid < 2 * KB) bad[tid] = 0;
     if (tid == 0) *flag = 0;
     __syncthreads();
-    int glo = ends[0], ghi = ends[kWaves], galo = ends[2 * kWaves], gahi = ends[3 * kWaves];
+    int glo = ends[0], ghi = ends[NW], galo = ends[2 * NW], gahi = ends[3 * NW];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) {
+    for (int w = 1; w < NW; ++w) {
         glo = min(glo, ends[w]);
-        ghi = max(ghi, ends[kWaves + w]);
-        galo = max(galo, ends[2 * kWaves + w]);
-        gahi = min(gahi, ends[3 * kWaves + w]);
+        ghi = max(ghi, ends[NW + w]);
+        galo = max(galo, ends[2 * NW + w]);
+        gahi = min(gahi, ends[3 * NW + w]);
     }
 
     const R *kp = (const R *)a.k + b * a.ks[0] + hk * a.ks[2];
@@ -151,6 +157,7 @@ __global__ __launch_bounds__(64 * kWaves, (bwd_occupancy<T, DP>())) void attn_dq
         gf[c] = load8<T>(gp, c * 16 + half * 8, a.D, a.vec);
     }
     const float2 rd = *(const float2 *)(a.rowd + 2 * ((int64_t)bh * a.Tq + ic));
+    const Scores sc = scores(a);
     float pq[3], sl[3];
     int64_t base[3];
 #pragma unroll
@@ -159,44 +166,61 @@ __global__ __launch_bounds__(64 * kWaves, (bwd_occupancy<T, DP>())) void attn_dq
         const int32_t *p = a.pos_q + ((int64_t)x * a.B + b) * a.Tq;
         base[x] = p[q0];
         pq[x] = (float)(p[ic] - base[x]);
-        sl[x] = a.slopes[h * a.axes + x] * kLog2e;
+        sl[x] = a.slopes[h * a.axes + x] * sc.slope;
     }
-    const Scores sc = scores(a);
 
     f32x16 o[ND];
 #pragma unroll
     for (int d = 0; d < ND; ++d) o[d] = f32x16(0.f);
 
     const int kbeg = ghi > 0 ? glo / KB * KB : 0, kend = ghi;
-    // (nothing in flight is touched before place: that would wait for it)
-    TileRegs<T, DP, KB, NT> kr, vr;
-    int32_t pr[3];
-    auto fetch = [&](int k0) {
-        kr.load(kp, a.ks[1], k0, glo, ghi, a.D, a.vec, tid);
-        vr.load(vp, a.vs[1], k0, glo, ghi, a.D, a.vec, tid);
+    TileDirect<T, DP, KB, NT> kd, vd;
+    kd.init(tid, a.ks[1], a.D);
+    vd.init(tid, a.vs[1], a.D);
+    const bool usable = kd.usable(a.vec, a.ks[1], a.D) && vd.usable(a.vec, a.vs[1], a.D);
+    if (a.D < DP) {                        // channels that no direct load writes
+        for (int x = tid; x < 4 * KB * DP * (int)sizeof(R) / 16; x += NT)
+            ((u32x4 *)kt)[x] = u32x4{0u, 0u, 0u, 0u};
+        __syncthreads();
+    }
+    auto direct = [&](int k0) {
+        return usable && max(glo, galo) <= k0 && k0 + KB <= min(ghi, gahi);
+    };
+    int32_t pr[3];                         // (not touched before place: that would wait)
+    auto fetch = [&](int k0, int buf) {
+        if (direct(k0)) {
+            kd.load(kp + k0 * a.ks[1], a.ks[1], kt + buf * KB * DP, wave);
+            vd.load(vp + k0 * a.vs[1], a.vs[1], vt + buf * KB * DP, wave);
+        }
 #pragma unroll
         for (int x = 0; x < 3; ++x)
             if (x < a.axes && tid < KB)
                 pr[x] = a.pos_k[((int64_t)x * a.B + b) * a.Tk + min(k0 + tid, a.Tk - 1)];
     };
     auto place = [&](int k0, int buf, int n) {
-        if (!(galo <= k0 && k0 + KB <= gahi) && kr.drop(bad + buf * KB, n + 1, tid)) *flag = 1;
-        kr.store(kt + buf * KB * DP, tid);
-        vr.store(vt + buf * KB * DP, tid);
+        if (!direct(k0)) {
+            TileRegs<T, DP, KB, NT> r;
+            r.load(kp, a.ks[1], k0, glo, ghi, a.D, a.vec, tid);
+            if (!(galo <= k0 && k0 + KB <= gahi) && r.drop(bad + buf * KB, n + 1, tid)) *flag = 1;
+            r.store(kt + buf * KB * DP, tid);
+            r.load(vp, a.vs[1], k0, glo, ghi, a.D, a.vec, tid);
+            r.store(vt + buf * KB * DP, tid);
+        }
 #pragma unroll
         for (int x = 0; x < 3; ++x)
             if (x < a.axes && tid < KB) pk[(buf * 3 + x) * KB + tid] = (float)(pr[x] - base[x]);
     };
     if (kbeg < kend) {
-        fetch(kbeg);
+        fetch(kbeg, 0);
         place(kbeg, 0, 0);
     }
+    wait_direct();
     __syncthreads();
     int n = 0;
     for (int k0 = kbeg; k0 < kend; k0 += KB, ++n) {
         const int buf = n & 1;
         const bool more = k0 + KB < kend;
-        if (more) fetch(k0 + KB);
+        if (more) fetch(k0 + KB, buf ^ 1);
         if (k0 < whi && k0 + KB > wlo) {
             const R *kb = kt + buf * KB * DP, *vb = vt + buf * KB * DP;
             f32x16 s = f32x16(0.f), dp = f32x16(0.f);
@@ -213,8 +237,8 @@ __global__ __launch_bounds__(64 * kWaves, (bwd_occupancy<T, DP>())) void attn_dq
 #pragma unroll
                 for (int r = 0; r < 16; ++r) dp[r] *= fmaf(-s[r], s[r], 1.f);
             }
-            if (sc.multiply) {
-                s *= sc.c2;
+            if (sc.multiply || a.axes > 0) {
+                if (sc.multiply) s *= sc.scale;
 #pragma unroll
                 for (int x = 0; x < 3; ++x) {
                     if (x >= a.axes) break;
@@ -245,6 +269,7 @@ __global__ __launch_bounds__(64 * kWaves, (bwd_occupancy<T, DP>())) void attn_dq
             }
         }
         if (more) place(k0 + KB, buf ^ 1, n + 1);
+        wait_direct();
         __syncthreads();
     }
     if (i >= a.Tq) return;
@@ -257,10 +282,10 @@ template <typename T, int DP>
 constexpr int dkv_occupancy() { return sizeof(typename T::raw) * DP > 128 ? 1 : 2; }
 
 template <typename T, int DP>
-__global__ __launch_bounds__(64 * kWaves, (dkv_occupancy<T, DP>())) void attn_dkv_kernel(AttnArgs a)
+__global__ __launch_bounds__(64 * bwd_waves<DP>(), (dkv_occupancy<T, DP>())) void attn_dkv_kernel(AttnArgs a)
 {
     using R = typename T::raw;
-    constexpr int NT = 64 * kWaves, QB = kStep, NC = DP / 16, ND = DP / 32;
+    constexpr int NW = bwd_waves<DP>(), NT = 64 * NW, QB = kStep, NC = DP / 16, ND = DP / 32;
     extern __shared__ __align__(16) unsigned char smem[];
     R *const qt = (R *)smem;                               // [2][QB * DP]
     R *const gt = qt + 2 * QB * DP;                        // [2][QB * DP]
@@ -273,7 +298,7 @@ __global__ __launch_bounds__(64 * kWaves, (dkv_occupancy<T, DP>())) void attn_dk
     int *const ends = flag + 1;                            // [2] first and last tile
 
     // parts of one key head, and the key blocks of one sequence, on one XCD
-    const int nk = (a.Tk + 32 * kWaves - 1) / (32 * kWaves);
+    const int nk = (a.Tk + 32 * NW - 1) / (32 * NW);
     const uint32_t id = xcd_local_block(blockIdx.x, gridDim.x);
     const int kb = id % nk;
     int64_t rest = id / nk;
@@ -284,7 +309,7 @@ __global__ __launch_bounds__(64 * kWaves, (dkv_occupancy<T, DP>())) void attn_dk
     const int g1 = (int)((int64_t)a.G * (gpart + 1) / a.gsplit);
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, col = lane & 31,
               half = lane >> 5;
-    const int k0 = kb * 32 * kWaves, kw = k0 + wave * 32, key = kw + col;
+    const int k0 = kb * 32 * NW, kw = k0 + wave * 32, key = kw + col;
     const int kc = min(key, a.Tk - 1);
     const int nt = (a.Tq + QB - 1) / QB;
     const int32_t *tiles = a.tiles + 4 * (int64_t)b * nt;
@@ -297,7 +322,7 @@ __global__ __launch_bounds__(64 * kWaves, (dkv_occupancy<T, DP>())) void attn_dk
         int first = nt, last = -1;
         for (int t = tid; t < nt; t += NT) {
             const int4 u = *(const int4 *)(tiles + 4 * (int64_t)t);
-            if (u.x < k0 + 32 * kWaves && u.y > k0) {
+            if (u.x < k0 + 32 * NW && u.y > k0) {
                 first = min(first, t);
                 last = t;
             }
@@ -333,31 +358,49 @@ __global__ __launch_bounds__(64 * kWaves, (dkv_occupancy<T, DP>())) void attn_dk
 #pragma unroll
     for (int d = 0; d < ND; ++d) dk[d] = dv[d] = f32x16(0.f);
 
+    TileDirect<T, DP, QB, NT> qd, gd;
+    qd.init(tid, a.qs[1], a.D);
+    gd.init(tid, a.gs[1], a.D);
+    const bool usable = qd.usable(a.vec, a.qs[1], a.D) && gd.usable(a.vec, a.gs[1], a.D);
+    if (a.D < DP) {                        // channels that no direct load writes
+        for (int x = tid; x < 4 * QB * DP * (int)sizeof(R) / 16; x += NT)
+            ((u32x4 *)qt)[x] = u32x4{0u, 0u, 0u, 0u};
+        __syncthreads();
+    }
     // (nothing in flight is touched before place: that would wait for it)
-    TileRegs<T, DP, QB, NT> qr, gr;
     int32_t prq[3];
-    int4 nu = make_int4(0, 0, 0, 0);       // the tile's keys (see AttnArgs::tiles)
-    float nsl[3] = {0.f, 0.f, 0.f}, sl[3];  // the head's slopes
     float2 prd = make_float2(0.f, 0.f);
     int2 psp = make_int2(0, 0);
-    // the next step's head and tile of queries
-    int fh = hk * a.G + g0, ft = first;
     bool past = false;
-    auto fetch = [&]() {
-        const int h = fh, q0 = ft * QB;
-        qr.load((const R *)a.q + b * a.qs[0] + h * a.qs[2], a.qs[1], q0, 0, a.Tq, a.D, a.vec, tid);
-        gr.load((const R *)a.dout + b * a.gs[0] + h * a.gs[2], a.gs[1], q0, 0, a.Tq, a.D, a.vec,
-                tid);
+    float nsl[3] = {0.f, 0.f, 0.f}, sl[3];  // the head's slopes
+    // the next step's head and tile of queries; the keys of its tile (see
+    // AttnArgs::tiles) and, one step ahead, of the one after it
+    int fh = hk * a.G + g0, ft = first;
+    int4 nu = make_int4(0, 0, 0, 0), nnu = nu;
+    const R *fq = nullptr, *fg = nullptr;
+    int fq0 = 0;
+    bool fdirect = false;
+    auto fetch = [&](int buf) {
+        const int h = fh;
+        fq0 = ft * QB;
+        nu = nnu;
+        fq = (const R *)a.q + b * a.qs[0] + h * a.qs[2];
+        fg = (const R *)a.dout + b * a.gs[0] + h * a.gs[2];
+        fdirect = usable && fq0 + QB <= a.Tq &&
+                  __builtin_amdgcn_readfirstlane(nu.z <= k0 && k0 + 32 * NW <= nu.w);
+        if (fdirect) {
+            qd.load(fq + fq0 * a.qs[1], a.qs[1], qt + buf * QB * DP, wave);
+            gd.load(fg + fq0 * a.gs[1], a.gs[1], gt + buf * QB * DP, wave);
+        }
         if (tid < QB) {
-            const int i = min(q0 + tid, a.Tq - 1);
-            past = q0 + tid >= a.Tq;
+            const int i = min(fq0 + tid, a.Tq - 1);
+            past = fq0 + tid >= a.Tq;
             prd = *(const float2 *)(a.rowd + 2 * (((int64_t)b * a.Hq + h) * a.Tq + i));
             psp = *(const int2 *)(a.spans + 2 * ((int64_t)b * a.Tq + i));
 #pragma unroll
             for (int x = 0; x < 3; ++x)
                 if (x < a.axes) prq[x] = a.pos_q[((int64_t)x * a.B + b) * a.Tq + i];
         }
-        nu = *(const int4 *)(tiles + 4 * (int64_t)ft);
 #pragma unroll
         for (int x = 0; x < 3; ++x)
             if (x < a.axes) nsl[x] = a.slopes[h * a.axes + x];
@@ -365,14 +408,19 @@ __global__ __launch_bounds__(64 * kWaves, (dkv_occupancy<T, DP>())) void attn_dk
             ft = first;
             ++fh;
         }
+        nnu = *(const int4 *)(tiles + 4 * (int64_t)ft);
     };
     auto place = [&](int buf) {
-        if (!(nu.z <= k0 && k0 + 32 * kWaves <= nu.w)) {
-            const bool x = qr.drop(), y = gr.drop();
-            if (x || y) *flag = 1;
+        if (!fdirect) {
+            const bool drop = !(nu.z <= k0 && k0 + 32 * NW <= nu.w);
+            TileRegs<T, DP, QB, NT> r;
+            r.load(fq, a.qs[1], fq0, 0, a.Tq, a.D, a.vec, tid);
+            if (drop && r.drop()) *flag = 1;
+            r.store(qt + buf * QB * DP, tid);
+            r.load(fg, a.gs[1], fq0, 0, a.Tq, a.D, a.vec, tid);
+            if (drop && r.drop()) *flag = 1;
+            r.store(gt + buf * QB * DP, tid);
         }
-        qr.store(qt + buf * QB * DP, tid);
-        gr.store(gt + buf * QB * DP, tid);
         if (tid < QB) {
             // past the last query: no weight
             rl[buf * QB + tid] = past ? kInf : prd.x;
@@ -385,17 +433,19 @@ __global__ __launch_bounds__(64 * kWaves, (dkv_occupancy<T, DP>())) void attn_dk
         }
     };
     if (steps > 0) {
-        fetch();
+        nnu = *(const int4 *)(tiles + 4 * (int64_t)first);
+        fetch(0);
         place(0);
     }
+    wait_direct();
     __syncthreads();
     for (int n = 0; n < steps; ++n) {
         const int buf = n & 1;
         const bool more = n + 1 < steps;
         const int4 u = nu;
 #pragma unroll
-        for (int x = 0; x < 3; ++x) sl[x] = nsl[x] * kLog2e;
-        if (more) fetch();
+        for (int x = 0; x < 3; ++x) sl[x] = nsl[x] * sc.slope;
+        if (more) fetch(buf ^ 1);
         if (__builtin_amdgcn_readfirstlane(u.x < kw + 32 && u.y > kw)) {
             const R *qb = qt + buf * QB * DP, *gb = gt + buf * QB * DP;
             const bool part = !__builtin_amdgcn_readfirstlane(u.z <= kw && kw + 32 <= u.w);
@@ -414,8 +464,8 @@ __global__ __launch_bounds__(64 * kWaves, (dkv_occupancy<T, DP>())) void attn_dk
 #pragma unroll
                 for (int r = 0; r < 16; ++r) dp[r] *= fmaf(-s[r], s[r], 1.f);
             }
-            if (sc.multiply) {
-                s *= sc.c2;
+            if (sc.multiply || a.axes > 0) {
+                if (sc.multiply) s *= sc.scale;
 #pragma unroll
                 for (int x = 0; x < 3; ++x) {
                     if (x >= a.axes) break;
@@ -449,6 +499,7 @@ __global__ __launch_bounds__(64 * kWaves, (dkv_occupancy<T, DP>())) void attn_dk
             }
         }
         if (more) place(buf ^ 1);
+        wait_direct();
         __syncthreads();
     }
     if (*flag) {                           // (the loop's last barrier is behind us)
@@ -456,7 +507,7 @@ __global__ __launch_bounds__(64 * kWaves, (dkv_occupancy<T, DP>())) void attn_dk
         // (in dk they are there already: e is NaN with them)
         for (int n = 0; n < steps; ++n) {
             const int32_t *u = tiles + 4 * (int64_t)(first + n % span);
-            if (u[2] <= k0 && k0 + 32 * kWaves <= u[3]) continue;
+            if (u[2] <= k0 && k0 + 32 * NW <= u[3]) continue;
             const int h = hk * a.G + g0 + n / span, q0 = (first + n % span) * QB;
             for (int i = q0; i < min(q0 + QB, a.Tq); ++i) {
                 const int2 sp = *(const int2 *)(a.spans + 2 * ((int64_t)b * a.Tq + i));
@@ -504,12 +555,13 @@ __global__ __launch_bounds__(256) void attn_parts_kernel(AttnArgs a)
 template <typename T, int DP>
 void run(const AttnArgs &a, hipStream_t s)
 {
+    constexpr int NW = bwd_waves<DP>();
     constexpr uint32_t tiles = 4 * kStep * DP * sizeof(typename T::raw);
-    const int64_t nq = (a.Tq + 32 * kWaves - 1) / (32 * kWaves);
-    const int64_t nk = (a.Tk + 32 * kWaves - 1) / (32 * kWaves);
+    const int64_t nq = (a.Tq + 32 * NW - 1) / (32 * NW);
+    const int64_t nk = (a.Tk + 32 * NW - 1) / (32 * NW);
     if (nk > 0)
         launch_kernel((attn_dkv_kernel<T, DP>), dim3((uint32_t)(nk * a.B * a.Hk * a.gsplit)),
-                      dim3(64 * kWaves), tiles + (2 * 3 + 8) * kStep * 4 + 3 * 4, s, a);
+                      dim3(64 * NW), tiles + (2 * 3 + 8) * kStep * 4 + 3 * 4, s, a);
     if (nk > 0 && a.gsplit > 1) {
         const int64_t need = ((int64_t)a.B * a.Tk * a.Hk * a.D + 255) / 256;
         launch_kernel((attn_parts_kernel<T>),
@@ -518,7 +570,7 @@ void run(const AttnArgs &a, hipStream_t s)
     }
     if (nq > 0)
         launch_kernel((attn_dq_kernel<T, DP>), dim3((uint32_t)(nq * a.B * a.Hq)),
-                      dim3(64 * kWaves), tiles + (2 * 3 + 2) * kStep * 4 + (1 + 4 * kWaves) * 4, s, a);
+                      dim3(64 * NW), tiles + (2 * 3 + 2) * kStep * 4 + (1 + 4 * NW) * 4, s, a);
 }
 
 int64_t round16(int64_t bytes) { return (bytes + 15) & ~(int64_t)15; }
@@ -529,7 +581,8 @@ int64_t round16(int64_t bytes) { return (bytes + 15) & ~(int64_t)15; }
 // bytes).
 size_t plan_attn_backward(AttnArgs *a)
 {
-    const int64_t blocks = (int64_t)((a->Tk + 127) / 128) * a->B * a->Hk;
+    const int per = 32 * (a->D <= 64 ? bwd_waves<64>() : bwd_waves<128>());
+    const int64_t blocks = (int64_t)((a->Tk + per - 1) / per) * a->B * a->Hk;
     const int64_t want = 2 * device_cus();
     int64_t g = blocks > 0 ? (want + blocks - 1) / blocks : 1;
     a->gsplit = (int32_t)(g < 1 ? 1 : g > a->G ? a->G : g);

@@ -2,9 +2,8 @@
 //
 //   out_i = sum_j p_ij v_j,  p_ij = exp(s_ij - lse_i),  lse_i = log sum_j exp(s_ij)
 // over the keys j that query i sees, in one pass with a running maximum and
-// sum per query.  A workgroup of four waves takes 128 queries of one head,
-// each wave 32 of them, and walks the keys that any of its queries sees in
-// tiles of 64, read once into LDS for the four waves (attention.hpp has the
+// sum per query.  A workgroup takes 32 queries of one head for each of its waves, and walks the keys that any of its queries sees in
+// tiles of 64, read once into LDS for all waves (attention.hpp has the
 // layout).  The scores are formed as (keys x queries), so a query's scores
 // lie in two lanes: its maximum and sum are sums over registers and one
 // exchange between the wave's halves, and the weights go into the second
@@ -22,30 +21,38 @@ namespace mp3d {
 
 namespace {
 
-constexpr int kFwdWaves = 4;
 constexpr int kFwdKeys = 64;
 constexpr float kRaise = 8.f;
+
+// Waves of a workgroup.  Two for up to 64 channels: the tiles then leave
+// room for many workgroups on a CU, and short and long spans (documents)
+// even out better; four share the wider tiles.
+template <int DP>
+constexpr int fwd_waves() { return 4; }
 
 // float32 tiles of 128 channels take twice the LDS and the registers: one
 // workgroup on a CU
 template <typename T, int DP>
-constexpr int fwd_occupancy() { return sizeof(typename T::raw) * DP > 256 ? 1 : 2; }
+constexpr int fwd_occupancy()
+{
+    return sizeof(typename T::raw) * DP > 256 ? 1 : sizeof(typename T::raw) * DP > 128 ? 2 : 3;
+}
 
 template <typename T, int DP>
-__global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn_fwd_kernel(AttnArgs a)
+__global__ __launch_bounds__(64 * fwd_waves<DP>(), (fwd_occupancy<T, DP>())) void attn_fwd_kernel(AttnArgs a)
 {
     using R = typename T::raw;
-    constexpr int NT = 64 * kFwdWaves, KB = kFwdKeys, NC = DP / 16, ND = DP / 32;
+    constexpr int NW = fwd_waves<DP>(), NT = 64 * NW, KB = kFwdKeys, NC = DP / 16, ND = DP / 32;
     extern __shared__ __align__(16) unsigned char smem[];
     R *const kt = (R *)smem;                               // [2][KB * DP]
     R *const vt = kt + 2 * KB * DP;                        // [2][KB * DP]
     float *const pk = (float *)(vt + 2 * KB * DP);         // [2][3][KB] key positions
     int *const flag = (int *)(pk + 2 * 3 * KB);            // an infinity or a NaN was dropped
-    int *const ends = flag + 1;                            // [4][kFwdWaves]
+    int *const ends = flag + 1;                            // [4][NW]
 
     // The heads of one sequence that share keys run on one XCD, and the
     // queries that see most keys (the last, if causal) come first.
-    const int nq = (a.Tq + 32 * kFwdWaves - 1) / (32 * kFwdWaves);
+    const int nq = (a.Tq + 32 * NW - 1) / (32 * NW);
     const int heads = a.B * a.Hq;
     int bh, qt;
     if (heads % 8 == 0) {
@@ -58,7 +65,7 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
     }
     const int b = bh / a.Hq, h = bh - b * a.Hq, hk = h / a.G;
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, col = lane & 31, half = lane >> 5;
-    const int q0 = qt * 32 * kFwdWaves, i = q0 + wave * 32 + col;
+    const int q0 = qt * 32 * NW, i = q0 + wave * 32 + col;
     const int ic = min(i, a.Tq - 1);
     const Span sp = row_span(a, b, ic);
 
@@ -77,20 +84,20 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
     ahi = __builtin_amdgcn_readfirstlane(ahi);
     if ((tid & 63) == 0) {
         ends[wave] = wlo;
-        ends[kFwdWaves + wave] = whi;
-        ends[2 * kFwdWaves + wave] = alo;
-        ends[3 * kFwdWaves + wave] = ahi;
+        ends[NW + wave] = whi;
+        ends[2 * NW + wave] = alo;
+        ends[3 * NW + wave] = ahi;
     }
     if (tid == 0) *flag = 0;
     __syncthreads();
-    int glo = ends[0], ghi = ends[kFwdWaves], galo = ends[2 * kFwdWaves],
-        gahi = ends[3 * kFwdWaves];
+    int glo = ends[0], ghi = ends[NW], galo = ends[2 * NW],
+        gahi = ends[3 * NW];
 #pragma unroll
-    for (int w = 1; w < kFwdWaves; ++w) {
+    for (int w = 1; w < NW; ++w) {
         glo = min(glo, ends[w]);
-        ghi = max(ghi, ends[kFwdWaves + w]);
-        galo = max(galo, ends[2 * kFwdWaves + w]);
-        gahi = min(gahi, ends[3 * kFwdWaves + w]);
+        ghi = max(ghi, ends[NW + w]);
+        galo = max(galo, ends[2 * NW + w]);
+        gahi = min(gahi, ends[3 * NW + w]);
     }
 
     const R *kp = (const R *)a.k + b * a.ks[0] + hk * a.ks[2];
@@ -102,6 +109,7 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
 
     // positions relative to the workgroup's first query: differences of
     // tokens near each other stay exact in binary32
+    const Scores sc = scores(a);
     float pq[3], sl[3];
     int64_t base[3];
 #pragma unroll
@@ -110,9 +118,8 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
         const int32_t *p = a.pos_q + ((int64_t)x * a.B + b) * a.Tq;
         base[x] = p[q0];
         pq[x] = (float)(p[ic] - base[x]);
-        sl[x] = a.slopes[h * a.axes + x] * kLog2e;
+        sl[x] = a.slopes[h * a.axes + x] * sc.slope;
     }
-    const Scores sc = scores(a);
 
     f32x16 o[ND];
 #pragma unroll
@@ -120,34 +127,53 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
     float m = kNegInf, l = 0.f;            // l: this half's sum
 
     const int kbeg = ghi > 0 ? glo / KB * KB : 0, kend = ghi;
-    TileRegs<T, DP, KB, NT> kr, vr;
+    TileDirect<T, DP, KB, NT> kd, vd;
+    kd.init(tid, a.ks[1], a.D);
+    vd.init(tid, a.vs[1], a.D);
+    const bool usable = kd.usable(a.vec, a.ks[1], a.D) && vd.usable(a.vec, a.vs[1], a.D);
+    if (a.D < DP) {                        // channels that no direct load writes
+        for (int x = tid; x < 4 * KB * DP * (int)sizeof(R) / 16; x += NT)
+            ((u32x4 *)kt)[x] = u32x4{0u, 0u, 0u, 0u};
+        __syncthreads();
+    }
+    auto direct = [&](int k0) {
+        return usable && max(glo, galo) <= k0 && k0 + KB <= min(ghi, gahi);
+    };
     int32_t pr[3];                         // (not touched before place: that would wait)
-    auto fetch = [&](int k0) {
-        kr.load(kp, a.ks[1], k0, glo, ghi, a.D, a.vec, tid);
-        vr.load(vp, a.vs[1], k0, glo, ghi, a.D, a.vec, tid);
+    auto fetch = [&](int k0, int buf) {
+        if (direct(k0)) {
+            kd.load(kp + k0 * a.ks[1], a.ks[1], kt + buf * KB * DP, wave);
+            vd.load(vp + k0 * a.vs[1], a.vs[1], vt + buf * KB * DP, wave);
+        }
 #pragma unroll
         for (int x = 0; x < 3; ++x)
             if (x < a.axes && tid < KB)
                 pr[x] = a.pos_k[((int64_t)x * a.B + b) * a.Tk + min(k0 + tid, a.Tk - 1)];
     };
     auto place = [&](int k0, int buf) {
-        if (!(galo <= k0 && k0 + KB <= gahi) && vr.drop()) *flag = 1;
-        kr.store(kt + buf * KB * DP, tid);
-        vr.store(vt + buf * KB * DP, tid);
+        if (!direct(k0)) {
+            TileRegs<T, DP, KB, NT> r;
+            r.load(vp, a.vs[1], k0, glo, ghi, a.D, a.vec, tid);
+            if (!(galo <= k0 && k0 + KB <= gahi) && r.drop()) *flag = 1;
+            r.store(vt + buf * KB * DP, tid);
+            r.load(kp, a.ks[1], k0, glo, ghi, a.D, a.vec, tid);
+            r.store(kt + buf * KB * DP, tid);
+        }
 #pragma unroll
         for (int x = 0; x < 3; ++x)
             if (x < a.axes && tid < KB) pk[(buf * 3 + x) * KB + tid] = (float)(pr[x] - base[x]);
     };
     if (kbeg < kend) {
-        fetch(kbeg);
+        fetch(kbeg, 0);
         place(kbeg, 0);
     }
+    wait_direct();
     __syncthreads();
     int n = 0;
     for (int k0 = kbeg; k0 < kend; k0 += KB, ++n) {
         const int buf = n & 1;
         const bool more = k0 + KB < kend;
-        if (more) fetch(k0 + KB);
+        if (more) fetch(k0 + KB, buf ^ 1);
         if (k0 < whi && k0 + KB > wlo) {
             const R *kb = kt + buf * KB * DP, *vb = vt + buf * KB * DP;
             f32x16 s[2];
@@ -163,10 +189,10 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
 #pragma unroll
                 for (int u = 0; u < 2; ++u) cap_tanh<T>(s[u], sc.capin);
             }
-            if (sc.multiply) {
+            if (sc.multiply || a.axes > 0) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    s[u] *= sc.c2;
+                    if (sc.multiply) s[u] *= sc.scale;
 #pragma unroll
                     for (int x = 0; x < 3; ++x) {
                         if (x >= a.axes) break;
@@ -222,6 +248,7 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
                     o[d] = mma<T>(col_frag<T, DP>(vb, c, d * 32, lane), pf[c], o[d]);
         }
         if (more) place(k0 + KB, buf ^ 1);
+        wait_direct();
         __syncthreads();
     }
 
@@ -252,11 +279,12 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
 template <typename T, int DP>
 hipError_t run(const AttnArgs &a, hipStream_t s)
 {
+    constexpr int NW = fwd_waves<DP>();
     constexpr uint32_t lds = 4 * kFwdKeys * DP * sizeof(typename T::raw) +
-                             2 * 3 * kFwdKeys * sizeof(float) + (1 + 4 * kFwdWaves) * sizeof(int);
-    const int64_t nq = (a.Tq + 32 * kFwdWaves - 1) / (32 * kFwdWaves);
+                             2 * 3 * kFwdKeys * sizeof(float) + (1 + 4 * NW) * sizeof(int);
+    const int64_t nq = (a.Tq + 32 * NW - 1) / (32 * NW);
     launch_kernel((attn_fwd_kernel<T, DP>), dim3((uint32_t)(nq * a.B * a.Hq)),
-                  dim3(64 * kFwdWaves), lds, s, a);
+                  dim3(64 * NW), lds, s, a);
     return hipGetLastError();
 }
 

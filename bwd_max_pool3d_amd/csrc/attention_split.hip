@@ -82,6 +82,7 @@ void attn_split_kernel(AttnArgs a)
         Frag<T> qf[NC];
 #pragma unroll
         for (int c = 0; c < NC; ++c) qf[c] = load8<T>(qp, c * 16 + half * 8, a.D, a.vec);
+        const Scores sc = scores(a);
         float pq[3], sl[3];
         int64_t base[3];
 #pragma unroll
@@ -90,9 +91,8 @@ void attn_split_kernel(AttnArgs a)
             const int32_t *p = a.pos_q + ((int64_t)x * a.B + b) * a.Tq;
             base[x] = p[0];
             pq[x] = (float)(p[t] - base[x]);
-            sl[x] = a.slopes[h * a.axes + x] * kLog2e;
+            sl[x] = a.slopes[h * a.axes + x] * sc.slope;
         }
-        const Scores sc = scores(a);
         TileRegs<T, DP, KB, 64> kr, vr;
         int32_t pr[3];
         auto fetch = [&](int k0) {
@@ -126,8 +126,8 @@ void attn_split_kernel(AttnArgs a)
             for (int c = 0; c < NC; ++c)
                 s = mma<T>(row_frag<T, DP>(kt, col, c * 16 + half * 8), qf[c], s);
             if (a.cap > 0.f) cap_tanh<T>(s, sc.capin);
-            if (sc.multiply) {
-                s *= sc.c2;
+            if (sc.multiply || a.axes > 0) {
+                if (sc.multiply) s *= sc.scale;
 #pragma unroll
                 for (int x = 0; x < 3; ++x) {
                     if (x >= a.axes) break;
