@@ -16,7 +16,7 @@ OBJDIR = os.path.join(HERE, "_build")
 SOURCES = ["api.hip", "plan.hip", "forward.hip", "forward_fixed.hip", "forward_col.hip",
            "backward.hip", "backward_owner.hip", "small.hip", "forward_ex.hip",
            "api_tokens.hip", "rope.hip", "gated_norm.hip", "attention_fwd.hip",
-           "attention_split.hip", "attention_bwd.hip"]
+           "attention_split.hip", "attention_bwd.hip", "attention_order.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

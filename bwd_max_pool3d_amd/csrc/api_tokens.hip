@@ -426,6 +426,7 @@ int mp3d_attention_workspace_bytes(const mp3d_attention *d, int backward, size_t
     if (a.B == 0 || a.Tq == 0) return MP3D_OK;
     if (backward) *bytes = plan_attn_backward(&a);
     else if (attn_split_wanted(a)) *bytes = plan_attn_split(&a);
+    else *bytes = (size_t)attn_order_bytes(a, false);
     return MP3D_OK;
 }
 
@@ -455,8 +456,12 @@ int mp3d_attention_forward(const mp3d_attention *d, const void *q, const void *k
         if ((rc = check_workspace(workspace, workspace_bytes, plan_attn_split(&a)))) return rc;
         if ((rc = check_launch((int64_t)a.nrb * a.Hk * a.B * a.nsplit))) return rc;
         place_attn_split(&a, workspace);
-    } else if ((rc = check_launch((int64_t)((a.Tq + 63) / 64) * a.B * a.Hq))) {
-        return rc;
+    } else {
+        const size_t need = (size_t)attn_order_bytes(a, false);
+        if ((rc = check_workspace(workspace, workspace_bytes, need))) return rc;
+        if ((rc = check_launch((int64_t)((a.Tq + kAttnRows - 1) / kAttnRows) * a.B * a.Hq)))
+            return rc;
+        a.order_q = need ? (int32_t *)workspace : nullptr;
     }
     if (log_enabled())
         fprintf(stderr, "[mp3d] attention forward dtype=%d %s vec=%d nsplit=%d\n", d->dtype,
@@ -502,8 +507,8 @@ int mp3d_attention_backward(const mp3d_attention *d, const void *dout, const int
     a.vec = wide_rows(q, a.qs, es) && wide_rows(k, a.ks, es) && wide_rows(v, a.vs, es) &&
             wide_rows(dout, a.gs, es);
     if ((rc = check_workspace(workspace, workspace_bytes, plan_attn_backward(&a)))) return rc;
-    if ((rc = check_launch((int64_t)((a.Tq + 63) / 64) * a.B * a.Hq)) ||
-        (rc = check_launch((int64_t)((a.Tk + 63) / 64) * a.B * a.Hk * a.gsplit)))
+    if ((rc = check_launch((int64_t)((a.Tq + kAttnRows - 1) / kAttnRows) * a.B * a.Hq)) ||
+        (rc = check_launch((int64_t)((a.Tk + kAttnRows - 1) / kAttnRows) * a.B * a.Hk * a.gsplit)))
         return rc;
     place_attn_backward(&a, workspace);
     if (log_enabled())

@@ -145,22 +145,30 @@ __device__ __forceinline__ float halves_sum(float v)
 }
 
 // --- tiles in LDS: rows of DP elements in chunks of 8, the chunks of a row
-// swapped by the row's number so that neither the row fragments (the same
-// chunk of 32 rows) nor the column fragments (4 rows by 16 columns) meet on
-// a bank.
-__device__ __forceinline__ int tile_swap(int row) { return ((row & 3) << 1) | ((row >> 2) & 1); }
+// swapped by the row's number.  LDS has 64 banks of 4 bytes, and serves 16
+// lanes of 16 bytes, or 32 of 8, at once.  So that they spread over all
+// banks, the same chunk of 16 rows (row fragments) must take 16 places of
+// 256 bytes, and so must 4 chunks of 4 rows (column fragments).  A row of
+// 128 16-bit elements is 256 bytes, one of 64 half of that.
+template <typename R, int DP>
+__device__ __forceinline__ int tile_swap(int row)
+{
+    if constexpr (sizeof(R) == 2 && DP == 128) return ((row & 3) << 2) | ((row >> 2) & 3);
+    if constexpr (sizeof(R) == 2) return ((row & 2) << 1) | ((row >> 2) & 3);
+    return row & 7;
+}
 
-template <int DP>
+template <typename R, int DP>
 __device__ __forceinline__ int tile_at(int row, int chunk)
 {
-    return row * DP + ((chunk ^ tile_swap(row)) << 3);
+    return row * DP + ((chunk ^ tile_swap<R, DP>(row)) << 3);
 }
 
 // Elements d0 .. d0 + 7 (d0 a multiple of 8) of a row.
 template <typename T, int DP>
 __device__ __forceinline__ Frag<T> row_frag(const typename T::raw *tile, int row, int d0)
 {
-    const u32x4 *p = (const u32x4 *)(tile + tile_at<DP>(row, d0 >> 3));
+    const u32x4 *p = (const u32x4 *)(tile + tile_at<typename T::raw, DP>(row, d0 >> 3));
     Frag<T> f;
 #pragma unroll
     for (int i = 0; i < Frag<T>::NV; ++i) f.w[i] = p[i];
@@ -184,7 +192,7 @@ __device__ __forceinline__ Frag<T> col_frag(const typename T::raw *tile, int c, 
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const typename T::raw *p =
-                tile + tile_at<DP>(row + 8 * k, col >> 3) + (col & 7);
+                tile + tile_at<typename T::raw, DP>(row + 8 * k, col >> 3) + (col & 7);
             o.v[k] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t *)p);
         }
         f = __builtin_bit_cast(Frag<T>, o);
@@ -196,7 +204,7 @@ __device__ __forceinline__ Frag<T> col_frag(const typename T::raw *tile, int c, 
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int row = 16 * c + 4 * half + (i < 4 ? i : i + 4);
-            o.e[i] = tile[tile_at<DP>(row, col >> 3) + (col & 7)];
+            o.e[i] = tile[tile_at<typename T::raw, DP>(row, col >> 3) + (col & 7)];
         }
         f = __builtin_bit_cast(Frag<T>, o);
     }
@@ -294,7 +302,7 @@ struct TileRegs {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const int id = t + NT * j;
-            u32x4 *p = (u32x4 *)(tile + tile_at<DP>(id / (DP / 8), id % (DP / 8)));
+            u32x4 *p = (u32x4 *)(tile + tile_at<typename T::raw, DP>(id / (DP / 8), id % (DP / 8)));
 #pragma unroll
             for (int i = 0; i < Frag<T>::NV; ++i) p[i] = f[j].w[i];
         }
@@ -332,13 +340,14 @@ struct TileDirect {
     static constexpr int UNITS = DP / PER;                 // of a row
     static constexpr int STEP = NT / UNITS;                // rows of one round over the threads
     static constexpr int N = ROWS / STEP;
-    static_assert(N * STEP == ROWS && STEP % 8 == 0, "every round swaps alike");
+    static_assert(N * STEP == ROWS && STEP % (sizeof(R) == 2 ? 16 : 8) == 0,
+                  "every round swaps alike");
     uint32_t off;                                          // bytes from the round's first row
     bool on;                                               // the lane's channels are there
 
     __device__ __forceinline__ void init(int t, int64_t stride, int D)
     {
-        const int row = t / UNITS, u = t % UNITS, c = (u * PER / 8) ^ tile_swap(row);
+        const int row = t / UNITS, u = t % UNITS, c = (u * PER / 8) ^ tile_swap<R, DP>(row);
         const int e = c * 8 + (u * PER) % 8;
         off = (uint32_t)(row * stride + e) * (uint32_t)sizeof(R);
         on = e < D;
@@ -379,6 +388,30 @@ __device__ __forceinline__ void wait_direct() { asm volatile("s_waitcnt vmcnt(0)
 // score of such a key to -infinity, which gives both.  A query that is not
 // finite has no finite score, so its lse is NaN, or -infinity.)
 //
+// --- which block of which head a workgroup takes.  Heads go to the XCDs in
+// contiguous runs (those that share keys share an L2).  Within an XCD the
+// longest blocks of all its heads come first; every second round over the
+// CUs runs backwards, so that where two rounds fit at once a CU gets a long
+// and a short one.
+struct Block {
+    int head, no;                          // no: in order of falling length
+};
+
+__device__ __forceinline__ Block block_of(uint32_t id, int heads, int blocks)
+{
+    constexpr int kCus = 32;               // of an XCD
+    const bool split = heads % 8 == 0;
+    const int per = split ? heads / 8 : heads, round = split ? kCus : 8 * kCus;
+    const int total = per * blocks;
+    int j = split ? id / 8 : id;
+    const int c = j / round;
+    if (c & 1) {
+        const int first = c * round;
+        j = first + min(round, total - first) - 1 - (j - first);
+    }
+    return {(split ? (int)(id % 8) * per : 0) + j % per, j / per};
+}
+
 // --- the keys a query sees
 struct Span {
     int lo, hi;                            // [lo, hi) within [0, Tk); {0, 0}: none

@@ -25,6 +25,7 @@ namespace mp3d {
 
 namespace {
 
+constexpr int kBwdWaves = kAttnRows / 32;
 constexpr int kStep = 32;                  // keys (dq) or queries (dk, dv) per step
 constexpr float kInf = __builtin_huge_valf();
 
@@ -82,10 +83,6 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a)
     }
 }
 
-// Waves of a workgroup (see attention_fwd.hip)
-template <int DP>
-constexpr int bwd_waves() { return 4; }
-
 // ------------------------------------------------------------------- dq
 
 template <typename T, int DP>
@@ -95,10 +92,10 @@ constexpr int bwd_occupancy()
 }
 
 template <typename T, int DP>
-__global__ __launch_bounds__(64 * bwd_waves<DP>(), (bwd_occupancy<T, DP>())) void attn_dq_kernel(AttnArgs a)
+__global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn_dq_kernel(AttnArgs a)
 {
     using R = typename T::raw;
-    constexpr int NW = bwd_waves<DP>(), NT = 64 * NW, KB = kStep, NC = DP / 16, ND = DP / 32;
+    constexpr int NW = kBwdWaves, NT = 64 * NW, KB = kStep, NC = DP / 16, ND = DP / 32;
     extern __shared__ __align__(16) unsigned char smem[];
     R *const kt = (R *)smem;                               // [2][KB * DP]
     R *const vt = kt + 2 * KB * DP;                        // [2][KB * DP]
@@ -108,17 +105,10 @@ __global__ __launch_bounds__(64 * bwd_waves<DP>(), (bwd_occupancy<T, DP>())) voi
     int *const ends = flag + 1;                            // [4][NW]
 
     const int nq = (a.Tq + 32 * NW - 1) / (32 * NW);
-    const int heads = a.B * a.Hq;
-    int bh, qt;
-    if (heads % 8 == 0) {
-        const int per = heads / 8, j = blockIdx.x / 8;
-        bh = (blockIdx.x % 8) * per + j % per;
-        qt = nq - 1 - j / per;
-    } else {
-        bh = blockIdx.x % heads;
-        qt = nq - 1 - blockIdx.x / heads;
-    }
+    const Block blk = block_of(blockIdx.x, a.B * a.Hq, nq);
+    const int bh = blk.head;
     const int b = bh / a.Hq, h = bh - b * a.Hq, hk = h / a.G;
+    const int qt = a.order_q ? a.order_q[(int64_t)b * nq + blk.no] : nq - 1 - blk.no;
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, col = lane & 31,
               half = lane >> 5;
     const int q0 = qt * 32 * NW, i = q0 + wave * 32 + col;
@@ -282,10 +272,10 @@ template <typename T, int DP>
 constexpr int dkv_occupancy() { return sizeof(typename T::raw) * DP > 128 ? 1 : 2; }
 
 template <typename T, int DP>
-__global__ __launch_bounds__(64 * bwd_waves<DP>(), (dkv_occupancy<T, DP>())) void attn_dkv_kernel(AttnArgs a)
+__global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn_dkv_kernel(AttnArgs a)
 {
     using R = typename T::raw;
-    constexpr int NW = bwd_waves<DP>(), NT = 64 * NW, QB = kStep, NC = DP / 16, ND = DP / 32;
+    constexpr int NW = kBwdWaves, NT = 64 * NW, QB = kStep, NC = DP / 16, ND = DP / 32;
     extern __shared__ __align__(16) unsigned char smem[];
     R *const qt = (R *)smem;                               // [2][QB * DP]
     R *const gt = qt + 2 * QB * DP;                        // [2][QB * DP]
@@ -297,14 +287,12 @@ __global__ __launch_bounds__(64 * bwd_waves<DP>(), (dkv_occupancy<T, DP>())) voi
     int *const flag = sln + 2 * QB;                        // an infinity or a NaN was dropped
     int *const ends = flag + 1;                            // [2] first and last tile
 
-    // parts of one key head, and the key blocks of one sequence, on one XCD
     const int nk = (a.Tk + 32 * NW - 1) / (32 * NW);
-    const uint32_t id = xcd_local_block(blockIdx.x, gridDim.x);
-    const int kb = id % nk;
-    int64_t rest = id / nk;
-    const int gpart = (int)(rest % a.gsplit);
-    rest /= a.gsplit;
-    const int hk = (int)(rest % a.Hk), b = (int)(rest / a.Hk);
+    const Block blk = block_of(blockIdx.x, a.B * a.Hk * a.gsplit, nk);
+    const int gpart = blk.head % a.gsplit, bhk = blk.head / a.gsplit;
+    const int b = bhk / a.Hk, hk = bhk - b * a.Hk;
+    // (without documents the first keys are seen by the most queries, if causal)
+    const int kb = a.order_k ? a.order_k[(int64_t)b * nk + blk.no] : blk.no;
     const int g0 = (int)((int64_t)a.G * gpart / a.gsplit);
     const int g1 = (int)((int64_t)a.G * (gpart + 1) / a.gsplit);
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, col = lane & 31,
@@ -555,7 +543,7 @@ __global__ __launch_bounds__(256) void attn_parts_kernel(AttnArgs a)
 template <typename T, int DP>
 void run(const AttnArgs &a, hipStream_t s)
 {
-    constexpr int NW = bwd_waves<DP>();
+    constexpr int NW = kBwdWaves;
     constexpr uint32_t tiles = 4 * kStep * DP * sizeof(typename T::raw);
     const int64_t nq = (a.Tq + 32 * NW - 1) / (32 * NW);
     const int64_t nk = (a.Tk + 32 * NW - 1) / (32 * NW);
@@ -577,17 +565,17 @@ int64_t round16(int64_t bytes) { return (bytes + 15) & ~(int64_t)15; }
 
 }  // namespace
 
-// Workspace: tiles, spans, rowd, then the parts (each at a multiple of 16
+// Workspace: tiles, spans, rowd, the blocks' orders, then the parts (each at a multiple of 16
 // bytes).
 size_t plan_attn_backward(AttnArgs *a)
 {
-    const int per = 32 * (a->D <= 64 ? bwd_waves<64>() : bwd_waves<128>());
-    const int64_t blocks = (int64_t)((a->Tk + per - 1) / per) * a->B * a->Hk;
+    const int64_t blocks = (int64_t)((a->Tk + kAttnRows - 1) / kAttnRows) * a->B * a->Hk;
     const int64_t want = 2 * device_cus();
     int64_t g = blocks > 0 ? (want + blocks - 1) / blocks : 1;
     a->gsplit = (int32_t)(g < 1 ? 1 : g > a->G ? a->G : g);
     const int64_t nt = (a->Tq + 31) / 32, rows = (int64_t)a->B * a->Tq;
-    int64_t n = round16(rows * a->Hq * 8) + round16(rows * 8) + (int64_t)a->B * nt * 16;
+    int64_t n = round16(rows * a->Hq * 8) + round16(rows * 8) + (int64_t)a->B * nt * 16 +
+                attn_order_bytes(*a, false) + attn_order_bytes(*a, true);
     if (a->gsplit > 1)
         n += 2 * round16((int64_t)a->gsplit * a->B * a->Tk * a->Hk * a->D * 4);
     return (size_t)n;
@@ -603,6 +591,11 @@ void place_attn_backward(AttnArgs *a, void *workspace)
     p += round16(rows * 8);
     a->rowd = (float *)p;
     p += round16(rows * a->Hq * 8);
+    const int64_t oq = attn_order_bytes(*a, false), ok = attn_order_bytes(*a, true);
+    a->order_q = oq ? (int32_t *)p : nullptr;
+    p += oq;
+    a->order_k = ok ? (int32_t *)p : nullptr;
+    p += ok;
     a->part_dk = (float *)p;
     p += round16((int64_t)a->gsplit * a->B * a->Tk * a->Hk * a->D * 4);
     a->part_dv = (float *)p;
@@ -614,6 +607,7 @@ hipError_t launch_attn_backward(const AttnArgs &a, hipStream_t s)
     const int64_t nt = (a.Tq + 31) / 32;
     if (nt > 0)
         launch_kernel((attn_rows_kernel<T>), dim3((uint32_t)(nt * a.B * a.Hq)), dim3(256), 0, s, a);
+    if (nt > 0) launch_attn_order(a, true, s);
     if (a.D <= 64) run<T, 64>(a, s);
     else run<T, 128>(a, s);
     return hipGetLastError();

@@ -21,14 +21,9 @@ namespace mp3d {
 
 namespace {
 
+constexpr int kFwdWaves = kAttnRows / 32;
 constexpr int kFwdKeys = 64;
 constexpr float kRaise = 8.f;
-
-// Waves of a workgroup.  Two for up to 64 channels: the tiles then leave
-// room for many workgroups on a CU, and short and long spans (documents)
-// even out better; four share the wider tiles.
-template <int DP>
-constexpr int fwd_waves() { return 4; }
 
 // float32 tiles of 128 channels take twice the LDS and the registers: one
 // workgroup on a CU
@@ -39,10 +34,10 @@ constexpr int fwd_occupancy()
 }
 
 template <typename T, int DP>
-__global__ __launch_bounds__(64 * fwd_waves<DP>(), (fwd_occupancy<T, DP>())) void attn_fwd_kernel(AttnArgs a)
+__global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn_fwd_kernel(AttnArgs a)
 {
     using R = typename T::raw;
-    constexpr int NW = fwd_waves<DP>(), NT = 64 * NW, KB = kFwdKeys, NC = DP / 16, ND = DP / 32;
+    constexpr int NW = kFwdWaves, NT = 64 * NW, KB = kFwdKeys, NC = DP / 16, ND = DP / 32;
     extern __shared__ __align__(16) unsigned char smem[];
     R *const kt = (R *)smem;                               // [2][KB * DP]
     R *const vt = kt + 2 * KB * DP;                        // [2][KB * DP]
@@ -50,20 +45,12 @@ __global__ __launch_bounds__(64 * fwd_waves<DP>(), (fwd_occupancy<T, DP>())) voi
     int *const flag = (int *)(pk + 2 * 3 * KB);            // an infinity or a NaN was dropped
     int *const ends = flag + 1;                            // [4][NW]
 
-    // The heads of one sequence that share keys run on one XCD, and the
-    // queries that see most keys (the last, if causal) come first.
     const int nq = (a.Tq + 32 * NW - 1) / (32 * NW);
-    const int heads = a.B * a.Hq;
-    int bh, qt;
-    if (heads % 8 == 0) {
-        const int per = heads / 8, j = blockIdx.x / 8;
-        bh = (blockIdx.x % 8) * per + j % per;
-        qt = nq - 1 - j / per;
-    } else {
-        bh = blockIdx.x % heads;
-        qt = nq - 1 - blockIdx.x / heads;
-    }
+    const Block blk = block_of(blockIdx.x, a.B * a.Hq, nq);
+    const int bh = blk.head;
     const int b = bh / a.Hq, h = bh - b * a.Hq, hk = h / a.G;
+    // (without documents the last queries see the most, if causal)
+    const int qt = a.order_q ? a.order_q[(int64_t)b * nq + blk.no] : nq - 1 - blk.no;
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, col = lane & 31, half = lane >> 5;
     const int q0 = qt * 32 * NW, i = q0 + wave * 32 + col;
     const int ic = min(i, a.Tq - 1);
@@ -279,10 +266,11 @@ __global__ __launch_bounds__(64 * fwd_waves<DP>(), (fwd_occupancy<T, DP>())) voi
 template <typename T, int DP>
 hipError_t run(const AttnArgs &a, hipStream_t s)
 {
-    constexpr int NW = fwd_waves<DP>();
+    constexpr int NW = kFwdWaves;
     constexpr uint32_t lds = 4 * kFwdKeys * DP * sizeof(typename T::raw) +
                              2 * 3 * kFwdKeys * sizeof(float) + (1 + 4 * NW) * sizeof(int);
     const int64_t nq = (a.Tq + 32 * NW - 1) / (32 * NW);
+    launch_attn_order(a, false, s);
     launch_kernel((attn_fwd_kernel<T, DP>), dim3((uint32_t)(nq * a.B * a.Hq)),
                   dim3(64 * NW), lds, s, a);
     return hipGetLastError();

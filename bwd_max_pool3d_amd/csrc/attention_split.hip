@@ -289,7 +289,7 @@ void run(const AttnArgs &a, hipStream_t s)
 // The split form where the other one would leave most of the card idle.
 bool attn_split_wanted(const AttnArgs &a)
 {
-    const int64_t blocks = (int64_t)a.B * a.Hq * ((a.Tq + 127) / 128);
+    const int64_t blocks = (int64_t)a.B * a.Hq * ((a.Tq + kAttnRows - 1) / kAttnRows);
     return (int64_t)a.Tq * a.G <= 32 || (blocks < device_cus() && a.Tk >= 1024 && a.Tq < 256);
 }
 

@@ -70,6 +70,8 @@ hipError_t launch_norm_backward(const NormPlan &p, hipStream_t s);
 
 // --- attention (attention_*.hip)
 constexpr int kAttnMaxD = 128;
+constexpr int kAttnRows = 128;             // queries (keys, for dk and dv) of a workgroup
+constexpr int kOrderMax = 512;             // blocks of a sequence that are ordered by length
 struct AttnArgs {
     const void *q, *k, *v;
     void *out;                 // (B, Tq, Hq, D)
@@ -85,6 +87,7 @@ struct AttnArgs {
     int32_t causal, ndocs;
     const int32_t *docs, *prefix, *kv_len;
     int32_t vec;               // every row of q, k, v (and dout) starts at a multiple of 16 bytes
+    int32_t *order_q, *order_k;  // (B, blocks): blocks by falling length, or NULL
     // split form: rows of one key head (Tq * G) in blocks of 32, keys in chunks
     int32_t nrb, nsplit, chunk;
     float *part_o;             // (nsplit, B, Hk, Tq * G, D) sums, unnormalised
@@ -97,6 +100,8 @@ struct AttnArgs {
                                // their keys [lo, hi) and the keys all of them see
     float *part_dk, *part_dv;  // (gsplit, B, Tk, Hk, D), when gsplit > 1
 };
+int64_t attn_order_bytes(const AttnArgs &a, bool keys);
+void launch_attn_order(const AttnArgs &a, bool backward, hipStream_t s);
 bool attn_split_wanted(const AttnArgs &a);
 // nrb, nsplit and chunk; returns the workspace bytes
 size_t plan_attn_split(AttnArgs *a);
