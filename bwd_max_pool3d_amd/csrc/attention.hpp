@@ -78,6 +78,34 @@ __device__ __forceinline__ Frag<T> pack8(const f32x16 &s, int c)
     return __builtin_bit_cast(Frag<T>, o);
 }
 
+// The order in which a stretch of reads from LDS and matrix products is
+// issued, up to issued(): `ahead` reads, then a product and `per` reads at a
+// time.  Left to itself the compiler reads each fragment just before its use,
+// and a wave waits for LDS 30 times a tile; read all at once, the fragments
+// take registers that are not there.  float32 is left to the compiler (its
+// fragments are several reads and products each).
+template <typename T, int AHEAD>
+__device__ __forceinline__ void reads_ahead()
+{
+    if constexpr (sizeof(typename T::raw) == 2) __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+}
+template <typename T, int PRODUCTS, int PER>
+__device__ __forceinline__ void products_and_reads()
+{
+    if constexpr (sizeof(typename T::raw) == 2) {
+#pragma unroll
+        for (int i = 0; i < PRODUCTS; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            if constexpr (PER > 0) __builtin_amdgcn_sched_group_barrier(0x100, PER, 0);
+        }
+    }
+}
+template <typename T>
+__device__ __forceinline__ void issued()
+{
+    if constexpr (sizeof(typename T::raw) == 2) __builtin_amdgcn_sched_barrier(0);
+}
+
 // Row of a result's register r (see above).
 __device__ __forceinline__ constexpr int acc_row(int r, int half)
 {

@@ -88,7 +88,7 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a)
 template <typename T, int DP>
 constexpr int bwd_occupancy()
 {
-    return sizeof(typename T::raw) * DP > 256 ? 1 : sizeof(typename T::raw) * DP > 128 ? 2 : 3;
+    return sizeof(typename T::raw) * DP > 256 ? 1 : 2;
 }
 
 template <typename T, int DP>
@@ -213,13 +213,25 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
         if (more) fetch(k0 + KB, buf ^ 1);
         if (k0 < whi && k0 + KB > wlo) {
             const R *kb = kt + buf * KB * DP, *vb = vt + buf * KB * DP;
+            Frag<T> kr[NC], vr[NC], kc[ND][2];
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                kr[c] = row_frag<T, DP>(kb, col, c * 16 + half * 8);
+                vr[c] = row_frag<T, DP>(vb, col, c * 16 + half * 8);
+            }
             f32x16 s = f32x16(0.f), dp = f32x16(0.f);
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
-                s = mma<T>(row_frag<T, DP>(kb, col, c * 16 + half * 8), qf[c], s);
+            for (int c = 0; c < NC; ++c) s = mma<T>(kr[c], qf[c], s);
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
-                dp = mma<T>(row_frag<T, DP>(vb, col, c * 16 + half * 8), gf[c], dp);
+            for (int c = 0; c < NC; ++c) dp = mma<T>(vr[c], gf[c], dp);
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) kc[d][c] = col_frag<T, DP>(kb, c, d * 32, lane);
+            reads_ahead<T, NC>();
+            products_and_reads<T, NC, 1>();
+            products_and_reads<T, NC, 2>();
+            issued<T>();
 #pragma unroll
             for (int r = 0; r < 16; ++r) dp[r] -= rd.y;
             if (a.cap > 0.f) {
@@ -254,8 +266,8 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
             const Frag<T> e0 = pack8<T>(s, 0), e1 = pack8<T>(s, 1);
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
-                o[d] = mma<T>(col_frag<T, DP>(kb, 0, d * 32, lane), e0, o[d]);
-                o[d] = mma<T>(col_frag<T, DP>(kb, 1, d * 32, lane), e1, o[d]);
+                o[d] = mma<T>(kc[d][0], e0, o[d]);
+                o[d] = mma<T>(kc[d][1], e1, o[d]);
             }
         }
         if (more) place(k0 + KB, buf ^ 1, n + 1);
@@ -437,14 +449,29 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
         if (__builtin_amdgcn_readfirstlane(u.x < kw + 32 && u.y > kw)) {
             const R *qb = qt + buf * QB * DP, *gb = gt + buf * QB * DP;
             const bool part = !__builtin_amdgcn_readfirstlane(u.z <= kw && kw + 32 <= u.w);
+            Frag<T> qr[NC], gr[NC], qc[ND][2], gc[ND][2];
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                qr[c] = row_frag<T, DP>(qb, col, c * 16 + half * 8);
+                gr[c] = row_frag<T, DP>(gb, col, c * 16 + half * 8);
+            }
             f32x16 s = f32x16(0.f), dp = f32x16(0.f);
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
-                s = mma<T>(row_frag<T, DP>(qb, col, c * 16 + half * 8), kf[c], s);
+            for (int c = 0; c < NC; ++c) s = mma<T>(qr[c], kf[c], s);
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
-                dp = mma<T>(row_frag<T, DP>(gb, col, c * 16 + half * 8), vf[c], dp);
+            for (int c = 0; c < NC; ++c) dp = mma<T>(gr[c], vf[c], dp);
             const f32x16 lr = acc_rows(rl + buf * QB, half), dr = acc_rows(rd + buf * QB, half);
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    gc[d][c] = col_frag<T, DP>(gb, c, d * 32, lane);
+                    qc[d][c] = col_frag<T, DP>(qb, c, d * 32, lane);
+                }
+            reads_ahead<T, NC>();
+            products_and_reads<T, NC, 1>();
+            products_and_reads<T, NC, 4 + 8 / NC>();
+            issued<T>();
 #pragma unroll
             for (int r = 0; r < 16; ++r) dp[r] -= dr[r];
             if (a.cap > 0.f) {
@@ -480,10 +507,10 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
             const Frag<T> e0 = pack8<T>(dp, 0), e1 = pack8<T>(dp, 1);
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
-                dv[d] = mma<T>(col_frag<T, DP>(gb, 0, d * 32, lane), p0, dv[d]);
-                dv[d] = mma<T>(col_frag<T, DP>(gb, 1, d * 32, lane), p1, dv[d]);
-                dk[d] = mma<T>(col_frag<T, DP>(qb, 0, d * 32, lane), e0, dk[d]);
-                dk[d] = mma<T>(col_frag<T, DP>(qb, 1, d * 32, lane), e1, dk[d]);
+                dv[d] = mma<T>(gc[d][0], p0, dv[d]);
+                dk[d] = mma<T>(qc[d][0], e0, dk[d]);
+                dv[d] = mma<T>(gc[d][1], p1, dv[d]);
+                dk[d] = mma<T>(qc[d][1], e1, dk[d]);
             }
         }
         if (more) place(buf ^ 1);

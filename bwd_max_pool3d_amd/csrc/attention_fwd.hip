@@ -30,7 +30,7 @@ constexpr float kRaise = 8.f;
 template <typename T, int DP>
 constexpr int fwd_occupancy()
 {
-    return sizeof(typename T::raw) * DP > 256 ? 1 : sizeof(typename T::raw) * DP > 128 ? 2 : 3;
+    return sizeof(typename T::raw) * DP > 256 ? 1 : 2;
 }
 
 template <typename T, int DP>
@@ -163,15 +163,25 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
         if (more) fetch(k0 + KB, buf ^ 1);
         if (k0 < whi && k0 + KB > wlo) {
             const R *kb = kt + buf * KB * DP, *vb = vt + buf * KB * DP;
-            f32x16 s[2];
+            Frag<T> kf[NC][2], vf[ND][4];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                s[u] = f32x16(0.f);
+            for (int c = 0; c < NC; ++c)
 #pragma unroll
-                for (int c = 0; c < NC; ++c)
-                    s[u] = mma<T>(row_frag<T, DP>(kb, u * 32 + col, c * 16 + half * 8), qf[c],
-                                  s[u]);
-            }
+                for (int u = 0; u < 2; ++u)
+                    kf[c][u] = row_frag<T, DP>(kb, u * 32 + col, c * 16 + half * 8);
+            f32x16 s[2] = {f32x16(0.f), f32x16(0.f)};
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) s[u] = mma<T>(kf[c][u], qf[c], s[u]);
+#pragma unroll
+            for (int d = 0; d < ND / 2; ++d)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) vf[d][c] = col_frag<T, DP>(vb, c, d * 32, lane);
+            reads_ahead<T, NC>();
+            products_and_reads<T, NC, 1>();
+            products_and_reads<T, NC, 2>();
+            issued<T>();
             if (a.cap > 0.f) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) cap_tanh<T>(s[u], sc.capin);
@@ -229,10 +239,20 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
                 pf[2 * u + 1] = pack8<T>(s[u], 1);
             }
 #pragma unroll
-            for (int d = 0; d < ND; ++d)
+            for (int d = ND / 2; d < ND; ++d)
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    o[d] = mma<T>(col_frag<T, DP>(vb, c, d * 32, lane), pf[c], o[d]);
+                for (int c = 0; c < 4; ++c) vf[d][c] = col_frag<T, DP>(vb, c, d * 32, lane);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int d = 0; d < ND / 2; ++d) o[d] = mma<T>(vf[d][c], pf[c], o[d]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int d = ND / 2; d < ND; ++d) o[d] = mma<T>(vf[d][c], pf[c], o[d]);
+            products_and_reads<T, 2 * ND, 2>();
+            products_and_reads<T, 2 * ND, 0>();
+            issued<T>();
         }
         if (more) place(k0 + KB, buf ^ 1);
         wait_direct();
