@@ -271,6 +271,15 @@ __device__ __forceinline__ bool drop_nonfinite(Frag<T> &f)
     return bad;
 }
 
+// A value that the compiler may not reason about: what depends on it stays
+// inside a rarely taken branch of a loop (computed ahead of the loop, it
+// would cost the common path its registers).
+__device__ __forceinline__ int opaque(int v)
+{
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
 // Elements d0 .. d0 + 7 of a row of D in memory, zero past D.  vec: rows
 // start at multiples of 16 bytes.
 template <typename T>
@@ -470,60 +479,57 @@ __device__ __forceinline__ Span row_span(const AttnArgs &a, int b, int i)
     return hi > lo ? Span{lo, hi} : Span{0, 0};
 }
 
-// --- scores: from the accumulated products q.k to exponents of 2.  Their
-// factor (scale, or the cap) is left to the exponent's own multiply-add
-// (exponent = score * mul - maximum) and divided out of the bias' slopes,
-// unless it is not positive: the largest score would not have the largest
-// exponent.
+// --- scores: from the accumulated products q.k to exponents of 2.  The
+// scale is left to the exponent's own multiply-add (exponent = score * mul -
+// maximum) and divided out of the cap and of the bias' slopes, unless it is
+// not positive: the largest score would not have the largest exponent.
 struct Scores {
-    float capin;                           // scale / cap; 0: no cap
-    float scale;                           // the scores are multiplied by it first
-    float mul;
-    float slope;                           // factor of the slopes
-    bool multiply;                         // scale is not 1
+    bool multiply;                         // by `scale` first
+    float scale, mul;
+    float slope;                           // factor of the bias' slopes
+    float cap, per_cap;                    // the cap and its reciprocal, in these units
 };
 
 __device__ __forceinline__ Scores scores(const AttnArgs &a)
 {
-    const float f = a.cap > 0.f ? a.cap : a.scale;
-    // (a factor whose reciprocal overflows is applied first, too)
-    const bool multiply = !(f > 1e-30f);
-    return {a.cap > 0.f ? a.scale / a.cap : 0.f, multiply ? f : 1.f,
-            multiply ? kLog2e : f * kLog2e, multiply ? 1.f : 1.f / f, multiply};
+    const bool multiply = !(a.scale > 1e-30f);
+    const float unit = multiply ? 1.f : a.scale;
+    return {multiply, a.scale, unit * kLog2e, 1.f / unit, a.cap / unit, unit / a.cap};
 }
 
-// tanh of the 16 scores of a result times f.  float32: the library's tanhf,
-// for its relative accuracy near 0.  16-bit types, whose weights keep 2^-9
-// at best: 1 - 2 / (1 + e^2x), within 2e-7; and where no score of the wave
-// passes 0.35, as with a cap well above the scores, its odd Taylor
-// polynomial, within 1e-7, at half the cost (the exponential and the
-// reciprocal take four times an ordinary instruction each).
+// The 16 scores of a result to c tanh(s / c).  float32: the library's
+// tanhf, for its relative accuracy near 0.  16-bit types, whose weights keep
+// 2^-9 at best: 1 - 2 / (1 + e^2x), within 2e-7; and where no score of the
+// wave passes c / 4, as with a cap well above the scores, the odd Taylor
+// polynomial, within 1e-7, in 5 instructions instead of 5 of which two (the
+// exponential and the reciprocal) take twice the time or more.
 template <typename T>
-__device__ __forceinline__ void cap_tanh(f32x16 &s, float f)
+__device__ __forceinline__ void cap_scores(f32x16 &s, const Scores &sc)
 {
+    const float f = sc.per_cap;
     if constexpr (T::code == F32::code) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s[r] = tanhf(s[r] * f);
+        for (int r = 0; r < 16; ++r) s[r] = sc.cap * tanhf(s[r] * f);
         return;
     }
     float big = fabsf(s[0]);
 #pragma unroll
     for (int r = 1; r < 16; ++r) big = fmaxf(big, fabsf(s[r]));
     // (written so that a NaN takes the other branch)
-    if (!__any(!(big * fabsf(f) < 0.35f))) {
+    if (!__any(!(big * f < 0.25f))) {
+        const float f2 = f * f, c3 = -f2 / 3.f, c5 = f2 * f2 * (2.f / 15.f),
+                    c7 = f2 * f2 * f2 * (-17.f / 315.f);
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-            const float x = s[r] * f, y = x * x;
-            float t = fmaf(y, 62.f / 2835.f, -17.f / 315.f);
-            t = fmaf(t, y, 2.f / 15.f);
-            t = fmaf(t, y, -1.f / 3.f);
-            s[r] = fmaf(t * y, x, x);
+            const float y = s[r] * s[r];
+            s[r] = fmaf(fmaf(fmaf(c7, y, c5), y, c3) * y, s[r], s[r]);
         }
     } else {
         const float g = f * (2.f * kLog2e);
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-            s[r] = fmaf(-2.f, __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(s[r] * g)), 1.f);
+            s[r] = fmaf(-2.f * sc.cap,
+                        __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(s[r] * g)), sc.cap);
     }
 }
 

@@ -91,10 +91,11 @@ constexpr int bwd_occupancy()
     return sizeof(typename T::raw) * DP > 256 ? 1 : 2;
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool GEN>
 __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn_dq_kernel(AttnArgs a)
 {
     using R = typename T::raw;
+    const int axes = GEN ? a.axes : 0;
     constexpr int NW = kBwdWaves, NT = 64 * NW, KB = kStep, NC = DP / 16, ND = DP / 32;
     extern __shared__ __align__(16) unsigned char smem[];
     R *const kt = (R *)smem;                               // [2][KB * DP]
@@ -152,11 +153,11 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
     int64_t base[3];
 #pragma unroll
     for (int x = 0; x < 3; ++x) {
-        if (x >= a.axes) break;
+        if (x >= axes) break;
         const int32_t *p = a.pos_q + ((int64_t)x * a.B + b) * a.Tq;
         base[x] = p[q0];
         pq[x] = (float)(p[ic] - base[x]);
-        sl[x] = a.slopes[h * a.axes + x] * sc.slope;
+        sl[x] = a.slopes[h * axes + x] * sc.slope;
     }
 
     f32x16 o[ND];
@@ -184,11 +185,12 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
         }
 #pragma unroll
         for (int x = 0; x < 3; ++x)
-            if (x < a.axes && tid < KB)
+            if (x < axes && tid < KB)
                 pr[x] = a.pos_k[((int64_t)x * a.B + b) * a.Tk + min(k0 + tid, a.Tk - 1)];
     };
     auto place = [&](int k0, int buf, int n) {
         if (!direct(k0)) {
+            const int tid = opaque(threadIdx.x);
             TileRegs<T, DP, KB, NT> r;
             r.load(kp, a.ks[1], k0, glo, ghi, a.D, a.vec, tid);
             if (!(galo <= k0 && k0 + KB <= gahi) && r.drop(bad + buf * KB, n + 1, tid)) *flag = 1;
@@ -198,7 +200,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
         }
 #pragma unroll
         for (int x = 0; x < 3; ++x)
-            if (x < a.axes && tid < KB) pk[(buf * 3 + x) * KB + tid] = (float)(pr[x] - base[x]);
+            if (x < axes && tid < KB) pk[(buf * 3 + x) * KB + tid] = (float)(pr[x] - base[x]);
     };
     if (kbeg < kend) {
         fetch(kbeg, 0);
@@ -234,16 +236,17 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
             issued<T>();
 #pragma unroll
             for (int r = 0; r < 16; ++r) dp[r] -= rd.y;
-            if (a.cap > 0.f) {
-                cap_tanh<T>(s, sc.capin);
+            if (GEN && sc.multiply) s *= sc.scale;
+            if (GEN && a.cap > 0.f) {
+                cap_scores<T>(s, sc);
+                const float f2 = -sc.per_cap * sc.per_cap;
 #pragma unroll
-                for (int r = 0; r < 16; ++r) dp[r] *= fmaf(-s[r], s[r], 1.f);
+                for (int r = 0; r < 16; ++r) dp[r] *= fmaf(f2 * s[r], s[r], 1.f);
             }
-            if (sc.multiply || a.axes > 0) {
-                if (sc.multiply) s *= sc.scale;
+            if (axes > 0) {
 #pragma unroll
                 for (int x = 0; x < 3; ++x) {
-                    if (x >= a.axes) break;
+                    if (x >= axes) break;
                     const f32x16 p = acc_rows(pk + (buf * 3 + x) * KB, half);
 #pragma unroll
                     for (int r = 0; r < 16; ++r) s[r] = fmaf(-sl[x], fabsf(p[r] - pq[x]), s[r]);
@@ -283,10 +286,11 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
 template <typename T, int DP>
 constexpr int dkv_occupancy() { return sizeof(typename T::raw) * DP > 128 ? 1 : 2; }
 
-template <typename T, int DP>
+template <typename T, int DP, bool GEN>
 __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn_dkv_kernel(AttnArgs a)
 {
     using R = typename T::raw;
+    const int axes = GEN ? a.axes : 0;
     constexpr int NW = kBwdWaves, NT = 64 * NW, QB = kStep, NC = DP / 16, ND = DP / 32;
     extern __shared__ __align__(16) unsigned char smem[];
     R *const qt = (R *)smem;                               // [2][QB * DP]
@@ -348,7 +352,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
     int64_t base[3];
 #pragma unroll
     for (int x = 0; x < 3; ++x) {
-        if (x >= a.axes) break;
+        if (x >= axes) break;
         const int32_t *p = a.pos_k + ((int64_t)x * a.B + b) * a.Tk;
         base[x] = p[k0];
         pk[x] = (float)(p[kc] - base[x]);
@@ -399,11 +403,11 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
             psp = *(const int2 *)(a.spans + 2 * ((int64_t)b * a.Tq + i));
 #pragma unroll
             for (int x = 0; x < 3; ++x)
-                if (x < a.axes) prq[x] = a.pos_q[((int64_t)x * a.B + b) * a.Tq + i];
+                if (x < axes) prq[x] = a.pos_q[((int64_t)x * a.B + b) * a.Tq + i];
         }
 #pragma unroll
         for (int x = 0; x < 3; ++x)
-            if (x < a.axes) nsl[x] = a.slopes[h * a.axes + x];
+            if (x < axes) nsl[x] = a.slopes[h * axes + x];
         if (++ft > last) {
             ft = first;
             ++fh;
@@ -413,6 +417,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
     auto place = [&](int buf) {
         if (!fdirect) {
             const bool drop = !(nu.z <= k0 && k0 + 32 * NW <= nu.w);
+            const int tid = opaque(threadIdx.x);
             TileRegs<T, DP, QB, NT> r;
             r.load(fq, a.qs[1], fq0, 0, a.Tq, a.D, a.vec, tid);
             if (drop && r.drop()) *flag = 1;
@@ -429,7 +434,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
             sln[buf * QB + tid] = past ? 0 : psp.y - psp.x;
 #pragma unroll
             for (int x = 0; x < 3; ++x)
-                if (x < a.axes) pq[(buf * 3 + x) * QB + tid] = (float)(prq[x] - base[x]);
+                if (x < axes) pq[(buf * 3 + x) * QB + tid] = (float)(prq[x] - base[x]);
         }
     };
     if (steps > 0) {
@@ -466,24 +471,24 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     gc[d][c] = col_frag<T, DP>(gb, c, d * 32, lane);
-                    qc[d][c] = col_frag<T, DP>(qb, c, d * 32, lane);
                 }
             reads_ahead<T, NC>();
             products_and_reads<T, NC, 1>();
-            products_and_reads<T, NC, 4 + 8 / NC>();
+            products_and_reads<T, NC, 2 + 8 / NC>();
             issued<T>();
 #pragma unroll
             for (int r = 0; r < 16; ++r) dp[r] -= dr[r];
-            if (a.cap > 0.f) {
-                cap_tanh<T>(s, sc.capin);
+            if (GEN && sc.multiply) s *= sc.scale;
+            if (GEN && a.cap > 0.f) {
+                cap_scores<T>(s, sc);
+                const float f2 = -sc.per_cap * sc.per_cap;
 #pragma unroll
-                for (int r = 0; r < 16; ++r) dp[r] *= fmaf(-s[r], s[r], 1.f);
+                for (int r = 0; r < 16; ++r) dp[r] *= fmaf(f2 * s[r], s[r], 1.f);
             }
-            if (sc.multiply || a.axes > 0) {
-                if (sc.multiply) s *= sc.scale;
+            if (axes > 0) {
 #pragma unroll
                 for (int x = 0; x < 3; ++x) {
-                    if (x >= a.axes) break;
+                    if (x >= axes) break;
                     const f32x16 p = acc_rows(pq + (buf * 3 + x) * QB, half);
 #pragma unroll
                     for (int r = 0; r < 16; ++r) s[r] = fmaf(-sl[x], fabsf(p[r] - pk[x]), s[r]);
@@ -508,10 +513,18 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
                 dv[d] = mma<T>(gc[d][0], p0, dv[d]);
-                dk[d] = mma<T>(qc[d][0], e0, dk[d]);
                 dv[d] = mma<T>(gc[d][1], p1, dv[d]);
+                qc[d][0] = col_frag<T, DP>(qb, 0, d * 32, lane);
+                qc[d][1] = col_frag<T, DP>(qb, 1, d * 32, lane);
+            }
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+                dk[d] = mma<T>(qc[d][0], e0, dk[d]);
                 dk[d] = mma<T>(qc[d][1], e1, dk[d]);
             }
+            products_and_reads<T, 2 * ND, 2>();
+            products_and_reads<T, 2 * ND, 0>();
+            issued<T>();
         }
         if (more) place(buf ^ 1);
         wait_direct();
@@ -567,7 +580,7 @@ __global__ __launch_bounds__(256) void attn_parts_kernel(AttnArgs a)
     }
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool GEN>
 void run(const AttnArgs &a, hipStream_t s)
 {
     constexpr int NW = kBwdWaves;
@@ -575,7 +588,7 @@ void run(const AttnArgs &a, hipStream_t s)
     const int64_t nq = (a.Tq + 32 * NW - 1) / (32 * NW);
     const int64_t nk = (a.Tk + 32 * NW - 1) / (32 * NW);
     if (nk > 0)
-        launch_kernel((attn_dkv_kernel<T, DP>), dim3((uint32_t)(nk * a.B * a.Hk * a.gsplit)),
+        launch_kernel((attn_dkv_kernel<T, DP, GEN>), dim3((uint32_t)(nk * a.B * a.Hk * a.gsplit)),
                       dim3(64 * NW), tiles + (2 * 3 + 8) * kStep * 4 + 3 * 4, s, a);
     if (nk > 0 && a.gsplit > 1) {
         const int64_t need = ((int64_t)a.B * a.Tk * a.Hk * a.D + 255) / 256;
@@ -584,7 +597,7 @@ void run(const AttnArgs &a, hipStream_t s)
                       s, a);
     }
     if (nq > 0)
-        launch_kernel((attn_dq_kernel<T, DP>), dim3((uint32_t)(nq * a.B * a.Hq)),
+        launch_kernel((attn_dq_kernel<T, DP, GEN>), dim3((uint32_t)(nq * a.B * a.Hq)),
                       dim3(64 * NW), tiles + (2 * 3 + 2) * kStep * 4 + (1 + 4 * NW) * 4, s, a);
 }
 
@@ -635,8 +648,15 @@ hipError_t launch_attn_backward(const AttnArgs &a, hipStream_t s)
     if (nt > 0)
         launch_kernel((attn_rows_kernel<T>), dim3((uint32_t)(nt * a.B * a.Hq)), dim3(256), 0, s, a);
     if (nt > 0) launch_attn_order(a, true, s);
-    if (a.D <= 64) run<T, 64>(a, s);
-    else run<T, 128>(a, s);
+    const bool general = attn_general(a);
+    if (a.D <= 64) {
+        if (general) run<T, 64, true>(a, s);
+        else run<T, 64, false>(a, s);
+    } else if (general) {
+        run<T, 128, true>(a, s);
+    } else {
+        run<T, 128, false>(a, s);
+    }
     return hipGetLastError();
 }
 

@@ -33,10 +33,11 @@ constexpr int fwd_occupancy()
     return sizeof(typename T::raw) * DP > 256 ? 1 : 2;
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool GEN>
 __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn_fwd_kernel(AttnArgs a)
 {
     using R = typename T::raw;
+    const int axes = GEN ? a.axes : 0;
     constexpr int NW = kFwdWaves, NT = 64 * NW, KB = kFwdKeys, NC = DP / 16, ND = DP / 32;
     extern __shared__ __align__(16) unsigned char smem[];
     R *const kt = (R *)smem;                               // [2][KB * DP]
@@ -101,11 +102,11 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
     int64_t base[3];
 #pragma unroll
     for (int x = 0; x < 3; ++x) {
-        if (x >= a.axes) break;
+        if (x >= axes) break;
         const int32_t *p = a.pos_q + ((int64_t)x * a.B + b) * a.Tq;
         base[x] = p[q0];
         pq[x] = (float)(p[ic] - base[x]);
-        sl[x] = a.slopes[h * a.axes + x] * sc.slope;
+        sl[x] = a.slopes[h * axes + x] * sc.slope;
     }
 
     f32x16 o[ND];
@@ -134,11 +135,12 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
         }
 #pragma unroll
         for (int x = 0; x < 3; ++x)
-            if (x < a.axes && tid < KB)
+            if (x < axes && tid < KB)
                 pr[x] = a.pos_k[((int64_t)x * a.B + b) * a.Tk + min(k0 + tid, a.Tk - 1)];
     };
     auto place = [&](int k0, int buf) {
         if (!direct(k0)) {
+            const int tid = opaque(threadIdx.x);
             TileRegs<T, DP, KB, NT> r;
             r.load(vp, a.vs[1], k0, glo, ghi, a.D, a.vec, tid);
             if (!(galo <= k0 && k0 + KB <= gahi) && r.drop()) *flag = 1;
@@ -148,7 +150,7 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
         }
 #pragma unroll
         for (int x = 0; x < 3; ++x)
-            if (x < a.axes && tid < KB) pk[(buf * 3 + x) * KB + tid] = (float)(pr[x] - base[x]);
+            if (x < axes && tid < KB) pk[(buf * 3 + x) * KB + tid] = (float)(pr[x] - base[x]);
     };
     if (kbeg < kend) {
         fetch(kbeg, 0);
@@ -182,17 +184,20 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
             products_and_reads<T, NC, 1>();
             products_and_reads<T, NC, 2>();
             issued<T>();
-            if (a.cap > 0.f) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u) cap_tanh<T>(s[u], sc.capin);
+            if (GEN && sc.multiply) {
+                s[0] *= sc.scale;
+                s[1] *= sc.scale;
             }
-            if (sc.multiply || a.axes > 0) {
+            if (GEN && a.cap > 0.f) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) cap_scores<T>(s[u], sc);
+            }
+            if (axes > 0) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    if (sc.multiply) s[u] *= sc.scale;
 #pragma unroll
                     for (int x = 0; x < 3; ++x) {
-                        if (x >= a.axes) break;
+                        if (x >= axes) break;
                         const f32x16 p = acc_rows(pk + (buf * 3 + x) * KB + u * 32, half);
 #pragma unroll
                         for (int r = 0; r < 16; ++r)
@@ -283,7 +288,7 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
     store_cols<T, ND>((R *)a.out + (((int64_t)b * a.Tq + i) * a.Hq + h) * a.D, o, inv, a.D, half);
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool GEN>
 hipError_t run(const AttnArgs &a, hipStream_t s)
 {
     constexpr int NW = kFwdWaves;
@@ -291,7 +296,7 @@ hipError_t run(const AttnArgs &a, hipStream_t s)
                              2 * 3 * kFwdKeys * sizeof(float) + (1 + 4 * NW) * sizeof(int);
     const int64_t nq = (a.Tq + 32 * NW - 1) / (32 * NW);
     launch_attn_order(a, false, s);
-    launch_kernel((attn_fwd_kernel<T, DP>), dim3((uint32_t)(nq * a.B * a.Hq)),
+    launch_kernel((attn_fwd_kernel<T, DP, GEN>), dim3((uint32_t)(nq * a.B * a.Hq)),
                   dim3(64 * NW), lds, s, a);
     return hipGetLastError();
 }
@@ -301,7 +306,8 @@ hipError_t run(const AttnArgs &a, hipStream_t s)
 template <typename T>
 hipError_t launch_attn_forward(const AttnArgs &a, hipStream_t s)
 {
-    return a.D <= 64 ? run<T, 64>(a, s) : run<T, 128>(a, s);
+    if (attn_general(a)) return a.D <= 64 ? run<T, 64, true>(a, s) : run<T, 128, true>(a, s);
+    return a.D <= 64 ? run<T, 64, false>(a, s) : run<T, 128, false>(a, s);
 }
 
 template hipError_t launch_attn_forward<F32>(const AttnArgs &, hipStream_t);

@@ -125,16 +125,14 @@ void attn_split_kernel(AttnArgs a)
 #pragma unroll
             for (int c = 0; c < NC; ++c)
                 s = mma<T>(row_frag<T, DP>(kt, col, c * 16 + half * 8), qf[c], s);
-            if (a.cap > 0.f) cap_tanh<T>(s, sc.capin);
-            if (sc.multiply || a.axes > 0) {
-                if (sc.multiply) s *= sc.scale;
+            if (sc.multiply) s *= sc.scale;
+            if (a.cap > 0.f) cap_scores<T>(s, sc);
 #pragma unroll
-                for (int x = 0; x < 3; ++x) {
-                    if (x >= a.axes) break;
-                    const f32x16 p = acc_rows(pk + x * KB, half);
+            for (int x = 0; x < 3; ++x) {
+                if (x >= a.axes) break;
+                const f32x16 p = acc_rows(pk + x * KB, half);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) s[e] = fmaf(-sl[x], fabsf(p[e] - pq[x]), s[e]);
-                }
+                for (int e = 0; e < 16; ++e) s[e] = fmaf(-sl[x], fabsf(p[e] - pq[x]), s[e]);
             }
             // (a chunk's ends are multiples of the tile, or the ends of every span)
             if (part) {

@@ -100,6 +100,12 @@ struct AttnArgs {
                                // their keys [lo, hi) and the keys all of them see
     float *part_dk, *part_dv;  // (gsplit, B, Tk, Hk, D), when gsplit > 1
 };
+// Scores with a cap, a bias or a factor that is not positive: kernels of
+// their own, whose registers the plain ones do not carry.
+inline bool attn_general(const AttnArgs &a)
+{
+    return a.cap > 0.f || a.axes > 0 || !(a.scale > 1e-30f);
+}
 int64_t attn_order_bytes(const AttnArgs &a, bool keys);
 void launch_attn_order(const AttnArgs &a, bool backward, hipStream_t s);
 bool attn_split_wanted(const AttnArgs &a);
