@@ -25,6 +25,7 @@ constexpr float kNegInf = -__builtin_huge_valf();
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
@@ -156,6 +157,23 @@ __device__ __forceinline__ auto acc_rows(const E *v, int half)
     return o;
 }
 
+// The same from an array of 32 pairs.
+template <typename E, typename E16>
+__device__ __forceinline__ void acc_pairs(const E *v, int half, E16 *a, E16 *b)
+{
+    typedef E e4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+    for (int r = 0; r < 16; r += 4)
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            const e4 x = *(const e4 *)(v + 2 * (acc_row(r, half) + i));
+            (*a)[r + i] = x[0];
+            (*b)[r + i] = x[1];
+            (*a)[r + i + 1] = x[2];
+            (*b)[r + i + 1] = x[3];
+        }
+}
+
 // The larger, and the sum, of the two halves' values.
 __device__ __forceinline__ float halves_max(float v)
 {
@@ -241,33 +259,39 @@ __device__ __forceinline__ Frag<T> col_frag(const typename T::raw *tile, int c, 
 
 // Infinities and NaN set to 0; true if there was one.
 template <typename T>
+__device__ __forceinline__ bool drop_nonfinite16(u32x4 &v)
+{
+    bool bad = false;
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (T::code == F32::code) {
+            if ((w[j] & 0x7f800000u) == 0x7f800000u) {
+                bad = true;
+                w[j] = 0;
+            }
+        } else {
+            constexpr uint32_t e = T::code == F16::code ? 0x7c00u : 0x7f80u;
+            if ((w[j] & e) == e) {
+                bad = true;
+                w[j] &= 0xffff0000u;
+            }
+            if ((w[j] & (e << 16)) == (e << 16)) {
+                bad = true;
+                w[j] &= 0xffffu;
+            }
+        }
+    }
+    v = u32x4{w[0], w[1], w[2], w[3]};
+    return bad;
+}
+
+template <typename T>
 __device__ __forceinline__ bool drop_nonfinite(Frag<T> &f)
 {
     bool bad = false;
 #pragma unroll
-    for (int i = 0; i < Frag<T>::NV; ++i) {
-        uint32_t w[4] = {f.w[i].x, f.w[i].y, f.w[i].z, f.w[i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if constexpr (T::code == F32::code) {
-                if ((w[j] & 0x7f800000u) == 0x7f800000u) {
-                    bad = true;
-                    w[j] = 0;
-                }
-            } else {
-                constexpr uint32_t e = T::code == F16::code ? 0x7c00u : 0x7f80u;
-                if ((w[j] & e) == e) {
-                    bad = true;
-                    w[j] &= 0xffff0000u;
-                }
-                if ((w[j] & (e << 16)) == (e << 16)) {
-                    bad = true;
-                    w[j] &= 0xffffu;
-                }
-            }
-        }
-        f.w[i] = u32x4{w[0], w[1], w[2], w[3]};
-    }
+    for (int i = 0; i < Frag<T>::NV; ++i) bad |= drop_nonfinite16<T>(f.w[i]);
     return bad;
 }
 
@@ -301,6 +325,19 @@ __device__ __forceinline__ Frag<T> load8(const typename T::raw *p, int d0, int D
     }
     return f;
 }
+
+// Waits for loaded fragments.  Those that live through a loop must be there
+// before it: the compiler would otherwise wait for them in it, every time
+// round, and with them for every later load.
+template <typename T, int N>
+__device__ __forceinline__ void arrived(Frag<T> (&f)[N])
+{
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+#pragma unroll
+        for (int i = 0; i < Frag<T>::NV; ++i) asm volatile("" : "+v"(f[c].w[i]));
+}
+__device__ __forceinline__ void arrived(float &v) { asm volatile("" : "+v"(v)); }
 
 // A tile of ROWS rows on its way from memory to LDS, spread over NT threads.
 template <typename T, int DP, int ROWS, int NT>
@@ -365,11 +402,38 @@ struct TileRegs {
     }
 };
 
+// 16 (or 4) bytes a lane from p + off to LDS, lane after lane from address
+// `lds`; p and lds are the same in every lane.  Written as instructions with
+// no result: through the builtin the compiler knows that LDS is written, and
+// waits for all loads before each transposing read, whichever tile that is
+// from.  The kernels count these loads themselves (wait_loads).  (m0 is the
+// compiler's own only right around an instruction that takes it; these
+// kernels have no other.)
+__device__ __forceinline__ uint32_t lds_address(const void *p)
+{
+    typedef const __attribute__((address_space(3))) void lds_t;
+    return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_t *)p);
+}
+__device__ __forceinline__ void direct16(const void *p, uint32_t off, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(lds), "v"(off), "s"(p)
+                 : "memory");
+}
+__device__ __forceinline__ void direct4(const void *p, uint32_t off, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+                 :
+                 : "s"(lds), "v"(off), "s"(p)
+                 : "memory");
+}
+
 // The same tile straight from memory to LDS, 16 bytes a lane, with nothing
-// in registers meanwhile: for tiles that need no second look (every row
-// there, nothing to drop).  A wave's lanes fill 1 KiB of LDS in order, so the
-// swap of the chunks is made on the memory side.  What is not so goes
-// through place(), which waits for its loads.
+// in registers meanwhile.  A wave's lanes fill 1 KiB of LDS in order, so the
+// swap of the chunks is made on the memory side.  Rows outside [lo, hi) are
+// read from the nearest row inside, and set to zero (with what else is to be
+// dropped) in LDS once they are there, by the lanes that loaded them.
 template <typename T, int DP, int ROWS, int NT>
 struct TileDirect {
     using R = typename T::raw;
@@ -377,9 +441,10 @@ struct TileDirect {
     static constexpr int UNITS = DP / PER;                 // of a row
     static constexpr int STEP = NT / UNITS;                // rows of one round over the threads
     static constexpr int N = ROWS / STEP;
-    static_assert(N * STEP == ROWS && STEP % (sizeof(R) == 2 ? 16 : 8) == 0,
+    static_assert(N * STEP == ROWS && STEP % (sizeof(R) * DP < 512 ? 16 : 8) == 0,
                   "every round swaps alike");
     uint32_t off;                                          // bytes from the round's first row
+    int64_t step;                                          // bytes from round to round
     bool on;                                               // the lane's channels are there
 
     __device__ __forceinline__ void init(int t, int64_t stride, int D)
@@ -387,30 +452,105 @@ struct TileDirect {
         const int row = t / UNITS, u = t % UNITS, c = (u * PER / 8) ^ tile_swap<R, DP>(row);
         const int e = c * 8 + (u * PER) % 8;
         off = (uint32_t)(row * stride + e) * (uint32_t)sizeof(R);
+        step = STEP * stride * (int64_t)sizeof(R);
         on = e < D;
     }
-    // The tile's first row at p (the same in every lane).  Every wave waits
-    // for its loads (wait_direct) before the barrier that hands the tile over.
-    __device__ __forceinline__ void load(const R *p, int64_t stride, R *tile, int wave) const
+    // A whole tile, all channels there, whose first row is at p.  `lds`: the
+    // wave's first place in the tile.  Every wave waits for its loads before
+    // the barrier that hands the tile over.  (What is left to do a tile is
+    // little: a wave alone on its SIMD takes a scalar instruction every four
+    // cycles, and a taken branch costs tens.)
+    __device__ __forceinline__ void load(const R *p, uint32_t lds) const
     {
-        typedef const __attribute__((address_space(1))) void global_t;
-        typedef __attribute__((address_space(3))) void lds_t;
-        if (!on) return;
 #pragma unroll
         for (int j = 0; j < N; ++j)
-            __builtin_amdgcn_global_load_lds(
-                (global_t *)((const char *)(p + j * STEP * stride) + off),
-                (lds_t *)(tile + (j * NT + wave * 64) * PER), 16, 0, 0);
+            direct16((const char *)p + j * step, off, lds + j * NT * 16);
     }
-    // Can tiles be loaded this way at all?  Whole chunks, a row's offset
-    // within 31 bits, and LDS addresses within the 16 bits the load has.
+    // Any tile, from row r0 of base.
+    __device__ __forceinline__ void load_edge(const R *base, int64_t stride, int r0, int lo, int hi,
+                                              uint32_t lds) const
+    {
+        if (!on) return;
+        const int t = opaque(threadIdx.x) / UNITS;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            // (clamping keeps the order: no lane is before the first)
+            const int first = r0 + j * STEP, at = min(max(first, lo), hi - 1);
+            const int row = min(max(first + t, lo), hi - 1) - at;
+            direct16(base + at * stride,
+                     off + (uint32_t)((row - t) * stride) * (uint32_t)sizeof(R),
+                     lds + j * NT * 16);
+        }
+    }
+    // Rows outside [lo, hi) of a tile that has arrived to zero; with `drop`
+    // infinities and NaN too (true if there was one; its row marked).
+    __device__ __forceinline__ bool scrub(R *tile, int r0, int lo, int hi, bool drop,
+                                          int *row_mark, int mark) const
+    {
+        bool bad = false;
+        const int t = opaque(threadIdx.x);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int id = j * NT + t, row = r0 + id / UNITS;
+            u32x4 *p = (u32x4 *)(tile + id * PER);
+            if (row < lo || row >= hi) {
+                *p = u32x4{0u, 0u, 0u, 0u};
+            } else if (drop) {
+                u32x4 v = *p;
+                if (drop_nonfinite16<T>(v)) {
+                    *p = v;
+                    if (row_mark) row_mark[id / UNITS] = mark;
+                    bad = true;
+                }
+            }
+        }
+        return bad;
+    }
+    // Can tiles be loaded this way at all?  Whole chunks, and a row's offset
+    // within 31 bits.
     __device__ static __forceinline__ bool usable(bool vec, int64_t stride, int D)
     {
-        return 4 * ROWS * DP * sizeof(R) <= 65536 && vec && D % 8 == 0 && stride < (1 << 24);
+        return vec && D % 8 == 0 && stride < (1 << 24);
     }
+    // Loads that a wave has issued for a tile.
+    static constexpr int LOADS = N;
 };
 
-__device__ __forceinline__ void wait_direct() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// --- stages: kStages tiles in LDS, filled kStages - 1 steps ahead, so that a
+// step waits for loads that are that many steps old.  A wave's loads return
+// in order: when no more are outstanding than it issued for the later
+// stages, the next stage is there.  (Its own waits, and a barrier that adds
+// none: __syncthreads would wait for every load.)
+constexpr int kStages = 4;
+
+template <int OUTSTANDING>
+__device__ __forceinline__ void wait_loads(bool later)
+{
+    if (later) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(OUTSTANDING) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+// After loads through registers in a loop: none is waited for later on.
+__device__ __forceinline__ void wait_all() { __builtin_amdgcn_s_waitcnt(0x0f70); }  // vmcnt(0)
+
+__device__ __forceinline__ void hand_over()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// A value that is the same in every lane, as a scalar.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// A value that is the same in every lane, read through the scalar cache (a
+// vector load would have to wait for the stages before it).
+template <typename E>
+__device__ __forceinline__ E uniform_load(const E *p)
+{
+    typedef const __attribute__((address_space(4))) E constant_t;
+    return *(constant_t *)(uintptr_t)p;
+}
 
 // --- infinities and NaN in masked places
 //

@@ -64,6 +64,19 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a)
         // a row without weights: its exponents become -inf
         *(float2 *)(a.rowd + 2 * at) = make_float2(l == kNegInf ? kInf : l * kLog2e, s);
     }
+    if (h == 0) {
+        // this workgroup's share of the positions
+        const int per_q = 32, per_k = (a.Tk + nt - 1) / nt;
+        for (int x = 0; x < a.axes; ++x) {
+            const int64_t row = (int64_t)x * a.B + b;
+            const int32_t *pk = a.pos_k + row * a.Tk, *pq = a.pos_q + row * a.Tq;
+            const int64_t base = a.Tk > 0 ? pk[0] : 0;
+            for (int k = qt * per_k + threadIdx.x; k < min((qt + 1) * per_k, a.Tk); k += 256)
+                a.fpos_k[row * a.Tk + k] = (float)(pk[k] - base);
+            const int k = qt * per_q + threadIdx.x;
+            if (threadIdx.x < per_q && k < a.Tq) a.fpos_q[row * a.Tq + k] = (float)(pq[k] - base);
+        }
+    }
     if (h == 0 && threadIdx.x < 64) {
         const int j = qt * 32 + (threadIdx.x & 31);
         Span sp = {0, 0};                  // (past the last query: none)
@@ -98,19 +111,20 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
     const int axes = GEN ? a.axes : 0;
     constexpr int NW = kBwdWaves, NT = 64 * NW, KB = kStep, NC = DP / 16, ND = DP / 32;
     extern __shared__ __align__(16) unsigned char smem[];
-    R *const kt = (R *)smem;                               // [2][KB * DP]
-    R *const vt = kt + 2 * KB * DP;                        // [2][KB * DP]
-    float *const pk = (float *)(vt + 2 * KB * DP);         // [2][3][KB]
-    int *const bad = (int *)(pk + 2 * 3 * KB);             // [2][KB] 1 + last step with a key's inf or NaN
-    int *const flag = bad + 2 * KB;                        // there was one
+    constexpr int TS = KB * DP;                            // elements of a tile
+    R *const kt = (R *)smem;                               // [kStages][K tile, V tile]
+    float *const pk = (float *)(kt + kStages * 2 * TS);    // [kStages][3][KB] key positions
+    int *const bad = (int *)(pk + kStages * 3 * KB);       // [kStages][KB] 1 + last step whose key
+                                                           // held an infinity or a NaN
+    int *const flag = bad + kStages * KB;                  // there was one
     int *const ends = flag + 1;                            // [4][NW]
 
     const int nq = (a.Tq + 32 * NW - 1) / (32 * NW);
     const Block blk = block_of(blockIdx.x, a.B * a.Hq, nq);
     const int bh = blk.head;
     const int b = bh / a.Hq, h = bh - b * a.Hq, hk = h / a.G;
-    const int qt = a.order_q ? a.order_q[(int64_t)b * nq + blk.no] : nq - 1 - blk.no;
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, col = lane & 31,
+    const int qt = a.order_q ? uniform(a.order_q[(int64_t)b * nq + blk.no]) : nq - 1 - blk.no;
+    const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63, col = lane & 31,
               half = lane >> 5;
     const int q0 = qt * 32 * NW, i = q0 + wave * 32 + col;
     const int ic = min(i, a.Tq - 1);
@@ -125,7 +139,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
         ends[2 * NW + wave] = alo;
         ends[3 * NW + wave] = ahi;
     }
-    if (tid < 2 * KB) bad[tid] = 0;
+    if (tid < kStages * KB) bad[tid] = 0;
     if (tid == 0) *flag = 0;
     __syncthreads();
     int glo = ends[0], ghi = ends[NW], galo = ends[2 * NW], gahi = ends[3 * NW];
@@ -136,6 +150,11 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
         galo = max(galo, ends[2 * NW + w]);
         gahi = min(gahi, ends[3 * NW + w]);
     }
+
+    glo = uniform(glo);
+    ghi = uniform(ghi);
+    galo = uniform(galo);
+    gahi = uniform(gahi);
 
     const R *kp = (const R *)a.k + b * a.ks[0] + hk * a.ks[2];
     const R *vp = (const R *)a.v + b * a.vs[0] + hk * a.vs[2];
@@ -150,71 +169,82 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
     const float2 rd = *(const float2 *)(a.rowd + 2 * ((int64_t)bh * a.Tq + ic));
     const Scores sc = scores(a);
     float pq[3], sl[3];
-    int64_t base[3];
 #pragma unroll
     for (int x = 0; x < 3; ++x) {
         if (x >= axes) break;
-        const int32_t *p = a.pos_q + ((int64_t)x * a.B + b) * a.Tq;
-        base[x] = p[q0];
-        pq[x] = (float)(p[ic] - base[x]);
+        pq[x] = a.fpos_q[((int64_t)x * a.B + b) * a.Tq + ic];
         sl[x] = a.slopes[h * axes + x] * sc.slope;
+        arrived(pq[x]);
+        arrived(sl[x]);
     }
 
+    float lse2 = rd.x, delta = rd.y;
+    arrived(qf);
+    arrived(gf);
+    arrived(lse2);
+    arrived(delta);
     f32x16 o[ND];
 #pragma unroll
     for (int d = 0; d < ND; ++d) o[d] = f32x16(0.f);
 
     const int kbeg = ghi > 0 ? glo / KB * KB : 0, kend = ghi;
+    const int steps = kend > kbeg ? (kend - kbeg + KB - 1) / KB : 0;
     TileDirect<T, DP, KB, NT> kd, vd;
     kd.init(tid, a.ks[1], a.D);
     vd.init(tid, a.vs[1], a.D);
     const bool usable = kd.usable(a.vec, a.ks[1], a.D) && vd.usable(a.vec, a.vs[1], a.D);
-    if (a.D < DP) {                        // channels that no direct load writes
-        for (int x = tid; x < 4 * KB * DP * (int)sizeof(R) / 16; x += NT)
+    if (a.D < DP)                          // channels that no direct load writes
+        for (int x = tid; x < kStages * 2 * TS * (int)sizeof(R) / 16; x += NT)
             ((u32x4 *)kt)[x] = u32x4{0u, 0u, 0u, 0u};
-        __syncthreads();
-    }
-    auto direct = [&](int k0) {
-        return usable && max(glo, galo) <= k0 && k0 + KB <= min(ghi, gahi);
-    };
-    int32_t pr[3];                         // (not touched before place: that would wait)
-    auto fetch = [&](int k0, int buf) {
-        if (direct(k0)) {
-            kd.load(kp + k0 * a.ks[1], a.ks[1], kt + buf * KB * DP, wave);
-            vd.load(vp + k0 * a.vs[1], a.vs[1], vt + buf * KB * DP, wave);
-        }
-#pragma unroll
-        for (int x = 0; x < 3; ++x)
-            if (x < axes && tid < KB)
-                pr[x] = a.pos_k[((int64_t)x * a.B + b) * a.Tk + min(k0 + tid, a.Tk - 1)];
-    };
-    auto place = [&](int k0, int buf, int n) {
-        if (!direct(k0)) {
-            const int tid = opaque(threadIdx.x);
-            TileRegs<T, DP, KB, NT> r;
-            r.load(kp, a.ks[1], k0, glo, ghi, a.D, a.vec, tid);
-            if (!(galo <= k0 && k0 + KB <= gahi) && r.drop(bad + buf * KB, n + 1, tid)) *flag = 1;
-            r.store(kt + buf * KB * DP, tid);
-            r.load(vp, a.vs[1], k0, glo, ghi, a.D, a.vec, tid);
-            r.store(vt + buf * KB * DP, tid);
-        }
-#pragma unroll
-        for (int x = 0; x < 3; ++x)
-            if (x < axes && tid < KB) pk[(buf * 3 + x) * KB + tid] = (float)(pr[x] - base[x]);
-    };
-    if (kbeg < kend) {
-        fetch(kbeg, 0);
-        place(kbeg, 0, 0);
-    }
-    wait_direct();
     __syncthreads();
-    int n = 0;
-    for (int k0 = kbeg; k0 < kend; k0 += KB, ++n) {
-        const int buf = n & 1;
-        const bool more = k0 + KB < kend;
-        if (more) fetch(k0 + KB, buf ^ 1);
-        if (k0 < whi && k0 + KB > wlo) {
-            const R *kb = kt + buf * KB * DP, *vb = vt + buf * KB * DP;
+    const uint32_t lds = lds_address(smem) + wave * 1024, lds_pk = lds_address(pk);
+    const bool whole = usable && a.D == DP;
+    auto fetch = [&](int n) {
+        const int k0 = kbeg + n * KB, st = n % kStages;
+        const uint32_t at = lds + st * 2 * TS * (int)sizeof(R);
+        if (whole && glo <= k0 && k0 + KB <= ghi) {
+            kd.load(kp + k0 * a.ks[1], at);
+            vd.load(vp + k0 * a.vs[1], at + TS * (int)sizeof(R));
+        } else if (usable) {
+            kd.load_edge(kp, a.ks[1], k0, glo, ghi, at);
+            vd.load_edge(vp, a.vs[1], k0, glo, ghi, at + TS * (int)sizeof(R));
+        }
+        if (wave < axes && lane < KB)
+            direct4(a.fpos_k + ((int64_t)wave * a.B + b) * a.Tk + k0,
+                    (uint32_t)min(lane, a.Tk - 1 - k0) * 4, lds_pk + (st * 3 + wave) * KB * 4);
+    };
+    // Hands stage n over: `later` stages may still be on their way.
+    constexpr int kLater = (kStages - 2) * 2 * TileDirect<T, DP, KB, NT>::LOADS;
+    auto arrive = [&](int n, bool later) {
+        wait_loads<kLater>(later && usable);
+        const int k0 = kbeg + n * KB, st = n % kStages;
+        const bool edge = k0 < glo || k0 + KB > ghi;
+        const bool drop = !(galo <= k0 && k0 + KB <= gahi);
+        R *const ks = kt + st * 2 * TS;
+        if (!usable) {
+            const int t = opaque(threadIdx.x);
+            TileRegs<T, DP, KB, NT> r;
+            r.load(kp, a.ks[1], k0, glo, ghi, a.D, a.vec, t);
+            if (drop && r.drop(bad + st * KB, n + 1, t)) *flag = 1;
+            r.store(ks, t);
+            r.load(vp, a.vs[1], k0, glo, ghi, a.D, a.vec, t);
+            r.store(ks + TS, t);
+            wait_all();
+        } else if (edge || drop) {
+            if (kd.scrub(ks, k0, glo, ghi, drop, bad + st * KB, n + 1)) *flag = 1;
+            if (edge) vd.scrub(ks + TS, k0, glo, ghi, false, nullptr, 0);
+        }
+        hand_over();
+    };
+    for (int n = 0; n < kStages - 1; ++n)
+        if (n < steps) fetch(n);
+    if (steps > 0) arrive(0, steps >= kStages - 1);
+    for (int n = 0; n < steps; ++n) {
+        const int k0 = kbeg + n * KB, st = n % kStages;
+        const bool more = n + kStages - 1 < steps;
+        if (more) fetch(n + kStages - 1);
+        {
+            const R *kb = kt + st * 2 * TS, *vb = kb + TS;
             Frag<T> kr[NC], vr[NC], kc[ND][2];
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
@@ -235,7 +265,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
             products_and_reads<T, NC, 2>();
             issued<T>();
 #pragma unroll
-            for (int r = 0; r < 16; ++r) dp[r] -= rd.y;
+            for (int r = 0; r < 16; ++r) dp[r] -= delta;
             if (GEN && sc.multiply) s *= sc.scale;
             if (GEN && a.cap > 0.f) {
                 cap_scores<T>(s, sc);
@@ -247,20 +277,20 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
 #pragma unroll
                 for (int x = 0; x < 3; ++x) {
                     if (x >= axes) break;
-                    const f32x16 p = acc_rows(pk + (buf * 3 + x) * KB, half);
+                    const f32x16 p = acc_rows(pk + (st * 3 + x) * KB, half);
 #pragma unroll
                     for (int r = 0; r < 16; ++r) s[r] = fmaf(-sl[x], fabsf(p[r] - pq[x]), s[r]);
                 }
             }
             const bool part = !(alo <= k0 && k0 + KB <= ahi);
             if (part && *flag) {
-                const auto x = acc_rows(bad + buf * KB, half);
+                const auto x = acc_rows(bad + st * KB, half);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) s[r] = x[r] == n + 1 ? kNegInf : s[r];
             }
 #pragma unroll
             for (int r = 0; r < 16; ++r)
-                s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], sc.mul, -rd.x)) * dp[r];
+                s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], sc.mul, -lse2)) * dp[r];
             if (part) {
                 const uint32_t at = k0 + 4 * half - sp.x, len = sp.y - sp.x;
 #pragma unroll
@@ -273,9 +303,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
                 o[d] = mma<T>(kc[d][1], e1, o[d]);
             }
         }
-        if (more) place(k0 + KB, buf ^ 1, n + 1);
-        wait_direct();
-        __syncthreads();
+        if (n + 1 < steps) arrive(n + 1, more);
     }
     if (i >= a.Tq) return;
     store_cols<T, ND>((R *)a.dq + (((int64_t)b * a.Tq + i) * a.Hq + h) * a.D, o, a.scale, a.D, half);
@@ -293,14 +321,12 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
     const int axes = GEN ? a.axes : 0;
     constexpr int NW = kBwdWaves, NT = 64 * NW, QB = kStep, NC = DP / 16, ND = DP / 32;
     extern __shared__ __align__(16) unsigned char smem[];
-    R *const qt = (R *)smem;                               // [2][QB * DP]
-    R *const gt = qt + 2 * QB * DP;                        // [2][QB * DP]
-    float *const pq = (float *)(gt + 2 * QB * DP);         // [2][3][QB] positions
-    float *const rl = pq + 2 * 3 * QB;                     // [2][QB] lse * log2 e
-    float *const rd = rl + 2 * QB;                         // [2][QB] delta
-    int *const slo = (int *)(rd + 2 * QB);                 // [2][QB] first key seen
-    int *const sln = slo + 2 * QB;                         // [2][QB] keys seen
-    int *const flag = sln + 2 * QB;                        // an infinity or a NaN was dropped
+    constexpr int TS = QB * DP;                            // elements of a tile
+    R *const qt = (R *)smem;                               // [kStages][Q tile, dO tile]
+    float *const pq = (float *)(qt + kStages * 2 * TS);    // [kStages][3][QB] positions
+    float *const rc = pq + kStages * 3 * QB;               // [kStages][QB][2] lse * log2 e, delta
+    int *const sp = (int *)(rc + kStages * 2 * QB);        // [kStages][QB][2] spans of keys
+    int *const flag = sp + kStages * 2 * QB;               // an infinity or a NaN was dropped
     int *const ends = flag + 1;                            // [2] first and last tile
 
     const int nk = (a.Tk + 32 * NW - 1) / (32 * NW);
@@ -308,10 +334,10 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
     const int gpart = blk.head % a.gsplit, bhk = blk.head / a.gsplit;
     const int b = bhk / a.Hk, hk = bhk - b * a.Hk;
     // (without documents the first keys are seen by the most queries, if causal)
-    const int kb = a.order_k ? a.order_k[(int64_t)b * nk + blk.no] : blk.no;
+    const int kb = a.order_k ? uniform(a.order_k[(int64_t)b * nk + blk.no]) : blk.no;
     const int g0 = (int)((int64_t)a.G * gpart / a.gsplit);
     const int g1 = (int)((int64_t)a.G * (gpart + 1) / a.gsplit);
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, col = lane & 31,
+    const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63, col = lane & 31,
               half = lane >> 5;
     const int k0 = kb * 32 * NW, kw = k0 + wave * 32, key = kw + col;
     const int kc = min(key, a.Tk - 1);
@@ -337,7 +363,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
         }
     }
     __syncthreads();
-    const int first = ends[0], last = ends[1], span = last - first + 1;
+    const int first = uniform(ends[0]), last = uniform(ends[1]), span = last - first + 1;
     const int steps = span > 0 ? span * (g1 - g0) : 0;
 
     const R *kp = (const R *)a.k + b * a.ks[0] + hk * a.ks[2] + (int64_t)kc * a.ks[1];
@@ -349,15 +375,15 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
         vf[c] = load8<T>(vp, c * 16 + half * 8, a.D, a.vec);
     }
     float pk[3];
-    int64_t base[3];
 #pragma unroll
     for (int x = 0; x < 3; ++x) {
         if (x >= axes) break;
-        const int32_t *p = a.pos_k + ((int64_t)x * a.B + b) * a.Tk;
-        base[x] = p[k0];
-        pk[x] = (float)(p[kc] - base[x]);
+        pk[x] = a.fpos_k[((int64_t)x * a.B + b) * a.Tk + kc];
+        arrived(pk[x]);
     }
     const Scores sc = scores(a);
+    arrived(kf);
+    arrived(vf);
     f32x16 dk[ND], dv[ND];
 #pragma unroll
     for (int d = 0; d < ND; ++d) dk[d] = dv[d] = f32x16(0.f);
@@ -366,94 +392,96 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
     qd.init(tid, a.qs[1], a.D);
     gd.init(tid, a.gs[1], a.D);
     const bool usable = qd.usable(a.vec, a.qs[1], a.D) && gd.usable(a.vec, a.gs[1], a.D);
-    if (a.D < DP) {                        // channels that no direct load writes
-        for (int x = tid; x < 4 * QB * DP * (int)sizeof(R) / 16; x += NT)
+    if (a.D < DP)                          // channels that no direct load writes
+        for (int x = tid; x < kStages * 2 * TS * (int)sizeof(R) / 16; x += NT)
             ((u32x4 *)qt)[x] = u32x4{0u, 0u, 0u, 0u};
-        __syncthreads();
-    }
-    // (nothing in flight is touched before place: that would wait for it)
-    int32_t prq[3];
-    float2 prd = make_float2(0.f, 0.f);
-    int2 psp = make_int2(0, 0);
-    bool past = false;
-    float nsl[3] = {0.f, 0.f, 0.f}, sl[3];  // the head's slopes
-    // the next step's head and tile of queries; the keys of its tile (see
-    // AttnArgs::tiles) and, one step ahead, of the one after it
+    __syncthreads();
+    // the next fetch's head and tile of queries
     int fh = hk * a.G + g0, ft = first;
-    int4 nu = make_int4(0, 0, 0, 0), nnu = nu;
-    const R *fq = nullptr, *fg = nullptr;
-    int fq0 = 0;
-    bool fdirect = false;
-    auto fetch = [&](int buf) {
-        const int h = fh;
-        fq0 = ft * QB;
-        nu = nnu;
-        fq = (const R *)a.q + b * a.qs[0] + h * a.qs[2];
-        fg = (const R *)a.dout + b * a.gs[0] + h * a.gs[2];
-        fdirect = usable && fq0 + QB <= a.Tq &&
-                  __builtin_amdgcn_readfirstlane(nu.z <= k0 && k0 + 32 * NW <= nu.w);
-        if (fdirect) {
-            qd.load(fq + fq0 * a.qs[1], a.qs[1], qt + buf * QB * DP, wave);
-            gd.load(fg + fq0 * a.gs[1], a.gs[1], gt + buf * QB * DP, wave);
+    const uint32_t lds = lds_address(smem) + wave * 1024, lds_rc = lds_address(rc),
+                   lds_sp = lds_address(sp), lds_pq = lds_address(pq);
+    const bool whole = usable && a.D == DP;
+    const R *const qbase = (const R *)a.q + b * a.qs[0], *const gbase =
+        (const R *)a.dout + b * a.gs[0];
+    auto fetch = [&](int n) {
+        const int h = fh, q0 = ft * QB, st = n % kStages;
+        const uint32_t at = lds + st * 2 * TS * (int)sizeof(R);
+        const R *const q = qbase + h * a.qs[2], *const g = gbase + h * a.gs[2];
+        if (whole && q0 + QB <= a.Tq) {
+            qd.load(q + q0 * a.qs[1], at);
+            gd.load(g + q0 * a.gs[1], at + TS * (int)sizeof(R));
+        } else if (usable) {
+            qd.load_edge(q, a.qs[1], q0, 0, a.Tq, at);
+            gd.load_edge(g, a.gs[1], q0, 0, a.Tq, at + TS * (int)sizeof(R));
         }
-        if (tid < QB) {
-            const int i = min(fq0 + tid, a.Tq - 1);
-            past = fq0 + tid >= a.Tq;
-            prd = *(const float2 *)(a.rowd + 2 * (((int64_t)b * a.Hq + h) * a.Tq + i));
-            psp = *(const int2 *)(a.spans + 2 * ((int64_t)b * a.Tq + i));
-#pragma unroll
-            for (int x = 0; x < 3; ++x)
-                if (x < axes) prq[x] = a.pos_q[((int64_t)x * a.B + b) * a.Tq + i];
-        }
-#pragma unroll
-        for (int x = 0; x < 3; ++x)
-            if (x < axes) nsl[x] = a.slopes[h * axes + x];
+        // two values for each of 32 queries (the last query's for those past it)
+        const uint32_t two = (uint32_t)(2 * min(lane >> 1, a.Tq - 1 - q0) + (lane & 1)) * 4;
+        if (wave == 0)
+            direct4(a.rowd + 2 * (((int64_t)b * a.Hq + h) * a.Tq + q0), two,
+                    lds_rc + st * 2 * QB * 4);
+        if (wave == 1)
+            direct4(a.spans + 2 * ((int64_t)b * a.Tq + q0), two, lds_sp + st * 2 * QB * 4);
+        if (wave < axes && lane < QB)
+            direct4(a.fpos_q + ((int64_t)wave * a.B + b) * a.Tq + q0,
+                    (uint32_t)min(lane, a.Tq - 1 - q0) * 4, lds_pq + (st * 3 + wave) * QB * 4);
         if (++ft > last) {
             ft = first;
             ++fh;
         }
-        nnu = *(const int4 *)(tiles + 4 * (int64_t)ft);
     };
-    auto place = [&](int buf) {
-        if (!fdirect) {
-            const bool drop = !(nu.z <= k0 && k0 + 32 * NW <= nu.w);
-            const int tid = opaque(threadIdx.x);
+    // Hands stage n (tile t of head h, whose keys are u) over.
+    constexpr int kLater = (kStages - 2) * 2 * TileDirect<T, DP, QB, NT>::LOADS;
+    auto arrive = [&](int n, int h, int t32, const i32x4 &u, bool later) {
+        wait_loads<kLater>(later && usable);
+        const int q0 = t32 * QB, st = n % kStages;
+        const bool edge = q0 + QB > a.Tq, drop = !(u.z <= k0 && k0 + 32 * NW <= u.w);
+        R *const qs = qt + st * 2 * TS;
+        if (!usable) {
+            const int t = opaque(threadIdx.x);
             TileRegs<T, DP, QB, NT> r;
-            r.load(fq, a.qs[1], fq0, 0, a.Tq, a.D, a.vec, tid);
+            r.load((const R *)a.q + b * a.qs[0] + h * a.qs[2], a.qs[1], q0, 0, a.Tq, a.D, a.vec, t);
             if (drop && r.drop()) *flag = 1;
-            r.store(qt + buf * QB * DP, tid);
-            r.load(fg, a.gs[1], fq0, 0, a.Tq, a.D, a.vec, tid);
+            r.store(qs, t);
+            r.load((const R *)a.dout + b * a.gs[0] + h * a.gs[2], a.gs[1], q0, 0, a.Tq, a.D, a.vec,
+                   t);
             if (drop && r.drop()) *flag = 1;
-            r.store(gt + buf * QB * DP, tid);
+            r.store(qs + TS, t);
+            wait_all();
+        } else if (edge || drop) {
+            if (qd.scrub(qs, q0, 0, a.Tq, drop, nullptr, 0)) *flag = 1;
+            if (gd.scrub(qs + TS, q0, 0, a.Tq, drop, nullptr, 0)) *flag = 1;
         }
-        if (tid < QB) {
-            // past the last query: no weight
-            rl[buf * QB + tid] = past ? kInf : prd.x;
-            rd[buf * QB + tid] = past ? 0.f : prd.y;
-            slo[buf * QB + tid] = past ? 0 : psp.x;
-            sln[buf * QB + tid] = past ? 0 : psp.y - psp.x;
-#pragma unroll
-            for (int x = 0; x < 3; ++x)
-                if (x < axes) pq[(buf * 3 + x) * QB + tid] = (float)(prq[x] - base[x]);
+        if (edge) {                        // past the last query: no weight, no keys
+            const int i = opaque(lane);
+            if (q0 + (i >> 1) >= a.Tq) {
+                if (wave == 0) rc[st * 2 * QB + i] = i & 1 ? 0.f : kInf;
+                if (wave == 1) sp[st * 2 * QB + i] = 0;
+            }
         }
+        hand_over();
     };
+    for (int n = 0; n < kStages - 1; ++n)
+        if (n < steps) fetch(n);
+    int ch = hk * a.G + g0, ct = first;    // this step's head and tile, and its keys
+    i32x4 u = {0, 0, 0, 0};
     if (steps > 0) {
-        nnu = *(const int4 *)(tiles + 4 * (int64_t)first);
-        fetch(0);
-        place(0);
+        u = uniform_load((const i32x4 *)tiles + first);
+        arrive(0, ch, ct, u, steps >= kStages - 1);
     }
-    wait_direct();
-    __syncthreads();
     for (int n = 0; n < steps; ++n) {
-        const int buf = n & 1;
-        const bool more = n + 1 < steps;
-        const int4 u = nu;
+        const int st = n % kStages;
+        const bool more = n + kStages - 1 < steps;
+        // the next step's
+        const int nt2 = ct < last ? ct + 1 : first, nh = ct < last ? ch : ch + 1;
+        const i32x4 nu = uniform_load((const i32x4 *)tiles + nt2);
+        if (more) fetch(n + kStages - 1);
+        float sl[3];
 #pragma unroll
-        for (int x = 0; x < 3; ++x) sl[x] = nsl[x] * sc.slope;
-        if (more) fetch(buf ^ 1);
-        if (__builtin_amdgcn_readfirstlane(u.x < kw + 32 && u.y > kw)) {
-            const R *qb = qt + buf * QB * DP, *gb = gt + buf * QB * DP;
-            const bool part = !__builtin_amdgcn_readfirstlane(u.z <= kw && kw + 32 <= u.w);
+        for (int x = 0; x < 3; ++x)
+            if (x < axes) sl[x] = uniform_load(a.slopes + ch * axes + x) * sc.slope;
+        {
+            const R *qb = qt + st * 2 * TS, *gb = qb + TS;
+            const bool part = !(u.z <= kw && kw + 32 <= u.w);
             Frag<T> qr[NC], gr[NC], qc[ND][2], gc[ND][2];
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
@@ -465,7 +493,8 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
             for (int c = 0; c < NC; ++c) s = mma<T>(qr[c], kf[c], s);
 #pragma unroll
             for (int c = 0; c < NC; ++c) dp = mma<T>(gr[c], vf[c], dp);
-            const f32x16 lr = acc_rows(rl + buf * QB, half), dr = acc_rows(rd + buf * QB, half);
+            f32x16 lr, dr;
+            acc_pairs(rc + st * 2 * QB, half, &lr, &dr);
 #pragma unroll
             for (int d = 0; d < ND; ++d)
 #pragma unroll
@@ -489,7 +518,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
 #pragma unroll
                 for (int x = 0; x < 3; ++x) {
                     if (x >= axes) break;
-                    const f32x16 p = acc_rows(pq + (buf * 3 + x) * QB, half);
+                    const f32x16 p = acc_rows(pq + (st * 3 + x) * QB, half);
 #pragma unroll
                     for (int r = 0; r < 16; ++r) s[r] = fmaf(-sl[x], fabsf(p[r] - pk[x]), s[r]);
                 }
@@ -500,10 +529,11 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
                 dp[r] *= s[r];
             }
             if (part) {
-                const auto lo = acc_rows(slo + buf * QB, half), len = acc_rows(sln + buf * QB, half);
+                i32x16 lo, hi;
+                acc_pairs(sp + st * 2 * QB, half, &lo, &hi);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    const bool see = (uint32_t)(key - lo[r]) < (uint32_t)len[r];
+                    const bool see = key >= lo[r] && key < hi[r];
                     s[r] = see ? s[r] : 0.f;
                     dp[r] = see ? dp[r] : 0.f;
                 }
@@ -526,9 +556,10 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
             products_and_reads<T, 2 * ND, 0>();
             issued<T>();
         }
-        if (more) place(buf ^ 1);
-        wait_direct();
-        __syncthreads();
+        ct = nt2;
+        ch = nh;
+        u = nu;
+        if (n + 1 < steps) arrive(n + 1, ch, ct, u, more);
     }
     if (*flag) {                           // (the loop's last barrier is behind us)
         // infinities and NaN of do that were dropped, for the keys they reach
@@ -538,9 +569,9 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
             if (u[2] <= k0 && k0 + 32 * NW <= u[3]) continue;
             const int h = hk * a.G + g0 + n / span, q0 = (first + n % span) * QB;
             for (int i = q0; i < min(q0 + QB, a.Tq); ++i) {
-                const int2 sp = *(const int2 *)(a.spans + 2 * ((int64_t)b * a.Tq + i));
+                const int2 span2 = *(const int2 *)(a.spans + 2 * ((int64_t)b * a.Tq + i));
                 const R *g = (const R *)a.dout + b * a.gs[0] + (int64_t)i * a.gs[1] + h * a.gs[2];
-                if (key < sp.x || key >= sp.y) continue;
+                if (key < span2.x || key >= span2.y) continue;
 #pragma unroll
                 for (int d = 0; d < ND; ++d)
 #pragma unroll
@@ -584,12 +615,12 @@ template <typename T, int DP, bool GEN>
 void run(const AttnArgs &a, hipStream_t s)
 {
     constexpr int NW = kBwdWaves;
-    constexpr uint32_t tiles = 4 * kStep * DP * sizeof(typename T::raw);
+    constexpr uint32_t tiles = kStages * 2 * kStep * DP * sizeof(typename T::raw);
     const int64_t nq = (a.Tq + 32 * NW - 1) / (32 * NW);
     const int64_t nk = (a.Tk + 32 * NW - 1) / (32 * NW);
     if (nk > 0)
         launch_kernel((attn_dkv_kernel<T, DP, GEN>), dim3((uint32_t)(nk * a.B * a.Hk * a.gsplit)),
-                      dim3(64 * NW), tiles + (2 * 3 + 8) * kStep * 4 + 3 * 4, s, a);
+                      dim3(64 * NW), tiles + kStages * 7 * kStep * 4 + 3 * 4, s, a);
     if (nk > 0 && a.gsplit > 1) {
         const int64_t need = ((int64_t)a.B * a.Tk * a.Hk * a.D + 255) / 256;
         launch_kernel((attn_parts_kernel<T>),
@@ -598,14 +629,14 @@ void run(const AttnArgs &a, hipStream_t s)
     }
     if (nq > 0)
         launch_kernel((attn_dq_kernel<T, DP, GEN>), dim3((uint32_t)(nq * a.B * a.Hq)),
-                      dim3(64 * NW), tiles + (2 * 3 + 2) * kStep * 4 + (1 + 4 * NW) * 4, s, a);
+                      dim3(64 * NW), tiles + kStages * 4 * kStep * 4 + (1 + 4 * NW) * 4, s, a);
 }
 
 int64_t round16(int64_t bytes) { return (bytes + 15) & ~(int64_t)15; }
 
 }  // namespace
 
-// Workspace: tiles, spans, rowd, the blocks' orders, then the parts (each at a multiple of 16
+// Workspace: tiles, spans, rowd, the blocks' orders, the positions, then the parts (each at a multiple of 16
 // bytes).
 size_t plan_attn_backward(AttnArgs *a)
 {
@@ -615,7 +646,9 @@ size_t plan_attn_backward(AttnArgs *a)
     a->gsplit = (int32_t)(g < 1 ? 1 : g > a->G ? a->G : g);
     const int64_t nt = (a->Tq + 31) / 32, rows = (int64_t)a->B * a->Tq;
     int64_t n = round16(rows * a->Hq * 8) + round16(rows * 8) + (int64_t)a->B * nt * 16 +
-                attn_order_bytes(*a, false) + attn_order_bytes(*a, true);
+                attn_order_bytes(*a, false) + attn_order_bytes(*a, true) +
+                round16((int64_t)a->axes * rows * 4) +
+                round16((int64_t)a->axes * a->B * a->Tk * 4);
     if (a->gsplit > 1)
         n += 2 * round16((int64_t)a->gsplit * a->B * a->Tk * a->Hk * a->D * 4);
     return (size_t)n;
@@ -636,6 +669,10 @@ void place_attn_backward(AttnArgs *a, void *workspace)
     p += oq;
     a->order_k = ok ? (int32_t *)p : nullptr;
     p += ok;
+    a->fpos_q = (float *)p;
+    p += round16((int64_t)a->axes * rows * 4);
+    a->fpos_k = (float *)p;
+    p += round16((int64_t)a->axes * a->B * a->Tk * 4);
     a->part_dk = (float *)p;
     p += round16((int64_t)a->gsplit * a->B * a->Tk * a->Hk * a->D * 4);
     a->part_dv = (float *)p;

@@ -51,8 +51,8 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
     const int bh = blk.head;
     const int b = bh / a.Hq, h = bh - b * a.Hq, hk = h / a.G;
     // (without documents the last queries see the most, if causal)
-    const int qt = a.order_q ? a.order_q[(int64_t)b * nq + blk.no] : nq - 1 - blk.no;
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, col = lane & 31, half = lane >> 5;
+    const int qt = a.order_q ? uniform(a.order_q[(int64_t)b * nq + blk.no]) : nq - 1 - blk.no;
+    const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63, col = lane & 31, half = lane >> 5;
     const int q0 = qt * 32 * NW, i = q0 + wave * 32 + col;
     const int ic = min(i, a.Tq - 1);
     const Span sp = row_span(a, b, ic);
@@ -88,6 +88,11 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
         gahi = min(gahi, ends[3 * NW + w]);
     }
 
+    glo = uniform(glo);
+    ghi = uniform(ghi);
+    galo = uniform(galo);
+    gahi = uniform(gahi);
+
     const R *kp = (const R *)a.k + b * a.ks[0] + hk * a.ks[2];
     const R *vp = (const R *)a.v + b * a.vs[0] + hk * a.vs[2];
     const R *qp = (const R *)a.q + b * a.qs[0] + h * a.qs[2] + (int64_t)ic * a.qs[1];
@@ -107,8 +112,11 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
         base[x] = p[q0];
         pq[x] = (float)(p[ic] - base[x]);
         sl[x] = a.slopes[h * axes + x] * sc.slope;
+        arrived(pq[x]);
+        arrived(sl[x]);
     }
 
+    arrived(qf);
     f32x16 o[ND];
 #pragma unroll
     for (int d = 0; d < ND; ++d) o[d] = f32x16(0.f);
@@ -124,14 +132,18 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
             ((u32x4 *)kt)[x] = u32x4{0u, 0u, 0u, 0u};
         __syncthreads();
     }
-    auto direct = [&](int k0) {
-        return usable && max(glo, galo) <= k0 && k0 + KB <= min(ghi, gahi);
-    };
     int32_t pr[3];                         // (not touched before place: that would wait)
+    const uint32_t lds = lds_address(smem) + wave * 1024;
+    const bool whole = usable && a.D == DP;
     auto fetch = [&](int k0, int buf) {
-        if (direct(k0)) {
-            kd.load(kp + k0 * a.ks[1], a.ks[1], kt + buf * KB * DP, wave);
-            vd.load(vp + k0 * a.vs[1], a.vs[1], vt + buf * KB * DP, wave);
+        const uint32_t at = lds + buf * KB * DP * (int)sizeof(R);
+        constexpr uint32_t v0 = 2 * KB * DP * sizeof(R);
+        if (whole && glo <= k0 && k0 + KB <= ghi) {
+            kd.load(kp + k0 * a.ks[1], at);
+            vd.load(vp + k0 * a.vs[1], at + v0);
+        } else if (usable) {
+            kd.load_edge(kp, a.ks[1], k0, glo, ghi, at);
+            vd.load_edge(vp, a.vs[1], k0, glo, ghi, at + v0);
         }
 #pragma unroll
         for (int x = 0; x < 3; ++x)
@@ -139,132 +151,137 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
                 pr[x] = a.pos_k[((int64_t)x * a.B + b) * a.Tk + min(k0 + tid, a.Tk - 1)];
     };
     auto place = [&](int k0, int buf) {
-        if (!direct(k0)) {
-            const int tid = opaque(threadIdx.x);
+        const bool edge = k0 < glo || k0 + KB > ghi;
+        const bool drop = !(galo <= k0 && k0 + KB <= gahi);
+        R *const ks = kt + buf * KB * DP, *const vs = vt + buf * KB * DP;
+        wait_loads<0>(false);
+        if (!usable) {
+            const int t = opaque(threadIdx.x);
             TileRegs<T, DP, KB, NT> r;
-            r.load(vp, a.vs[1], k0, glo, ghi, a.D, a.vec, tid);
-            if (!(galo <= k0 && k0 + KB <= gahi) && r.drop()) *flag = 1;
-            r.store(vt + buf * KB * DP, tid);
-            r.load(kp, a.ks[1], k0, glo, ghi, a.D, a.vec, tid);
-            r.store(kt + buf * KB * DP, tid);
+            r.load(vp, a.vs[1], k0, glo, ghi, a.D, a.vec, t);
+            if (drop && r.drop()) *flag = 1;
+            r.store(vs, t);
+            r.load(kp, a.ks[1], k0, glo, ghi, a.D, a.vec, t);
+            r.store(ks, t);
+            wait_all();
+        } else if (edge || drop) {
+            if (vd.scrub(vs, k0, glo, ghi, drop, nullptr, 0)) *flag = 1;
+            if (edge) kd.scrub(ks, k0, glo, ghi, false, nullptr, 0);
         }
 #pragma unroll
         for (int x = 0; x < 3; ++x)
             if (x < axes && tid < KB) pk[(buf * 3 + x) * KB + tid] = (float)(pr[x] - base[x]);
+        hand_over();
     };
     if (kbeg < kend) {
         fetch(kbeg, 0);
         place(kbeg, 0);
     }
-    wait_direct();
-    __syncthreads();
     int n = 0;
     for (int k0 = kbeg; k0 < kend; k0 += KB, ++n) {
         const int buf = n & 1;
         const bool more = k0 + KB < kend;
         if (more) fetch(k0 + KB, buf ^ 1);
-        if (k0 < whi && k0 + KB > wlo) {
-            const R *kb = kt + buf * KB * DP, *vb = vt + buf * KB * DP;
-            Frag<T> kf[NC][2], vf[ND][4];
+        // (a wave none of whose queries sees the tile goes along: it would wait
+        // for the others anyway)
+        const R *kb = kt + buf * KB * DP, *vb = vt + buf * KB * DP;
+        Frag<T> kf[NC][2], vf[ND][4], pf[4];
+        f32x16 s[2] = {f32x16(0.f), f32x16(0.f)};
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    kf[c][u] = row_frag<T, DP>(kb, u * 32 + col, c * 16 + half * 8);
-            f32x16 s[2] = {f32x16(0.f), f32x16(0.f)};
+            for (int u = 0; u < 2; ++u)
+                kf[c][u] = row_frag<T, DP>(kb, u * 32 + col, c * 16 + half * 8);
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
-                for (int u = 0; u < 2; ++u) s[u] = mma<T>(kf[c][u], qf[c], s[u]);
+            for (int u = 0; u < 2; ++u) s[u] = mma<T>(kf[c][u], qf[c], s[u]);
 #pragma unroll
-            for (int d = 0; d < ND / 2; ++d)
+        for (int d = 0; d < ND / 2; ++d)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) vf[d][c] = col_frag<T, DP>(vb, c, d * 32, lane);
-            reads_ahead<T, NC>();
-            products_and_reads<T, NC, 1>();
-            products_and_reads<T, NC, 2>();
-            issued<T>();
-            if (GEN && sc.multiply) {
-                s[0] *= sc.scale;
-                s[1] *= sc.scale;
-            }
-            if (GEN && a.cap > 0.f) {
+            for (int c = 0; c < 4; ++c) vf[d][c] = col_frag<T, DP>(vb, c, d * 32, lane);
+        reads_ahead<T, NC>();
+        products_and_reads<T, NC, 1>();
+        products_and_reads<T, NC, 2>();
+        issued<T>();
+        if (GEN && sc.multiply) {
+            s[0] *= sc.scale;
+            s[1] *= sc.scale;
+        }
+        if (GEN && a.cap > 0.f) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u) cap_scores<T>(s[u], sc);
-            }
-            if (axes > 0) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-#pragma unroll
-                    for (int x = 0; x < 3; ++x) {
-                        if (x >= axes) break;
-                        const f32x16 p = acc_rows(pk + (buf * 3 + x) * KB + u * 32, half);
-#pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            s[u][r] = fmaf(-sl[x], fabsf(p[r] - pq[x]), s[u][r]);
-                    }
-                }
-            }
-            const bool part = !(alo <= k0 && k0 + KB <= ahi);
-            if (part) {
-                const uint32_t at = k0 + 4 * half - sp.lo, len = sp.hi - sp.lo;
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        s[u][r] = at + (u * 32 + acc_row(r, 0)) < len ? s[u][r] : kNegInf;
-            }
-            float mx = s[0][0];
-#pragma unroll
-            for (int r = 1; r < 16; ++r) mx = fmaxf(mx, s[0][r]);
-#pragma unroll
-            for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[1][r]);
-            mx = halves_max(mx) * sc.mul;
-            if (__any(mx > m + kRaise)) {
-                // (each query by itself: its result does not depend on its neighbours)
-                const float mn = mx > m + kRaise ? mx : m;
-                const float al = __builtin_amdgcn_exp2f(m - (mn == kNegInf ? 0.f : mn));
-                l *= al;
-#pragma unroll
-                for (int d = 0; d < ND; ++d)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) o[d][r] *= al;
-                m = mn;
-            }
-            const float ms = m == kNegInf ? 0.f : m;
-            Frag<T> pf[4];
+            for (int u = 0; u < 2; ++u) cap_scores<T>(s[u], sc);
+        }
+        if (axes > 0) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    s[u][r] = __builtin_amdgcn_exp2f(fmaf(s[u][r], sc.mul, -ms));
-                    l += s[u][r];
+                for (int x = 0; x < 3; ++x) {
+                    if (x >= axes) break;
+                    const f32x16 p = acc_rows(pk + (buf * 3 + x) * KB + u * 32, half);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        s[u][r] = fmaf(-sl[x], fabsf(p[r] - pq[x]), s[u][r]);
                 }
-                pf[2 * u] = pack8<T>(s[u], 0);
-                pf[2 * u + 1] = pack8<T>(s[u], 1);
             }
-#pragma unroll
-            for (int d = ND / 2; d < ND; ++d)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) vf[d][c] = col_frag<T, DP>(vb, c, d * 32, lane);
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-                for (int d = 0; d < ND / 2; ++d) o[d] = mma<T>(vf[d][c], pf[c], o[d]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-                for (int d = ND / 2; d < ND; ++d) o[d] = mma<T>(vf[d][c], pf[c], o[d]);
-            products_and_reads<T, 2 * ND, 2>();
-            products_and_reads<T, 2 * ND, 0>();
-            issued<T>();
         }
+        const bool part = !(alo <= k0 && k0 + KB <= ahi);
+        if (part) {
+            const uint32_t at = k0 + 4 * half - sp.lo, len = sp.hi - sp.lo;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    s[u][r] = at + (u * 32 + acc_row(r, 0)) < len ? s[u][r] : kNegInf;
+        }
+        float mx = s[0][0];
+#pragma unroll
+        for (int r = 1; r < 16; ++r) mx = fmaxf(mx, s[0][r]);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[1][r]);
+        mx = halves_max(mx) * sc.mul;
+        if (__any(mx > m + kRaise)) {
+            // (each query by itself: its result does not depend on its neighbours)
+            const float mn = mx > m + kRaise ? mx : m;
+            const float al = __builtin_amdgcn_exp2f(m - (mn == kNegInf ? 0.f : mn));
+            l *= al;
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[d][r] *= al;
+            m = mn;
+        }
+        const float ms = m == kNegInf ? 0.f : m;
+        auto weights = [&](int u) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                s[u][r] = __builtin_amdgcn_exp2f(fmaf(s[u][r], sc.mul, -ms));
+                l += s[u][r];
+            }
+            pf[2 * u] = pack8<T>(s[u], 0);
+            pf[2 * u + 1] = pack8<T>(s[u], 1);
+        };
+        weights(0);
+        weights(1);
+#pragma unroll
+        for (int d = ND / 2; d < ND; ++d)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) vf[d][c] = col_frag<T, DP>(vb, c, d * 32, lane);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int d = 0; d < ND / 2; ++d) o[d] = mma<T>(vf[d][c], pf[c], o[d]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int d = ND / 2; d < ND; ++d) o[d] = mma<T>(vf[d][c], pf[c], o[d]);
+        products_and_reads<T, 2 * ND, 2>();
+        products_and_reads<T, 2 * ND, 0>();
+        issued<T>();
         if (more) place(k0 + KB, buf ^ 1);
-        wait_direct();
-        __syncthreads();
     }
 
-    if (*flag) {                           // (the loop's last barrier is behind us)
+    if (*flag) {                           // (set before the last barrier)
         for (int key = kbeg; key < kend; ++key) {
             const int k0 = key / KB * KB;
             if ((galo <= k0 && k0 + KB <= gahi) || key < sp.lo || key >= sp.hi) continue;

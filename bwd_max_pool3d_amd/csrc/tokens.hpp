@@ -98,6 +98,8 @@ struct AttnArgs {
     int32_t *spans;            // (B, Tq, 2): the keys [lo, hi) of each query
     int32_t *tiles;            // (B, ceil(Tq / 32), 4): over 32 queries, the union of
                                // their keys [lo, hi) and the keys all of them see
+    float *fpos_q, *fpos_k;    // (axes, B, Tq) and (axes, B, Tk): positions from that of
+                               // the sequence's first key
     float *part_dk, *part_dv;  // (gsplit, B, Tk, Hk, D), when gsplit > 1
 };
 // Scores with a cap, a bias or a factor that is not positive: kernels of
