@@ -22,7 +22,7 @@ namespace mp3d {
 
 namespace {
 
-constexpr int kNormWg = 768;               // backward workgroups to aim for (256 threads)
+constexpr int kNormWg = 768;               // backward workgroups of 256 threads to aim for
 
 // The elements of a thread: V adjacent ones of every TPR * V, so that a
 // wave reads whole lines.
@@ -81,12 +81,73 @@ struct Row {
     }
 };
 
+// The same elements as they are stored: in flight, or kept, in half the
+// registers for 16-bit types.
+template <typename T, int TPR, int EPT, int V>
+struct RawRow {
+    using R = typename T::raw;
+    struct alignas(V > 1 ? 16 : sizeof(R)) Pack {
+        R r[V];
+    } q[EPT / V];
+
+    __device__ __forceinline__ void load(const void *p, int64_t off, int t, int C)
+    {
+#pragma unroll
+        for (int j = 0; j < EPT / V; ++j) {
+            const int c = (j * TPR + t) * V;
+            const R *s = (const R *)p + off + c;
+            if (c < C) {
+                if constexpr (V == 1) q[j].r[0] = *s;
+                else q[j] = __builtin_bit_cast(Pack, *(const u32x4 *)s);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) q[j].r[i] = 0;
+            }
+        }
+    }
+    __device__ __forceinline__ void fill(float v)
+    {
+#pragma unroll
+        for (int k = 0; k < EPT; ++k) q[k / V].r[k % V] = T::narrow(v);
+    }
+    __device__ __forceinline__ void load_or(const void *p, int64_t off, int t, int C, float v)
+    {
+        if (p) load(p, off, t, C);
+        else fill(v);
+    }
+    __device__ __forceinline__ float operator[](int k) const { return T::widen(q[k / V].r[k % V]); }
+};
+
+// Sum over the 64 lanes, in every lane (each step adds the same two values in
+// both of a pair's lanes, so all get the same bits), without LDS.
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v)
+{
+    return v + __builtin_bit_cast(
+                   float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf,
+                                                      0xf, true));
+}
+__device__ __forceinline__ float wave_sum(float v)
+{
+    v = dpp_add<0xb1>(v);                  // quads: lane ^ 1
+    v = dpp_add<0x4e>(v);                  // lane ^ 2
+    v = dpp_add<0x141>(v);                 // the other quad of 8 lanes (mirrored)
+    v = dpp_add<0x140>(v);                 // the other 8 of 16 lanes (mirrored)
+    const uint32_t a = __builtin_bit_cast(uint32_t, v);
+    const auto x = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+    const uint32_t x0 = x[0], x1 = x[1];
+    v = __builtin_bit_cast(float, x0) + __builtin_bit_cast(float, x1);
+    const uint32_t b = __builtin_bit_cast(uint32_t, v);
+    const auto y = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    const uint32_t y0 = y[0], y1 = y[1];
+    return __builtin_bit_cast(float, y0) + __builtin_bit_cast(float, y1);
+}
+
 // Sum over the TPR threads of a row; every thread gets it.
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float *red)
 {
-#pragma unroll
-    for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m);
+    v = wave_sum(v);
     if constexpr (TPR > 64) {
         __syncthreads();                   // the last sum's readers are done
         if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
@@ -211,41 +272,56 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void norm_bwd_kernel(NormPla
         }
     };
 
+    // (kept as stored, and the next row loaded while one is worked on: a wave
+    // has only its own loads to cover their latency with)
+    RawRow<T, TPR, EPT, V> wpost, wpre, wgate, rx, rh, ry, rz;
+    wpost.load_or(p.post, 0, t, p.C, 1.f);
+    wpre.load_or(p.pre, 0, t, p.C, 1.f);
     const int64_t g0 = p.wpg > 1 ? blockIdx.x / p.wpg : blockIdx.x;
     const int64_t gstep = p.wpg > 1 ? p.groups : gridDim.x;
     const int sub = p.wpg > 1 ? blockIdx.x % p.wpg : 0;
+    const int64_t istep = (int64_t)p.wpg * NW;
     for (int64_t g = g0; g < p.groups; g += gstep) {
 #pragma unroll
         for (int k = 0; k < EPT; ++k) dgate[k] = 0.f;
-        for (int64_t i = (int64_t)sub * NW + wv; i < p.rpg; i += (int64_t)p.wpg * NW) {
+        wgate.load_or(p.gate, g * p.C, t, p.C, 1.f);
+        float4 rst;
+        auto fetch = [&](int64_t i) {
             const int64_t row = g * p.rpg + i, off = row * p.C;
-            const float4 st = *(const float4 *)(p.stats + 4 * row);
-            RowT y, nh, f, d;              // f: rs * gate * post (the factor of n(h) in y)
-            y.load((const R *)p.x + off, t, p.C);
-            d.load_or(p.dy, off, t, p.C, 0.f);
+            rst = *(const float4 *)(p.stats + 4 * row);
+            rx.load(p.x, off, t, p.C);
+            if (p.h) rh.load(p.h, off, t, p.C);
+            ry.load_or(p.dy, off, t, p.C, 0.f);
+            if (p.has_pre) rz.load(p.dz, off, t, p.C);
+        };
+        int64_t i = (int64_t)sub * NW + wv;
+        if (i < p.rpg) fetch(i);
+        for (; i < p.rpg; i += istep) {
+            const int64_t off = (g * p.rpg + i) * p.C;
+            const float4 st = rst;
+            RowT y, nh, d, a;              // x then y; h then n(h); dy then dx; dz
+#pragma unroll
+            for (int k = 0; k < EPT; ++k) {
+                y.e[k] = rx[k];
+                nh.e[k] = p.h ? rh[k] : 0.f;
+                d.e[k] = ry[k];
+                a.e[k] = p.has_pre ? rz[k] : 0.f;
+            }
+            if (i + istep < p.rpg) fetch(i + istep);
             if (p.h) {
-                nh.load((const R *)p.h + off, t, p.C);
-                f.load_or(p.post, 0, t, p.C, 1.f);
-                RowT w;
-                w.load_or(p.gate, g * p.C, t, p.C, 1.f);
 #pragma unroll
                 for (int k = 0; k < EPT; ++k) {
                     if (p.has_post) nh.e[k] = (nh.e[k] - st.x) * st.y;
-                    f.e[k] *= w.e[k] * p.rs;
-                    y.e[k] = fmaf(f.e[k], nh.e[k], y.e[k]);
+                    y.e[k] = fmaf(wpost[k] * wgate[k] * p.rs, nh.e[k], y.e[k]);
                 }
             }
             if (p.has_pre) {
-                RowT a;
-                a.load((const R *)p.dz + off, t, p.C);
-                RowT w;
-                w.load_or(p.pre, 0, t, p.C, 1.f);
                 float s1 = 0.f, s2 = 0.f;
 #pragma unroll
                 for (int k = 0; k < EPT; ++k) {
                     y.e[k] = RowT::col(k, t) < p.C ? (y.e[k] - st.z) * st.w : 0.f;
                     dpre[k] = fmaf(a.e[k], y.e[k], dpre[k]);
-                    a.e[k] *= w.e[k];
+                    a.e[k] *= wpre[k];
                     s1 = fmaf(a.e[k], y.e[k], s1);
                     s2 += a.e[k];
                 }
@@ -258,21 +334,13 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void norm_bwd_kernel(NormPla
             d.store((R *)p.dx + off, t, p.C);
             if (p.h) {
                 float s1 = 0.f, s2 = 0.f;
-                {
-                    RowT wg, wp;
-                    wg.load_or(p.gate, g * p.C, t, p.C, 1.f);
-                    wp.load_or(p.post, 0, t, p.C, 1.f);
-#pragma unroll
-                    for (int k = 0; k < EPT; ++k) {
-                        if (RowT::col(k, t) >= p.C) d.e[k] = 0.f;
-                        const float u = d.e[k] * nh.e[k] * p.rs;
-                        dgate[k] = fmaf(u, wp.e[k], dgate[k]);
-                        dpost[k] = fmaf(u, wg.e[k], dpost[k]);
-                    }
-                }
 #pragma unroll
                 for (int k = 0; k < EPT; ++k) {
-                    d.e[k] *= f.e[k];
+                    if (RowT::col(k, t) >= p.C) d.e[k] = 0.f;
+                    const float u = d.e[k] * nh.e[k] * p.rs, w = wpost[k], wg = wgate[k];
+                    dgate[k] = fmaf(u, w, dgate[k]);
+                    dpost[k] = fmaf(u, wg, dpost[k]);
+                    d.e[k] *= w * wg * p.rs;
                     s1 = fmaf(d.e[k], nh.e[k], s1);
                     s2 += d.e[k];
                 }
@@ -376,9 +444,15 @@ void plan_norm(NormPlan *p, int es, bool aligned16)
     p->ept = p->C <= 8 * p->threads ? 8 : 16;
 }
 
+// The backward keeps three sums and four rows in registers, so a thread takes
+// 8 elements wherever a workgroup can hold the row with that (16 a thread:
+// over 256 registers, one wave on a SIMD).
 size_t plan_norm_backward(NormPlan *p)
 {
-    const int64_t target = p->threads == 1024 ? kNormWg / 3 : kNormWg;
+    p->threads = 64;
+    while (p->threads < 1024 && 8 * p->threads < p->C) p->threads *= 2;
+    p->ept = p->C <= 8 * p->threads ? 8 : 16;
+    const int64_t target = p->threads <= 128 ? 1024 : (int64_t)kNormWg * 256 / p->threads;
     const int64_t per = p->threads == 64 ? 4 : 1;
     p->groups = p->gate_rows > 0 ? p->gate_rows : 1;
     p->rpg = p->rows / p->groups;
@@ -415,16 +489,14 @@ hipError_t launch_norm_forward(const NormPlan &p, hipStream_t s)
 template <typename T>
 hipError_t launch_norm_backward(const NormPlan &p, hipStream_t s)
 {
-    if (p.threads == 64) {
-        if (p.ept == 8) backward_v<T, 64, 8>(p, s);
-        else backward_v<T, 64, 16>(p, s);
-    } else if (p.threads == 256) {
-        if (p.ept == 8) backward_v<T, 256, 8>(p, s);
-        else backward_v<T, 256, 16>(p, s);
-    } else if (p.ept == 8) {
-        backward_v<T, 1024, 8>(p, s);
-    } else {
-        backward_v<T, 1024, 16>(p, s);
+    switch (p.threads) {
+    case 64: backward_v<T, 64, 8>(p, s); break;
+    case 128: backward_v<T, 128, 8>(p, s); break;
+    case 256: backward_v<T, 256, 8>(p, s); break;
+    case 512: backward_v<T, 512, 8>(p, s); break;
+    default:
+        if (p.ept == 8) backward_v<T, 1024, 8>(p, s);
+        else backward_v<T, 1024, 16>(p, s);
     }
     const int64_t jobs = 2 + (p.gate && p.wpg > 1 ? p.groups : 0);
     if (p.dpost || p.dpre || jobs > 2)

@@ -52,7 +52,7 @@ struct NormPlan {
     float rs, eps;             // residual scale
     int32_t layer, has_post, has_pre;
     int32_t vec;               // 16-byte accesses possible
-    int32_t threads;           // threads per row: 64, 256 or 1024
+    int32_t threads;           // threads per row: 64 to 1024
     int32_t ept;               // elements per thread: 8 or 16
     // backward: workgroups walk groups of rows that share a gate row
     int64_t groups;            // gate rows (1 without a gate)
@@ -61,7 +61,7 @@ struct NormPlan {
 };
 // threads, ept and vec from C, the element size and the pointers' alignment
 void plan_norm(NormPlan *p, int es, bool aligned16);
-// groups, wpg and nwg; returns the workspace bytes
+// the backward's threads and ept, groups, wpg and nwg; returns the workspace bytes
 size_t plan_norm_backward(NormPlan *p);
 template <typename T>
 hipError_t launch_norm_forward(const NormPlan &p, hipStream_t s);
