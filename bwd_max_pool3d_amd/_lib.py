@@ -90,14 +90,16 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.mp3d_backward_recompute_static.argtypes = ([_vp, _vp, _vp, _vp, ctypes.c_int]
                                                    + [_i64] * 5 + [_i32] * 3 + [_a3] * 4
                                                    + [ctypes.c_int, _vp])
-    _a3l, _f32, _int, _size = ctypes.POINTER(_i64), ctypes.c_float, ctypes.c_int, ctypes.c_size_t
+    # (host arrays and the attention descriptor as void*: ctypes objects and
+    # packed bytes are both taken)
+    _f32, _int, _size = ctypes.c_float, ctypes.c_int, ctypes.c_size_t
     for name in ("mp3d_rope_forward", "mp3d_rope_backward"):
-        getattr(lib, name).argtypes = ([_vp] * 4 + [_int] + [_i64] * 2 + [_i32] * 3 + [_a3l] * 4
-                                       + [_vp, _a3, _vp, _a3, _int, _vp])
-    _attn = ctypes.POINTER(Attention)
+        getattr(lib, name).argtypes = ([_vp] * 4 + [_int] + [_i64] * 2 + [_i32] * 3 + [_vp] * 4
+                                       + [_vp] * 4 + [_int, _vp])
+    _attn = _vp
     lib.mp3d_attention_workspace_bytes.argtypes = [_attn, _int, ctypes.POINTER(_size)]
     lib.mp3d_attention_forward.argtypes = [_attn] + [_vp] * 6 + [_size, _vp]
-    lib.mp3d_attention_backward.argtypes = [_attn, _vp, _a3l] + [_vp] * 9 + [_size, _vp]
+    lib.mp3d_attention_backward.argtypes = [_attn] + [_vp] * 11 + [_size, _vp]
     lib.mp3d_gated_norm_forward.argtypes = ([_vp] * 8 + [_int, _i64, _i32, _i64, _f32, _int, _int,
                                                         _f32, _vp])
     lib.mp3d_gated_norm_workspace_bytes.argtypes = [_int, _i64, _i32, _i64,

@@ -441,19 +441,25 @@ struct TileDirect {
     static constexpr int UNITS = DP / PER;                 // of a row
     static constexpr int STEP = NT / UNITS;                // rows of one round over the threads
     static constexpr int N = ROWS / STEP;
-    static_assert(N * STEP == ROWS && STEP % (sizeof(R) * DP < 512 ? 16 : 8) == 0,
-                  "every round swaps alike");
-    uint32_t off;                                          // bytes from the round's first row
+    static_assert(N * STEP == ROWS && (STEP & (STEP - 1)) == 0, "whole rounds over the threads");
+    uint32_t row, ch;                                      // bytes from the round's first row
     int64_t step;                                          // bytes from round to round
-    bool on;                                               // the lane's channels are there
+    uint32_t end;                                          // bytes of a row's channels
 
     __device__ __forceinline__ void init(int t, int64_t stride, int D)
     {
-        const int row = t / UNITS, u = t % UNITS, c = (u * PER / 8) ^ tile_swap<R, DP>(row);
-        const int e = c * 8 + (u * PER) % 8;
-        off = (uint32_t)(row * stride + e) * (uint32_t)sizeof(R);
+        const int r = t / UNITS, u = t % UNITS, c = (u * PER / 8) ^ tile_swap<R, DP>(r);
+        row = (uint32_t)(r * stride) * (uint32_t)sizeof(R);
+        ch = (c * 8 + (u * PER) % 8) * (uint32_t)sizeof(R);
         step = STEP * stride * (int64_t)sizeof(R);
-        on = e < D;
+        end = D * (uint32_t)sizeof(R);
+    }
+    // The lane's channels in round j.  (The swap of a sum of rows without
+    // common bits is the exclusive or of their swaps; with 16 rows or more a
+    // round, all rounds swap alike.)
+    __device__ __forceinline__ uint32_t channels(int j) const
+    {
+        return ch ^ (tile_swap<R, DP>(j * STEP) * 8 * (uint32_t)sizeof(R));
     }
     // A whole tile, all channels there, whose first row is at p.  `lds`: the
     // wave's first place in the tile.  Every wave waits for its loads before
@@ -464,22 +470,21 @@ struct TileDirect {
     {
 #pragma unroll
         for (int j = 0; j < N; ++j)
-            direct16((const char *)p + j * step, off, lds + j * NT * 16);
+            direct16((const char *)p + j * step, row + channels(j), lds + j * NT * 16);
     }
     // Any tile, from row r0 of base.
     __device__ __forceinline__ void load_edge(const R *base, int64_t stride, int r0, int lo, int hi,
                                               uint32_t lds) const
     {
-        if (!on) return;
-        const int t = opaque(threadIdx.x) / UNITS;
+        const int t = opaque(threadIdx.x % NT) / UNITS;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             // (clamping keeps the order: no lane is before the first)
             const int first = r0 + j * STEP, at = min(max(first, lo), hi - 1);
-            const int row = min(max(first + t, lo), hi - 1) - at;
-            direct16(base + at * stride,
-                     off + (uint32_t)((row - t) * stride) * (uint32_t)sizeof(R),
-                     lds + j * NT * 16);
+            const int r = min(max(first + t, lo), hi - 1) - at;
+            if (channels(j) < end)
+                direct16(base + at * stride, (uint32_t)(r * stride) * (uint32_t)sizeof(R) + channels(j),
+                         lds + j * NT * 16);
         }
     }
     // Rows outside [lo, hi) of a tile that has arrived to zero; with `drop`
@@ -488,12 +493,12 @@ struct TileDirect {
                                           int *row_mark, int mark) const
     {
         bool bad = false;
-        const int t = opaque(threadIdx.x);
+        const int t = opaque(threadIdx.x % NT);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const int id = j * NT + t, row = r0 + id / UNITS;
+            const int id = j * NT + t, at = r0 + id / UNITS;
             u32x4 *p = (u32x4 *)(tile + id * PER);
-            if (row < lo || row >= hi) {
+            if (at < lo || at >= hi) {
                 *p = u32x4{0u, 0u, 0u, 0u};
             } else if (drop) {
                 u32x4 v = *p;
@@ -539,6 +544,9 @@ __device__ __forceinline__ void hand_over()
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
+
+// The reads from a part of LDS are done: loads may write there again.
+__device__ __forceinline__ void reads_done() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 // A value that is the same in every lane, as a scalar.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }

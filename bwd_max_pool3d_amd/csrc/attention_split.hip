@@ -6,8 +6,10 @@
 // rows of one block of up to 32, so a key is read once for all of them.  A
 // workgroup takes one block of rows and one chunk of keys; its four waves
 // take tiles of 32 keys in turn, each through a part of LDS of its own, so
-// no wave waits for another until the end.  The next tile's loads are in
-// flight while a tile is worked on.  Every wave keeps its own running
+// no wave waits for another until the end.  A tile's keys, and its values,
+// go to registers as soon as they are in LDS, and the next tile's take their
+// place there: loads are in flight all the time, with one tile of LDS a
+// wave, and two workgroups fit on a CU.  Every wave keeps its own running
 // maximum and sum; the four are joined in LDS, the chunks by a second
 // kernel.  Chunks have a fixed length whatever the sequence's: those past a
 // short sequence's end return at once, so long and short caches balance.
@@ -20,30 +22,38 @@ namespace {
 constexpr int kSplitWaves = 4;
 constexpr int kSplitKeys = 32;             // keys of a wave's tile
 constexpr int kSplitPad = 4;               // floats between the rows of the join
+constexpr int kJoinGroups = 8;
 constexpr float kRaise = 8.f;
 
+// floats between a chunk's rows, for loads of 4
+__host__ __device__ inline int split_stride(int D) { return (D + 3) & ~3; }
+
 template <typename T, int DP>
-constexpr uint32_t split_lds()
+constexpr uint32_t split_tiles()
 {
     const uint32_t tiles = kSplitWaves * 2 * kSplitKeys * DP * sizeof(typename T::raw);
     const uint32_t join = kSplitWaves * 32 * (DP + kSplitPad) * sizeof(float);
-    return (tiles > join ? tiles : join) + kSplitWaves * (3 * kSplitKeys + 64) * sizeof(float);
+    return tiles > join ? tiles : join;
+}
+template <typename T, int DP>
+constexpr uint32_t split_lds()
+{
+    return split_tiles<T, DP>() + kSplitWaves * (2 * 3 * kSplitKeys + 64) * sizeof(float);
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool GEN>
 __global__ __launch_bounds__(64 * kSplitWaves, (sizeof(typename T::raw) * DP > 256 ? 1 : 2))
 void attn_split_kernel(AttnArgs a)
 {
     using R = typename T::raw;
     constexpr int KB = kSplitKeys, NC = DP / 16, ND = DP / 32, NW = kSplitWaves;
     extern __shared__ __align__(16) unsigned char smem[];
-    constexpr uint32_t rest =
-        split_lds<T, DP>() - kSplitWaves * (3 * kSplitKeys + 64) * sizeof(float);
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, col = lane & 31,
+    const int axes = GEN ? a.axes : 0;
+    const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63, col = lane & 31,
               half = lane >> 5;
     R *const kt = (R *)smem + wave * 2 * KB * DP, *const vt = kt + KB * DP;
-    float *const pk = (float *)(smem + rest) + wave * 3 * KB;        // [3][KB]
-    float *const ml = (float *)(smem + rest) + NW * 3 * KB;          // [NW][32][2]
+    int *const pk = (int *)(smem + split_tiles<T, DP>()) + wave * 2 * 3 * KB;   // [2][3][KB]
+    float *const ml = (float *)(smem + split_tiles<T, DP>()) + NW * 2 * 3 * KB;  // [NW][32][2]
 
     // blocks of one (sequence, key head) and chunk follow each other
     int64_t id = blockIdx.x;
@@ -78,61 +88,106 @@ void attn_split_kernel(AttnArgs a)
     bool dropped = false;
 
     if (glo < ghi) {
+        TileDirect<T, DP, KB, 64> kd, vd;
+        kd.init(lane, a.ks[1], a.D);
+        vd.init(lane, a.vs[1], a.D);
+        const bool usable = kd.usable(a.vec, a.ks[1], a.D) && vd.usable(a.vec, a.vs[1], a.D);
+        const bool whole = usable && a.D == DP;
+        if (a.D < DP) {                        // channels that no direct load writes
+            for (int x = lane; x < 2 * KB * DP * (int)sizeof(R) / 16; x += 64)
+                ((u32x4 *)kt)[x] = u32x4{0u, 0u, 0u, 0u};
+            reads_done();                      // (these writes are)
+        }
+        const uint32_t lds_k = lds_address(kt), lds_v = lds_address(vt), lds_p = lds_address(pk);
+        auto fetch = [&](const TileDirect<T, DP, KB, 64> &d, const R *p, int64_t stride, int k0,
+                         uint32_t lds) {
+            if (whole && glo <= k0 && k0 + KB <= ghi) d.load(p + k0 * stride, lds);
+            else if (usable) d.load_edge(p, stride, k0, glo, ghi, lds);
+        };
+        auto place = [&](const R *p, int64_t stride, int k0, R *tile) {
+            TileRegs<T, DP, KB, 64> r;
+            r.load(p, stride, k0, glo, ghi, a.D, a.vec, lane);
+            r.store(tile, lane);
+            wait_all();
+        };
+        // three axes or none, so that what is in flight can be counted
+        auto fetch_pos = [&](int k0, int buf) {
+            if (axes > 0 && lane < KB)
+#pragma unroll
+                for (int x = 0; x < 3; ++x)
+                    direct4(a.pos_k + ((int64_t)min(x, axes - 1) * a.B + b) * a.Tk + k0,
+                            (uint32_t)min(lane, a.Tk - 1 - k0) * 4,
+                            lds_p + (buf * 3 + x) * KB * 4);
+        };
+        const int kbeg = glo / KB * KB + wave * KB;
+        if (kbeg < ghi) {
+            fetch_pos(kbeg, 0);
+            fetch(kd, kp, a.ks[1], kbeg, lds_k);
+            fetch(vd, vp, a.vs[1], kbeg, lds_v);
+        }
+
         const R *qp = (const R *)a.q + b * a.qs[0] + h * a.qs[2] + (int64_t)t * a.qs[1];
         Frag<T> qf[NC];
 #pragma unroll
         for (int c = 0; c < NC; ++c) qf[c] = load8<T>(qp, c * 16 + half * 8, a.D, a.vec);
         const Scores sc = scores(a);
         float pq[3], sl[3];
-        int64_t base[3];
+        double base[3];                        // (differences of int32 are exact in binary64)
 #pragma unroll
         for (int x = 0; x < 3; ++x) {
-            if (x >= a.axes) break;
+            if (x >= axes) break;
             const int32_t *p = a.pos_q + ((int64_t)x * a.B + b) * a.Tq;
-            base[x] = p[0];
-            pq[x] = (float)(p[t] - base[x]);
-            sl[x] = a.slopes[h * a.axes + x] * sc.slope;
+            base[x] = uniform_load(p);
+            pq[x] = (float)((double)p[t] - base[x]);
+            sl[x] = a.slopes[h * axes + x] * sc.slope;
+            arrived(pq[x]);
+            arrived(sl[x]);
         }
-        TileRegs<T, DP, KB, 64> kr, vr;
-        int32_t pr[3];
-        auto fetch = [&](int k0) {
-            kr.load(kp, a.ks[1], k0, glo, ghi, a.D, a.vec, lane);
-            vr.load(vp, a.vs[1], k0, glo, ghi, a.D, a.vec, lane);
+        arrived(qf);
+        constexpr int kTile = TileDirect<T, DP, KB, 64>::LOADS;
+        int buf = 0;
+        for (int k0 = kbeg; k0 < ghi; k0 += NW * KB, buf ^= 1) {
+            const bool part = !(alo <= k0 && k0 + KB <= ahi), more = k0 + NW * KB < ghi;
+            // keys: in flight after them are this tile's values.  (A wave's
+            // LDS operations keep their order: no barrier)
+            wait_loads<kTile>(usable);
+            if (!usable) place(kp, a.ks[1], k0, kt);
+            Frag<T> kf[NC], vf[ND][2];
 #pragma unroll
-            for (int x = 0; x < 3; ++x)
-                if (x < a.axes && lane < KB)
-                    pr[x] = a.pos_k[((int64_t)x * a.B + b) * a.Tk + min(k0 + lane, a.Tk - 1)];
-        };
-        const int kbeg = glo / KB * KB + wave * KB;
-        if (kbeg < ghi) fetch(kbeg);
-        for (int k0 = kbeg; k0 < ghi; k0 += NW * KB) {
-            const bool part = !(alo <= k0 && k0 + KB <= ahi);
-            // the wave's LDS operations keep their order: no barrier, only the
-            // compiler must not move them across
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            if (part) dropped |= vr.drop();
-            kr.store(kt, lane);
-            vr.store(vt, lane);
-#pragma unroll
-            for (int x = 0; x < 3; ++x)
-                if (x < a.axes && lane < KB) pk[x * KB + lane] = (float)(pr[x] - base[x]);
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            if (k0 + NW * KB < ghi) fetch(k0 + NW * KB);
-
+            for (int c = 0; c < NC; ++c) kf[c] = row_frag<T, DP>(kt, col, c * 16 + half * 8);
+            reads_done();
+            if (more) {
+                fetch_pos(k0 + NW * KB, buf ^ 1);
+                fetch(kd, kp, a.ks[1], k0 + NW * KB, lds_k);
+            }
             f32x16 s = f32x16(0.f);
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
-                s = mma<T>(row_frag<T, DP>(kt, col, c * 16 + half * 8), qf[c], s);
-            if (sc.multiply) s *= sc.scale;
-            if (a.cap > 0.f) cap_scores<T>(s, sc);
+            for (int c = 0; c < NC; ++c) s = mma<T>(kf[c], qf[c], s);
+            // values: in flight after them are the next tile's keys
+            if (axes > 0) wait_loads<kTile + 3>(more && usable);
+            else wait_loads<kTile>(more && usable);
+            if (!usable) place(vp, a.vs[1], k0, vt);
+            if (part) {
+                dropped |= vd.scrub(vt, k0, glo, ghi, true, nullptr, 0);
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            }
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) vf[d][c] = col_frag<T, DP>(vt, c, d * 32, lane);
+            reads_done();
+            if (more) fetch(vd, vp, a.vs[1], k0 + NW * KB, lds_v);
+
+            if (GEN && sc.multiply) s *= sc.scale;
+            if (GEN && a.cap > 0.f) cap_scores<T>(s, sc);
 #pragma unroll
             for (int x = 0; x < 3; ++x) {
-                if (x >= a.axes) break;
-                const f32x16 p = acc_rows(pk + x * KB, half);
+                if (x >= axes) break;
+                const int *p = pk + (buf * 3 + x) * KB + 4 * half;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) s[e] = fmaf(-sl[x], fabsf(p[e] - pq[x]), s[e]);
+                for (int e = 0; e < 16; ++e)
+                    s[e] = fmaf(-sl[x],
+                                fabsf((float)((double)p[acc_row(e, 0)] - base[x]) - pq[x]), s[e]);
             }
             // (a chunk's ends are multiples of the tile, or the ends of every span)
             if (part) {
@@ -164,8 +219,8 @@ void attn_split_kernel(AttnArgs a)
             const Frag<T> p0 = pack8<T>(s, 0), p1 = pack8<T>(s, 1);
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
-                o[d] = mma<T>(col_frag<T, DP>(vt, 0, d * 32, lane), p0, o[d]);
-                o[d] = mma<T>(col_frag<T, DP>(vt, 1, d * 32, lane), p1, o[d]);
+                o[d] = mma<T>(vf[d][0], p0, o[d]);
+                o[d] = mma<T>(vf[d][1], p1, o[d]);
             }
         }
         if (__any(dropped)) {
@@ -221,7 +276,7 @@ void attn_split_kernel(AttnArgs a)
         }
         if (a.nsplit > 1) {
             const int64_t at = sp_no * all + row0 + rr;
-            if (d < a.D) a.part_o[at * a.D + d] = ot;
+            if (d < split_stride(a.D)) a.part_o[at * split_stride(a.D) + d] = ot;
             if (d == 0) *(float2 *)(a.part_ml + 2 * at) = make_float2(mt, lt);
         } else {
             const int tt = (rb * 32 + rr) / a.G, hh = hk * a.G + (rb * 32 + rr) % a.G;
@@ -235,42 +290,58 @@ void attn_split_kernel(AttnArgs a)
     }
 }
 
-// Joins the chunks: one wave per row, its lanes over the channels.
+// Joins the chunks: a workgroup per row, 8 groups of 32 lanes with 4 channels
+// a lane.  The groups take the chunks in turn, each with a running maximum of
+// its own, and are joined in LDS in a fixed order.
 template <typename T>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a)
+__global__ __launch_bounds__(32 * kJoinGroups) void attn_join_kernel(AttnArgs a)
 {
     using R = typename T::raw;
-    const int lane = threadIdx.x & 63, rows = a.Tq * a.G;
-    const int64_t all = (int64_t)a.B * a.Hk * rows;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (row >= all) return;
-    float mt = kNegInf;
-    for (int s = lane; s < a.nsplit; s += 64) mt = fmaxf(mt, a.part_ml[2 * (s * all + row)]);
-#pragma unroll
-    for (int x = 32; x; x >>= 1) mt = fmaxf(mt, __shfl_xor(mt, x));
-    const float ms = mt == kNegInf ? 0.f : mt;
-    float lt = 0.f, o[kAttnMaxD / 64] = {0.f, 0.f};
+    constexpr int NG = kJoinGroups;
+    __shared__ __align__(16) float jo[NG][kAttnMaxD];
+    __shared__ float jm[NG], jl[NG];
+    const int tid = threadIdx.x, g = tid >> 5, d0 = (tid & 31) * 4, rows = a.Tq * a.G;
+    const int64_t all = (int64_t)a.B * a.Hk * rows, row = blockIdx.x;
+    const int ds = split_stride(a.D);
+    float m = kNegInf, l = 0.f;
+    f32x4 o = f32x4(0.f);
 #pragma unroll 4
-    for (int s = 0; s < a.nsplit; ++s) {
-        const float2 v = *(const float2 *)(a.part_ml + 2 * (s * all + row));
-        const float f = __builtin_amdgcn_exp2f(v.x - ms);
-        lt = fmaf(f, v.y, lt);
+    for (int s = g; s < a.nsplit; s += NG) {
+        const int64_t at = s * all + row;
+        const float2 v = *(const float2 *)(a.part_ml + 2 * at);
+        const f32x4 x = d0 < ds ? *(const f32x4 *)(a.part_o + at * ds + d0) : f32x4(0.f);
+        const float mn = fmaxf(m, v.x), ms = mn == kNegInf ? 0.f : mn;
+        const float fo = __builtin_amdgcn_exp2f(m - ms), fn = __builtin_amdgcn_exp2f(v.x - ms);
+        l = l * fo + fn * v.y;
 #pragma unroll
-        for (int x = 0; x < kAttnMaxD / 64; ++x)
-            if (lane + 64 * x < a.D)
-                o[x] = fmaf(f, a.part_o[(s * all + row) * a.D + lane + 64 * x], o[x]);
+        for (int e = 0; e < 4; ++e) o[e] = o[e] * fo + fn * x[e];
+        m = mn;
+    }
+    *(f32x4 *)&jo[g][d0] = o;
+    if (d0 == 0) {
+        jm[g] = m;
+        jl[g] = l;
+    }
+    __syncthreads();
+    if (tid >= kAttnMaxD) return;
+    float mt = kNegInf, lt = 0.f, ot = 0.f;
+#pragma unroll
+    for (int x = 0; x < NG; ++x) mt = fmaxf(mt, jm[x]);
+    const float ms = mt == kNegInf ? 0.f : mt;
+#pragma unroll
+    for (int x = 0; x < NG; ++x) {
+        const float f = __builtin_amdgcn_exp2f(jm[x] - ms);
+        lt = fmaf(f, jl[x], lt);
+        ot = fmaf(f, jo[x][tid], ot);
     }
     const int64_t bh = row / rows;
     const int r = (int)(row - bh * rows), t = r / a.G;
     const int64_t b = bh / a.Hk;
     const int h = (int)(bh - b * a.Hk) * a.G + (r - t * a.G);
-    const float inv = lt == 0.f ? 0.f : 1.f / lt;
-#pragma unroll
-    for (int x = 0; x < kAttnMaxD / 64; ++x)
-        if (lane + 64 * x < a.D)
-            ((R *)a.out)[((b * a.Tq + t) * a.Hq + h) * a.D + lane + 64 * x] =
-                T::narrow(o[x] * inv);
-    if (lane == 0)
+    if (tid < a.D)
+        ((R *)a.out)[((b * a.Tq + t) * a.Hq + h) * a.D + tid] =
+            T::narrow(lt == 0.f ? 0.f : ot / lt);
+    if (tid == 0)
         a.lse[(b * a.Hq + h) * a.Tq + t] = lt == 0.f ? kNegInf : (mt + log2f(lt)) * kLn2;
 }
 
@@ -278,8 +349,12 @@ template <typename T, int DP>
 void run(const AttnArgs &a, hipStream_t s)
 {
     const int64_t grid = (int64_t)a.nrb * a.Hk * a.B * a.nsplit;
-    launch_kernel((attn_split_kernel<T, DP>), dim3((uint32_t)grid), dim3(64 * kSplitWaves),
-                  (split_lds<T, DP>()), s, a);
+    if (attn_general(a))
+        launch_kernel((attn_split_kernel<T, DP, true>), dim3((uint32_t)grid),
+                      dim3(64 * kSplitWaves), (split_lds<T, DP>()), s, a);
+    else
+        launch_kernel((attn_split_kernel<T, DP, false>), dim3((uint32_t)grid),
+                      dim3(64 * kSplitWaves), (split_lds<T, DP>()), s, a);
 }
 
 }  // namespace
@@ -304,13 +379,15 @@ size_t plan_attn_split(AttnArgs *a)
     a->chunk = (int32_t)chunk;
     a->nsplit = a->Tk > 0 ? (int32_t)((a->Tk + chunk - 1) / chunk) : 1;
     if (a->nsplit == 1) return 0;
-    return (size_t)a->nsplit * a->B * a->Hk * rows * (a->D + 2) * sizeof(float);
+    const size_t all = (size_t)a->nsplit * a->B * a->Hk * rows;
+    return ((2 * all + 3) / 4 * 4 + all * split_stride(a->D)) * sizeof(float);
 }
 
 void place_attn_split(AttnArgs *a, void *workspace)
 {
     a->part_ml = (float *)workspace;
-    a->part_o = a->part_ml + (int64_t)a->nsplit * a->B * a->Hk * a->Tq * a->G * 2;
+    const int64_t all = (int64_t)a->nsplit * a->B * a->Hk * a->Tq * a->G;
+    a->part_o = a->part_ml + (2 * all + 3) / 4 * 4;
 }
 
 template <typename T>
@@ -320,7 +397,8 @@ hipError_t launch_attn_split(const AttnArgs &a, hipStream_t s)
     else run<T, 128>(a, s);
     const int64_t all = (int64_t)a.B * a.Hk * a.Tq * a.G;
     if (a.nsplit > 1)
-        launch_kernel((attn_join_kernel<T>), dim3((uint32_t)((all + 3) / 4)), dim3(256), 0, s, a);
+        launch_kernel((attn_join_kernel<T>), dim3((uint32_t)all),
+                      dim3(32 * kJoinGroups), 0, s, a);
     return hipGetLastError();
 }
 

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 import torch
 
@@ -24,8 +25,14 @@ __all__ = ["mp3d_rope_forward", "mp3d_rope_backward", "mp3d_attention_forward",
 _DTYPE = {torch.float32: _lib.MP3D_F32, torch.float16: _lib.MP3D_F16,
           torch.bfloat16: _lib.MP3D_BF16}
 _NORM = {"rms": _lib.MP3D_NORM_RMS, "layer": _lib.MP3D_NORM_LAYER}
-_I64x3 = ctypes.c_int64 * 3
-_I32x3 = ctypes.c_int32 * 3
+# Host arrays and the attention descriptor go to the library as packed bytes:
+# for one token the calls are bound by the host, and ctypes arrays and
+# structure fields cost several times as much.
+_i64x3 = struct.Struct("=qqq").pack
+_i32x3 = struct.Struct("=iii").pack
+_attention_struct = struct.Struct("@iqqqiii9qffiPPiPiPPP").pack
+_contiguous = torch.contiguous_format
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _code(t: torch.Tensor, name: str) -> int:
@@ -36,24 +43,30 @@ def _code(t: torch.Tensor, name: str) -> int:
 
 
 def _stream(t: torch.Tensor) -> int:
+    """The current stream of t's device, as a hipStream_t."""
+    if _raw_stream is not None:
+        return _raw_stream(t.device.index)
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
-def _heads(t: torch.Tensor, name: str, like: torch.Tensor | None = None) -> None:
-    """A (B, T, H, D) device tensor with adjacent channels."""
+def _heads(t: torch.Tensor, name: str, like: torch.Tensor | None = None):
+    """(shape, first three strides) of a (B, T, H, D) device tensor with
+    adjacent channels."""
     if not t.is_cuda:
         raise ValueError("%s must be a device tensor" % name)
-    if t.dim() != 4:
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 4:
         raise ValueError("%s must be 4-D (B, T, H, D)" % name)
-    if t.stride(3) != 1 and t.shape[3] > 1:
+    if strides[3] != 1 and shape[3] > 1:
         raise ValueError("%s: a head's channels must be adjacent (stride 1)" % name)
     if like is not None and (t.dtype != like.dtype or t.device != like.device):
         raise ValueError("%s must have the dtype and device of the first tensor" % name)
+    return shape, strides[:3]
 
 
 def _same(t: torch.Tensor, name: str, shape, dtype, device) -> torch.Tensor:
     """A contiguous device tensor of this shape and dtype."""
-    if (tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device
+    if (t.shape != shape or t.dtype != dtype or t.device != device
             or not t.is_contiguous()):
         raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
                          % (name, dtype, tuple(shape), device))
@@ -64,24 +77,18 @@ def _ptr(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
 
-def _strides(t: torch.Tensor):
-    return _I64x3(*t.stride()[:3])
-
 
 # ------------------------------------------------------------ rotary positions
 
 def _rope(name, q, k, inv_freq, pairs, positions, grid, interleaved, out):
     lib = _lib.load()
-    _heads(q, "q")
-    B, T, Hq, D = q.shape
+    (B, T, Hq, D), qs = _heads(q, "q")
     code, dev = _code(q, "q"), q.device
-    Hk = 0
+    Hk, ks = 0, None
     if k is not None:
-        _heads(k, "k", q)
-        Hk = k.shape[2]
-        if k.shape[:2] != q.shape[:2] or k.shape[3] != D:
+        (Bk, T2, Hk, Dk), ks = _heads(k, "k", q)
+        if (Bk, T2, Dk) != (B, T, D):
             raise ValueError("q and k must share B, T and D")
-    pairs = tuple(int(p) for p in pairs)
     if len(pairs) != 3:
         raise ValueError("pairs must be three counts, one for each axis")
     _same(inv_freq, "inv_freq", (sum(pairs),), torch.float32, dev)
@@ -89,26 +96,29 @@ def _rope(name, q, k, inv_freq, pairs, positions, grid, interleaved, out):
         raise ValueError("give either positions or grid")
     if positions is not None:
         _same(positions, "positions", (3, B, T), torch.int32, dev)
-    else:
-        grid = tuple(int(g) for g in grid)
-        if len(grid) != 3:
-            raise ValueError("grid must be three extents (D, H, W)")
-        grid = _I32x3(*grid)
+    elif len(grid) != 3:
+        raise ValueError("grid must be three extents (D, H, W)")
     if out is None:
-        qo = torch.empty((B, T, Hq, D), dtype=q.dtype, device=dev)
-        ko = None if k is None else torch.empty((B, T, Hk, D), dtype=q.dtype, device=dev)
+        qo = torch.empty_like(q, memory_format=_contiguous)
+        ko = None if k is None else torch.empty_like(k, memory_format=_contiguous)
+        row = T * Hq * D, Hq * D, D
+        qos, kos = _i64x3(*row), _i64x3(T * Hk * D, Hk * D, D)
     else:
         qo, ko = out if k is not None else (out, None)
-        for o, t, n in ((qo, q, "out for q"), (ko, k, "out for k")):
-            if t is not None:
-                _heads(o, n, q)
-                if o.shape != t.shape:
-                    raise ValueError("%s must have its input's shape" % n)
-    qs, qos = _strides(q), _strides(qo)
-    ks, kos = (None, None) if k is None else (_strides(k), _strides(ko))
+        shape, st = _heads(qo, "out for q", q)
+        qos = _i64x3(*st)
+        if shape != q.shape:
+            raise ValueError("out for q must have its input's shape")
+        kos = None
+        if k is not None:
+            shape, st = _heads(ko, "out for k", q)
+            kos = _i64x3(*st)
+            if shape != k.shape:
+                raise ValueError("out for k must have its input's shape")
     _lib.check(getattr(lib, name)(
-        q.data_ptr(), _ptr(k), qo.data_ptr(), _ptr(ko), code, B, T, Hq, Hk, D, qs, ks, qos, kos,
-        inv_freq.data_ptr(), _I32x3(*pairs), _ptr(positions), grid, int(bool(interleaved)),
+        q.data_ptr(), _ptr(k), qo.data_ptr(), _ptr(ko), code, B, T, Hq, Hk, D, _i64x3(*qs),
+        None if k is None else _i64x3(*ks), qos, kos, inv_freq.data_ptr(), _i32x3(*pairs),
+        _ptr(positions), None if grid is None else _i32x3(*grid), 1 if interleaved else 0,
         _stream(q)))
     return qo if k is None else (qo, ko)
 
@@ -138,57 +148,47 @@ def mp3d_rope_backward(gq: torch.Tensor, gk: torch.Tensor | None, inv_freq: torc
 # ------------------------------------------------------------------- attention
 
 def _attention(q, k, v, scale, softcap, causal, kv_len, doc_offsets, prefix, slopes, pos_q, pos_k):
-    """The call's descriptor (include/mp3d.h, struct mp3d_attention)."""
-    _heads(q, "q")
-    _heads(k, "k", q)
-    _heads(v, "v", q)
-    B, Tq, Hq, D = q.shape
-    Tk, Hk = k.shape[1], k.shape[2]
-    if v.shape != k.shape or k.shape[0] != B or k.shape[3] != D:
+    """The call's descriptor (include/mp3d.h, struct mp3d_attention), packed."""
+    (B, Tq, Hq, D), qs = _heads(q, "q")
+    kshape, ks = _heads(k, "k", q)
+    vshape, vs = _heads(v, "v", q)
+    Tk, Hk = kshape[1], kshape[2]
+    if vshape != kshape or kshape[0] != B or kshape[3] != D:
         raise ValueError("k and v must have the shape (B, Tk, Hk, D) with q's B and D")
     dev = q.device
-    a = _lib.Attention()
-    a.dtype = _code(q, "q")
-    a.B, a.Tq, a.Tk, a.Hq, a.Hk, a.D = B, Tq, Tk, Hq, Hk, D
-    a.q_stride[:] = q.stride()[:3]
-    a.k_stride[:] = k.stride()[:3]
-    a.v_stride[:] = v.stride()[:3]
-    a.scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    a.softcap = float(softcap)
-    a.causal = int(bool(causal))
+    kv = docs = pre = 0
+    n_docs = axes = psl = ppq = ppk = 0
     if kv_len is not None:
-        a.kv_len = _same(kv_len, "kv_len", (B,), torch.int32, dev).data_ptr()
-    docs = 1
+        kv = _same(kv_len, "kv_len", (B,), torch.int32, dev).data_ptr()
     if doc_offsets is not None:
         if doc_offsets.dim() != 2 or doc_offsets.shape[1] < 2:
             raise ValueError("doc_offsets must be (B, n_docs + 1)")
-        docs = doc_offsets.shape[1] - 1
-        a.doc_offsets = _same(doc_offsets, "doc_offsets", (B, docs + 1), torch.int32,
-                              dev).data_ptr()
-        a.n_docs = docs
+        n_docs = doc_offsets.shape[1] - 1
+        docs = _same(doc_offsets, "doc_offsets", (B, n_docs + 1), torch.int32, dev).data_ptr()
     if prefix is not None:
         if prefix.dim() == 1:
             prefix = prefix[:, None]
-        a.prefix = _same(prefix, "prefix", (B, docs), torch.int32, dev).data_ptr()
+        pre = _same(prefix, "prefix", (B, n_docs or 1), torch.int32, dev).data_ptr()
     if slopes is not None:
         if slopes.dim() != 2 or pos_q is None or pos_k is None:
             raise ValueError("a distance bias needs slopes (Hq, axes), pos_q and pos_k")
         axes = slopes.shape[1]
         if not 1 <= axes <= 3:
             raise ValueError("slopes must have 1 to 3 axes")
-        a.slopes = _same(slopes, "slopes", (Hq, axes), torch.float32, dev).data_ptr()
-        a.pos_q = _same(pos_q, "pos_q", (axes, B, Tq), torch.int32, dev).data_ptr()
-        a.pos_k = _same(pos_k, "pos_k", (axes, B, Tk), torch.int32, dev).data_ptr()
-        a.axes = axes
+        psl = _same(slopes, "slopes", (Hq, axes), torch.float32, dev).data_ptr()
+        ppq = _same(pos_q, "pos_q", (axes, B, Tq), torch.int32, dev).data_ptr()
+        ppk = _same(pos_k, "pos_k", (axes, B, Tk), torch.int32, dev).data_ptr()
     elif pos_q is not None or pos_k is not None:
         raise ValueError("pos_q and pos_k go with slopes")
-    return a
+    return _attention_struct(_code(q, "q"), B, Tq, Tk, Hq, Hk, D, *qs, *ks, *vs,
+                             1.0 / math.sqrt(D) if scale is None and D else float(scale or 0.0),
+                             softcap, 1 if causal else 0, kv, docs, n_docs, pre, axes, psl, ppq,
+                             ppk)
 
 
 def _workspace(lib, a, backward, workspace, device):
     nbytes = ctypes.c_size_t()
-    _lib.check(lib.mp3d_attention_workspace_bytes(ctypes.byref(a), backward,
-                                                  ctypes.byref(nbytes)))
+    _lib.check(lib.mp3d_attention_workspace_bytes(a, backward, ctypes.byref(nbytes)))
     return _lend(nbytes.value, workspace, device)
 
 
@@ -211,7 +211,7 @@ def mp3d_attention_workspace_bytes(q, k, v, backward: bool = False, *, scale=Non
     a = _attention(q, k, v, scale, softcap, causal, kv_len, doc_offsets, prefix, slopes, pos_q,
                    pos_k)
     nbytes = ctypes.c_size_t()
-    _lib.check(_lib.load().mp3d_attention_workspace_bytes(ctypes.byref(a), int(backward),
+    _lib.check(_lib.load().mp3d_attention_workspace_bytes(a, int(backward),
                                                           ctypes.byref(nbytes)))
     return nbytes.value
 
@@ -240,16 +240,16 @@ def mp3d_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
     lib = _lib.load()
     a = _attention(q, k, v, scale, softcap, causal, kv_len, doc_offsets, prefix, slopes, pos_q,
                    pos_k)
-    shape = (a.B, a.Tq, a.Hq, a.D)
+    B, Tq, Hq, _ = q.shape
     if out is None:
-        o = torch.empty(shape, dtype=q.dtype, device=q.device)
-        lse = torch.empty((a.B, a.Hq, a.Tq), dtype=torch.float32, device=q.device)
+        o = torch.empty_like(q, memory_format=_contiguous)
+        lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=q.device)
     else:
         o, lse = out
-        _same(o, "out", shape, q.dtype, q.device)
-        _same(lse, "lse", (a.B, a.Hq, a.Tq), torch.float32, q.device)
+        _same(o, "out", q.shape, q.dtype, q.device)
+        _same(lse, "lse", (B, Hq, Tq), torch.float32, q.device)
     ws, n = _workspace(lib, a, 0, workspace, q.device)
-    _lib.check(lib.mp3d_attention_forward(ctypes.byref(a), q.data_ptr(), k.data_ptr(),
+    _lib.check(lib.mp3d_attention_forward(a, q.data_ptr(), k.data_ptr(),
                                           v.data_ptr(), o.data_ptr(), lse.data_ptr(), _ptr(ws), n,
                                           _stream(q)))
     return o, lse
@@ -272,21 +272,21 @@ def mp3d_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor
     lib = _lib.load()
     a = _attention(q, k, v, scale, softcap, causal, kv_len, doc_offsets, prefix, slopes, pos_q,
                    pos_k)
-    _heads(dout, "dout", q)
-    if dout.shape != q.shape:
+    shape, gs = _heads(dout, "dout", q)
+    if shape != q.shape:
         raise ValueError("dout must have q's shape")
     _same(out, "out", q.shape, q.dtype, q.device)
-    _same(lse, "lse", (a.B, a.Hq, a.Tq), torch.float32, q.device)
+    _same(lse, "lse", (q.shape[0], q.shape[2], q.shape[1]), torch.float32, q.device)
     if grads is None:
-        dq = torch.empty(tuple(q.shape), dtype=q.dtype, device=q.device)
-        dk = torch.empty(tuple(k.shape), dtype=q.dtype, device=q.device)
-        dv = torch.empty(tuple(k.shape), dtype=q.dtype, device=q.device)
+        dq = torch.empty_like(q, memory_format=_contiguous)
+        dk = torch.empty_like(k, memory_format=_contiguous)
+        dv = torch.empty_like(k, memory_format=_contiguous)
     else:
         dq, dk, dv = grads
         for t, like, n in ((dq, q, "dq"), (dk, k, "dk"), (dv, k, "dv")):
             _same(t, n, like.shape, q.dtype, q.device)
     ws, n = _workspace(lib, a, 1, workspace, q.device)
-    _lib.check(lib.mp3d_attention_backward(ctypes.byref(a), dout.data_ptr(), _strides(dout),
+    _lib.check(lib.mp3d_attention_backward(a, dout.data_ptr(), _i64x3(*gs),
                                            q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                            out.data_ptr(), lse.data_ptr(), dq.data_ptr(),
                                            dk.data_ptr(), dv.data_ptr(), _ptr(ws), n, _stream(q)))
