@@ -645,6 +645,50 @@ __device__ __forceinline__ Scores scores(const AttnArgs &a)
     return {multiply, a.scale, unit * kLog2e, 1.f / unit, a.cap / unit, unit / a.cap};
 }
 
+// (a branch: as a choice between two results it would be in every tile)
+__device__ __forceinline__ void multiply_scores(f32x16 &s, const Scores &sc)
+{
+    if (!sc.multiply) return;
+    asm volatile("");
+    s *= sc.scale;
+}
+
+// --- distances of positions: the differences of 32 rows' and 32 columns'
+// positions, as a matrix product.  A binary32 number is the sum of three
+// bfloat16 (each takes the next 8 of its 24 bits), so
+//   p - k = (p1, p2, p3, 0, 1, 1, 1, 0) . (1, 1, 1, 0, -k1, -k2, -k3, 0),
+// eight products that one matrix instruction forms for all pairs, without
+// error where the numbers are integers below 2^24.  The vector units, which
+// bound these kernels at 64 channels, are left with one operation a score
+// and axis where they had two, and LDS with one read where it had four.
+constexpr uint32_t kOnes[2] = {0x3f803f80u, 0x00003f80u};
+
+__device__ __forceinline__ u32x2 position_parts(float p)
+{
+    const uint32_t hi = __builtin_bit_cast(uint32_t, p) & 0xffff0000u;
+    const float r = p - __builtin_bit_cast(float, hi);
+    const uint32_t mid = __builtin_bit_cast(uint32_t, r) & 0xffff0000u;
+    const float lo = r - __builtin_bit_cast(float, mid);
+    return u32x2{(hi >> 16) | mid, __builtin_bit_cast(uint32_t, lo) >> 16};
+}
+
+// The columns' operand: lanes 0 .. 31 ones, 32 .. 63 the parts, negated.
+__device__ __forceinline__ u32x2 position_cols(u32x2 parts, int half)
+{
+    u32x2 c = half ? parts ^ 0x80008000u : u32x2{kOnes[0], kOnes[1]};
+    asm volatile("" : "+v"(c));
+    return c;
+}
+
+// The rows' is read from LDS: `lane` points to the lane's parts, for lanes
+// 32 .. 63 to ones.
+__device__ __forceinline__ f32x16 differences(const u32x2 *lane, u32x2 cols)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x8bf16_1k(__builtin_bit_cast(s16x4, *lane),
+                                                    __builtin_bit_cast(s16x4, cols), f32x16(0.f),
+                                                    0, 0, 0);
+}
+
 // The 16 scores of a result to c tanh(s / c).  float32: the library's
 // tanhf, for its relative accuracy near 0.  16-bit types, whose weights keep
 // 2^-9 at best: 1 - 2 / (1 + e^2x), within 2e-7; and where no score of the

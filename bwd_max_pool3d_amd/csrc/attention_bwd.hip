@@ -27,6 +27,7 @@ namespace {
 
 constexpr int kBwdWaves = kAttnRows / 32;
 constexpr int kStep = 32;                  // keys (dq) or queries (dk, dv) per step
+constexpr int kPos = kStep + 2;            // places of a step's positions on one axis (16 bytes)
 constexpr float kInf = __builtin_huge_valf();
 
 // ------------------------------------------------------------ constants
@@ -62,7 +63,7 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a)
         const int64_t at = bh * a.Tq + i;
         const float l = a.lse[at];
         // a row without weights: its exponents become -inf
-        *(float2 *)(a.rowd + 2 * at) = make_float2(l == kNegInf ? kInf : l * kLog2e, s);
+        *(float2 *)(a.rowd + 2 * at) = make_float2(l == kNegInf ? kInf : l * kLog2e, -s);
     }
     if (h == 0) {
         // this workgroup's share of the positions
@@ -72,9 +73,10 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a)
             const int32_t *pk = a.pos_k + row * a.Tk, *pq = a.pos_q + row * a.Tq;
             const int64_t base = a.Tk > 0 ? pk[0] : 0;
             for (int k = qt * per_k + threadIdx.x; k < min((qt + 1) * per_k, a.Tk); k += 256)
-                a.fpos_k[row * a.Tk + k] = (float)(pk[k] - base);
+                ((u32x2 *)a.parts_k)[row * a.Tk + k] = position_parts((float)(pk[k] - base));
             const int k = qt * per_q + threadIdx.x;
-            if (threadIdx.x < per_q && k < a.Tq) a.fpos_q[row * a.Tq + k] = (float)(pq[k] - base);
+            if (threadIdx.x < per_q && k < a.Tq)
+                ((u32x2 *)a.parts_q)[row * a.Tq + k] = position_parts((float)(pq[k] - base));
         }
     }
     if (h == 0 && threadIdx.x < 64) {
@@ -113,8 +115,9 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
     extern __shared__ __align__(16) unsigned char smem[];
     constexpr int TS = KB * DP;                            // elements of a tile
     R *const kt = (R *)smem;                               // [kStages][K tile, V tile]
-    float *const pk = (float *)(kt + kStages * 2 * TS);    // [kStages][3][KB] key positions
-    int *const bad = (int *)(pk + kStages * 3 * KB);       // [kStages][KB] 1 + last step whose key
+    // [kStages][3][KB keys' positions, and ones]
+    u32x2 *const pk = (u32x2 *)(kt + kStages * 2 * TS);
+    int *const bad = (int *)(pk + kStages * 3 * kPos);     // [kStages][KB] 1 + last step whose key
                                                            // held an infinity or a NaN
     int *const flag = bad + kStages * KB;                  // there was one
     int *const ends = flag + 1;                            // [4][NW]
@@ -140,6 +143,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
         ends[3 * NW + wave] = ahi;
     }
     if (tid < kStages * KB) bad[tid] = 0;
+    if (axes > 0 && tid < kStages * 3) pk[tid * kPos + KB] = u32x2{kOnes[0], kOnes[1]};
     if (tid == 0) *flag = 0;
     __syncthreads();
     int glo = ends[0], ghi = ends[NW], galo = ends[2 * NW], gahi = ends[3 * NW];
@@ -168,17 +172,17 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
     }
     const float2 rd = *(const float2 *)(a.rowd + 2 * ((int64_t)bh * a.Tq + ic));
     const Scores sc = scores(a);
-    float pq[3], sl[3];
+    u32x2 pq[3];
+    float sl[3];
 #pragma unroll
     for (int x = 0; x < 3; ++x) {
         if (x >= axes) break;
-        pq[x] = a.fpos_q[((int64_t)x * a.B + b) * a.Tq + ic];
+        pq[x] = position_cols(((const u32x2 *)a.parts_q)[((int64_t)x * a.B + b) * a.Tq + ic], half);
         sl[x] = a.slopes[h * axes + x] * sc.slope;
-        arrived(pq[x]);
         arrived(sl[x]);
     }
 
-    float lse2 = rd.x, delta = rd.y;
+    float lse2 = rd.x, delta = rd.y;       // (delta negated)
     arrived(qf);
     arrived(gf);
     arrived(lse2);
@@ -209,9 +213,10 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
             kd.load_edge(kp, a.ks[1], k0, glo, ghi, at);
             vd.load_edge(vp, a.vs[1], k0, glo, ghi, at + TS * (int)sizeof(R));
         }
-        if (wave < axes && lane < KB)
-            direct4(a.fpos_k + ((int64_t)wave * a.B + b) * a.Tk + k0,
-                    (uint32_t)min(lane, a.Tk - 1 - k0) * 4, lds_pk + (st * 3 + wave) * KB * 4);
+        if (wave < axes)
+            direct4(a.parts_k + 2 * (((int64_t)wave * a.B + b) * a.Tk + k0),
+                    (uint32_t)(2 * min(lane >> 1, a.Tk - 1 - k0) + (lane & 1)) * 4,
+                    lds_pk + (st * 3 + wave) * kPos * 8);
     };
     // Hands stage n over: `later` stages may still be on their way.
     constexpr int kLater = (kStages - 2) * 2 * TileDirect<T, DP, KB, NT>::LOADS;
@@ -251,7 +256,9 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
                 kr[c] = row_frag<T, DP>(kb, col, c * 16 + half * 8);
                 vr[c] = row_frag<T, DP>(vb, col, c * 16 + half * 8);
             }
-            f32x16 s = f32x16(0.f), dp = f32x16(0.f);
+            // (16 registers of delta, where they are there)
+            constexpr bool kept = DP * sizeof(R) <= 128;
+            f32x16 s = f32x16(0.f), dp = f32x16(kept ? delta : 0.f);
 #pragma unroll
             for (int c = 0; c < NC; ++c) s = mma<T>(kr[c], qf[c], s);
 #pragma unroll
@@ -264,9 +271,11 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
             products_and_reads<T, NC, 1>();
             products_and_reads<T, NC, 2>();
             issued<T>();
+            if constexpr (!kept) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) dp[r] -= delta;
-            if (GEN && sc.multiply) s *= sc.scale;
+                for (int r = 0; r < 16; ++r) dp[r] += delta;
+            }
+            if (GEN) multiply_scores(s, sc);
             if (GEN && a.cap > 0.f) {
                 cap_scores<T>(s, sc);
                 const float f2 = -sc.per_cap * sc.per_cap;
@@ -277,9 +286,10 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
 #pragma unroll
                 for (int x = 0; x < 3; ++x) {
                     if (x >= axes) break;
-                    const f32x16 p = acc_rows(pk + (st * 3 + x) * KB, half);
+                    const f32x16 p =
+                        differences(pk + (st * 3 + x) * kPos + (half ? KB : col), pq[x]);
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) s[r] = fmaf(-sl[x], fabsf(p[r] - pq[x]), s[r]);
+                    for (int r = 0; r < 16; ++r) s[r] = fmaf(-sl[x], fabsf(p[r]), s[r]);
                 }
             }
             const bool part = !(alo <= k0 && k0 + KB <= ahi);
@@ -323,8 +333,9 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
     extern __shared__ __align__(16) unsigned char smem[];
     constexpr int TS = QB * DP;                            // elements of a tile
     R *const qt = (R *)smem;                               // [kStages][Q tile, dO tile]
-    float *const pq = (float *)(qt + kStages * 2 * TS);    // [kStages][3][QB] positions
-    float *const rc = pq + kStages * 3 * QB;               // [kStages][QB][2] lse * log2 e, delta
+    // [kStages][3][QB queries' positions, and ones]
+    u32x2 *const pq = (u32x2 *)(qt + kStages * 2 * TS);
+    float *const rc = (float *)(pq + kStages * 3 * kPos);  // [kStages][2][QB] lse * log2 e, -delta
     int *const sp = (int *)(rc + kStages * 2 * QB);        // [kStages][QB][2] spans of keys
     int *const flag = sp + kStages * 2 * QB;               // an infinity or a NaN was dropped
     int *const ends = flag + 1;                            // [2] first and last tile
@@ -347,6 +358,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
     // the tiles of queries that see a key of this block
     if (tid == 0) *flag = 0;
     if (tid < 2) ends[tid] = tid ? -1 : nt;
+    if (axes > 0 && tid < kStages * 3) pq[tid * kPos + QB] = u32x2{kOnes[0], kOnes[1]};
     __syncthreads();
     {
         int first = nt, last = -1;
@@ -374,12 +386,11 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
         kf[c] = load8<T>(kp, c * 16 + half * 8, a.D, a.vec);
         vf[c] = load8<T>(vp, c * 16 + half * 8, a.D, a.vec);
     }
-    float pk[3];
+    u32x2 pk[3];
 #pragma unroll
     for (int x = 0; x < 3; ++x) {
         if (x >= axes) break;
-        pk[x] = a.fpos_k[((int64_t)x * a.B + b) * a.Tk + kc];
-        arrived(pk[x]);
+        pk[x] = position_cols(((const u32x2 *)a.parts_k)[((int64_t)x * a.B + b) * a.Tk + kc], half);
     }
     const Scores sc = scores(a);
     arrived(kf);
@@ -416,14 +427,14 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
         }
         // two values for each of 32 queries (the last query's for those past it)
         const uint32_t two = (uint32_t)(2 * min(lane >> 1, a.Tq - 1 - q0) + (lane & 1)) * 4;
-        if (wave == 0)
-            direct4(a.rowd + 2 * (((int64_t)b * a.Hq + h) * a.Tq + q0), two,
-                    lds_rc + st * 2 * QB * 4);
+        if (wave == 0)                     // (parted on the way)
+            direct4(a.rowd + 2 * (((int64_t)b * a.Hq + h) * a.Tq + q0),
+                    (uint32_t)(2 * min(col, a.Tq - 1 - q0) + half) * 4, lds_rc + st * 2 * QB * 4);
         if (wave == 1)
             direct4(a.spans + 2 * ((int64_t)b * a.Tq + q0), two, lds_sp + st * 2 * QB * 4);
-        if (wave < axes && lane < QB)
-            direct4(a.fpos_q + ((int64_t)wave * a.B + b) * a.Tq + q0,
-                    (uint32_t)min(lane, a.Tq - 1 - q0) * 4, lds_pq + (st * 3 + wave) * QB * 4);
+        if (wave < axes)
+            direct4(a.parts_q + 2 * (((int64_t)wave * a.B + b) * a.Tq + q0), two,
+                    lds_pq + (st * 3 + wave) * kPos * 8);
         if (++ft > last) {
             ft = first;
             ++fh;
@@ -453,10 +464,8 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
         }
         if (edge) {                        // past the last query: no weight, no keys
             const int i = opaque(lane);
-            if (q0 + (i >> 1) >= a.Tq) {
-                if (wave == 0) rc[st * 2 * QB + i] = i & 1 ? 0.f : kInf;
-                if (wave == 1) sp[st * 2 * QB + i] = 0;
-            }
+            if (wave == 0 && q0 + (i & 31) >= a.Tq) rc[st * 2 * QB + i] = i < QB ? kInf : 0.f;
+            if (wave == 1 && q0 + (i >> 1) >= a.Tq) sp[st * 2 * QB + i] = 0;
         }
         hand_over();
     };
@@ -488,13 +497,12 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
                 qr[c] = row_frag<T, DP>(qb, col, c * 16 + half * 8);
                 gr[c] = row_frag<T, DP>(gb, col, c * 16 + half * 8);
             }
-            f32x16 s = f32x16(0.f), dp = f32x16(0.f);
+            f32x16 s = f32x16(0.f), dp = acc_rows(rc + (st * 2 + 1) * QB, half);
 #pragma unroll
             for (int c = 0; c < NC; ++c) s = mma<T>(qr[c], kf[c], s);
 #pragma unroll
             for (int c = 0; c < NC; ++c) dp = mma<T>(gr[c], vf[c], dp);
-            f32x16 lr, dr;
-            acc_pairs(rc + st * 2 * QB, half, &lr, &dr);
+            const f32x16 lr = acc_rows(rc + st * 2 * QB, half);
 #pragma unroll
             for (int d = 0; d < ND; ++d)
 #pragma unroll
@@ -505,9 +513,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
             products_and_reads<T, NC, 1>();
             products_and_reads<T, NC, 2 + 8 / NC>();
             issued<T>();
-#pragma unroll
-            for (int r = 0; r < 16; ++r) dp[r] -= dr[r];
-            if (GEN && sc.multiply) s *= sc.scale;
+            if (GEN) multiply_scores(s, sc);
             if (GEN && a.cap > 0.f) {
                 cap_scores<T>(s, sc);
                 const float f2 = -sc.per_cap * sc.per_cap;
@@ -518,9 +524,10 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
 #pragma unroll
                 for (int x = 0; x < 3; ++x) {
                     if (x >= axes) break;
-                    const f32x16 p = acc_rows(pq + (st * 3 + x) * QB, half);
+                    const f32x16 p =
+                        differences(pq + (st * 3 + x) * kPos + (half ? QB : col), pk[x]);
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) s[r] = fmaf(-sl[x], fabsf(p[r] - pk[x]), s[r]);
+                    for (int r = 0; r < 16; ++r) s[r] = fmaf(-sl[x], fabsf(p[r]), s[r]);
                 }
             }
 #pragma unroll
@@ -620,7 +627,7 @@ void run(const AttnArgs &a, hipStream_t s)
     const int64_t nk = (a.Tk + 32 * NW - 1) / (32 * NW);
     if (nk > 0)
         launch_kernel((attn_dkv_kernel<T, DP, GEN>), dim3((uint32_t)(nk * a.B * a.Hk * a.gsplit)),
-                      dim3(64 * NW), tiles + kStages * 7 * kStep * 4 + 3 * 4, s, a);
+                      dim3(64 * NW), tiles + kStages * (3 * kPos * 8 + 4 * kStep * 4) + 3 * 4, s, a);
     if (nk > 0 && a.gsplit > 1) {
         const int64_t need = ((int64_t)a.B * a.Tk * a.Hk * a.D + 255) / 256;
         launch_kernel((attn_parts_kernel<T>),
@@ -629,7 +636,7 @@ void run(const AttnArgs &a, hipStream_t s)
     }
     if (nq > 0)
         launch_kernel((attn_dq_kernel<T, DP, GEN>), dim3((uint32_t)(nq * a.B * a.Hq)),
-                      dim3(64 * NW), tiles + kStages * 4 * kStep * 4 + (1 + 4 * NW) * 4, s, a);
+                      dim3(64 * NW), tiles + kStages * (3 * kPos * 8 + kStep * 4) + (1 + 4 * NW) * 4, s, a);
 }
 
 int64_t round16(int64_t bytes) { return (bytes + 15) & ~(int64_t)15; }
@@ -647,8 +654,8 @@ size_t plan_attn_backward(AttnArgs *a)
     const int64_t nt = (a->Tq + 31) / 32, rows = (int64_t)a->B * a->Tq;
     int64_t n = round16(rows * a->Hq * 8) + round16(rows * 8) + (int64_t)a->B * nt * 16 +
                 attn_order_bytes(*a, false) + attn_order_bytes(*a, true) +
-                round16((int64_t)a->axes * rows * 4) +
-                round16((int64_t)a->axes * a->B * a->Tk * 4);
+                round16((int64_t)a->axes * rows * 8) +
+                round16((int64_t)a->axes * a->B * a->Tk * 8);
     if (a->gsplit > 1)
         n += 2 * round16((int64_t)a->gsplit * a->B * a->Tk * a->Hk * a->D * 4);
     return (size_t)n;
@@ -669,10 +676,10 @@ void place_attn_backward(AttnArgs *a, void *workspace)
     p += oq;
     a->order_k = ok ? (int32_t *)p : nullptr;
     p += ok;
-    a->fpos_q = (float *)p;
-    p += round16((int64_t)a->axes * rows * 4);
-    a->fpos_k = (float *)p;
-    p += round16((int64_t)a->axes * a->B * a->Tk * 4);
+    a->parts_q = (uint32_t *)p;
+    p += round16((int64_t)a->axes * rows * 8);
+    a->parts_k = (uint32_t *)p;
+    p += round16((int64_t)a->axes * a->B * a->Tk * 8);
     a->part_dk = (float *)p;
     p += round16((int64_t)a->gsplit * a->B * a->Tk * a->Hk * a->D * 4);
     a->part_dv = (float *)p;

@@ -23,6 +23,7 @@ namespace {
 
 constexpr int kFwdWaves = kAttnRows / 32;
 constexpr int kFwdKeys = 64;
+constexpr int kFwdPos = kFwdKeys + 33;     // places of a tile's positions on one axis
 constexpr float kRaise = 8.f;
 
 // float32 tiles of 128 channels take twice the LDS and the registers: one
@@ -42,8 +43,9 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
     extern __shared__ __align__(16) unsigned char smem[];
     R *const kt = (R *)smem;                               // [2][KB * DP]
     R *const vt = kt + 2 * KB * DP;                        // [2][KB * DP]
-    float *const pk = (float *)(vt + 2 * KB * DP);         // [2][3][KB] key positions
-    int *const flag = (int *)(pk + 2 * 3 * KB);            // an infinity or a NaN was dropped
+    // [2][3][KB keys' positions, and ones 32 apart]
+    u32x2 *const pk = (u32x2 *)(vt + 2 * KB * DP);
+    int *const flag = (int *)(pk + 2 * 3 * kFwdPos);       // an infinity or a NaN was dropped
     int *const ends = flag + 1;                            // [4][NW]
 
     const int nq = (a.Tq + 32 * NW - 1) / (32 * NW);
@@ -77,9 +79,10 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
         ends[3 * NW + wave] = ahi;
     }
     if (tid == 0) *flag = 0;
+    if (axes > 0 && tid < 2 * 3 * 2)
+        pk[(tid >> 1) * kFwdPos + KB + (tid & 1) * 32] = u32x2{kOnes[0], kOnes[1]};
     __syncthreads();
-    int glo = ends[0], ghi = ends[NW], galo = ends[2 * NW],
-        gahi = ends[3 * NW];
+    int glo = ends[0], ghi = ends[NW], galo = ends[2 * NW], gahi = ends[3 * NW];
 #pragma unroll
     for (int w = 1; w < NW; ++w) {
         glo = min(glo, ends[w]);
@@ -103,16 +106,16 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
     // positions relative to the workgroup's first query: differences of
     // tokens near each other stay exact in binary32
     const Scores sc = scores(a);
-    float pq[3], sl[3];
+    u32x2 pq[3];
+    float sl[3];
     int64_t base[3];
 #pragma unroll
     for (int x = 0; x < 3; ++x) {
         if (x >= axes) break;
         const int32_t *p = a.pos_q + ((int64_t)x * a.B + b) * a.Tq;
         base[x] = p[q0];
-        pq[x] = (float)(p[ic] - base[x]);
+        pq[x] = position_cols(position_parts((float)(p[ic] - base[x])), half);
         sl[x] = a.slopes[h * axes + x] * sc.slope;
-        arrived(pq[x]);
         arrived(sl[x]);
     }
 
@@ -170,7 +173,8 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
         }
 #pragma unroll
         for (int x = 0; x < 3; ++x)
-            if (x < axes && tid < KB) pk[(buf * 3 + x) * KB + tid] = (float)(pr[x] - base[x]);
+            if (x < axes && tid < KB)
+                pk[(buf * 3 + x) * kFwdPos + tid] = position_parts((float)(pr[x] - base[x]));
         hand_over();
     };
     if (kbeg < kend) {
@@ -204,9 +208,9 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
         products_and_reads<T, NC, 1>();
         products_and_reads<T, NC, 2>();
         issued<T>();
-        if (GEN && sc.multiply) {
-            s[0] *= sc.scale;
-            s[1] *= sc.scale;
+        if (GEN) {
+            multiply_scores(s[0], sc);
+            multiply_scores(s[1], sc);
         }
         if (GEN && a.cap > 0.f) {
 #pragma unroll
@@ -218,10 +222,10 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
 #pragma unroll
                 for (int x = 0; x < 3; ++x) {
                     if (x >= axes) break;
-                    const f32x16 p = acc_rows(pk + (buf * 3 + x) * KB + u * 32, half);
+                    const f32x16 p = differences(
+                        pk + (buf * 3 + x) * kFwdPos + u * 32 + (half ? KB : col), pq[x]);
 #pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        s[u][r] = fmaf(-sl[x], fabsf(p[r] - pq[x]), s[u][r]);
+                    for (int r = 0; r < 16; ++r) s[u][r] = fmaf(-sl[x], fabsf(p[r]), s[u][r]);
                 }
             }
         }
@@ -310,7 +314,7 @@ hipError_t run(const AttnArgs &a, hipStream_t s)
 {
     constexpr int NW = kFwdWaves;
     constexpr uint32_t lds = 4 * kFwdKeys * DP * sizeof(typename T::raw) +
-                             2 * 3 * kFwdKeys * sizeof(float) + (1 + 4 * NW) * sizeof(int);
+                             2 * 3 * kFwdPos * sizeof(u32x2) + (1 + 4 * NW) * sizeof(int);
     const int64_t nq = (a.Tq + 32 * NW - 1) / (32 * NW);
     launch_attn_order(a, false, s);
     launch_kernel((attn_fwd_kernel<T, DP, GEN>), dim3((uint32_t)(nq * a.B * a.Hq)),

@@ -178,7 +178,7 @@ void attn_split_kernel(AttnArgs a)
             reads_done();
             if (more) fetch(vd, vp, a.vs[1], k0 + NW * KB, lds_v);
 
-            if (GEN && sc.multiply) s *= sc.scale;
+            if (GEN) multiply_scores(s, sc);
             if (GEN && a.cap > 0.f) cap_scores<T>(s, sc);
 #pragma unroll
             for (int x = 0; x < 3; ++x) {

@@ -94,12 +94,12 @@ struct AttnArgs {
     float *part_ml;            // (nsplit, B, Hk, Tq * G, 2) maximum and sum
     // backward: a key head's query heads in gsplit parts
     int32_t gsplit;
-    float *rowd;               // (B, Hq, Tq, 2): lse * log2 e, and delta
+    float *rowd;               // (B, Hq, Tq, 2): lse * log2 e, and -delta
     int32_t *spans;            // (B, Tq, 2): the keys [lo, hi) of each query
     int32_t *tiles;            // (B, ceil(Tq / 32), 4): over 32 queries, the union of
                                // their keys [lo, hi) and the keys all of them see
-    float *fpos_q, *fpos_k;    // (axes, B, Tq) and (axes, B, Tk): positions from that of
-                               // the sequence's first key
+    uint32_t *parts_q, *parts_k;  // (axes, B, Tq, 2) and (axes, B, Tk, 2): positions from that
+                                  // of the sequence's first key, in parts of 8 bits
     float *part_dk, *part_dv;  // (gsplit, B, Tk, Hk, D), when gsplit > 1
 };
 // Scores with a cap, a bias or a factor that is not positive: kernels of
