@@ -521,12 +521,14 @@ struct TileDirect {
     static constexpr int LOADS = N;
 };
 
-// --- stages: kStages tiles in LDS, filled kStages - 1 steps ahead, so that a
-// step waits for loads that are that many steps old.  A wave's loads return
-// in order: when no more are outstanding than it issued for the later
-// stages, the next stage is there.  (Its own waits, and a barrier that adds
-// none: __syncthreads would wait for every load.)
-constexpr int kStages = 4;
+// --- stages: LDS holds several tiles, filled all but two steps ahead of
+// their use.  Steps go in pairs, with one wait and one barrier a pair.  A
+// wave's loads return in order: when no more are outstanding than it issued
+// for the later steps, the next pair is there.  (Its own waits, and a barrier
+// that adds none: __syncthreads would wait for every load.)  Six stages, or
+// four where six would not leave room for a second workgroup.
+template <typename T, int DP>
+constexpr int stages() { return sizeof(typename T::raw) * DP <= 128 ? 6 : 4; }
 
 template <int OUTSTANDING>
 __device__ __forceinline__ void wait_loads(bool later)
@@ -550,6 +552,11 @@ __device__ __forceinline__ void reads_done() { asm volatile("s_waitcnt lgkmcnt(0
 
 // A value that is the same in every lane, as a scalar.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// A value in a vector or a scalar register that has been loaded, here and
+// not where it is used (see arrived).
+__device__ __forceinline__ void arrived(int &v) { asm volatile("" : "+v"(v)); }
+__device__ __forceinline__ void arrived_scalar(float &v) { asm volatile("" : "+s"(v)); }
 
 // A value that is the same in every lane, read through the scalar cache (a
 // vector load would have to wait for the stages before it).

@@ -28,6 +28,7 @@ namespace {
 constexpr int kBwdWaves = kAttnRows / 32;
 constexpr int kStep = 32;                  // keys (dq) or queries (dk, dv) per step
 constexpr int kPos = kStep + 2;            // places of a step's positions on one axis (16 bytes)
+constexpr int kSmall = 16 * kStep + 3 * 8 * kPos;      // bytes of a step's constants, spans, positions
 constexpr float kInf = __builtin_huge_valf();
 
 // ------------------------------------------------------------ constants
@@ -111,6 +112,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
 {
     using R = typename T::raw;
     const int axes = GEN ? a.axes : 0;
+    constexpr int kStages = stages<T, DP>();
     constexpr int NW = kBwdWaves, NT = 64 * NW, KB = kStep, NC = DP / 16, ND = DP / 32;
     extern __shared__ __align__(16) unsigned char smem[];
     constexpr int TS = KB * DP;                            // elements of a tile
@@ -201,28 +203,35 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
         for (int x = tid; x < kStages * 2 * TS * (int)sizeof(R) / 16; x += NT)
             ((u32x4 *)kt)[x] = u32x4{0u, 0u, 0u, 0u};
     __syncthreads();
-    const uint32_t lds = lds_address(smem) + wave * 1024, lds_pk = lds_address(pk);
     const bool whole = usable && a.D == DP;
-    auto fetch = [&](int n) {
-        const int k0 = kbeg + n * KB, st = n % kStages;
-        const uint32_t at = lds + st * 2 * TS * (int)sizeof(R);
+    // the next fetch: its step, its stage and where it reads
+    const uint32_t lds = lds_address(smem) + wave * 1024,
+                   lds_pk = lds_address(pk) + wave * kPos * 8;
+    int fn = 0, fst = 0;
+    const R *fk = kp + (int64_t)kbeg * a.ks[1], *fv = vp + (int64_t)kbeg * a.vs[1];
+    const uint32_t *fpos =
+        wave < axes ? a.parts_k + 2 * (((int64_t)wave * a.B + b) * a.Tk + kbeg) : nullptr;
+    auto fetch = [&]() {
+        const int k0 = kbeg + fn * KB;
+        const uint32_t at = lds + fst * 2 * TS * (int)sizeof(R);
         if (whole && glo <= k0 && k0 + KB <= ghi) {
-            kd.load(kp + k0 * a.ks[1], at);
-            vd.load(vp + k0 * a.vs[1], at + TS * (int)sizeof(R));
+            kd.load(fk, at);
+            vd.load(fv, at + TS * (int)sizeof(R));
         } else if (usable) {
             kd.load_edge(kp, a.ks[1], k0, glo, ghi, at);
             vd.load_edge(vp, a.vs[1], k0, glo, ghi, at + TS * (int)sizeof(R));
         }
         if (wave < axes)
-            direct4(a.parts_k + 2 * (((int64_t)wave * a.B + b) * a.Tk + k0),
-                    (uint32_t)(2 * min(lane >> 1, a.Tk - 1 - k0) + (lane & 1)) * 4,
-                    lds_pk + (st * 3 + wave) * kPos * 8);
+            direct4(fpos, (uint32_t)(2 * min(lane >> 1, a.Tk - 1 - k0) + (lane & 1)) * 4,
+                    lds_pk + fst * 3 * kPos * 8);
+        ++fn;
+        fst = fst + 1 < kStages ? fst + 1 : 0;
+        fk += KB * a.ks[1];
+        fv += KB * a.vs[1];
+        fpos += 2 * KB;
     };
-    // Hands stage n over: `later` stages may still be on their way.
-    constexpr int kLater = (kStages - 2) * 2 * TileDirect<T, DP, KB, NT>::LOADS;
-    auto arrive = [&](int n, bool later) {
-        wait_loads<kLater>(later && usable);
-        const int k0 = kbeg + n * KB, st = n % kStages;
+    auto clean = [&](int n, int st) {
+        const int k0 = kbeg + n * KB;
         const bool edge = k0 < glo || k0 + KB > ghi;
         const bool drop = !(galo <= k0 && k0 + KB <= gahi);
         R *const ks = kt + st * 2 * TS;
@@ -239,15 +248,23 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
             if (kd.scrub(ks, k0, glo, ghi, drop, bad + st * KB, n + 1)) *flag = 1;
             if (edge) vd.scrub(ks + TS, k0, glo, ghi, false, nullptr, 0);
         }
+    };
+    // Hands steps n and n + 1 over, which are in stages st and st + 1.
+    constexpr int kLater = (kStages - 4) * 2 * TileDirect<T, DP, KB, NT>::LOADS;
+    auto arrive = [&](int n, int st) {
+        // (all of the later loads are there to be counted only if no step is
+        // the last)
+        wait_loads<kLater>(usable && n + kStages - 2 <= steps);
+#pragma unroll 1
+        for (int u = 0; u < 2 && n + u < steps; ++u) clean(n + u, st + u);
         hand_over();
     };
-    for (int n = 0; n < kStages - 1; ++n)
-        if (n < steps) fetch(n);
-    if (steps > 0) arrive(0, steps >= kStages - 1);
-    for (int n = 0; n < steps; ++n) {
-        const int k0 = kbeg + n * KB, st = n % kStages;
-        const bool more = n + kStages - 1 < steps;
-        if (more) fetch(n + kStages - 1);
+#pragma unroll 1
+    while (fn < min(steps, kStages - 2)) fetch();
+    if (steps > 0) arrive(0, 0);
+    for (int n = 0, st = 0; n < steps; ++n) {
+        const int k0 = kbeg + n * KB;
+        if (fn < steps) fetch();
         {
             const R *kb = kt + st * 2 * TS, *vb = kb + TS;
             Frag<T> kr[NC], vr[NC], kc[ND][2];
@@ -313,7 +330,8 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
                 o[d] = mma<T>(kc[d][1], e1, o[d]);
             }
         }
-        if (n + 1 < steps) arrive(n + 1, more);
+        st = st + 1 < kStages ? st + 1 : 0;
+        if ((n & 1) && n + 1 < steps) arrive(n + 1, st);
     }
     if (i >= a.Tq) return;
     store_cols<T, ND>((R *)a.dq + (((int64_t)b * a.Tq + i) * a.Hq + h) * a.D, o, a.scale, a.D, half);
@@ -329,15 +347,18 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
 {
     using R = typename T::raw;
     const int axes = GEN ? a.axes : 0;
+    constexpr int kStages = stages<T, DP>();
     constexpr int NW = kBwdWaves, NT = 64 * NW, QB = kStep, NC = DP / 16, ND = DP / 32;
     extern __shared__ __align__(16) unsigned char smem[];
     constexpr int TS = QB * DP;                            // elements of a tile
     R *const qt = (R *)smem;                               // [kStages][Q tile, dO tile]
-    // [kStages][3][QB queries' positions, and ones]
-    u32x2 *const pq = (u32x2 *)(qt + kStages * 2 * TS);
-    float *const rc = (float *)(pq + kStages * 3 * kPos);  // [kStages][2][QB] lse * log2 e, -delta
-    int *const sp = (int *)(rc + kStages * 2 * QB);        // [kStages][QB][2] spans of keys
-    int *const flag = sp + kStages * 2 * QB;               // an infinity or a NaN was dropped
+    // [kStages] of: [2][QB] lse * log2 e and -delta, [QB][2] spans of keys,
+    // [3][QB positions, and ones]
+    unsigned char *const small = (unsigned char *)(qt + kStages * 2 * TS);
+    auto rc = [&](int st) { return (float *)(small + st * kSmall); };
+    auto sp = [&](int st) { return (int *)(small + st * kSmall + 8 * QB); };
+    auto pq = [&](int st) { return (u32x2 *)(small + st * kSmall + 16 * QB); };
+    int *const flag = (int *)(small + kStages * kSmall);   // an infinity or a NaN was dropped
     int *const ends = flag + 1;                            // [2] first and last tile
 
     const int nk = (a.Tk + 32 * NW - 1) / (32 * NW);
@@ -358,7 +379,8 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
     // the tiles of queries that see a key of this block
     if (tid == 0) *flag = 0;
     if (tid < 2) ends[tid] = tid ? -1 : nt;
-    if (axes > 0 && tid < kStages * 3) pq[tid * kPos + QB] = u32x2{kOnes[0], kOnes[1]};
+    if (axes > 0 && tid < kStages * 3)
+        pq(tid / 3)[tid % 3 * kPos + QB] = u32x2{kOnes[0], kOnes[1]};
     __syncthreads();
     {
         int first = nt, last = -1;
@@ -407,54 +429,93 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
         for (int x = tid; x < kStages * 2 * TS * (int)sizeof(R) / 16; x += NT)
             ((u32x4 *)qt)[x] = u32x4{0u, 0u, 0u, 0u};
     __syncthreads();
-    // the next fetch's head and tile of queries
-    int fh = hk * a.G + g0, ft = first;
-    const uint32_t lds = lds_address(smem) + wave * 1024, lds_rc = lds_address(rc),
-                   lds_sp = lds_address(sp), lds_pq = lds_address(pq);
     const bool whole = usable && a.D == DP;
     const R *const qbase = (const R *)a.q + b * a.qs[0], *const gbase =
         (const R *)a.dout + b * a.gs[0];
-    auto fetch = [&](int n) {
-        const int h = fh, q0 = ft * QB, st = n % kStages;
-        const uint32_t at = lds + st * 2 * TS * (int)sizeof(R);
-        const R *const q = qbase + h * a.qs[2], *const g = gbase + h * a.gs[2];
+    // The next fetch: its step, stage, head and tile, and where it reads.
+    // Each wave reads 256 bytes with the tile: the rows' constants, the spans,
+    // the positions on two axes (wave 3 those on the third too).
+    int fn = 0, fst = 0, fh = hk * a.G + g0, ft = first;
+    const uint32_t lds = lds_address(smem) + wave * 1024,
+                   lds_small = lds_address(small) +
+                               (wave < 2 ? wave * 8 * QB : 16 * QB + (wave - 2) * kPos * 8);
+    const R *fq, *fg;
+    const char *fs;
+    auto rewind = [&]() {                  // to tile ft of head fh
+        const int64_t at = (int64_t)ft * QB;
+        fq = qbase + fh * a.qs[2] + at * a.qs[1];
+        fg = gbase + fh * a.gs[2] + at * a.gs[1];
+        if (wave == 0) fs = (const char *)(a.rowd + 2 * (((int64_t)b * a.Hq + fh) * a.Tq + at));
+        else if (wave == 1) fs = (const char *)(a.spans + 2 * ((int64_t)b * a.Tq + at));
+        else fs = (const char *)(a.parts_q + 2 * (((int64_t)(wave - 2) * a.B + b) * a.Tq + at));
+    };
+    rewind();
+    const uint32_t pair_of = lane * 4, parted = (2 * col + half) * 4;
+    const uint32_t mine = wave == 0 ? parted : pair_of;    // (constants are parted on the way)
+    const int64_t third = (int64_t)a.B * a.Tq * 8;
+    auto fetch = [&]() {
+        const int q0 = ft * QB;
+        const uint32_t at = lds + fst * 2 * TS * (int)sizeof(R), as = lds_small + fst * kSmall;
+        uint32_t off = mine;
         if (whole && q0 + QB <= a.Tq) {
-            qd.load(q + q0 * a.qs[1], at);
-            gd.load(g + q0 * a.gs[1], at + TS * (int)sizeof(R));
-        } else if (usable) {
-            qd.load_edge(q, a.qs[1], q0, 0, a.Tq, at);
-            gd.load_edge(g, a.gs[1], q0, 0, a.Tq, at + TS * (int)sizeof(R));
+            qd.load(fq, at);
+            gd.load(fg, at + TS * (int)sizeof(R));
+        } else {
+            if (usable) {
+                qd.load_edge(qbase + fh * a.qs[2], a.qs[1], q0, 0, a.Tq, at);
+                gd.load_edge(gbase + fh * a.gs[2], a.gs[1], q0, 0, a.Tq, at + TS * (int)sizeof(R));
+            }
+            // (the last query's for those past it)
+            off = min(mine, (uint32_t)(a.Tq - 1 - q0) * 8 + (mine & 4));
         }
-        // two values for each of 32 queries (the last query's for those past it)
-        const uint32_t two = (uint32_t)(2 * min(lane >> 1, a.Tq - 1 - q0) + (lane & 1)) * 4;
-        if (wave == 0)                     // (parted on the way)
-            direct4(a.rowd + 2 * (((int64_t)b * a.Hq + h) * a.Tq + q0),
-                    (uint32_t)(2 * min(col, a.Tq - 1 - q0) + half) * 4, lds_rc + st * 2 * QB * 4);
-        if (wave == 1)
-            direct4(a.spans + 2 * ((int64_t)b * a.Tq + q0), two, lds_sp + st * 2 * QB * 4);
-        if (wave < axes)
-            direct4(a.parts_q + 2 * (((int64_t)wave * a.B + b) * a.Tq + q0), two,
-                    lds_pq + (st * 3 + wave) * kPos * 8);
+        if (wave < 2 + min(axes, 2)) direct4(fs, off, as);
+        if (wave == 3 && axes == 3) direct4(fs + third, off, as + kPos * 8);
+        ++fn;
+        fst = fst + 1 < kStages ? fst + 1 : 0;
         if (++ft > last) {
             ft = first;
             ++fh;
+            rewind();
+        } else {
+            fq += QB * a.qs[1];
+            fg += QB * a.gs[1];
+            fs += 8 * QB;
         }
     };
-    // Hands stage n (tile t of head h, whose keys are u) over.
-    constexpr int kLater = (kStages - 2) * 2 * TileDirect<T, DP, QB, NT>::LOADS;
-    auto arrive = [&](int n, int h, int t32, const i32x4 &u, bool later) {
-        wait_loads<kLater>(later && usable);
-        const int q0 = t32 * QB, st = n % kStages;
-        const bool edge = q0 + QB > a.Tq, drop = !(u.z <= k0 && k0 + 32 * NW <= u.w);
+    // What the 32 queries of a tile see together, for 64 tiles in the lanes.
+    int all_lo = 0, all_hi = 0, have = 0x7fffffff;
+    auto seen_by_all = [&](int t, int *lo, int *hi) {
+        if (t < have || t >= have + 64) {
+            have = t;
+            const int2 u = *(const int2 *)(tiles + 4 * (int64_t)min(t + lane, nt - 1) + 2);
+            all_lo = u.x;
+            all_hi = u.y;
+            arrived(all_lo);
+            arrived(all_hi);
+        }
+        *lo = __builtin_amdgcn_readlane(all_lo, t - have);
+        *hi = __builtin_amdgcn_readlane(all_hi, t - have);
+    };
+    struct Step {
+        int h, t;                          // head and tile
+        int lo, hi;                        // the keys that all of its queries see
+    };
+    auto following = [&](Step x) {
+        Step y = {x.t < last ? x.h : x.h + 1, x.t < last ? x.t + 1 : first, 0, 0};
+        seen_by_all(y.t, &y.lo, &y.hi);
+        return y;
+    };
+    auto clean = [&](const Step &x, int st) {
+        const int q0 = x.t * QB;
+        const bool edge = q0 + QB > a.Tq, drop = !(x.lo <= k0 && k0 + 32 * NW <= x.hi);
         R *const qs = qt + st * 2 * TS;
         if (!usable) {
             const int t = opaque(threadIdx.x);
             TileRegs<T, DP, QB, NT> r;
-            r.load((const R *)a.q + b * a.qs[0] + h * a.qs[2], a.qs[1], q0, 0, a.Tq, a.D, a.vec, t);
+            r.load(qbase + x.h * a.qs[2], a.qs[1], q0, 0, a.Tq, a.D, a.vec, t);
             if (drop && r.drop()) *flag = 1;
             r.store(qs, t);
-            r.load((const R *)a.dout + b * a.gs[0] + h * a.gs[2], a.gs[1], q0, 0, a.Tq, a.D, a.vec,
-                   t);
+            r.load(gbase + x.h * a.gs[2], a.gs[1], q0, 0, a.Tq, a.D, a.vec, t);
             if (drop && r.drop()) *flag = 1;
             r.store(qs + TS, t);
             wait_all();
@@ -464,45 +525,57 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
         }
         if (edge) {                        // past the last query: no weight, no keys
             const int i = opaque(lane);
-            if (wave == 0 && q0 + (i & 31) >= a.Tq) rc[st * 2 * QB + i] = i < QB ? kInf : 0.f;
-            if (wave == 1 && q0 + (i >> 1) >= a.Tq) sp[st * 2 * QB + i] = 0;
+            if (wave == 0 && q0 + (i & 31) >= a.Tq) rc(st)[i] = i < QB ? kInf : 0.f;
+            if (wave == 1 && q0 + (i >> 1) >= a.Tq) sp(st)[i] = 0;
+        }
+    };
+    // Hands steps n (x) and n + 1 over, which are in stages st and st + 1.
+    constexpr int kLater = (kStages - 4) * 2 * TileDirect<T, DP, QB, NT>::LOADS;
+    auto arrive = [&](int n, int st, Step x) {
+        // (all of the later loads are there to be counted only if no step is
+        // the last)
+        wait_loads<kLater>(usable && n + kStages - 2 <= steps);
+#pragma unroll 1
+        for (int u = 0; u < 2 && n + u < steps; ++u) {
+            clean(x, st + u);
+            x = following(x);
         }
         hand_over();
     };
-    for (int n = 0; n < kStages - 1; ++n)
-        if (n < steps) fetch(n);
-    int ch = hk * a.G + g0, ct = first;    // this step's head and tile, and its keys
-    i32x4 u = {0, 0, 0, 0};
+    float sl[3] = {0.f, 0.f, 0.f};
+    int sl_of = -1;                        // the head they are of
+#pragma unroll 1
+    while (fn < min(steps, kStages - 2)) fetch();
+    Step x = {hk * a.G + g0, first, 0, 0};
     if (steps > 0) {
-        u = uniform_load((const i32x4 *)tiles + first);
-        arrive(0, ch, ct, u, steps >= kStages - 1);
+        seen_by_all(x.t, &x.lo, &x.hi);
+        arrive(0, 0, x);
     }
-    for (int n = 0; n < steps; ++n) {
-        const int st = n % kStages;
-        const bool more = n + kStages - 1 < steps;
-        // the next step's
-        const int nt2 = ct < last ? ct + 1 : first, nh = ct < last ? ch : ch + 1;
-        const i32x4 nu = uniform_load((const i32x4 *)tiles + nt2);
-        if (more) fetch(n + kStages - 1);
-        float sl[3];
+    for (int n = 0, st = 0; n < steps; ++n) {
+        if (fn < steps) fetch();
+        if (axes > 0 && x.h != sl_of) {
+            sl_of = x.h;
 #pragma unroll
-        for (int x = 0; x < 3; ++x)
-            if (x < axes) sl[x] = uniform_load(a.slopes + ch * axes + x) * sc.slope;
+            for (int c = 0; c < 3; ++c) {
+                sl[c] = uniform_load(a.slopes + x.h * axes + min(c, axes - 1)) * sc.slope;
+                arrived(sl[c]);
+            }
+        }
         {
             const R *qb = qt + st * 2 * TS, *gb = qb + TS;
-            const bool part = !(u.z <= kw && kw + 32 <= u.w);
+            const bool part = !(x.lo <= kw && kw + 32 <= x.hi);
             Frag<T> qr[NC], gr[NC], qc[ND][2], gc[ND][2];
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 qr[c] = row_frag<T, DP>(qb, col, c * 16 + half * 8);
                 gr[c] = row_frag<T, DP>(gb, col, c * 16 + half * 8);
             }
-            f32x16 s = f32x16(0.f), dp = acc_rows(rc + (st * 2 + 1) * QB, half);
+            f32x16 s = f32x16(0.f), dp = acc_rows(rc(st) + QB, half);
 #pragma unroll
             for (int c = 0; c < NC; ++c) s = mma<T>(qr[c], kf[c], s);
 #pragma unroll
             for (int c = 0; c < NC; ++c) dp = mma<T>(gr[c], vf[c], dp);
-            const f32x16 lr = acc_rows(rc + st * 2 * QB, half);
+            const f32x16 lr = acc_rows(rc(st), half);
 #pragma unroll
             for (int d = 0; d < ND; ++d)
 #pragma unroll
@@ -522,12 +595,12 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
             }
             if (axes > 0) {
 #pragma unroll
-                for (int x = 0; x < 3; ++x) {
-                    if (x >= axes) break;
+                for (int c = 0; c < 3; ++c) {
+                    if (c >= axes) break;
                     const f32x16 p =
-                        differences(pq + (st * 3 + x) * kPos + (half ? QB : col), pk[x]);
+                        differences(pq(st) + c * kPos + (half ? QB : col), pk[c]);
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) s[r] = fmaf(-sl[x], fabsf(p[r]), s[r]);
+                    for (int r = 0; r < 16; ++r) s[r] = fmaf(-sl[c], fabsf(p[r]), s[r]);
                 }
             }
 #pragma unroll
@@ -537,7 +610,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
             }
             if (part) {
                 i32x16 lo, hi;
-                acc_pairs(sp + st * 2 * QB, half, &lo, &hi);
+                acc_pairs(sp(st), half, &lo, &hi);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     const bool see = key >= lo[r] && key < hi[r];
@@ -563,10 +636,9 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
             products_and_reads<T, 2 * ND, 0>();
             issued<T>();
         }
-        ct = nt2;
-        ch = nh;
-        u = nu;
-        if (n + 1 < steps) arrive(n + 1, ch, ct, u, more);
+        x = following(x);
+        st = st + 1 < kStages ? st + 1 : 0;
+        if ((n & 1) && n + 1 < steps) arrive(n + 1, st, x);
     }
     if (*flag) {                           // (the loop's last barrier is behind us)
         // infinities and NaN of do that were dropped, for the keys they reach
@@ -622,12 +694,13 @@ template <typename T, int DP, bool GEN>
 void run(const AttnArgs &a, hipStream_t s)
 {
     constexpr int NW = kBwdWaves;
+    constexpr int kStages = stages<T, DP>();
     constexpr uint32_t tiles = kStages * 2 * kStep * DP * sizeof(typename T::raw);
     const int64_t nq = (a.Tq + 32 * NW - 1) / (32 * NW);
     const int64_t nk = (a.Tk + 32 * NW - 1) / (32 * NW);
     if (nk > 0)
         launch_kernel((attn_dkv_kernel<T, DP, GEN>), dim3((uint32_t)(nk * a.B * a.Hk * a.gsplit)),
-                      dim3(64 * NW), tiles + kStages * (3 * kPos * 8 + 4 * kStep * 4) + 3 * 4, s, a);
+                      dim3(64 * NW), tiles + kStages * kSmall + 3 * 4, s, a);
     if (nk > 0 && a.gsplit > 1) {
         const int64_t need = ((int64_t)a.B * a.Tk * a.Hk * a.D + 255) / 256;
         launch_kernel((attn_parts_kernel<T>),
