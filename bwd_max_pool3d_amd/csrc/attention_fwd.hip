@@ -22,7 +22,7 @@ namespace mp3d {
 namespace {
 
 constexpr int kFwdWaves = kAttnRows / 32;
-constexpr int kFwdKeys = 64;
+constexpr int kFwdKeys = 64;               // one for each lane
 constexpr int kFwdPos = kFwdKeys + 33;     // places of a tile's positions on one axis
 constexpr float kRaise = 8.f;
 
@@ -108,13 +108,15 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
     const Scores sc = scores(a);
     u32x2 pq[3];
     float sl[3];
-    int64_t base[3];
+    double from = 0.;                      // of the axis of the wave's number
 #pragma unroll
     for (int x = 0; x < 3; ++x) {
         if (x >= axes) break;
         const int32_t *p = a.pos_q + ((int64_t)x * a.B + b) * a.Tq;
-        base[x] = p[q0];
-        pq[x] = position_cols(position_parts((float)(p[ic] - base[x])), half);
+        // (differences of int32 are exact in binary64)
+        const double base = uniform_load(p + q0);
+        if (wave == x) from = base;
+        pq[x] = position_cols(position_parts((float)((double)p[ic] - base)), half);
         sl[x] = a.slopes[h * axes + x] * sc.slope;
         arrived(sl[x]);
     }
@@ -135,23 +137,26 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
             ((u32x4 *)kt)[x] = u32x4{0u, 0u, 0u, 0u};
         __syncthreads();
     }
-    int32_t pr[3];                         // (not touched before place: that would wait)
+    // Positions go by way of a register, one axis a wave.  (It is not touched
+    // before place: that would wait for it)
+    const int32_t *pos = a.pos_k + ((int64_t)min(wave, 2) * a.B + b) * a.Tk;
+    int32_t pr = 0;
     const uint32_t lds = lds_address(smem) + wave * 1024;
     const bool whole = usable && a.D == DP;
+    const R *fk = kp + (int64_t)kbeg * a.ks[1], *fv = vp + (int64_t)kbeg * a.vs[1];
     auto fetch = [&](int k0, int buf) {
         const uint32_t at = lds + buf * KB * DP * (int)sizeof(R);
         constexpr uint32_t v0 = 2 * KB * DP * sizeof(R);
         if (whole && glo <= k0 && k0 + KB <= ghi) {
-            kd.load(kp + k0 * a.ks[1], at);
-            vd.load(vp + k0 * a.vs[1], at + v0);
+            kd.load(fk, at);
+            vd.load(fv, at + v0);
         } else if (usable) {
             kd.load_edge(kp, a.ks[1], k0, glo, ghi, at);
             vd.load_edge(vp, a.vs[1], k0, glo, ghi, at + v0);
         }
-#pragma unroll
-        for (int x = 0; x < 3; ++x)
-            if (x < axes && tid < KB)
-                pr[x] = a.pos_k[((int64_t)x * a.B + b) * a.Tk + min(k0 + tid, a.Tk - 1)];
+        fk += KB * a.ks[1];
+        fv += KB * a.vs[1];
+        if (wave < axes) pr = pos[min(k0 + lane, a.Tk - 1)];
     };
     auto place = [&](int k0, int buf) {
         const bool edge = k0 < glo || k0 + KB > ghi;
@@ -171,10 +176,8 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
             if (vd.scrub(vs, k0, glo, ghi, drop, nullptr, 0)) *flag = 1;
             if (edge) kd.scrub(ks, k0, glo, ghi, false, nullptr, 0);
         }
-#pragma unroll
-        for (int x = 0; x < 3; ++x)
-            if (x < axes && tid < KB)
-                pk[(buf * 3 + x) * kFwdPos + tid] = position_parts((float)(pr[x] - base[x]));
+        if (wave < axes)
+            pk[(buf * 3 + wave) * kFwdPos + lane] = position_parts((float)((double)pr - from));
         hand_over();
     };
     if (kbeg < kend) {
