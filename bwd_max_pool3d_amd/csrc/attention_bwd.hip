@@ -19,7 +19,13 @@
 //
 // p and e are rounded to the storage type for the second products, as the
 // forward's weights are.
+#include <type_traits>
+
 #include "attention.hpp"
+
+// (lambdas that two branches call are not always inlined otherwise, and
+// their values would go through memory)
+#define MP3D_INLINE __attribute__((always_inline))
 
 namespace mp3d {
 
@@ -339,16 +345,27 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
 
 // -------------------------------------------------------------- dk and dv
 
+// Where one wave cannot hold keys, values and both sums in the registers
+// that leave room for a second wave on its SIMD, two waves share 32 keys:
+// one sums dv, the other dk (and both form the scores: 5 products where 4
+// would do, but the matrix unit is not left waiting for a wave by itself).
 template <typename T, int DP>
-constexpr int dkv_occupancy() { return sizeof(typename T::raw) * DP > 128 ? 1 : 2; }
+constexpr bool dkv_pairs()
+{
+    return sizeof(typename T::raw) * DP > 128 && sizeof(typename T::raw) * DP <= 256;
+}
 
 template <typename T, int DP, bool GEN>
-__global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn_dkv_kernel(AttnArgs a)
+__global__ __launch_bounds__(64 * kBwdWaves * (dkv_pairs<T, DP>() ? 2 : 1),
+                             (sizeof(typename T::raw) * DP > 256 ? 1 : 2))
+void attn_dkv_kernel(AttnArgs a)
 {
     using R = typename T::raw;
     const int axes = GEN ? a.axes : 0;
+    constexpr bool PAIRS = dkv_pairs<T, DP>();
     constexpr int kStages = stages<T, DP>();
-    constexpr int NW = kBwdWaves, NT = 64 * NW, QB = kStep, NC = DP / 16, ND = DP / 32;
+    constexpr int NW = kBwdWaves, NT = 64 * NW * (PAIRS ? 2 : 1), QB = kStep, NC = DP / 16,
+                  ND = DP / 32;
     extern __shared__ __align__(16) unsigned char smem[];
     constexpr int TS = QB * DP;                            // elements of a tile
     R *const qt = (R *)smem;                               // [kStages][Q tile, dO tile]
@@ -371,7 +388,8 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
     const int g1 = (int)((int64_t)a.G * (gpart + 1) / a.gsplit);
     const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63, col = lane & 31,
               half = lane >> 5;
-    const int k0 = kb * 32 * NW, kw = k0 + wave * 32, key = kw + col;
+    const int k0 = kb * 32 * NW, kw = k0 + wave % NW * 32, key = kw + col;
+    const bool second = PAIRS && wave >= NW;              // sums dk
     const int kc = min(key, a.Tk - 1);
     const int nt = (a.Tq + QB - 1) / QB;
     const int32_t *tiles = a.tiles + 4 * (int64_t)b * nt;
@@ -417,7 +435,8 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
     const Scores sc = scores(a);
     arrived(kf);
     arrived(vf);
-    f32x16 dk[ND], dv[ND];
+    f32x16 dv[ND], more[PAIRS ? 1 : ND];   // (the second wave's sums are in dv too)
+    f32x16 *const dk = PAIRS ? dv : more;
 #pragma unroll
     for (int d = 0; d < ND; ++d) dk[d] = dv[d] = f32x16(0.f);
 
@@ -433,27 +452,28 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
     const R *const qbase = (const R *)a.q + b * a.qs[0], *const gbase =
         (const R *)a.dout + b * a.gs[0];
     // The next fetch: its step, stage, head and tile, and where it reads.
-    // Each wave reads 256 bytes with the tile: the rows' constants, the spans,
-    // the positions on two axes (wave 3 those on the third too).
+    // Of the first waves each reads 256 bytes with the tile: the rows'
+    // constants, the spans, the positions on two axes (wave 3 those on the
+    // third too).
     int fn = 0, fst = 0, fh = hk * a.G + g0, ft = first;
     const uint32_t lds = lds_address(smem) + wave * 1024,
                    lds_small = lds_address(small) +
-                               (wave < 2 ? wave * 8 * QB : 16 * QB + (wave - 2) * kPos * 8);
+                               (wave < 2 ? wave * 8 * QB : 16 * QB + (wave % NW - 2) * kPos * 8);
     const R *fq, *fg;
     const char *fs;
-    auto rewind = [&]() {                  // to tile ft of head fh
+    auto rewind = [&]() MP3D_INLINE {                  // to tile ft of head fh
         const int64_t at = (int64_t)ft * QB;
         fq = qbase + fh * a.qs[2] + at * a.qs[1];
         fg = gbase + fh * a.gs[2] + at * a.gs[1];
         if (wave == 0) fs = (const char *)(a.rowd + 2 * (((int64_t)b * a.Hq + fh) * a.Tq + at));
         else if (wave == 1) fs = (const char *)(a.spans + 2 * ((int64_t)b * a.Tq + at));
-        else fs = (const char *)(a.parts_q + 2 * (((int64_t)(wave - 2) * a.B + b) * a.Tq + at));
+        else fs = (const char *)(a.parts_q + 2 * (((int64_t)(wave % NW - 2) * a.B + b) * a.Tq + at));
     };
     rewind();
     const uint32_t pair_of = lane * 4, parted = (2 * col + half) * 4;
     const uint32_t mine = wave == 0 ? parted : pair_of;    // (constants are parted on the way)
     const int64_t third = (int64_t)a.B * a.Tq * 8;
-    auto fetch = [&]() {
+    auto fetch = [&]() MP3D_INLINE {
         const int q0 = ft * QB;
         const uint32_t at = lds + fst * 2 * TS * (int)sizeof(R), as = lds_small + fst * kSmall;
         uint32_t off = mine;
@@ -484,7 +504,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
     };
     // What the 32 queries of a tile see together, for 64 tiles in the lanes.
     int all_lo = 0, all_hi = 0, have = 0x7fffffff;
-    auto seen_by_all = [&](int t, int *lo, int *hi) {
+    auto seen_by_all = [&](int t, int *lo, int *hi) MP3D_INLINE {
         if (t < have || t >= have + 64) {
             have = t;
             const int2 u = *(const int2 *)(tiles + 4 * (int64_t)min(t + lane, nt - 1) + 2);
@@ -500,18 +520,20 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
         int h, t;                          // head and tile
         int lo, hi;                        // the keys that all of its queries see
     };
-    auto following = [&](Step x) {
+    auto following = [&](Step x) MP3D_INLINE {
         Step y = {x.t < last ? x.h : x.h + 1, x.t < last ? x.t + 1 : first, 0, 0};
         seen_by_all(y.t, &y.lo, &y.hi);
         return y;
     };
-    auto clean = [&](const Step &x, int st) {
+    auto clean = [&](const Step &x, int st) MP3D_INLINE {
         const int q0 = x.t * QB;
         const bool edge = q0 + QB > a.Tq, drop = !(x.lo <= k0 && k0 + 32 * NW <= x.hi);
         R *const qs = qt + st * 2 * TS;
-        if (!usable) {
+        if (!usable && second) {
+            // the other half of the workgroup does it
+        } else if (!usable) {
             const int t = opaque(threadIdx.x);
-            TileRegs<T, DP, QB, NT> r;
+            TileRegs<T, DP, QB, 64 * NW> r;
             r.load(qbase + x.h * a.qs[2], a.qs[1], q0, 0, a.Tq, a.D, a.vec, t);
             if (drop && r.drop()) *flag = 1;
             r.store(qs, t);
@@ -531,7 +553,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
     };
     // Hands steps n (x) and n + 1 over, which are in stages st and st + 1.
     constexpr int kLater = (kStages - 4) * 2 * TileDirect<T, DP, QB, NT>::LOADS;
-    auto arrive = [&](int n, int st, Step x) {
+    auto arrive = [&](int n, int st, Step x) MP3D_INLINE {
         // (all of the later loads are there to be counted only if no step is
         // the last)
         wait_loads<kLater>(usable && n + kStages - 2 <= steps);
@@ -544,103 +566,129 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
     };
     float sl[3] = {0.f, 0.f, 0.f};
     int sl_of = -1;                        // the head they are of
-#pragma unroll 1
-    while (fn < min(steps, kStages - 2)) fetch();
-    Step x = {hk * a.G + g0, first, 0, 0};
-    if (steps > 0) {
-        seen_by_all(x.t, &x.lo, &x.hi);
-        arrive(0, 0, x);
-    }
-    for (int n = 0, st = 0; n < steps; ++n) {
-        if (fn < steps) fetch();
-        if (axes > 0 && x.h != sl_of) {
-            sl_of = x.h;
+    // A step's part of dv, of dk, or of both.
+    auto sums = [&](auto want_v, auto want_k, const Step &x, int st) MP3D_INLINE {
+        constexpr bool V = decltype(want_v)::value, K = decltype(want_k)::value;
+        const R *qb = qt + st * 2 * TS, *gb = qb + TS;
+        const bool part = !(x.lo <= kw && kw + 32 <= x.hi);
+        Frag<T> qr[NC], gr[NC], qc[ND][2], gc[ND][2];
+        f32x16 s = f32x16(0.f), dp;
 #pragma unroll
-            for (int c = 0; c < 3; ++c) {
-                sl[c] = uniform_load(a.slopes + x.h * axes + min(c, axes - 1)) * sc.slope;
-                arrived(sl[c]);
-            }
-        }
-        {
-            const R *qb = qt + st * 2 * TS, *gb = qb + TS;
-            const bool part = !(x.lo <= kw && kw + 32 <= x.hi);
-            Frag<T> qr[NC], gr[NC], qc[ND][2], gc[ND][2];
+        for (int c = 0; c < NC; ++c) qr[c] = row_frag<T, DP>(qb, col, c * 16 + half * 8);
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                qr[c] = row_frag<T, DP>(qb, col, c * 16 + half * 8);
-                gr[c] = row_frag<T, DP>(gb, col, c * 16 + half * 8);
-            }
-            f32x16 s = f32x16(0.f), dp = acc_rows(rc(st) + QB, half);
+        for (int c = 0; c < NC; ++c) s = mma<T>(qr[c], kf[c], s);
+        if constexpr (K) {
+            dp = acc_rows(rc(st) + QB, half);
 #pragma unroll
-            for (int c = 0; c < NC; ++c) s = mma<T>(qr[c], kf[c], s);
+            for (int c = 0; c < NC; ++c) gr[c] = row_frag<T, DP>(gb, col, c * 16 + half * 8);
 #pragma unroll
             for (int c = 0; c < NC; ++c) dp = mma<T>(gr[c], vf[c], dp);
-            const f32x16 lr = acc_rows(rc(st), half);
+        }
+        const f32x16 lr = acc_rows(rc(st), half);
+        if constexpr (V) {
 #pragma unroll
             for (int d = 0; d < ND; ++d)
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    gc[d][c] = col_frag<T, DP>(gb, c, d * 32, lane);
-                }
-            reads_ahead<T, NC>();
-            products_and_reads<T, NC, 1>();
-            products_and_reads<T, NC, 2 + 8 / NC>();
-            issued<T>();
-            if (GEN) multiply_scores(s, sc);
-            if (GEN && a.cap > 0.f) {
-                cap_scores<T>(s, sc);
+                for (int c = 0; c < 2; ++c) gc[d][c] = col_frag<T, DP>(gb, c, d * 32, lane);
+        }
+        reads_ahead<T, NC>();
+        if constexpr (K) products_and_reads<T, NC, 1>();
+        products_and_reads<T, NC, V ? 2 + 8 / NC : 8 / NC>();
+        issued<T>();
+        if (GEN) multiply_scores(s, sc);
+        if (GEN && a.cap > 0.f) {
+            cap_scores<T>(s, sc);
+            if constexpr (K) {
                 const float f2 = -sc.per_cap * sc.per_cap;
 #pragma unroll
                 for (int r = 0; r < 16; ++r) dp[r] *= fmaf(f2 * s[r], s[r], 1.f);
             }
-            if (axes > 0) {
+        }
+        if (axes > 0) {
 #pragma unroll
-                for (int c = 0; c < 3; ++c) {
-                    if (c >= axes) break;
-                    const f32x16 p =
-                        differences(pq(st) + c * kPos + (half ? QB : col), pk[c]);
+            for (int c = 0; c < 3; ++c) {
+                if (c >= axes) break;
+                const f32x16 p = differences(pq(st) + c * kPos + (half ? QB : col), pk[c]);
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) s[r] = fmaf(-sl[c], fabsf(p[r]), s[r]);
-                }
+                for (int r = 0; r < 16; ++r) s[r] = fmaf(-sl[c], fabsf(p[r]), s[r]);
             }
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], sc.mul, -lr[r]));
+            if constexpr (K) dp[r] *= s[r];
+        }
+        if (part) {
+            i32x16 lo, hi;
+            acc_pairs(sp(st), half, &lo, &hi);
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], sc.mul, -lr[r]));
-                dp[r] *= s[r];
+                const bool see = key >= lo[r] && key < hi[r];
+                if constexpr (V) s[r] = see ? s[r] : 0.f;
+                if constexpr (K) dp[r] = see ? dp[r] : 0.f;
             }
-            if (part) {
-                i32x16 lo, hi;
-                acc_pairs(sp(st), half, &lo, &hi);
+        }
+        Frag<T> p0, p1, e0, e1;
+        if constexpr (V) {
+            p0 = pack8<T>(s, 0);
+            p1 = pack8<T>(s, 1);
+        }
+        if constexpr (K) {
+            e0 = pack8<T>(dp, 0);
+            e1 = pack8<T>(dp, 1);
+        }
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const bool see = key >= lo[r] && key < hi[r];
-                    s[r] = see ? s[r] : 0.f;
-                    dp[r] = see ? dp[r] : 0.f;
-                }
-            }
-            const Frag<T> p0 = pack8<T>(s, 0), p1 = pack8<T>(s, 1);
-            const Frag<T> e0 = pack8<T>(dp, 0), e1 = pack8<T>(dp, 1);
-#pragma unroll
-            for (int d = 0; d < ND; ++d) {
+        for (int d = 0; d < ND; ++d) {
+            if constexpr (V) {
                 dv[d] = mma<T>(gc[d][0], p0, dv[d]);
                 dv[d] = mma<T>(gc[d][1], p1, dv[d]);
+            }
+            if constexpr (K) {
                 qc[d][0] = col_frag<T, DP>(qb, 0, d * 32, lane);
                 qc[d][1] = col_frag<T, DP>(qb, 1, d * 32, lane);
             }
+        }
+        if constexpr (K) {
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
                 dk[d] = mma<T>(qc[d][0], e0, dk[d]);
                 dk[d] = mma<T>(qc[d][1], e1, dk[d]);
             }
-            products_and_reads<T, 2 * ND, 2>();
-            products_and_reads<T, 2 * ND, 0>();
-            issued<T>();
         }
-        x = following(x);
-        st = st + 1 < kStages ? st + 1 : 0;
-        if ((n & 1) && n + 1 < steps) arrive(n + 1, st, x);
-    }
-    if (*flag) {                           // (the loop's last barrier is behind us)
+        if constexpr (V && K) products_and_reads<T, 2 * ND, 2>();
+        else if constexpr (K) reads_ahead<T, 4>();
+        if constexpr (V) products_and_reads<T, 2 * ND, 0>();
+        else products_and_reads<T, 2 * ND, 2>();
+        issued<T>();
+    };
+    auto walk = [&](auto want_v, auto want_k) MP3D_INLINE {
+#pragma unroll 1
+        while (fn < min(steps, kStages - 2)) fetch();
+        Step x = {hk * a.G + g0, first, 0, 0};
+        if (steps > 0) {
+            seen_by_all(x.t, &x.lo, &x.hi);
+            arrive(0, 0, x);
+        }
+        for (int n = 0, st = 0; n < steps; ++n) {
+            if (fn < steps) fetch();
+            if (axes > 0 && x.h != sl_of) {
+                sl_of = x.h;
+#pragma unroll
+                for (int c = 0; c < 3; ++c) {
+                    sl[c] = uniform_load(a.slopes + x.h * axes + min(c, axes - 1)) * sc.slope;
+                    arrived(sl[c]);
+                }
+            }
+            sums(want_v, want_k, x, st);
+            x = following(x);
+            st = st + 1 < kStages ? st + 1 : 0;
+            if ((n & 1) && n + 1 < steps) arrive(n + 1, st, x);
+        }
+    };
+    if constexpr (!PAIRS) walk(std::true_type(), std::true_type());
+    else if (second) walk(std::false_type(), std::true_type());
+    else walk(std::true_type(), std::false_type());
+    if (*flag && !second) {                // (the loop's last barrier is behind us)
         // infinities and NaN of do that were dropped, for the keys they reach
         // (in dk they are there already: e is NaN with them)
         for (int n = 0; n < steps; ++n) {
@@ -664,13 +712,14 @@ __global__ __launch_bounds__(64 * kBwdWaves, (dkv_occupancy<T, DP>())) void attn
     }
     if (key >= a.Tk) return;
     const int64_t at = (((int64_t)b * a.Tk + key) * a.Hk + hk) * a.D;
-    if (a.gsplit == 1) {
-        store_cols<T, ND>((R *)a.dk + at, dk, a.scale, a.D, half);
-        store_cols<T, ND>((R *)a.dv + at, dv, 1.f, a.D, half);
-    } else {
-        const int64_t all = (int64_t)a.B * a.Tk * a.Hk * a.D;
-        store_cols<F32, ND>(a.part_dk + gpart * all + at, dk, a.scale, a.D, half);
-        store_cols<F32, ND>(a.part_dv + gpart * all + at, dv, 1.f, a.D, half);
+    const int64_t part = gpart * (int64_t)a.B * a.Tk * a.Hk * a.D + at;
+    if (!PAIRS || second) {
+        if (a.gsplit == 1) store_cols<T, ND>((R *)a.dk + at, dk, a.scale, a.D, half);
+        else store_cols<F32, ND>(a.part_dk + part, dk, a.scale, a.D, half);
+    }
+    if (!second) {
+        if (a.gsplit == 1) store_cols<T, ND>((R *)a.dv + at, dv, 1.f, a.D, half);
+        else store_cols<F32, ND>(a.part_dv + part, dv, 1.f, a.D, half);
     }
 }
 
@@ -700,7 +749,7 @@ void run(const AttnArgs &a, hipStream_t s)
     const int64_t nk = (a.Tk + 32 * NW - 1) / (32 * NW);
     if (nk > 0)
         launch_kernel((attn_dkv_kernel<T, DP, GEN>), dim3((uint32_t)(nk * a.B * a.Hk * a.gsplit)),
-                      dim3(64 * NW), tiles + kStages * kSmall + 3 * 4, s, a);
+                      dim3(64 * NW * (dkv_pairs<T, DP>() ? 2 : 1)), tiles + kStages * kSmall + 3 * 4, s, a);
     if (nk > 0 && a.gsplit > 1) {
         const int64_t need = ((int64_t)a.B * a.Tk * a.Hk * a.D + 255) / 256;
         launch_kernel((attn_parts_kernel<T>),
