@@ -354,6 +354,9 @@ constexpr bool dkv_pairs()
 {
     return sizeof(typename T::raw) * DP > 128 && sizeof(typename T::raw) * DP <= 256;
 }
+// (with pairs the CU holds one workgroup)
+template <typename T, int DP>
+constexpr int dkv_stages() { return dkv_pairs<T, DP>() ? 6 : stages<T, DP>(); }
 
 template <typename T, int DP, bool GEN>
 __global__ __launch_bounds__(64 * kBwdWaves * (dkv_pairs<T, DP>() ? 2 : 1),
@@ -363,7 +366,7 @@ void attn_dkv_kernel(AttnArgs a)
     using R = typename T::raw;
     const int axes = GEN ? a.axes : 0;
     constexpr bool PAIRS = dkv_pairs<T, DP>();
-    constexpr int kStages = stages<T, DP>();
+    constexpr int kStages = dkv_stages<T, DP>();
     constexpr int NW = kBwdWaves, NT = 64 * NW * (PAIRS ? 2 : 1), QB = kStep, NC = DP / 16,
                   ND = DP / 32;
     extern __shared__ __align__(16) unsigned char smem[];
@@ -743,13 +746,13 @@ template <typename T, int DP, bool GEN>
 void run(const AttnArgs &a, hipStream_t s)
 {
     constexpr int NW = kBwdWaves;
-    constexpr int kStages = stages<T, DP>();
-    constexpr uint32_t tiles = kStages * 2 * kStep * DP * sizeof(typename T::raw);
+    constexpr uint32_t tile = 2 * kStep * DP * sizeof(typename T::raw);
+    constexpr int sq = stages<T, DP>(), sk = dkv_stages<T, DP>();
     const int64_t nq = (a.Tq + 32 * NW - 1) / (32 * NW);
     const int64_t nk = (a.Tk + 32 * NW - 1) / (32 * NW);
     if (nk > 0)
         launch_kernel((attn_dkv_kernel<T, DP, GEN>), dim3((uint32_t)(nk * a.B * a.Hk * a.gsplit)),
-                      dim3(64 * NW * (dkv_pairs<T, DP>() ? 2 : 1)), tiles + kStages * kSmall + 3 * 4, s, a);
+                      dim3(64 * NW * (dkv_pairs<T, DP>() ? 2 : 1)), sk * (tile + kSmall) + 3 * 4, s, a);
     if (nk > 0 && a.gsplit > 1) {
         const int64_t need = ((int64_t)a.B * a.Tk * a.Hk * a.D + 255) / 256;
         launch_kernel((attn_parts_kernel<T>),
@@ -758,7 +761,7 @@ void run(const AttnArgs &a, hipStream_t s)
     }
     if (nq > 0)
         launch_kernel((attn_dq_kernel<T, DP, GEN>), dim3((uint32_t)(nq * a.B * a.Hq)),
-                      dim3(64 * NW), tiles + kStages * (3 * kPos * 8 + kStep * 4) + (1 + 4 * NW) * 4, s, a);
+                      dim3(64 * NW), sq * (tile + 3 * kPos * 8 + kStep * 4) + (1 + 4 * NW) * 4, s, a);
 }
 
 int64_t round16(int64_t bytes) { return (bytes + 15) & ~(int64_t)15; }
