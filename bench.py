@@ -64,14 +64,12 @@ PR308_CONTEXT_US = 3.0
 
 
 def kernel_source_hash() -> str:
-    """Hash of the HIP sources; stored traffic counters are reported only
-    while it matches the hash they were measured at."""
+    """Hash of the pooling kernels' sources; stored traffic counters are
+    reported only while it matches the hash they were measured at."""
     from bwd_max_pool3d_amd import _build
     h = hashlib.sha256()
-    headers = sorted(os.path.join(_build.CSRC, f) for f in os.listdir(_build.CSRC)
-                     if f.endswith(".hpp"))
-    for path in _build.sources() + headers:
-        with open(path, "rb") as f:
+    for name in _build.POOL_KERNELS:
+        with open(os.path.join(_build.CSRC, name), "rb") as f:
             h.update(f.read())
     return h.hexdigest()[:16]
 
