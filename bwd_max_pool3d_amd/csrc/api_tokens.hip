@@ -425,7 +425,7 @@ int mp3d_attention_workspace_bytes(const mp3d_attention *d, int backward, size_t
     *bytes = 0;
     if (a.B == 0 || a.Tq == 0) return MP3D_OK;
     if (backward) *bytes = plan_attn_backward(&a);
-    else if (attn_split_wanted(a)) *bytes = plan_attn_split(&a);
+    else if (attn_split_wanted(a, d->dtype == MP3D_F32)) *bytes = plan_attn_split(&a);
     else *bytes = (size_t)attn_order_bytes(a, false);
     return MP3D_OK;
 }
@@ -451,7 +451,7 @@ int mp3d_attention_forward(const mp3d_attention *d, const void *q, const void *k
     a.out = out;
     a.lse = lse;
     a.vec = wide_rows(q, a.qs, es) && wide_rows(k, a.ks, es) && wide_rows(v, a.vs, es);
-    const bool split = attn_split_wanted(a);
+    const bool split = attn_split_wanted(a, d->dtype == MP3D_F32);
     if (split) {
         if ((rc = check_workspace(workspace, workspace_bytes, plan_attn_split(&a)))) return rc;
         if ((rc = check_launch((int64_t)a.nrb * a.Hk * a.B * a.nsplit))) return rc;

@@ -1,5 +1,5 @@
 // attention_split.hip -- attention forward for few queries over many keys
-// (single new tokens, short chunks), split over the keys and joined.
+// (single new tokens, short chunks, few heads), split over the keys and joined.
 //
 // Bound: HBM (the keys and values are read once; 4 G flop for each 2 bytes
 // of them).  All query heads that share a key head, and all new tokens, are
@@ -365,13 +365,24 @@ void run(const AttnArgs &a, hipStream_t s)
 }  // namespace
 
 // The split form for rows that fit one block (the other kernel has 128 rows
-// a workgroup; figures above), and for short chunks where the other one
-// would leave most of the card idle (64 queries of 8 heads, 8192 keys: 36 us,
-// 160 by the other; 200 of 8 on 2: 57 and 163; 250 over 1024 keys: 15 and 20).
-bool attn_split_wanted(const AttnArgs &a)
+// a workgroup; figures above), for short chunks where the other one would
+// leave most of the card idle (64 queries of 8 heads, 8192 keys: 36 us, 160
+// by the other; 200 of 8 on 2: 57 and 163; 250 over 1024 keys: 15 and 20), and
+// for long ones of few heads.  There the waves do not share their keys, which
+// costs 16-bit types more than float32, whose matrix instructions are 16 times
+// slower: it pays from 4096 keys and a quarter of the CUs on (4096 tokens, 2
+// heads of 128: 68 to 73 us, 84 by the other; 2048, 4 heads: 62 and 45), in
+// float32 from 512 (512, 8 heads of 64: 21 and 42; 4096, 2 heads of 128: 202 to
+// 256 and 574), and to five eighths of the CUs from 2048 (3 x 3302, 2 heads of
+// 128: 311 to 470 and 472; 1024, 16 heads: 184 and 152).
+bool attn_split_wanted(const AttnArgs &a, bool f32)
 {
     const int64_t blocks = (int64_t)a.B * a.Hq * ((a.Tq + kAttnRows - 1) / kAttnRows);
-    return (int64_t)a.Tq * a.G <= 32 || (blocks < device_cus() && a.Tk >= 1024 && a.Tq < 256);
+    const int64_t cus = device_cus();
+    if ((int64_t)a.Tq * a.G <= 32) return true;
+    if (a.Tk >= 1024 && a.Tq < 256) return blocks < cus;
+    if (f32) return a.Tk >= 512 && blocks * 8 <= cus * (a.Tk >= 2048 ? 5 : 2);
+    return a.Tk >= 4096 && blocks * 4 <= cus;
 }
 
 // Eight workgroups a CU: 4, 12 and 16 measured 2 % more on long caches, 32

@@ -110,7 +110,7 @@ inline bool attn_general(const AttnArgs &a)
 }
 int64_t attn_order_bytes(const AttnArgs &a, bool keys);
 void launch_attn_order(const AttnArgs &a, bool backward, hipStream_t s);
-bool attn_split_wanted(const AttnArgs &a);
+bool attn_split_wanted(const AttnArgs &a, bool f32);
 // nrb, nsplit and chunk; returns the workspace bytes
 size_t plan_attn_split(AttnArgs *a);
 void place_attn_split(AttnArgs *a, void *workspace);

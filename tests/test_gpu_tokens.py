@@ -153,3 +153,24 @@ def test_binding_refusals():
     for kind, call in bad:
         with pytest.raises(kind):
             call()
+
+
+@pytest.mark.parametrize("dt,T,Hq,Hk,D", [(torch.float32, 520, 4, 2, 64),
+                                          (torch.float32, 2049, 2, 1, 128),
+                                          (torch.bfloat16, 4100, 2, 2, 72)], ids=str)
+def test_long_chunks_of_few_heads(dt, T, Hq, Hk, D):
+    """Many queries dealt out by chunks of keys give what the same queries
+    give in a batch that fills the card."""
+    q, k, v = (tk.randn((1, T, h, D), 95 + i, dt).cuda() for i, h in enumerate((Hq, Hk, Hk)))
+    n = 128                                                 # workgroups: over 5/8 of the CUs
+    how = dict(causal=True, softcap=20.0)
+    a, la = mp.mp3d_attention_forward(q, k, v, **how)
+    rep = [t.expand(n, -1, -1, -1) for t in (q, k, v)]
+    b, lb = mp.mp3d_attention_forward(*rep, **how)
+    # both are within the bounds of one result: out is a mean of |v| <= 6
+    # deviations, its weights rounded (2^-9 for bfloat16), itself rounded
+    # (2^-9), exponents off by the binary32 products' error (D 2^-24 of |s| <= 20)
+    unit = 2.0 ** -9 if dt == torch.bfloat16 else 2.0 ** -24
+    tol = 2 * (2 * unit + 20 * D * 2.0 ** -24) * 6
+    assert (a.float() - b[0].float()).abs().max().item() <= tol
+    assert (la - lb[0]).abs().max().item() <= 2 * 20 * D * 2.0 ** -24 + T * 2.0 ** -24
