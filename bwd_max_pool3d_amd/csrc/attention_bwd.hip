@@ -201,13 +201,14 @@ constexpr int bwd_occupancy()
     return sizeof(typename T::raw) * DP > 256 ? 1 : 2;
 }
 
-template <typename T, int DP, bool GEN>
+template <typename T, int DP, int DU, bool GEN>
 __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn_dq_kernel(AttnArgs a)
 {
     using R = typename T::raw;
     const int axes = GEN ? a.axes : 0;
     constexpr int kStages = stages<T, DP>();
-    constexpr int NW = kBwdWaves, NT = 64 * NW, KB = kStep, NC = DP / 16, ND = DP / 32;
+    constexpr int NW = kBwdWaves, NT = 64 * NW, KB = kStep, NC = DU / 16, ND = DU / 32;
+    constexpr bool ALL = DU == DP;         // whole tiles with all their channels
     extern __shared__ __align__(16) unsigned char smem[];
     constexpr int TS = KB * DP;                            // elements of a tile
     R *const kt = (R *)smem;                               // [kStages][K tile, V tile]
@@ -297,7 +298,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
         for (int x = tid; x < kStages * 2 * TS * (int)sizeof(R) / 16; x += NT)
             ((u32x4 *)kt)[x] = u32x4{0u, 0u, 0u, 0u};
     __syncthreads();
-    const bool whole = usable && a.D == DP;
+    const bool whole = usable && (!ALL || a.D == DP);
     // the next fetch: its step, its stage and where it reads
     const uint32_t lds = lds_address(smem) + wave * 1024,
                    lds_pk = lds_address(pk) + wave * kPos * 8;
@@ -309,8 +310,8 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
         const int k0 = kbeg + fn * KB;
         const uint32_t at = lds + fst * 2 * TS * (int)sizeof(R);
         if (whole && glo <= k0 && k0 + KB <= ghi) {
-            kd.load(fk, at);
-            vd.load(fv, at + TS * (int)sizeof(R));
+            kd.template load<ALL>(fk, at);
+            vd.template load<ALL>(fv, at + TS * (int)sizeof(R));
         } else if (usable) {
             kd.load_edge(kp, a.ks[1], k0, glo, ghi, at);
             vd.load_edge(vp, a.vs[1], k0, glo, ghi, at + TS * (int)sizeof(R));
@@ -448,7 +449,7 @@ constexpr bool dkv_pairs()
 template <typename T, int DP>
 constexpr int dkv_stages() { return dkv_pairs<T, DP>() ? 6 : stages<T, DP>(); }
 
-template <typename T, int DP, bool GEN>
+template <typename T, int DP, int DU, bool GEN>
 __global__ __launch_bounds__(64 * kBwdWaves * (dkv_pairs<T, DP>() ? 2 : 1),
                              (sizeof(typename T::raw) * DP > 256 ? 1 : 2))
 void attn_dkv_kernel(AttnArgs a)
@@ -457,8 +458,9 @@ void attn_dkv_kernel(AttnArgs a)
     const int axes = GEN ? a.axes : 0;
     constexpr bool PAIRS = dkv_pairs<T, DP>();
     constexpr int kStages = dkv_stages<T, DP>();
-    constexpr int NW = kBwdWaves, NT = 64 * NW * (PAIRS ? 2 : 1), QB = kStep, NC = DP / 16,
-                  ND = DP / 32;
+    constexpr int NW = kBwdWaves, NT = 64 * NW * (PAIRS ? 2 : 1), QB = kStep, NC = DU / 16,
+                  ND = DU / 32;
+    constexpr bool ALL = DU == DP;         // whole tiles with all their channels
     extern __shared__ __align__(16) unsigned char smem[];
     constexpr int TS = QB * DP;                            // elements of a tile
     R *const qt = (R *)smem;                               // [kStages][Q tile, dO tile]
@@ -541,7 +543,7 @@ void attn_dkv_kernel(AttnArgs a)
         for (int x = tid; x < kStages * 2 * TS * (int)sizeof(R) / 16; x += NT)
             ((u32x4 *)qt)[x] = u32x4{0u, 0u, 0u, 0u};
     __syncthreads();
-    const bool whole = usable && a.D == DP;
+    const bool whole = usable && (!ALL || a.D == DP);
     const R *const qbase = (const R *)a.q + b * a.qs[0], *const gbase =
         (const R *)a.dout + b * a.gs[0];
     // The next fetch: its step, stage, head and tile, and where it reads.
@@ -571,8 +573,8 @@ void attn_dkv_kernel(AttnArgs a)
         const uint32_t at = lds + fst * 2 * TS * (int)sizeof(R), as = lds_small + fst * kSmall;
         uint32_t off = mine;
         if (whole && q0 + QB <= a.Tq) {
-            qd.load(fq, at);
-            gd.load(fg, at + TS * (int)sizeof(R));
+            qd.template load<ALL>(fq, at);
+            gd.template load<ALL>(fg, at + TS * (int)sizeof(R));
         } else {
             if (usable) {
                 qd.load_edge(qbase + fh * a.qs[2], a.qs[1], q0, 0, a.Tq, at);
@@ -832,7 +834,7 @@ __global__ __launch_bounds__(256) void attn_parts_kernel(AttnArgs a)
     }
 }
 
-template <typename T, int DP, bool GEN>
+template <typename T, int DP, int DU, bool GEN>
 void run(const AttnArgs &a, hipStream_t s)
 {
     constexpr int NW = kBwdWaves;
@@ -841,7 +843,7 @@ void run(const AttnArgs &a, hipStream_t s)
     const int64_t nq = (a.Tq + 32 * NW - 1) / (32 * NW);
     const int64_t nk = (a.Tk + 32 * NW - 1) / (32 * NW);
     if (nk > 0)
-        launch_kernel((attn_dkv_kernel<T, DP, GEN>), dim3((uint32_t)(nk * a.B * a.Hk * a.gsplit)),
+        launch_kernel((attn_dkv_kernel<T, DP, DU, GEN>), dim3((uint32_t)(nk * a.B * a.Hk * a.gsplit)),
                       dim3(64 * NW * (dkv_pairs<T, DP>() ? 2 : 1)), sk * (tile + kSmall) + 3 * 4, s, a);
     if (nk > 0 && a.gsplit > 1) {
         const int64_t need = ((int64_t)a.B * a.Tk * a.Hk * a.D + 255) / 256;
@@ -850,8 +852,17 @@ void run(const AttnArgs &a, hipStream_t s)
                       s, a);
     }
     if (nq > 0)
-        launch_kernel((attn_dq_kernel<T, DP, GEN>), dim3((uint32_t)(nq * a.B * a.Hq)),
+        launch_kernel((attn_dq_kernel<T, DP, DU, GEN>), dim3((uint32_t)(nq * a.B * a.Hq)),
                       dim3(64 * NW), sq * (tile + 3 * kPos * 8 + kStep * 4) + (1 + 4 * NW) * 4, s, a);
+}
+
+template <typename T, bool GEN>
+void run_width(const AttnArgs &a, hipStream_t s)
+{
+    if (a.D <= 32) run<T, 64, 32, GEN>(a, s);
+    else if (a.D <= 64) run<T, 64, 64, GEN>(a, s);
+    else if (a.D <= 96) run<T, 128, 96, GEN>(a, s);
+    else run<T, 128, 128, GEN>(a, s);
 }
 
 int64_t round16(int64_t bytes) { return (bytes + 15) & ~(int64_t)15; }
@@ -909,15 +920,8 @@ hipError_t launch_attn_backward(const AttnArgs &a, hipStream_t s)
     if (nt > 0)
         launch_kernel((attn_rows_kernel<T>), dim3((uint32_t)(nt * a.B * a.Hq)), dim3(256), 0, s, a);
     if (nt > 0) launch_attn_order(a, true, s);
-    const bool general = attn_general(a);
-    if (a.D <= 64) {
-        if (general) run<T, 64, true>(a, s);
-        else run<T, 64, false>(a, s);
-    } else if (general) {
-        run<T, 128, true>(a, s);
-    } else {
-        run<T, 128, false>(a, s);
-    }
+    if (attn_general(a)) run_width<T, true>(a, s);
+    else run_width<T, false>(a, s);
     return hipGetLastError();
 }
 

@@ -47,12 +47,13 @@ constexpr int fwd_occupancy()
     return sizeof(typename T::raw) * DP > 256 ? 1 : 2;
 }
 
-template <typename T, int DP, bool GEN>
+template <typename T, int DP, int DU, bool GEN>
 __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn_fwd_kernel(AttnArgs a)
 {
     using R = typename T::raw;
     const int axes = GEN ? a.axes : 0;
-    constexpr int NW = kFwdWaves, NT = 64 * NW, KB = kFwdKeys, NC = DP / 16, ND = DP / 32;
+    constexpr int NW = kFwdWaves, NT = 64 * NW, KB = kFwdKeys, NC = DU / 16, ND = DU / 32;
+    constexpr bool ALL = DU == DP;         // whole tiles with all their channels
     extern __shared__ __align__(16) unsigned char smem[];
     R *const kt = (R *)smem;                               // [2][KB * DP]
     R *const vt = kt + 2 * KB * DP;                        // [2][KB * DP]
@@ -155,14 +156,14 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
     const int32_t *pos = a.pos_k + ((int64_t)min(wave, 2) * a.B + b) * a.Tk;
     int32_t pr = 0;
     const uint32_t lds = lds_address(smem) + wave * 1024;
-    const bool whole = usable && a.D == DP;
+    const bool whole = usable && (!ALL || a.D == DP);
     const R *fk = kp + (int64_t)kbeg * a.ks[1], *fv = vp + (int64_t)kbeg * a.vs[1];
     auto fetch = [&](int k0, int buf) {
         const uint32_t at = lds + buf * KB * DP * (int)sizeof(R);
         constexpr uint32_t v0 = 2 * KB * DP * sizeof(R);
         if (whole && glo <= k0 && k0 + KB <= ghi) {
-            kd.load(fk, at);
-            vd.load(fv, at + v0);
+            kd.template load<ALL>(fk, at);
+            vd.template load<ALL>(fv, at + v0);
         } else if (usable) {
             kd.load_edge(kp, a.ks[1], k0, glo, ghi, at);
             vd.load_edge(vp, a.vs[1], k0, glo, ghi, at + v0);
@@ -325,7 +326,7 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
     store_cols<T, ND>((R *)a.out + (((int64_t)b * a.Tq + i) * a.Hq + h) * a.D, o, inv, a.D, half);
 }
 
-template <typename T, int DP, bool GEN>
+template <typename T, int DP, int DU, bool GEN>
 hipError_t run(const AttnArgs &a, hipStream_t s)
 {
     constexpr int NW = kFwdWaves;
@@ -333,9 +334,18 @@ hipError_t run(const AttnArgs &a, hipStream_t s)
                              2 * 3 * kFwdPos * sizeof(u32x2) + (1 + 4 * NW) * sizeof(int);
     const int64_t nq = (a.Tq + 32 * NW - 1) / (32 * NW);
     launch_attn_order(a, false, s);
-    launch_kernel((attn_fwd_kernel<T, DP, GEN>), dim3((uint32_t)(nq * a.B * a.Hq)),
+    launch_kernel((attn_fwd_kernel<T, DP, DU, GEN>), dim3((uint32_t)(nq * a.B * a.Hq)),
                   dim3(64 * NW), lds, s, a);
     return hipGetLastError();
+}
+
+template <typename T, bool GEN>
+hipError_t run_width(const AttnArgs &a, hipStream_t s)
+{
+    if (a.D <= 32) return run<T, 64, 32, GEN>(a, s);
+    if (a.D <= 64) return run<T, 64, 64, GEN>(a, s);
+    if (a.D <= 96) return run<T, 128, 96, GEN>(a, s);
+    return run<T, 128, 128, GEN>(a, s);
 }
 
 }  // namespace
@@ -343,8 +353,7 @@ hipError_t run(const AttnArgs &a, hipStream_t s)
 template <typename T>
 hipError_t launch_attn_forward(const AttnArgs &a, hipStream_t s)
 {
-    if (attn_general(a)) return a.D <= 64 ? run<T, 64, true>(a, s) : run<T, 128, true>(a, s);
-    return a.D <= 64 ? run<T, 64, false>(a, s) : run<T, 128, false>(a, s);
+    return attn_general(a) ? run_width<T, true>(a, s) : run_width<T, false>(a, s);
 }
 
 template hipError_t launch_attn_forward<F32>(const AttnArgs &, hipStream_t);

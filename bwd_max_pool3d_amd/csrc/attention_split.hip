@@ -46,12 +46,13 @@ constexpr uint32_t split_lds()
     return split_tiles<T, DP>() + kSplitWaves * (2 * 3 * kSplitKeys + 64) * sizeof(float);
 }
 
-template <typename T, int DP, bool GEN>
+template <typename T, int DP, int DU, bool GEN>
 __global__ __launch_bounds__(64 * kSplitWaves, (sizeof(typename T::raw) * DP > 256 ? 1 : 2))
 void attn_split_kernel(AttnArgs a)
 {
     using R = typename T::raw;
-    constexpr int KB = kSplitKeys, NC = DP / 16, ND = DP / 32, NW = kSplitWaves;
+    constexpr int KB = kSplitKeys, NC = DU / 16, ND = DU / 32, NW = kSplitWaves;
+    constexpr bool ALL = DU == DP;         // whole tiles with all their channels
     extern __shared__ __align__(16) unsigned char smem[];
     const int axes = GEN ? a.axes : 0;
     const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63, col = lane & 31,
@@ -97,7 +98,7 @@ void attn_split_kernel(AttnArgs a)
         kd.init(lane, a.ks[1], a.D);
         vd.init(lane, a.vs[1], a.D);
         const bool usable = kd.usable(a.vec, a.ks[1], a.D) && vd.usable(a.vec, a.vs[1], a.D);
-        const bool whole = usable && a.D == DP;
+        const bool whole = usable && (!ALL || a.D == DP);
         if (a.D < DP) {                        // channels that no direct load writes
             for (int x = lane; x < 2 * KB * DP * (int)sizeof(R) / 16; x += 64)
                 ((u32x4 *)kt)[x] = u32x4{0u, 0u, 0u, 0u};
@@ -106,7 +107,7 @@ void attn_split_kernel(AttnArgs a)
         const uint32_t lds_k = lds_address(kt), lds_v = lds_address(vt), lds_p = lds_address(pk);
         auto fetch = [&](const TileDirect<T, DP, KB, 64> &d, const R *p, int64_t stride, int k0,
                          uint32_t lds) {
-            if (whole && glo <= k0 && k0 + KB <= ghi) d.load(p + k0 * stride, lds);
+            if (whole && glo <= k0 && k0 + KB <= ghi) d.template load<ALL>(p + k0 * stride, lds);
             else if (usable) d.load_edge(p, stride, k0, glo, ghi, lds);
         };
         auto place = [&](const R *p, int64_t stride, int k0, R *tile) {
@@ -350,15 +351,15 @@ __global__ __launch_bounds__(32 * kJoinGroups) void attn_join_kernel(AttnArgs a)
         a.lse[(b * a.Hq + h) * a.Tq + t] = lt == 0.f ? kNegInf : (mt + log2f(lt)) * kLn2;
 }
 
-template <typename T, int DP>
+template <typename T, int DP, int DU>
 void run(const AttnArgs &a, hipStream_t s)
 {
     const int64_t grid = (int64_t)a.nrb * a.Hk * a.B * a.nsplit;
     if (attn_general(a))
-        launch_kernel((attn_split_kernel<T, DP, true>), dim3((uint32_t)grid),
+        launch_kernel((attn_split_kernel<T, DP, DU, true>), dim3((uint32_t)grid),
                       dim3(64 * kSplitWaves), (split_lds<T, DP>()), s, a);
     else
-        launch_kernel((attn_split_kernel<T, DP, false>), dim3((uint32_t)grid),
+        launch_kernel((attn_split_kernel<T, DP, DU, false>), dim3((uint32_t)grid),
                       dim3(64 * kSplitWaves), (split_lds<T, DP>()), s, a);
 }
 
@@ -414,8 +415,10 @@ void place_attn_split(AttnArgs *a, void *workspace)
 template <typename T>
 hipError_t launch_attn_split(const AttnArgs &a, hipStream_t s)
 {
-    if (a.D <= 64) run<T, 64>(a, s);
-    else run<T, 128>(a, s);
+    if (a.D <= 32) run<T, 64, 32>(a, s);
+    else if (a.D <= 64) run<T, 64, 64>(a, s);
+    else if (a.D <= 96) run<T, 128, 96>(a, s);
+    else run<T, 128, 128>(a, s);
     const int64_t all = (int64_t)a.B * a.Hk * a.Tq * a.G;
     if (a.nsplit > 1)
         launch_kernel((attn_join_kernel<T>), dim3((uint32_t)all),
