@@ -67,6 +67,19 @@ __device__ __forceinline__ f32x16 mma(const Frag<T> &a, const Frag<T> &b, f32x16
     }
 }
 
+// c plus a step's 32 products, a0 b0 the first 16.  float32, whose results
+// show it: the step is summed by itself and then added, or a sum over
+// thousands would be rounded every two products (gradients over 2 x 4000
+// queries: 1.5e-6 off that way).  In 16-bit types the operands' own rounding
+// is a thousand times that.
+template <typename T>
+__device__ __forceinline__ f32x16 add_step(const Frag<T> &a0, const Frag<T> &b0, const Frag<T> &a1,
+                                           const Frag<T> &b1, f32x16 c)
+{
+    if constexpr (T::code == F32::code) return c + mma<T>(a1, b1, mma<T>(a0, b0, f32x16(0.f)));
+    else return mma<T>(a1, b1, mma<T>(a0, b0, c));
+}
+
 // Registers 8c .. 8c + 7 of a result as an operand.
 template <typename T>
 __device__ __forceinline__ Frag<T> pack8(const f32x16 &s, int c)

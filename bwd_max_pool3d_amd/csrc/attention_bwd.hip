@@ -421,8 +421,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
             const Frag<T> e0 = pack8<T>(s, 0), e1 = pack8<T>(s, 1);
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
-                o[d] = mma<T>(kc[d][0], e0, o[d]);
-                o[d] = mma<T>(kc[d][1], e1, o[d]);
+                o[d] = add_step<T>(kc[d][0], e0, kc[d][1], e1, o[d]);
             }
         }
         st = st + 1 < kStages ? st + 1 : 0;
@@ -735,8 +734,7 @@ void attn_dkv_kernel(AttnArgs a)
 #pragma unroll
         for (int d = 0; d < ND; ++d) {
             if constexpr (V) {
-                dv[d] = mma<T>(gc[d][0], p0, dv[d]);
-                dv[d] = mma<T>(gc[d][1], p1, dv[d]);
+                dv[d] = add_step<T>(gc[d][0], p0, gc[d][1], p1, dv[d]);
             }
             if constexpr (K) {
                 qc[d][0] = col_frag<T, DP>(qb, 0, d * 32, lane);
@@ -746,8 +744,7 @@ void attn_dkv_kernel(AttnArgs a)
         if constexpr (K) {
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
-                dk[d] = mma<T>(qc[d][0], e0, dk[d]);
-                dk[d] = mma<T>(qc[d][1], e1, dk[d]);
+                dk[d] = add_step<T>(qc[d][0], e0, qc[d][1], e1, dk[d]);
             }
         }
         if constexpr (V && K) products_and_reads<T, 2 * ND, 2>();
