@@ -66,11 +66,12 @@ __global__ __launch_bounds__(kOrderMax) void attn_order_kernel(AttnArgs a, int b
 }  // namespace
 
 // Bytes of the order of the queries' blocks (and the keys', backward); 0
-// where blocks are alike or too many to need one.
+// where blocks are alike, too many to need one, or walk nothing: without
+// queries nothing ranks the keys' blocks, and they go by number.
 int64_t attn_order_bytes(const AttnArgs &a, bool keys)
 {
     const int64_t n = ((keys ? a.Tk : a.Tq) + kAttnRows - 1) / kAttnRows;
-    return a.docs && n > 1 && n <= kOrderMax ? (n * a.B * 4 + 15) / 16 * 16 : 0;
+    return a.docs && a.Tq > 0 && n > 1 && n <= kOrderMax ? (n * a.B * 4 + 15) / 16 * 16 : 0;
 }
 
 void launch_attn_order(const AttnArgs &a, bool backward, hipStream_t s)

@@ -1,0 +1,21 @@
+"""The token operators at the ends of their ranges: no queries, no rows."""
+import pytest
+import torch
+
+import bwd_max_pool3d_amd as mp
+from test_gpu_attention import make
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("Tk", [1, 128, 129, 700])
+def test_backward_without_queries_in_documents(Tk):
+    """No query: dk and dv are zeros in every block of keys, also with a
+    workspace that is larger than needed and holds other numbers."""
+    q, k, v, do = (t.cuda() for t in make(2, 0, Tk, 2, 2, 64, torch.float32, 75))
+    docs = torch.tensor([[0, Tk // 2, Tk]] * 2, dtype=torch.int32, device="cuda")
+    out, lse = mp.mp3d_attention_forward(q, k, v, doc_offsets=docs)
+    ws = torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda")
+    grads = [torch.full(t.shape, float("nan"), device="cuda") for t in (q, k, v)]
+    mp.mp3d_attention_backward(do, q, k, v, out, lse, doc_offsets=docs, grads=grads, workspace=ws)
+    assert torch.equal(grads[1], torch.zeros_like(k)) and torch.equal(grads[2], torch.zeros_like(v))
