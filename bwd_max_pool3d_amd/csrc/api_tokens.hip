@@ -423,7 +423,8 @@ int mp3d_attention_workspace_bytes(const mp3d_attention *d, int backward, size_t
     int rc = attn_args(d, &a);
     if (rc) return rc;
     *bytes = 0;
-    if (a.B == 0 || a.Tq == 0) return MP3D_OK;
+    // (the backward without queries still writes dk and dv)
+    if (a.B == 0 || (a.Tq == 0 && (!backward || a.Tk == 0))) return MP3D_OK;
     if (backward) *bytes = plan_attn_backward(&a);
     else if (attn_split_wanted(a, d->dtype == MP3D_F32)) *bytes = plan_attn_split(&a);
     else *bytes = (size_t)attn_order_bytes(a, false);

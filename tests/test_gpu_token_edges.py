@@ -19,3 +19,24 @@ def test_backward_without_queries_in_documents(Tk):
     grads = [torch.full(t.shape, float("nan"), device="cuda") for t in (q, k, v)]
     mp.mp3d_attention_backward(do, q, k, v, out, lse, doc_offsets=docs, grads=grads, workspace=ws)
     assert torch.equal(grads[1], torch.zeros_like(k)) and torch.equal(grads[2], torch.zeros_like(v))
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.float16, torch.bfloat16], ids=str)
+@pytest.mark.parametrize("Hq,Hk", [(4, 4), (8, 2)])
+@pytest.mark.parametrize("Tk", [3, 300])
+@pytest.mark.parametrize("more", ["", "documents", "bias"])
+def test_backward_without_queries(more, Tk, Hq, Hk, dt):
+    """No query, the workspace that the call itself asks for: shared heads,
+    documents and a bias take some."""
+    q, k, v, do = (t.cuda() for t in make(2, 0, Tk, Hq, Hk, 64, dt, 76))
+    how = {}
+    if more == "documents":
+        how["doc_offsets"] = torch.tensor([[0, Tk]] * 2, dtype=torch.int32, device="cuda")
+    if more == "bias":
+        how["slopes"] = torch.ones((Hq, 2), device="cuda")
+        how["pos_q"] = torch.zeros((2, 2, 0), dtype=torch.int32, device="cuda")
+        how["pos_k"] = torch.ones((2, 2, Tk), dtype=torch.int32, device="cuda")
+    out, lse = mp.mp3d_attention_forward(q, k, v, **how)
+    dq, dk, dv = mp.mp3d_attention_backward(do, q, k, v, out, lse, **how)
+    assert dq.shape == q.shape
+    assert torch.equal(dk, torch.zeros_like(k)) and torch.equal(dv, torch.zeros_like(v))
