@@ -242,7 +242,9 @@ int attn_args(const mp3d_attention *d, AttnArgs *a)
     if (d->doc_offsets && (d->n_docs < 1 || d->n_docs > kInt32Max - 1))
         return fail(MP3D_EINVAL, "n_docs must be >= 1");
     if (d->axes < 0 || d->axes > 3) return fail(MP3D_EINVAL, "axes must be in 0 .. 3");
-    if (d->axes > 0 && (!d->slopes || !d->pos_q || !d->pos_k))
+    // (a tensor without elements may be NULL)
+    if (d->axes > 0 && (!d->slopes || (d->B * d->Tq > 0 && !d->pos_q) ||
+                        (d->B * d->Tk > 0 && !d->pos_k)))
         return fail(MP3D_EINVAL, "a distance bias needs slopes, pos_q and pos_k");
     if ((rc = check_strides(d->q_stride, "q")) || (rc = check_strides(d->k_stride, "k")) ||
         (rc = check_strides(d->v_stride, "v")))

@@ -30,3 +30,15 @@ def test_backward_takes_the_workspace_it_asks_for(over):
         assert n.value > 0 or how.get("Hq", 4) == 2 or "doc_offsets" in how
     else:
         assert (n.value > 0) == (how["Tq"] > 0)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(Tq=0, pos_k=FAKE), _lib.MP3D_OK), (dict(Tk=0, pos_q=FAKE), _lib.MP3D_OK),
+    (dict(Tq=0, Tk=0), _lib.MP3D_OK), (dict(B=0), _lib.MP3D_OK),
+    (dict(pos_k=FAKE), _lib.MP3D_EINVAL), (dict(pos_q=FAKE), _lib.MP3D_EINVAL),
+    (dict(Tq=0), _lib.MP3D_EINVAL), (dict(Tk=0), _lib.MP3D_EINVAL)], ids=str)
+def test_positions_of_no_tokens_may_be_null(over, code):
+    lib, n = _lib.load(), ctypes.c_size_t()
+    a = ctypes.byref(desc(axes=1, slopes=FAKE, **over))
+    for backward in (0, 1):
+        assert lib.mp3d_attention_workspace_bytes(a, backward, ctypes.byref(n)) == code
