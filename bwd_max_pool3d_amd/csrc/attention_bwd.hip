@@ -44,6 +44,7 @@ constexpr int kStep = 32;                  // keys (dq) or queries (dk, dv) per 
 constexpr int kPos = kStep + 2;            // places of a step's positions on one axis (16 bytes)
 constexpr int kSmall = 16 * kStep + 3 * 8 * kPos;      // bytes of a step's constants, spans, positions
 constexpr float kInf = __builtin_huge_valf();
+constexpr int64_t kRowsGrid = (int64_t)1 << 23;        // workgroups of the constants along x
 
 // ------------------------------------------------------------ constants
 
@@ -126,8 +127,9 @@ __global__ __launch_bounds__(256, 6) void attn_rows_kernel(AttnArgs a)
 {
     using R = typename T::raw;
     const int nt = (a.Tq + 31) / 32;
-    const int qt = blockIdx.x % nt;
-    const int64_t bh = blockIdx.x / nt;
+    const int64_t id = (int64_t)blockIdx.y * gridDim.x + blockIdx.x, bh = id / nt;
+    if (bh >= (int64_t)a.B * a.Hq) return;
+    const int qt = (int)(id - bh * nt);
     const int b = (int)(bh / a.Hq), h = (int)(bh - (int64_t)b * a.Hq);
     const int row = threadIdx.x >> 3, sub = threadIdx.x & 7, i = qt * 32 + row;
     float s = 0.f;
@@ -832,34 +834,39 @@ __global__ __launch_bounds__(256) void attn_parts_kernel(AttnArgs a)
 }
 
 template <typename T, int DP, int DU, bool GEN>
-void run(const AttnArgs &a, hipStream_t s)
+hipError_t run(const AttnArgs &a, hipStream_t s)
 {
     constexpr int NW = kBwdWaves;
+    hipError_t e;
     constexpr uint32_t tile = 2 * kStep * DP * sizeof(typename T::raw);
     constexpr int sq = stages<T, DP>(), sk = dkv_stages<T, DP>();
     const int64_t nq = (a.Tq + 32 * NW - 1) / (32 * NW);
     const int64_t nk = (a.Tk + 32 * NW - 1) / (32 * NW);
-    if (nk > 0)
+    if (nk > 0) {
         launch_kernel((attn_dkv_kernel<T, DP, DU, GEN>), dim3((uint32_t)(nk * a.B * a.Hk * a.gsplit)),
                       dim3(64 * NW * (dkv_pairs<T, DP>() ? 2 : 1)), sk * (tile + kSmall) + 3 * 4, s, a);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
     if (nk > 0 && a.gsplit > 1) {
         const int64_t need = ((int64_t)a.B * a.Tk * a.Hk * a.D + 255) / 256;
         launch_kernel((attn_parts_kernel<T>),
                       dim3((uint32_t)(need < kMaxTileGrid ? need : kMaxTileGrid), 2), dim3(256), 0,
                       s, a);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (nq > 0)
         launch_kernel((attn_dq_kernel<T, DP, DU, GEN>), dim3((uint32_t)(nq * a.B * a.Hq)),
                       dim3(64 * NW), sq * (tile + 3 * kPos * 8 + kStep * 4) + (1 + 4 * NW) * 4, s, a);
+    return hipGetLastError();
 }
 
 template <typename T, bool GEN>
-void run_width(const AttnArgs &a, hipStream_t s)
+hipError_t run_width(const AttnArgs &a, hipStream_t s)
 {
-    if (a.D <= 32) run<T, 64, 32, GEN>(a, s);
-    else if (a.D <= 64) run<T, 64, 64, GEN>(a, s);
-    else if (a.D <= 96) run<T, 128, 96, GEN>(a, s);
-    else run<T, 128, 128, GEN>(a, s);
+    if (a.D <= 32) return run<T, 64, 32, GEN>(a, s);
+    if (a.D <= 64) return run<T, 64, 64, GEN>(a, s);
+    if (a.D <= 96) return run<T, 128, 96, GEN>(a, s);
+    return run<T, 128, 128, GEN>(a, s);
 }
 
 int64_t round16(int64_t bytes) { return (bytes + 15) & ~(int64_t)15; }
@@ -914,12 +921,19 @@ template <typename T>
 hipError_t launch_attn_backward(const AttnArgs &a, hipStream_t s)
 {
     const int64_t nt = (a.Tq + 31) / 32;
-    if (nt > 0)
-        launch_kernel((attn_rows_kernel<T>), dim3((uint32_t)(nt * a.B * a.Hq)), dim3(256), 0, s, a);
-    if (nt > 0) launch_attn_order(a, true, s);
-    if (attn_general(a)) run_width<T, true>(a, s);
-    else run_width<T, false>(a, s);
-    return hipGetLastError();
+    // (a kernel reads what the one before it wrote: none follows a failed launch)
+    hipError_t e;
+    if (nt > 0) {
+        // four times the workgroups of the other kernels, which may pass the
+        // 2^32 threads of a launch along x
+        const int64_t blocks = nt * a.B * a.Hq, x = blocks < kRowsGrid ? blocks : kRowsGrid;
+        launch_kernel((attn_rows_kernel<T>), dim3((uint32_t)x, (uint32_t)((blocks + x - 1) / x)),
+                      dim3(256), 0, s, a);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        launch_attn_order(a, true, s);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    return attn_general(a) ? run_width<T, true>(a, s) : run_width<T, false>(a, s);
 }
 
 template hipError_t launch_attn_backward<F32>(const AttnArgs &, hipStream_t);

@@ -334,6 +334,9 @@ hipError_t run(const AttnArgs &a, hipStream_t s)
                              2 * 3 * kFwdPos * sizeof(u32x2) + (1 + 4 * NW) * sizeof(int);
     const int64_t nq = (a.Tq + 32 * NW - 1) / (32 * NW);
     launch_attn_order(a, false, s);
+    // (none that reads the order follows a failed launch)
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
     launch_kernel((attn_fwd_kernel<T, DP, DU, GEN>), dim3((uint32_t)(nq * a.B * a.Hq)),
                   dim3(64 * NW), lds, s, a);
     return hipGetLastError();

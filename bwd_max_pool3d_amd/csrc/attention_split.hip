@@ -419,6 +419,8 @@ hipError_t launch_attn_split(const AttnArgs &a, hipStream_t s)
     else if (a.D <= 64) run<T, 64, 64>(a, s);
     else if (a.D <= 96) run<T, 128, 96>(a, s);
     else run<T, 128, 128>(a, s);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;         // the join would read what was not written
     const int64_t all = (int64_t)a.B * a.Hk * a.Tq * a.G;
     if (a.nsplit > 1)
         launch_kernel((attn_join_kernel<T>), dim3((uint32_t)all),

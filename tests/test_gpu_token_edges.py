@@ -40,3 +40,26 @@ def test_backward_without_queries(more, Tk, Hq, Hk, dt):
     dq, dk, dv = mp.mp3d_attention_backward(do, q, k, v, out, lse, **how)
     assert dq.shape == q.shape
     assert torch.equal(dk, torch.zeros_like(k)) and torch.equal(dv, torch.zeros_like(v))
+
+
+def test_backward_of_more_rows_than_one_launch_takes():
+    """553 million rows of queries: the rows' constants take 2^32 threads and
+    more.  Sequences from both sides of every 2^23 workgroups, and the last,
+    give the bits of a call by themselves."""
+    B, Tq, H = 540000, 128, 8
+    assert Tq // 32 * B * H * 256 > 1 << 32
+    g = torch.Generator(device="cuda").manual_seed(77)
+    q, do = (torch.randn((B, Tq, H, 1), dtype=torch.float16, device="cuda", generator=g)
+             for _ in range(2))
+    k, v = (torch.randn((B, 2, H, 1), dtype=torch.float16, device="cuda", generator=g)
+            for _ in range(2))
+    out, lse = mp.mp3d_attention_forward(q, k, v)
+    grads = mp.mp3d_attention_backward(do, q, k, v, out, lse)
+    per = Tq // 32 * H                                     # workgroups of a sequence
+    for b in (0, (1 << 23) // per, (1 << 23) // per - 1, (1 << 24) // per, B - 1):
+        one = [t[b:b + 1].contiguous() for t in (do, q, k, v, out, lse)]
+        o1 = mp.mp3d_attention_forward(*one[1:4])
+        assert torch.equal(o1[0], one[4]) and torch.equal(o1[1], one[5])
+        for whole, part in zip(grads, mp.mp3d_attention_backward(*one)):
+            assert torch.equal(whole[b:b + 1], part)
+            assert part.abs().sum() > 0
