@@ -681,39 +681,88 @@ __device__ __forceinline__ void multiply_scores(f32x16 &s, const Scores &sc)
 }
 
 // --- distances of positions: the differences of 32 rows' and 32 columns'
-// positions, as a matrix product.  A binary32 number is the sum of three
-// bfloat16 (each takes the next 8 of its 24 bits), so
-//   p - k = (p1, p2, p3, 0, 1, 1, 1, 0) . (1, 1, 1, 0, -k1, -k2, -k3, 0),
-// eight products that one matrix instruction forms for all pairs, without
-// error where the numbers are integers below 2^24.  The vector units, which
-// bound these kernels at 64 channels, are left with one operation a score
-// and axis where they had two, and LDS with one read where it had four.
-constexpr uint32_t kOnes[2] = {0x3f803f80u, 0x00003f80u};
+// positions, as a matrix product.  A position is the sum of its four bytes
+// p3 2^24 + p2 2^16 + p1 2^8 + p0, with its sign, each exact in bfloat16, so
+//   p - k = (p3, p2, p1, p0, 1, 1, 1, 1) . (1, 1, 1, 1, -k3, -k2, -k1, -k0),
+// eight products that one matrix instruction forms for all pairs.  Below 2^24
+// (p3 and k3 are 0) the terms of a distance under 2^24 have no partial sum
+// past it, in whatever order they are added: no error.  Else a first
+// instruction forms the difference of the upper halves, 17 bits wide, and a
+// second adds the lower ones: exact below 2^23, and the distance of any two
+// int32 within a few units of 2^-24 of it.  The vector units, which bound these
+// kernels at 64 channels, are left with one operation a score and axis where
+// they had two, and LDS with one read where it had four.
+constexpr uint32_t kOnes = 0x3f803f80u;    // two
+constexpr uint32_t kUpper = 0x7fff0000u;   // p3's place, without its sign
 
-__device__ __forceinline__ u32x2 position_parts(float p)
+// (p3 above p2, p1 above p0)
+__device__ __forceinline__ u32x2 position_parts(int32_t p)
 {
-    const uint32_t hi = __builtin_bit_cast(uint32_t, p) & 0xffff0000u;
-    const float r = p - __builtin_bit_cast(float, hi);
-    const uint32_t mid = __builtin_bit_cast(uint32_t, r) & 0xffff0000u;
-    const float lo = r - __builtin_bit_cast(float, mid);
-    return u32x2{(hi >> 16) | mid, __builtin_bit_cast(uint32_t, lo) >> 16};
+    const uint32_t m = p < 0 ? 0u - (uint32_t)p : (uint32_t)p;
+    const uint32_t sign = (uint32_t)(p >> 31) & 0x80008000u;
+    auto part = [](uint32_t byte, float unit) {
+        return __builtin_bit_cast(uint32_t, (float)byte * unit);
+    };
+    return u32x2{(part(m >> 24, 16777216.f) | part(m >> 16 & 0xffu, 65536.f) >> 16) ^ sign,
+                 (part(m >> 8 & 0xffu, 256.f) | part(m & 0xffu, 1.f) >> 16) ^ sign};
 }
 
 // The columns' operand: lanes 0 .. 31 ones, 32 .. 63 the parts, negated.
 __device__ __forceinline__ u32x2 position_cols(u32x2 parts, int half)
 {
-    u32x2 c = half ? parts ^ 0x80008000u : u32x2{kOnes[0], kOnes[1]};
+    u32x2 c = half ? parts ^ 0x80008000u : u32x2{kOnes, kOnes};
     asm volatile("" : "+v"(c));
     return c;
 }
 
+__device__ __forceinline__ bool is_far_position(int32_t p)
+{
+    return (uint32_t)p + (1u << 24) - 1u > (2u << 24) - 2u;
+}
+__device__ __forceinline__ bool is_far_position(u32x2 parts) { return parts.x & kUpper; }
+
 // The rows' is read from LDS: `lane` points to the lane's parts, for lanes
-// 32 .. 63 to ones.
+// 32 .. 63 to ones.  FAR: some position that the workgroup walks is 2^24 or
+// more.
+template <bool FAR>
 __device__ __forceinline__ f32x16 differences(const u32x2 *lane, u32x2 cols)
 {
-    return __builtin_amdgcn_mfma_f32_32x32x8bf16_1k(__builtin_bit_cast(s16x4, *lane),
-                                                    __builtin_bit_cast(s16x4, cols), f32x16(0.f),
-                                                    0, 0, 0);
+    auto product = [&](u32x2 rows, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x8bf16_1k(__builtin_bit_cast(s16x4, rows),
+                                                        __builtin_bit_cast(s16x4, cols), c, 0, 0,
+                                                        0);
+    };
+    const u32x2 rows = *lane;
+    if constexpr (FAR)
+        return product(u32x2{0u, rows.y}, product(u32x2{rows.x, 0u}, f32x16(0.f)));
+    else return product(rows, f32x16(0.f));
+}
+
+// Minus slope times distance on each axis, from scores s: `rows` the tile's
+// parts on the first axis, those of an axis `step` after it.  axes negative:
+// the wave may meet a far position.  (Two branches without an else, on a
+// number that is there anyway: as one with an else the kernels took 16
+// registers more, and dk, dv of packed documents 290 us instead of 208; with
+// both products in every step 216, and the forward 135 instead of 124.)
+template <bool FAR>
+__device__ __forceinline__ void add_axes(f32x16 &s, const u32x2 *rows, int step, int axes,
+                                         const u32x2 *cols, const float *slopes)
+{
+#pragma unroll
+    for (int x = 0; x < 3; ++x) {
+        if (x >= axes) break;
+        const f32x16 p = differences<FAR>(rows + x * step, cols[x]);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[r] = fmaf(-slopes[x], fabsf(p[r]), s[r]);
+        if constexpr (FAR) asm volatile("" : "+v"(s));
+    }
+}
+__device__ __forceinline__ void add_bias(f32x16 &s, const u32x2 *rows, int step, int axes,
+                                         const u32x2 *cols, const float *slopes)
+{
+    if (__builtin_expect_with_probability(axes < 0, 0, 1.0))
+        add_axes<true>(s, rows, step, -axes, cols, slopes);
+    add_axes<false>(s, rows, step, axes, cols, slopes);
 }
 
 // The 16 scores of a result to c tanh(s / c).  float32: the library's

@@ -121,6 +121,13 @@ __device__ __forceinline__ bool few_keys_delta(const AttnArgs &a, int b, int h, 
     return true;
 }
 
+// Keys whose positions a workgroup of the constants prepares.
+__device__ __forceinline__ int keys_share(const AttnArgs &a)
+{
+    const int nt = (a.Tq + 31) / 32;
+    return max((a.Tk + nt - 1) / nt, 1);
+}
+
 // One workgroup per 32 queries of one head: 8 threads per row.
 template <typename T>
 __global__ __launch_bounds__(256, 6) void attn_rows_kernel(AttnArgs a)
@@ -162,19 +169,30 @@ __global__ __launch_bounds__(256, 6) void attn_rows_kernel(AttnArgs a)
         // a row without weights: its exponents become -inf
         *(float2 *)(a.rowd + 2 * at) = make_float2(l == kNegInf ? kInf : l * kLog2e, -s);
     }
-    if (h == 0) {
-        // this workgroup's share of the positions
-        const int per_q = 32, per_k = (a.Tk + nt - 1) / nt;
+    if (h == 0 && a.axes > 0) {
+        // this workgroup's share of the positions, and whether one is far
+        __shared__ int far[2];
+        if (threadIdx.x < 2) far[threadIdx.x] = 0;
+        __syncthreads();
+        const int per_q = 32, per_k = keys_share(a);
         for (int x = 0; x < a.axes; ++x) {
             const int64_t row = (int64_t)x * a.B + b;
             const int32_t *pk = a.pos_k + row * a.Tk, *pq = a.pos_q + row * a.Tq;
-            const int64_t base = a.Tk > 0 ? pk[0] : 0;
-            for (int k = qt * per_k + threadIdx.x; k < min((qt + 1) * per_k, a.Tk); k += 256)
-                ((u32x2 *)a.parts_k)[row * a.Tk + k] = position_parts((float)(pk[k] - base));
+            for (int k = qt * per_k + threadIdx.x; k < min((qt + 1) * per_k, a.Tk); k += 256) {
+                const u32x2 p = position_parts(pk[k]);
+                ((u32x2 *)a.parts_k)[row * a.Tk + k] = p;
+                if (is_far_position(p)) far[1] = 1;
+            }
             const int k = qt * per_q + threadIdx.x;
-            if (threadIdx.x < per_q && k < a.Tq)
-                ((u32x2 *)a.parts_q)[row * a.Tq + k] = position_parts((float)(pq[k] - base));
+            if (threadIdx.x < per_q && k < a.Tq) {
+                const u32x2 p = position_parts(pq[k]);
+                ((u32x2 *)a.parts_q)[row * a.Tq + k] = p;
+                if (is_far_position(p)) far[0] = 1;
+            }
         }
+        __syncthreads();
+        if (threadIdx.x == 0)
+            *(int2 *)(a.fars + 2 * ((int64_t)b * nt + qt)) = make_int2(far[0], far[1]);
     }
     if (h == 0 && threadIdx.x < 64) {
         const int j = qt * 32 + (threadIdx.x & 31);
@@ -242,7 +260,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
         ends[3 * NW + wave] = ahi;
     }
     if (tid < kStages * KB) bad[tid] = 0;
-    if (axes > 0 && tid < kStages * 3) pk[tid * kPos + KB] = u32x2{kOnes[0], kOnes[1]};
+    if (axes > 0 && tid < kStages * 3) pk[tid * kPos + KB] = u32x2{kOnes, kOnes};
     if (tid == 0) *flag = 0;
     __syncthreads();
     int glo = ends[0], ghi = ends[NW], galo = ends[2 * NW], gahi = ends[3 * NW];
@@ -273,13 +291,22 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
     const Scores sc = scores(a);
     u32x2 pq[3];
     float sl[3];
+    bool far = false;                      // a query's or a key's position is
+    if (axes > 0) {
+        const int per = keys_share(a);
+        for (int t = max(glo, 0) / per + lane; t * (int64_t)per < ghi; t += 64)
+            far |= a.fars[2 * ((int64_t)b * nt + t) + 1] != 0;
+    }
 #pragma unroll
     for (int x = 0; x < 3; ++x) {
         if (x >= axes) break;
-        pq[x] = position_cols(((const u32x2 *)a.parts_q)[((int64_t)x * a.B + b) * a.Tq + ic], half);
+        const u32x2 p = ((const u32x2 *)a.parts_q)[((int64_t)x * a.B + b) * a.Tq + ic];
+        far |= is_far_position(p);
+        pq[x] = position_cols(p, half);
         sl[x] = a.slopes[h * axes + x] * sc.slope;
         arrived(sl[x]);
     }
+    const int signed_axes = __any(far) ? -axes : axes;     // (add_bias)
 
     float lse2 = rd.x, delta = rd.y;       // (delta negated)
     arrived(qf);
@@ -396,16 +423,8 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
 #pragma unroll
                 for (int r = 0; r < 16; ++r) dp[r] *= fmaf(f2 * s[r], s[r], 1.f);
             }
-            if (axes > 0) {
-#pragma unroll
-                for (int x = 0; x < 3; ++x) {
-                    if (x >= axes) break;
-                    const f32x16 p =
-                        differences(pk + (st * 3 + x) * kPos + (half ? KB : col), pq[x]);
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) s[r] = fmaf(-sl[x], fabsf(p[r]), s[r]);
-                }
-            }
+            if (GEN)
+                add_bias(s, pk + st * 3 * kPos + (half ? KB : col), kPos, signed_axes, pq, sl);
             const bool part = !(alo <= k0 && k0 + KB <= ahi);
             if (part && *flag) {
                 const auto x = acc_rows(bad + st * KB, half);
@@ -473,6 +492,7 @@ void attn_dkv_kernel(AttnArgs a)
     auto pq = [&](int st) { return (u32x2 *)(small + st * kSmall + 16 * QB); };
     int *const flag = (int *)(small + kStages * kSmall);   // an infinity or a NaN was dropped
     int *const ends = flag + 1;                            // [2] first and last tile
+    int *const fars = ends + 2;                            // a query's position is far
 
     const int nk = (a.Tk + 32 * NW - 1) / (32 * NW);
     const Block blk = block_of(blockIdx.x, a.B * a.Hk * a.gsplit, nk);
@@ -491,18 +511,20 @@ void attn_dkv_kernel(AttnArgs a)
     const int32_t *tiles = a.tiles + 4 * (int64_t)b * nt;
 
     // the tiles of queries that see a key of this block
-    if (tid == 0) *flag = 0;
+    if (tid == 0) *flag = *fars = 0;
     if (tid < 2) ends[tid] = tid ? -1 : nt;
     if (axes > 0 && tid < kStages * 3)
-        pq(tid / 3)[tid % 3 * kPos + QB] = u32x2{kOnes[0], kOnes[1]};
+        pq(tid / 3)[tid % 3 * kPos + QB] = u32x2{kOnes, kOnes};
     __syncthreads();
     {
         int first = nt, last = -1;
         for (int t = tid; t < nt; t += NT) {
             const int4 u = *(const int4 *)(tiles + 4 * (int64_t)t);
+            const int far = axes > 0 ? a.fars[2 * ((int64_t)b * nt + t)] : 0;
             if (u.x < k0 + 32 * NW && u.y > k0) {
                 first = min(first, t);
                 last = t;
+                if (far) *fars = 1;
             }
         }
         if (last >= 0) {
@@ -523,11 +545,15 @@ void attn_dkv_kernel(AttnArgs a)
         vf[c] = load8<T>(vp, c * 16 + half * 8, a.D, a.vec);
     }
     u32x2 pk[3];
+    bool far = axes > 0 && *fars;          // a query's or a key's position is
 #pragma unroll
     for (int x = 0; x < 3; ++x) {
         if (x >= axes) break;
-        pk[x] = position_cols(((const u32x2 *)a.parts_k)[((int64_t)x * a.B + b) * a.Tk + kc], half);
+        const u32x2 p = ((const u32x2 *)a.parts_k)[((int64_t)x * a.B + b) * a.Tk + kc];
+        far |= is_far_position(p);
+        pk[x] = position_cols(p, half);
     }
+    const int signed_axes = __any(far) ? -axes : axes;     // (add_bias)
     const Scores sc = scores(a);
     arrived(kf);
     arrived(vf);
@@ -700,15 +726,7 @@ void attn_dkv_kernel(AttnArgs a)
                 for (int r = 0; r < 16; ++r) dp[r] *= fmaf(f2 * s[r], s[r], 1.f);
             }
         }
-        if (axes > 0) {
-#pragma unroll
-            for (int c = 0; c < 3; ++c) {
-                if (c >= axes) break;
-                const f32x16 p = differences(pq(st) + c * kPos + (half ? QB : col), pk[c]);
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[r] = fmaf(-sl[c], fabsf(p[r]), s[r]);
-            }
-        }
+        if (GEN) add_bias(s, pq(st) + (half ? QB : col), kPos, signed_axes, pk, sl);
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
             s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], sc.mul, -lr[r]));
@@ -844,7 +862,7 @@ hipError_t run(const AttnArgs &a, hipStream_t s)
     const int64_t nk = (a.Tk + 32 * NW - 1) / (32 * NW);
     if (nk > 0) {
         launch_kernel((attn_dkv_kernel<T, DP, DU, GEN>), dim3((uint32_t)(nk * a.B * a.Hk * a.gsplit)),
-                      dim3(64 * NW * (dkv_pairs<T, DP>() ? 2 : 1)), sk * (tile + kSmall) + 3 * 4, s, a);
+                      dim3(64 * NW * (dkv_pairs<T, DP>() ? 2 : 1)), sk * (tile + kSmall) + 4 * 4, s, a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (nk > 0 && a.gsplit > 1) {
@@ -876,7 +894,7 @@ int64_t round16(int64_t bytes) { return (bytes + 15) & ~(int64_t)15; }
 // A key head's query heads are dealt out until two workgroups a CU are there
 // (2 x 2047 with 8 heads a key head: dk, dv 174 us and 15.5 for the sum of the
 // parts, 740 without).  Workspace: tiles, spans, rowd, the blocks' orders, the
-// positions, then the parts (each at a multiple of 16 bytes).
+// positions and what is far of them, then the parts (each at a multiple of 16 bytes).
 size_t plan_attn_backward(AttnArgs *a)
 {
     const int64_t blocks = (int64_t)((a->Tk + kAttnRows - 1) / kAttnRows) * a->B * a->Hk;
@@ -887,7 +905,8 @@ size_t plan_attn_backward(AttnArgs *a)
     int64_t n = round16(rows * a->Hq * 8) + round16(rows * 8) + (int64_t)a->B * nt * 16 +
                 attn_order_bytes(*a, false) + attn_order_bytes(*a, true) +
                 round16((int64_t)a->axes * rows * 8) +
-                round16((int64_t)a->axes * a->B * a->Tk * 8);
+                round16((int64_t)a->axes * a->B * a->Tk * 8) +
+                round16(a->axes > 0 ? a->B * nt * 8 : 0);
     if (a->gsplit > 1)
         n += 2 * round16((int64_t)a->gsplit * a->B * a->Tk * a->Hk * a->D * 4);
     return (size_t)n;
@@ -912,6 +931,8 @@ void place_attn_backward(AttnArgs *a, void *workspace)
     p += round16((int64_t)a->axes * rows * 8);
     a->parts_k = (uint32_t *)p;
     p += round16((int64_t)a->axes * a->B * a->Tk * 8);
+    a->fars = (int32_t *)p;
+    p += round16(a->axes > 0 ? a->B * nt * 8 : 0);
     a->part_dk = (float *)p;
     p += round16((int64_t)a->gsplit * a->B * a->Tk * a->Hk * a->D * 4);
     a->part_dv = (float *)p;

@@ -61,6 +61,7 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
     u32x2 *const pk = (u32x2 *)(vt + 2 * KB * DP);
     int *const flag = (int *)(pk + 2 * 3 * kFwdPos);       // an infinity or a NaN was dropped
     int *const ends = flag + 1;                            // [4][NW]
+    int *const fars = ends + 4 * NW;                       // a position is far
 
     const int nq = (a.Tq + 32 * NW - 1) / (32 * NW);
     const Block blk = block_of(blockIdx.x, a.B * a.Hq, nq);
@@ -92,9 +93,9 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
         ends[2 * NW + wave] = alo;
         ends[3 * NW + wave] = ahi;
     }
-    if (tid == 0) *flag = 0;
+    if (tid == 0) *flag = *fars = 0;
     if (axes > 0 && tid < 2 * 3 * 2)
-        pk[(tid >> 1) * kFwdPos + KB + (tid & 1) * 32] = u32x2{kOnes[0], kOnes[1]};
+        pk[(tid >> 1) * kFwdPos + KB + (tid & 1) * 32] = u32x2{kOnes, kOnes};
     __syncthreads();
     int glo = ends[0], ghi = ends[NW], galo = ends[2 * NW], gahi = ends[3 * NW];
 #pragma unroll
@@ -117,20 +118,16 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
 #pragma unroll
     for (int c = 0; c < NC; ++c) qf[c] = load8<T>(qp, c * 16 + half * 8, a.D, a.vec);
 
-    // positions relative to the workgroup's first query: differences of
-    // tokens near each other stay exact in binary32
     const Scores sc = scores(a);
     u32x2 pq[3];
     float sl[3];
-    double from = 0.;                      // of the axis of the wave's number
+    bool far = false;                      // a query's or a key's position is
 #pragma unroll
     for (int x = 0; x < 3; ++x) {
         if (x >= axes) break;
-        const int32_t *p = a.pos_q + ((int64_t)x * a.B + b) * a.Tq;
-        // (differences of int32 are exact in binary64)
-        const double base = uniform_load(p + q0);
-        if (wave == x) from = base;
-        pq[x] = position_cols(position_parts((float)((double)p[ic] - base)), half);
+        const u32x2 p = position_parts(a.pos_q[((int64_t)x * a.B + b) * a.Tq + ic]);
+        far |= is_far_position(p);
+        pq[x] = position_cols(p, half);
         sl[x] = a.slopes[h * axes + x] * sc.slope;
         arrived(sl[x]);
     }
@@ -191,14 +188,27 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
             if (edge) kd.scrub(ks, k0, glo, ghi, false, nullptr, 0);
         }
         if (wave < axes)
-            pk[(buf * 3 + wave) * kFwdPos + lane] = position_parts((float)((double)pr - from));
+            pk[(buf * 3 + wave) * kFwdPos + lane] = position_parts(pr);
         hand_over();
     };
+    int signed_axes = axes;                // negative with a far position (add_bias)
     if (kbeg < kend) {
         fetch(kbeg, 0);
+        if (axes > 0) {                    // (while the first tile is on its way)
+            const int32_t *p = a.pos_k + (int64_t)b * a.Tk;
+            const int64_t y = axes > 1 ? (int64_t)a.B * a.Tk : 0, z = axes > 2 ? 2 * y : 0;
+#pragma unroll 4
+            for (int k = glo + tid; k < ghi; k += NT) {
+                far |= is_far_position(p[k]);
+                far |= is_far_position(p[k + y]);
+                far |= is_far_position(p[k + z]);
+            }
+            if (far) *fars = 1;
+        }
         place(kbeg, 0);
+        if (axes > 0 && uniform(*fars)) signed_axes = -axes;
     }
-    int n = 0;
+int n = 0;
     for (int k0 = kbeg; k0 < kend; k0 += KB, ++n) {
         const int buf = n & 1;
         const bool more = k0 + KB < kend;
@@ -233,18 +243,11 @@ __global__ __launch_bounds__(64 * kFwdWaves, (fwd_occupancy<T, DP>())) void attn
 #pragma unroll
             for (int u = 0; u < 2; ++u) cap_scores<T>(s[u], sc);
         }
-        if (axes > 0) {
+        if (GEN) {
+            const u32x2 *const rows = pk + buf * 3 * kFwdPos + (half ? KB : col);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-#pragma unroll
-                for (int x = 0; x < 3; ++x) {
-                    if (x >= axes) break;
-                    const f32x16 p = differences(
-                        pk + (buf * 3 + x) * kFwdPos + u * 32 + (half ? KB : col), pq[x]);
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) s[u][r] = fmaf(-sl[x], fabsf(p[r]), s[u][r]);
-                }
-            }
+            for (int u = 0; u < 2; ++u)
+                add_bias(s[u], rows + u * 32, kFwdPos, signed_axes, pq, sl);
         }
         const bool part = !(alo <= k0 && k0 + KB <= ahi);
         if (part) {
@@ -331,7 +334,7 @@ hipError_t run(const AttnArgs &a, hipStream_t s)
 {
     constexpr int NW = kFwdWaves;
     constexpr uint32_t lds = 4 * kFwdKeys * DP * sizeof(typename T::raw) +
-                             2 * 3 * kFwdPos * sizeof(u32x2) + (1 + 4 * NW) * sizeof(int);
+                             2 * 3 * kFwdPos * sizeof(u32x2) + (2 + 4 * NW) * sizeof(int);
     const int64_t nq = (a.Tq + 32 * NW - 1) / (32 * NW);
     launch_attn_order(a, false, s);
     // (none that reads the order follows a failed launch)

@@ -137,14 +137,12 @@ void attn_split_kernel(AttnArgs a)
 #pragma unroll
         for (int c = 0; c < NC; ++c) qf[c] = load8<T>(qp, c * 16 + half * 8, a.D, a.vec);
         const Scores sc = scores(a);
-        float pq[3], sl[3];
-        double base[3];                        // (differences of int32 are exact in binary64)
+        int pq[3];
+        float sl[3];
 #pragma unroll
         for (int x = 0; x < 3; ++x) {
             if (x >= axes) break;
-            const int32_t *p = a.pos_q + ((int64_t)x * a.B + b) * a.Tq;
-            base[x] = uniform_load(p);
-            pq[x] = (float)((double)p[t] - base[x]);
+            pq[x] = a.pos_q[((int64_t)x * a.B + b) * a.Tq + t];
             sl[x] = a.slopes[h * axes + x] * sc.slope;
             arrived(pq[x]);
             arrived(sl[x]);
@@ -191,9 +189,11 @@ void attn_split_kernel(AttnArgs a)
                 if (x >= axes) break;
                 const int *p = pk + (buf * 3 + x) * KB + 4 * half;
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    s[e] = fmaf(-sl[x],
-                                fabsf((float)((double)p[acc_row(e, 0)] - base[x]) - pq[x]), s[e]);
+                for (int e = 0; e < 16; ++e) {
+                    const int k = p[acc_row(e, 0)];        // (up to 2^32 apart)
+                    s[e] = fmaf(-sl[x], (float)((uint32_t)max(k, pq[x]) - (uint32_t)min(k, pq[x])),
+                                s[e]);
+                }
             }
             // (a chunk's ends are multiples of the tile, or the ends of every span)
             if (part) {

@@ -98,8 +98,10 @@ struct AttnArgs {
     int32_t *spans;            // (B, Tq, 2): the keys [lo, hi) of each query
     int32_t *tiles;            // (B, ceil(Tq / 32), 4): over 32 queries, the union of
                                // their keys [lo, hi) and the keys all of them see
-    uint32_t *parts_q, *parts_k;  // (axes, B, Tq, 2) and (axes, B, Tk, 2): positions from that
-                                  // of the sequence's first key, in parts of 8 bits
+    uint32_t *parts_q, *parts_k;  // (axes, B, Tq, 2) and (axes, B, Tk, 2): positions in parts of
+                                  // 8 bits
+    int32_t *fars;             // (B, ceil(Tq / 32), 2): is a position 2^24 or more among these 32
+                               // queries, among this share of the keys (with a bias)
     float *part_dk, *part_dv;  // (gsplit, B, Tk, Hk, D), when gsplit > 1
 };
 // Scores with a cap, a bias or a factor that is not positive: kernels of
