@@ -426,7 +426,9 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
             if (GEN)
                 add_bias(s, pk + st * 3 * kPos + (half ? KB : col), kPos, signed_axes, pq, sl);
             const bool part = !(alo <= k0 && k0 + KB <= ahi);
-            if (part && *flag) {
+            // (rows were dropped for the whole workgroup: a wave that sees all
+            // of the tile meets them too)
+            if (!(galo <= k0 && k0 + KB <= gahi) && *flag) {
                 const auto x = acc_rows(bad + st * KB, half);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) s[r] = x[r] == n + 1 ? kNegInf : s[r];

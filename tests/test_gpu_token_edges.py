@@ -1,9 +1,11 @@
-"""The token operators at the ends of their ranges: no queries, no rows."""
+"""The token operators at the ends of their ranges: no queries, no rows, more
+rows than one launch takes, keys that are not finite."""
 import pytest
 import torch
 
+import _tokens as tk
 import bwd_max_pool3d_amd as mp
-from test_gpu_attention import make
+from test_gpu_attention import make, run
 
 pytestmark = pytest.mark.gpu
 
@@ -63,3 +65,24 @@ def test_backward_of_more_rows_than_one_launch_takes():
         for whole, part in zip(grads, mp.mp3d_attention_backward(*one)):
             assert torch.equal(whole[b:b + 1], part)
             assert part.abs().sum() > 0
+
+
+@pytest.mark.parametrize("dt", tk.TYPES, ids=tk.name_of)
+@pytest.mark.parametrize("D", [64, 128])
+def test_dq_of_a_key_with_score_minus_infinity(D, dt):
+    """A key whose score is -infinity has no weight: the gradient of every
+    query that sees it, in all other channels, is as if the key were not
+    there.  Its tile is seen in part by some waves of the first workgroup, in
+    full by others, and in full by the whole second workgroup."""
+    T, at = 200, 70
+    q, k, v, do = make(1, T, T, 1, 1, D, dt, 66)
+    q[..., 0] = q[..., 0].abs() + 0.1
+    k[0, at, 0, 0] = float("-inf")
+    got = run(q, k, v, do, dict(causal=True))
+    keep = [j for j in range(T) if j != at]
+    n = T - at - 1                                       # the queries after the key
+    want = tk.attention(q[:, -n:], k[:, keep], v[:, keep], do[:, -n:], causal=True)
+    for name in ("out", "dq"):
+        value, tol = want[name]
+        first = 1 if name == "dq" else 0
+        tk.close(got[name][:, -n:, :, first:], value[..., first:], tol[..., first:], name)
