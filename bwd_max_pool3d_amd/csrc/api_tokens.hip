@@ -273,6 +273,7 @@ int attn_args(const mp3d_attention *d, AttnArgs *a)
     a->docs = d->doc_offsets;
     a->prefix = d->prefix;
     a->kv_len = d->kv_len;
+    a->f16 = d->dtype == MP3D_F16;
     return MP3D_OK;
 }
 

@@ -18,7 +18,18 @@
 // sums a fourth launch adds in a fixed order.
 //
 // p and e are rounded to the storage type for the second products, as the
-// forward's weights are.
+// forward's weights are.  Range: float16 ends at 65504 and has its full bits
+// down to 2^-14 only.  Over many keys p and e are below that, and gradients
+// scaled against just this take e beyond 65504 while dq and dk are not.  So in
+// float16 p is rounded times 2^12, and e over 2^x, taken out where dq, dk and
+// dv are stored.  |do . v_j| and |delta| are at most |do|_1 max |v|, so with
+//   x = 1 + exponent of |do|_1 max |v| - 15
+// no |e| 2^-x reaches 2^15.  dq takes each query's x (in the exponential, at no
+// cost); dk is a sum over queries, and takes the largest x of those that the
+// workgroup walks (one operation a score).  The first kernel leaves |do|_1
+// and its and |v|'s maxima over small groups, and the others join them as they
+// start (2 x 2047 tokens, 16 heads of 128 on 2, forward and backward: 352 -> 361
+// us; max |v| by a launch of its own 372).
 //
 // Bound: with 64 channels and a bias the vector unit and the waits between
 // its work and the matrix unit's (vector 42 %, matrix 25 % of the cycles busy
@@ -121,6 +132,41 @@ __device__ __forceinline__ bool few_keys_delta(const AttnArgs &a, int b, int h, 
     return true;
 }
 
+// float16: what p is rounded times.
+constexpr int kWeightBits = 12;
+
+template <typename T>
+constexpr bool ranged() { return T::code == F16::code; }
+
+// The largest of 64 lanes' numbers, none negative, without LDS.
+template <int CTRL>
+__device__ __forceinline__ float dpp_max(float v)
+{
+    return fmaxf(v, __builtin_bit_cast(
+                        float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf,
+                                                           0xf, true)));
+}
+__device__ __forceinline__ float wave_max(float v)
+{
+    v = dpp_max<0xb1>(v);                  // quads: lane ^ 1
+    v = dpp_max<0x4e>(v);                  // lane ^ 2
+    v = dpp_max<0x141>(v);                 // the other quad of 8 lanes (mirrored)
+    v = dpp_max<0x140>(v);                 // the other 8 of 16 lanes (mirrored)
+    const uint32_t a = __builtin_bit_cast(uint32_t, v);
+    const auto x = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+    const uint32_t x0 = x[0], x1 = x[1];
+    return halves_max(fmaxf(__builtin_bit_cast(float, x0), __builtin_bit_cast(float, x1)));
+}
+
+// What e is rounded over, its exponent: of norms of up to `norm` against
+// values of up to `most`.  0 where there is no gradient, or one that is not
+// finite.
+__device__ __forceinline__ int range_exponent(float norm, float most)
+{
+    const float bound = norm * most;
+    return bound > 0.f && bound < kInf ? __builtin_amdgcn_frexp_expf(bound) + 1 - 15 : 0;
+}
+
 // Keys whose positions a workgroup of the constants prepares.
 __device__ __forceinline__ int keys_share(const AttnArgs &a)
 {
@@ -139,7 +185,25 @@ __global__ __launch_bounds__(256, 6) void attn_rows_kernel(AttnArgs a)
     const int qt = (int)(id - bh * nt);
     const int b = (int)(bh / a.Hq), h = (int)(bh - (int64_t)b * a.Hq);
     const int row = threadIdx.x >> 3, sub = threadIdx.x & 7, i = qt * 32 + row;
-    float s = 0.f;
+    float s = 0.f, norm = 0.f, value = 0.f;    // norm: |do|_1; value: |v| of a share of the keys
+    if constexpr (ranged<T>()) {
+        const int hk = h / a.G, shares = nt * a.G, per = (a.Tk + shares - 1) / shares;
+        const int L = a.kv_len ? min(a.kv_len[b], a.Tk) : a.Tk;        // (past it: nobody's)
+        const int first = ((h - hk * a.G) * nt + qt) * per, c = (threadIdx.x & 15) * 8;
+        const R *v = (const R *)a.v + b * a.vs[0] + hk * a.vs[2];
+#pragma unroll 2
+        for (int k = first + (threadIdx.x >> 4); k < min(first + per, L); k += 16) {
+            struct alignas(16) {
+                R e[8];
+            } x = __builtin_bit_cast(decltype(x),
+                                     load8<T>(v + (int64_t)k * a.vs[1], c, a.D, a.vec));
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                const float y = fabsf(T::widen(x.e[n]));
+                value = fmaxf(value, y < kInf ? y : 0.f);
+            }
+        }
+    }
     if (i < a.Tq) {
         const R *o = (const R *)a.out + (((int64_t)b * a.Tq + i) * a.Hq + h) * a.D;
         const R *g = (const R *)a.dout + b * a.gs[0] + (int64_t)i * a.gs[1] + h * a.gs[2];
@@ -151,11 +215,37 @@ __global__ __launch_bounds__(256, 6) void attn_rows_kernel(AttnArgs a)
             } x = __builtin_bit_cast(decltype(x), load8<T>(o, d, a.D, ovec)),
               y = __builtin_bit_cast(decltype(y), load8<T>(g, d, a.D, a.vec));
 #pragma unroll
-            for (int k = 0; k < 8; ++k) s = fmaf(T::widen(x.e[k]), T::widen(y.e[k]), s);
+            for (int k = 0; k < 8; ++k) {
+                s = fmaf(T::widen(x.e[k]), T::widen(y.e[k]), s);
+                if (ranged<T>()) norm += fabsf(T::widen(y.e[k]));
+            }
         }
     }
 #pragma unroll
-    for (int m = 4; m; m >>= 1) s += __shfl_xor(s, m);
+    for (int m = 4; m; m >>= 1) {
+        s += __shfl_xor(s, m);
+        if (ranged<T>()) norm += __shfl_xor(norm, m);
+    }
+    if constexpr (ranged<T>()) {
+        // (what is not finite has no bound; a query that sees nothing no say)
+        const bool some = i < a.Tq && norm < kInf &&
+                          a.lse[bh * a.Tq + min(i, a.Tq - 1)] != kNegInf;
+        norm = some ? norm : 0.f;
+        if (sub == 0 && i < a.Tq) a.norms[bh * a.Tq + i] = norm;
+        __shared__ float most[2][4];
+        norm = wave_max(norm);
+        value = wave_max(value);
+        if ((threadIdx.x & 63) == 0) {
+            most[0][threadIdx.x >> 6] = norm;
+            most[1][threadIdx.x >> 6] = value;
+        }
+        __syncthreads();
+        if (threadIdx.x < 2) {
+            const float *m = most[threadIdx.x];
+            (threadIdx.x ? a.v_most : a.norm_most)[bh * nt + qt] =
+                fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+        }
+    }
     if (sizeof(R) == 2) {
         __shared__ float few[4][32];
         if (few_keys_delta<T>(a, b, h, qt, few)) {
@@ -167,7 +257,8 @@ __global__ __launch_bounds__(256, 6) void attn_rows_kernel(AttnArgs a)
         const int64_t at = bh * a.Tq + i;
         const float l = a.lse[at];
         // a row without weights: its exponents become -inf
-        *(float2 *)(a.rowd + 2 * at) = make_float2(l == kNegInf ? kInf : l * kLog2e, -s);
+        *(float2 *)(a.rowd + 2 * at) = make_float2(
+            l == kNegInf ? kInf : fmaf(l, kLog2e, ranged<T>() ? -(float)kWeightBits : 0.f), -s);
     }
     if (h == 0 && a.axes > 0) {
         // this workgroup's share of the positions, and whether one is far
@@ -309,6 +400,15 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
     const int signed_axes = __any(far) ? -axes : axes;     // (add_bias)
 
     float lse2 = rd.x, delta = rd.y;       // (delta negated)
+    int xq = 0;                            // what e is rounded over, its exponent
+    if constexpr (ranged<T>()) {
+        float most = 0.f;
+        const float *v = a.v_most + ((int64_t)b * a.Hq + hk * a.G) * nt;
+#pragma unroll 4
+        for (int t = lane; t < nt * a.G; t += 64) most = fmaxf(most, v[t]);
+        xq = range_exponent(a.norms[(int64_t)bh * a.Tq + ic], wave_max(most));
+        lse2 += (float)(kWeightBits + xq);
+    }
     arrived(qf);
     arrived(gf);
     arrived(lse2);
@@ -451,7 +551,8 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
         if ((n & 1) && n + 1 < steps) arrive(n + 1, st);
     }
     if (i >= a.Tq) return;
-    store_cols<T, ND>((R *)a.dq + (((int64_t)b * a.Tq + i) * a.Hq + h) * a.D, o, a.scale, a.D, half);
+    store_cols<T, ND>((R *)a.dq + (((int64_t)b * a.Tq + i) * a.Hq + h) * a.D, o,
+                      ranged<T>() ? ldexpf(a.scale, xq) : a.scale, a.D, half);
 }
 
 // -------------------------------------------------------------- dk and dv
@@ -495,6 +596,7 @@ void attn_dkv_kernel(AttnArgs a)
     int *const flag = (int *)(small + kStages * kSmall);   // an infinity or a NaN was dropped
     int *const ends = flag + 1;                            // [2] first and last tile
     int *const fars = ends + 2;                            // a query's position is far
+    int *const most = fars + 1;                            // [2] bits of |do|_1's and |v|'s maxima
 
     const int nk = (a.Tk + 32 * NW - 1) / (32 * NW);
     const Block blk = block_of(blockIdx.x, a.B * a.Hk * a.gsplit, nk);
@@ -513,20 +615,41 @@ void attn_dkv_kernel(AttnArgs a)
     const int32_t *tiles = a.tiles + 4 * (int64_t)b * nt;
 
     // the tiles of queries that see a key of this block
-    if (tid == 0) *flag = *fars = 0;
+    if (tid == 0) {
+        *flag = *fars = 0;
+        most[0] = most[1] = 0;
+    }
     if (tid < 2) ends[tid] = tid ? -1 : nt;
     if (axes > 0 && tid < kStages * 3)
         pq(tid / 3)[tid % 3 * kPos + QB] = u32x2{kOnes, kOnes};
     __syncthreads();
     {
         int first = nt, last = -1;
+        float norm = 0.f, value = 0.f;
+        if constexpr (ranged<T>()) {
+            const float *v = a.v_most + ((int64_t)b * a.Hq + hk * a.G) * nt;
+            for (int t = tid; t < nt * a.G; t += NT) value = fmaxf(value, v[t]);
+        }
         for (int t = tid; t < nt; t += NT) {
+            float here = 0.f;
+            if constexpr (ranged<T>())
+                for (int g = g0; g < g1; ++g)
+                    here = fmaxf(here, a.norm_most[((int64_t)b * a.Hq + hk * a.G + g) * nt + t]);
             const int4 u = *(const int4 *)(tiles + 4 * (int64_t)t);
             const int far = axes > 0 ? a.fars[2 * ((int64_t)b * nt + t)] : 0;
             if (u.x < k0 + 32 * NW && u.y > k0) {
                 first = min(first, t);
                 last = t;
                 if (far) *fars = 1;
+                norm = fmaxf(norm, here);
+            }
+        }
+        if constexpr (ranged<T>()) {       // (not negative: their bits are in their order)
+            norm = wave_max(norm);
+            value = wave_max(value);
+            if (lane == 0) {
+                atomicMax(most, __builtin_bit_cast(int, norm));
+                atomicMax(most + 1, __builtin_bit_cast(int, value));
             }
         }
         if (last >= 0) {
@@ -537,6 +660,11 @@ void attn_dkv_kernel(AttnArgs a)
     __syncthreads();
     const int first = uniform(ends[0]), last = uniform(ends[1]), span = last - first + 1;
     const int steps = span > 0 ? span * (g1 - g0) : 0;
+    // (float16: p is there times 2^kWeightBits)
+    const int xk = ranged<T>() ? uniform(range_exponent(__builtin_bit_cast(float, most[0]),
+                                                        __builtin_bit_cast(float, most[1])))
+                               : 0;
+    const float e_unit = ranged<T>() ? ldexpf(1.f, -xk - kWeightBits) : 1.f;
 
     const R *kp = (const R *)a.k + b * a.ks[0] + hk * a.ks[2] + (int64_t)kc * a.ks[1];
     const R *vp = (const R *)a.v + b * a.vs[0] + hk * a.vs[2] + (int64_t)kc * a.vs[1];
@@ -732,7 +860,7 @@ void attn_dkv_kernel(AttnArgs a)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
             s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], sc.mul, -lr[r]));
-            if constexpr (K) dp[r] *= s[r];
+            if constexpr (K) dp[r] *= ranged<T>() ? s[r] * e_unit : s[r];
         }
         if (part) {
             i32x16 lo, hi;
@@ -828,12 +956,14 @@ void attn_dkv_kernel(AttnArgs a)
     const int64_t at = (((int64_t)b * a.Tk + key) * a.Hk + hk) * a.D;
     const int64_t part = gpart * (int64_t)a.B * a.Tk * a.Hk * a.D + at;
     if (!PAIRS || second) {
-        if (a.gsplit == 1) store_cols<T, ND>((R *)a.dk + at, dk, a.scale, a.D, half);
-        else store_cols<F32, ND>(a.part_dk + part, dk, a.scale, a.D, half);
+        const float f = ranged<T>() ? ldexpf(a.scale, xk) : a.scale;
+        if (a.gsplit == 1) store_cols<T, ND>((R *)a.dk + at, dk, f, a.D, half);
+        else store_cols<F32, ND>(a.part_dk + part, dk, f, a.D, half);
     }
     if (!second) {
-        if (a.gsplit == 1) store_cols<T, ND>((R *)a.dv + at, dv, 1.f, a.D, half);
-        else store_cols<F32, ND>(a.part_dv + part, dv, 1.f, a.D, half);
+        constexpr float f = ranged<T>() ? 1.f / (1 << kWeightBits) : 1.f;
+        if (a.gsplit == 1) store_cols<T, ND>((R *)a.dv + at, dv, f, a.D, half);
+        else store_cols<F32, ND>(a.part_dv + part, dv, f, a.D, half);
     }
 }
 
@@ -864,7 +994,7 @@ hipError_t run(const AttnArgs &a, hipStream_t s)
     const int64_t nk = (a.Tk + 32 * NW - 1) / (32 * NW);
     if (nk > 0) {
         launch_kernel((attn_dkv_kernel<T, DP, DU, GEN>), dim3((uint32_t)(nk * a.B * a.Hk * a.gsplit)),
-                      dim3(64 * NW * (dkv_pairs<T, DP>() ? 2 : 1)), sk * (tile + kSmall) + 4 * 4, s, a);
+                      dim3(64 * NW * (dkv_pairs<T, DP>() ? 2 : 1)), sk * (tile + kSmall) + 6 * 4, s, a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (nk > 0 && a.gsplit > 1) {
@@ -896,7 +1026,8 @@ int64_t round16(int64_t bytes) { return (bytes + 15) & ~(int64_t)15; }
 // A key head's query heads are dealt out until two workgroups a CU are there
 // (2 x 2047 with 8 heads a key head: dk, dv 174 us and 15.5 for the sum of the
 // parts, 740 without).  Workspace: tiles, spans, rowd, the blocks' orders, the
-// positions and what is far of them, then the parts (each at a multiple of 16 bytes).
+// positions and what is far of them, float16's bounds, then the parts (each
+// at a multiple of 16 bytes).
 size_t plan_attn_backward(AttnArgs *a)
 {
     const int64_t blocks = (int64_t)((a->Tk + kAttnRows - 1) / kAttnRows) * a->B * a->Hk;
@@ -909,6 +1040,7 @@ size_t plan_attn_backward(AttnArgs *a)
                 round16((int64_t)a->axes * rows * 8) +
                 round16((int64_t)a->axes * a->B * a->Tk * 8) +
                 round16(a->axes > 0 ? a->B * nt * 8 : 0);
+    if (a->f16) n += round16(rows * a->Hq * 4) + 2 * round16(a->B * nt * a->Hq * 4);
     if (a->gsplit > 1)
         n += 2 * round16((int64_t)a->gsplit * a->B * a->Tk * a->Hk * a->D * 4);
     return (size_t)n;
@@ -935,6 +1067,14 @@ void place_attn_backward(AttnArgs *a, void *workspace)
     p += round16((int64_t)a->axes * a->B * a->Tk * 8);
     a->fars = (int32_t *)p;
     p += round16(a->axes > 0 ? a->B * nt * 8 : 0);
+    if (a->f16) {
+        a->norm_most = (float *)p;
+        p += round16(a->B * nt * a->Hq * 4);
+        a->v_most = (float *)p;
+        p += round16(a->B * nt * a->Hq * 4);
+        a->norms = (float *)p;
+        p += round16(rows * a->Hq * 4);
+    }
     a->part_dk = (float *)p;
     p += round16((int64_t)a->gsplit * a->B * a->Tk * a->Hk * a->D * 4);
     a->part_dv = (float *)p;

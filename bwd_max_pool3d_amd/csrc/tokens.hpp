@@ -103,6 +103,12 @@ struct AttnArgs {
     int32_t *fars;             // (B, ceil(Tq / 32), 2): is a position 2^24 or more among these 32
                                // queries, among this share of the keys (with a bias)
     float *part_dk, *part_dv;  // (gsplit, B, Tk, Hk, D), when gsplit > 1
+    // backward in float16 (attention_bwd.hip, range): |do|_1 of each query, the
+    // largest of each 32, and the largest finite |v| of a workgroup's share of the
+    // keys
+    int32_t f16;
+    float *norms;              // (B, Hq, Tq)
+    float *norm_most, *v_most; // (B, Hq, ceil(Tq / 32)) each
 };
 // Scores with a cap, a bias or a factor that is not positive: kernels of
 // their own, whose registers the plain ones do not carry.
