@@ -523,7 +523,7 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
 #pragma unroll
                 for (int r = 0; r < 16; ++r) dp[r] *= fmaf(f2 * s[r], s[r], 1.f);
             }
-            if (GEN)
+            if (GEN && signed_axes != 0)
                 add_bias(s, pk + st * 3 * kPos + (half ? KB : col), kPos, signed_axes, pq, sl);
             const bool part = !(alo <= k0 && k0 + KB <= ahi);
             // (rows were dropped for the whole workgroup: a wave that sees all
@@ -856,7 +856,8 @@ void attn_dkv_kernel(AttnArgs a)
                 for (int r = 0; r < 16; ++r) dp[r] *= fmaf(f2 * s[r], s[r], 1.f);
             }
         }
-        if (GEN) add_bias(s, pq(st) + (half ? QB : col), kPos, signed_axes, pk, sl);
+        if (GEN && signed_axes != 0)
+            add_bias(s, pq(st) + (half ? QB : col), kPos, signed_axes, pk, sl);
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
             s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], sc.mul, -lr[r]));

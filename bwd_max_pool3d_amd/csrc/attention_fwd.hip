@@ -243,7 +243,7 @@ int n = 0;
 #pragma unroll
             for (int u = 0; u < 2; ++u) cap_scores<T>(s[u], sc);
         }
-        if (GEN) {
+        if (GEN && signed_axes != 0) {
             const u32x2 *const rows = pk + buf * 3 * kFwdPos + (half ? KB : col);
 #pragma unroll
             for (int u = 0; u < 2; ++u)
