@@ -234,8 +234,8 @@ int attn_args(const mp3d_attention *d, AttnArgs *a)
         too_many(d->B, d->Tq, d->Hq, d->D) || too_many(d->B, d->Tk, d->Hk, d->D))
         return fail(MP3D_EOVERFLOW, "B*T*H*D is out of range");
     if (d->causal != 0 && d->causal != 1) return fail(MP3D_EINVAL, "causal must be 0 or 1");
-    if (!(d->softcap >= 0.f) || d->softcap > 1e30f)
-        return fail(MP3D_EINVAL, "softcap must be finite and >= 0 (0: none)");
+    if (!(d->softcap == 0.f || (d->softcap >= 1e-30f && d->softcap <= 1e30f)))
+        return fail(MP3D_EINVAL, "softcap must be 0 (none) or in 1e-30 .. 1e30");
     if (!(d->scale == d->scale) || d->scale > 1e30f || d->scale < -1e30f)
         return fail(MP3D_EINVAL, "scale must be finite");
     if (d->prefix && !d->causal) return fail(MP3D_EINVAL, "a prefix needs causal");

@@ -657,7 +657,10 @@ __device__ __forceinline__ Span row_span(const AttnArgs &a, int b, int i)
 // --- scores: from the accumulated products q.k to exponents of 2.  The
 // scale is left to the exponent's own multiply-add (exponent = score * mul -
 // maximum) and divided out of the cap and of the bias' slopes, unless it is
-// not positive: the largest score would not have the largest exponent.
+// not positive: the largest score would not have the largest exponent.  With a
+// cap it is left only where the cap in these units and its reciprocal (its
+// sixth power, in cap_scores) are well within binary32; else the scores are
+// multiplied by the scale, or for a small cap by scale / cap.
 struct Scores {
     bool multiply;                         // by `scale` first
     float scale, mul;
@@ -667,9 +670,17 @@ struct Scores {
 
 __device__ __forceinline__ Scores scores(const AttnArgs &a)
 {
+    if (a.cap > 0.f) {
+        const float per = a.scale / a.cap;
+        if (a.scale > 1e-6f && a.scale < 1e6f && per < 1e6f)
+            return {false, a.scale, a.scale * kLog2e, 1.f / a.scale, a.cap / a.scale, per};
+        if (a.cap < 1e-3f)                 // (past 1e38 a score is 0 or beyond the cap)
+            return {true, fminf(fmaxf(per, -1e38f), 1e38f), a.cap * kLog2e, 1.f / a.cap, 1.f, 1.f};
+        return {true, a.scale, kLog2e, 1.f, a.cap, 1.f / a.cap};
+    }
     const bool multiply = !(a.scale > 1e-30f);
     const float unit = multiply ? 1.f : a.scale;
-    return {multiply, a.scale, unit * kLog2e, 1.f / unit, a.cap / unit, unit / a.cap};
+    return {multiply, a.scale, unit * kLog2e, 1.f / unit, 0.f, 0.f};
 }
 
 // (a branch: as a choice between two results it would be in every tile)
@@ -783,7 +794,6 @@ __device__ __forceinline__ void cap_scores(f32x16 &s, const Scores &sc)
     float big = fabsf(s[0]);
 #pragma unroll
     for (int r = 1; r < 16; ++r) big = fmaxf(big, fabsf(s[r]));
-    // (written so that a NaN takes the other branch)
     if (!__any(!(big * f < 0.25f))) {
         const float f2 = f * f, c3 = -f2 / 3.f, c5 = f2 * f2 * (2.f / 15.f),
                     c7 = f2 * f2 * f2 * (-17.f / 315.f);
@@ -799,6 +809,14 @@ __device__ __forceinline__ void cap_scores(f32x16 &s, const Scores &sc)
             s[r] = fmaf(-2.f * sc.cap,
                         __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(s[r] * g)), sc.cap);
     }
+}
+
+// The derivative of a capped score by the score: 1 - tanh^2 (the square of the
+// quotient: the cap's own may leave binary32).
+__device__ __forceinline__ float cap_slope(float s, const Scores &sc)
+{
+    const float t = s * sc.per_cap;
+    return fmaf(-t, t, 1.f);
 }
 
 }  // namespace mp3d

@@ -519,9 +519,8 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
             if (GEN) multiply_scores(s, sc);
             if (GEN && a.cap > 0.f) {
                 cap_scores<T>(s, sc);
-                const float f2 = -sc.per_cap * sc.per_cap;
 #pragma unroll
-                for (int r = 0; r < 16; ++r) dp[r] *= fmaf(f2 * s[r], s[r], 1.f);
+                for (int r = 0; r < 16; ++r) dp[r] *= cap_slope(s[r], sc);
             }
             if (GEN && signed_axes != 0)
                 add_bias(s, pk + st * 3 * kPos + (half ? KB : col), kPos, signed_axes, pq, sl);
@@ -851,9 +850,8 @@ void attn_dkv_kernel(AttnArgs a)
         if (GEN && a.cap > 0.f) {
             cap_scores<T>(s, sc);
             if constexpr (K) {
-                const float f2 = -sc.per_cap * sc.per_cap;
 #pragma unroll
-                for (int r = 0; r < 16; ++r) dp[r] *= fmaf(f2 * s[r], s[r], 1.f);
+                for (int r = 0; r < 16; ++r) dp[r] *= cap_slope(s[r], sc);
             }
         }
         if (GEN && signed_axes != 0)

@@ -356,7 +356,7 @@ int mp3d_rope_backward(const void *gq, const void *gk, void *gq_out, void *gk_ou
 /* Attention of q (B, Tq, Hq, D) over k, v (B, Tk, Hk, D), D <= 128; Hq is a
  * multiple of Hk, and Hq / Hk consecutive query heads share a key head.
  *   s_ij = scale q_i . k_j
- *   s_ij = softcap tanh(s_ij / softcap)                    (softcap > 0)
+ *   s_ij = softcap tanh(s_ij / softcap)      (softcap > 0: 1e-30 .. 1e30)
  *   s_ij = s_ij - sum_a slopes[h, a] |pos_q[a, i] - pos_k[a, j]|   (axes > 0;
  *          any int32: a distance is exact below 2^23, and to its 24 bits beyond)
  *   out_i = sum_j exp(s_ij - lse_i) v_j,  lse_i = log sum_j exp(s_ij)

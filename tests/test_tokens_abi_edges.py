@@ -42,3 +42,12 @@ def test_positions_of_no_tokens_may_be_null(over, code):
     a = ctypes.byref(desc(axes=1, slopes=FAKE, **over))
     for backward in (0, 1):
         assert lib.mp3d_attention_workspace_bytes(a, backward, ctypes.byref(n)) == code
+
+
+@pytest.mark.parametrize("cap,code", [(0.0, _lib.MP3D_OK), (1e-30, _lib.MP3D_OK),
+                                      (1e30, _lib.MP3D_OK), (1e-31, _lib.MP3D_EINVAL),
+                                      (1e-42, _lib.MP3D_EINVAL), (1e31, _lib.MP3D_EINVAL)])
+def test_range_of_caps(cap, code):
+    n = ctypes.c_size_t()
+    a = ctypes.byref(desc(softcap=cap))
+    assert _lib.load().mp3d_attention_workspace_bytes(a, 1, ctypes.byref(n)) == code
