@@ -777,13 +777,15 @@ __device__ __forceinline__ void add_bias(f32x16 &s, const u32x2 *rows, int step,
 }
 
 // The 16 scores of a result to c tanh(s / c).  float32: the library's
-// tanhf, for its relative accuracy near 0.  16-bit types, whose weights keep
-// 2^-9 at best: 1 - 2 / (1 + e^2x), within 2e-7; and where no score of the
+// tanhf, for its relative accuracy near 0.  16-bit types, which keep 2^-9 or
+// 2^-12 of a weight: 1 - 2 / (1 + e^2x), within 2e-7; and where no score of the
 // wave passes c / 4, as with a cap well above the scores, the odd Taylor
 // polynomial, within 1e-7, in 5 instructions instead of 5 of which two (the
-// exponential and the reciprocal) take twice the time or more.
+// exponential and the reciprocal) take twice the time or more.  So a query's
+// last bits depend on the scores of the wave's other queries, but not on what
+// it does not see: a tile of which some is masked (`part`) takes the first form.
 template <typename T>
-__device__ __forceinline__ void cap_scores(f32x16 &s, const Scores &sc)
+__device__ __forceinline__ void cap_scores(f32x16 &s, const Scores &sc, bool part)
 {
     const float f = sc.per_cap;
     if constexpr (T::code == F32::code) {
@@ -794,7 +796,7 @@ __device__ __forceinline__ void cap_scores(f32x16 &s, const Scores &sc)
     float big = fabsf(s[0]);
 #pragma unroll
     for (int r = 1; r < 16; ++r) big = fmaxf(big, fabsf(s[r]));
-    if (!__any(!(big * f < 0.25f))) {
+    if (!part && !__any(!(big * f < 0.25f))) {
         const float f2 = f * f, c3 = -f2 / 3.f, c5 = f2 * f2 * (2.f / 15.f),
                     c7 = f2 * f2 * f2 * (-17.f / 315.f);
 #pragma unroll

@@ -105,7 +105,7 @@ __device__ __forceinline__ bool few_keys_delta(const AttnArgs &a, int b, int h, 
         }
         const Scores sc = scores(a);
         multiply_scores(s, sc);
-        if (a.cap > 0.f) cap_scores<T>(s, sc);
+        if (a.cap > 0.f) cap_scores<T>(s, sc, true);
         for (int x = 0; x < a.axes; ++x) {
             const int64_t row = (int64_t)x * a.B + b;
             const double pq = a.pos_q[row * a.Tq + i];
@@ -516,15 +516,15 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
 #pragma unroll
                 for (int r = 0; r < 16; ++r) dp[r] += delta;
             }
+            const bool part = !(alo <= k0 && k0 + KB <= ahi);
             if (GEN) multiply_scores(s, sc);
             if (GEN && a.cap > 0.f) {
-                cap_scores<T>(s, sc);
+                cap_scores<T>(s, sc, part);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) dp[r] *= cap_slope(s[r], sc);
             }
             if (GEN && signed_axes != 0)
                 add_bias(s, pk + st * 3 * kPos + (half ? KB : col), kPos, signed_axes, pq, sl);
-            const bool part = !(alo <= k0 && k0 + KB <= ahi);
             // (rows were dropped for the whole workgroup: a wave that sees all
             // of the tile meets them too)
             if (!(galo <= k0 && k0 + KB <= gahi) && *flag) {
@@ -848,7 +848,7 @@ void attn_dkv_kernel(AttnArgs a)
         issued<T>();
         if (GEN) multiply_scores(s, sc);
         if (GEN && a.cap > 0.f) {
-            cap_scores<T>(s, sc);
+            cap_scores<T>(s, sc, part);
             if constexpr (K) {
 #pragma unroll
                 for (int r = 0; r < 16; ++r) dp[r] *= cap_slope(s[r], sc);

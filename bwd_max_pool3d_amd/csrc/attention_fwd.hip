@@ -235,13 +235,14 @@ int n = 0;
         products_and_reads<T, NC, 1>();
         products_and_reads<T, NC, 2>();
         issued<T>();
+        const bool part = !(alo <= k0 && k0 + KB <= ahi);
         if (GEN) {
             multiply_scores(s[0], sc);
             multiply_scores(s[1], sc);
         }
         if (GEN && a.cap > 0.f) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) cap_scores<T>(s[u], sc);
+            for (int u = 0; u < 2; ++u) cap_scores<T>(s[u], sc, part);
         }
         if (GEN && signed_axes != 0) {
             const u32x2 *const rows = pk + buf * 3 * kFwdPos + (half ? KB : col);
@@ -249,7 +250,6 @@ int n = 0;
             for (int u = 0; u < 2; ++u)
                 add_bias(s[u], rows + u * 32, kFwdPos, signed_axes, pq, sl);
         }
-        const bool part = !(alo <= k0 && k0 + KB <= ahi);
         if (part) {
             const uint32_t at = k0 + 4 * half - sp.lo, len = sp.hi - sp.lo;
 #pragma unroll
@@ -265,7 +265,7 @@ int n = 0;
         for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[1][r]);
         mx = halves_max(mx) * sc.mul;
         if (__any(mx > m + kRaise)) {
-            // (each query by itself: its result does not depend on its neighbours)
+            // (each query by itself: its sums do not depend on its neighbours')
             const float mn = mx > m + kRaise ? mx : m;
             const float al = __builtin_amdgcn_exp2f(m - (mn == kNegInf ? 0.f : mn));
             l *= al;

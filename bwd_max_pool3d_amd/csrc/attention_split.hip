@@ -183,7 +183,7 @@ void attn_split_kernel(AttnArgs a)
             if (more) fetch(vd, vp, a.vs[1], k0 + NW * KB, lds_v);
 
             if (GEN) multiply_scores(s, sc);
-            if (GEN && a.cap > 0.f) cap_scores<T>(s, sc);
+            if (GEN && a.cap > 0.f) cap_scores<T>(s, sc, part);
 #pragma unroll
             for (int x = 0; x < 3; ++x) {
                 if (x >= axes) break;
@@ -206,7 +206,7 @@ void attn_split_kernel(AttnArgs a)
             for (int e = 1; e < 16; ++e) mx = fmaxf(mx, s[e]);
             mx = halves_max(mx) * sc.mul;
             if (__any(mx > m + kRaise)) {
-                // (each query by itself: its result does not depend on its neighbours)
+                // (each query by itself: its sums do not depend on its neighbours')
                 const float mn = mx > m + kRaise ? mx : m;
                 const float al = __builtin_amdgcn_exp2f(m - (mn == kNegInf ? 0.f : mn));
                 l *= al;
