@@ -387,7 +387,15 @@ int mp3d_gated_norm_backward(const void *dy, const void *dz, const void *x, cons
     int rc = norm_plan(&p, x, h, gate, post_weight, pre_weight, dtype, rows, C, gate_rows,
                        residual_scale, kind, parts, eps);
     if (rc) return rc;
-    if (rows == 0) return MP3D_OK;
+    if (rows == 0) {
+        // sums over no rows
+        if (gate && dgate && too_many(gate_rows, C, 1, 1))
+            return fail(MP3D_EOVERFLOW, "gate_rows*C is out of range");
+        p.dgate = gate ? dgate : nullptr;
+        p.dpost = dpost_weight;
+        p.dpre = dpre_weight;
+        return hip_status(launch_norm_no_rows(p, (hipStream_t)stream), "gated norm launch");
+    }
     if (!stats || !dx || (h && !dh) || (p.has_pre && !dz))
         return fail(MP3D_EINVAL, "stats, dz or an output is NULL");
     if ((dgate == nullptr) != (gate == nullptr))

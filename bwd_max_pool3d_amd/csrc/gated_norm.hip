@@ -415,6 +415,16 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(NormPlan p)
     }
 }
 
+// Zeros to one of the sums: blockIdx.y 0 dpost, 1 dpre, 2 dgate.
+__global__ __launch_bounds__(256) void norm_zero_kernel(NormPlan p)
+{
+    float *out = blockIdx.y == 0 ? p.dpost : blockIdx.y == 1 ? p.dpre : p.dgate;
+    if (!out) return;
+    const int64_t n = blockIdx.y == 2 ? p.gate_rows * p.C : p.C;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+        out[i] = 0.f;
+}
+
 template <typename T, int TPR, int EPT>
 void forward_v(const NormPlan &p, hipStream_t s)
 {
@@ -511,6 +521,17 @@ hipError_t launch_norm_backward(const NormPlan &p, hipStream_t s)
     if (p.dpost || p.dpre || jobs > 2)
         launch_kernel(norm_join_kernel, dim3((uint32_t)((p.C + 63) / 64), (uint32_t)jobs),
                       dim3(1024), 0, s, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_norm_no_rows(const NormPlan &p, hipStream_t s)
+{
+    if (!p.dpost && !p.dpre && !p.dgate) return hipSuccess;
+    const int64_t n = p.dgate && p.gate_rows > 1 ? p.gate_rows * p.C : p.C;
+    const int64_t blocks = (n + 255) / 256;
+    launch_kernel(norm_zero_kernel,
+                  dim3((uint32_t)(blocks < kMaxTileGrid ? blocks : kMaxTileGrid), 3), dim3(256), 0, s,
+                  p);
     return hipGetLastError();
 }
 

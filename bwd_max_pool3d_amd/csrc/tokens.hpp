@@ -67,6 +67,8 @@ template <typename T>
 hipError_t launch_norm_forward(const NormPlan &p, hipStream_t s);
 template <typename T>
 hipError_t launch_norm_backward(const NormPlan &p, hipStream_t s);
+// zeros to dgate, dpost and dpre, where they are given
+hipError_t launch_norm_no_rows(const NormPlan &p, hipStream_t s);
 
 // --- attention (attention_*.hip)
 constexpr int kAttnMaxD = 128;

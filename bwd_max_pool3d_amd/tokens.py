@@ -391,10 +391,6 @@ def mp3d_gated_norm_backward(dy: torch.Tensor | None, dz: torch.Tensor | None, x
     dgate = None if gate is None else new(gate_rows, C).view(gate.shape)
     dpost = None if post_weight is None else new(C)
     dpre = None if pre_weight is None else new(C)
-    if rows == 0:
-        for t in (dgate, dpost, dpre):
-            if t is not None:
-                t.zero_()
     nbytes = ctypes.c_size_t()
     _lib.check(lib.mp3d_gated_norm_workspace_bytes(code, rows, C, gate_rows,
                                                    ctypes.byref(nbytes)))

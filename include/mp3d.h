@@ -439,7 +439,7 @@ int mp3d_gated_norm_workspace_bytes(int dtype, int64_t rows, int32_t C, int64_t 
 
 /* Gradients from those of y (dy, or NULL: 0) and z (dz): dx and dh in the
  * storage type, dgate (gate_rows, C) and the weights' in float32, summed
- * over the rows in a fixed order.  dgate goes with gate; a weight's
+ * over the rows in a fixed order (0 without rows).  dgate goes with gate; a weight's
  * gradient may be NULL (not wanted). */
 int mp3d_gated_norm_backward(const void *dy, const void *dz, const void *x, const void *h,
                              const void *gate, const void *post_weight, const void *pre_weight,

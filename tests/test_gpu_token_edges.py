@@ -1,10 +1,13 @@
 """The token operators at the ends of their ranges: no queries, no rows, more
 rows than one launch takes, keys that are not finite."""
+import ctypes
+
 import pytest
 import torch
 
 import _tokens as tk
 import bwd_max_pool3d_amd as mp
+from bwd_max_pool3d_amd import _lib
 from test_gpu_attention import make, run
 
 pytestmark = pytest.mark.gpu
@@ -86,3 +89,29 @@ def test_dq_of_a_key_with_score_minus_infinity(D, dt):
         value, tol = want[name]
         first = 1 if name == "dq" else 0
         tk.close(got[name][:, -n:, :, first:], value[..., first:], tol[..., first:], name)
+
+
+def test_norm_sums_of_no_rows():
+    """The gradients of the weights and the gate over no rows are zeros, by
+    the C entry as by the binding."""
+    C, G = 100, 3
+    lib = _lib.load()
+    need = ctypes.c_size_t()
+    assert lib.mp3d_gated_norm_workspace_bytes(_lib.MP3D_F32, 0, C, G, ctypes.byref(need)) == 0
+    w = torch.ones(C, device="cuda")
+    gate = torch.ones(G, C, device="cuda")
+    sums = [torch.full((n, C), float("nan"), device="cuda") for n in (G, 1, 1)]
+    assert lib.mp3d_gated_norm_backward(
+        None, None, None, None, gate.data_ptr(), w.data_ptr(), w.data_ptr(), None, None, None,
+        *[t.data_ptr() for t in sums], _lib.MP3D_F32, 0, C, G, 1.0, _lib.MP3D_NORM_RMS, 3, 1e-6,
+        None, 0, torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    for t in sums:
+        assert torch.equal(t, torch.zeros_like(t))
+    e = torch.empty((0, C), device="cuda")
+    how = dict(gate=gate, post_weight=w, pre_weight=w)
+    _, _, stats = mp.mp3d_gated_norm_forward(e, e, **how)
+    dx, dh, *got = mp.mp3d_gated_norm_backward(e, e, e, e, stats, **how)
+    assert dx.shape == dh.shape == e.shape
+    for t, like in zip(got, (gate, w, w)):
+        assert torch.equal(t, torch.zeros_like(like))
