@@ -64,10 +64,11 @@ PR308_CONTEXT_US = 3.0
 
 
 def kernel_source_hash() -> str:
-    """Hash of the pooling kernels' sources; stored traffic counters are
-    reported only while it matches the hash they were measured at."""
+    """Hash of the pooling kernels' sources, of what chooses among them and
+    of the compiler's flags; stored traffic counters are reported only while
+    it matches the hash they were measured at."""
     from bwd_max_pool3d_amd import _build
-    h = hashlib.sha256()
+    h = hashlib.sha256(" ".join(_build.HIPCC_FLAGS).encode())
     for name in _build.POOL_KERNELS:
         with open(os.path.join(_build.CSRC, name), "rb") as f:
             h.update(f.read())

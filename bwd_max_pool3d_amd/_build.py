@@ -17,9 +17,10 @@ SOURCES = ["api.hip", "plan.hip", "forward.hip", "forward_fixed.hip", "forward_c
            "backward.hip", "backward_owner.hip", "small.hip", "forward_ex.hip",
            "api_tokens.hip", "rope.hip", "gated_norm.hip", "attention_fwd.hip",
            "attention_split.hip", "attention_bwd.hip", "attention_order.hip"]
-# the pooling kernels and what they include
-POOL_KERNELS = ["plan.hip", "forward.hip", "forward_fixed.hip", "forward_col.hip",
-                "backward.hip", "backward_owner.hip", "small.hip", "forward_ex.hip",
+# the pooling kernels, what chooses among them, and what they include
+POOL_KERNELS = ["api.hip", "api_common.hpp", "plan.hip", "forward.hip", "forward_fixed.hip",
+                "forward_col.hip", "backward.hip", "backward_owner.hip", "small.hip",
+                "forward_ex.hip",
                 "colstage.hpp", "dtype.hpp", "geometry.hpp", "idxsrc.hpp", "kernels.hpp"]
 
 HIPCC_FLAGS = [
