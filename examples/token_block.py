@@ -58,8 +58,7 @@ class Block:
         q, k = mp.mp3d_rope_forward(q, k, self.inv_freq, PAIRS, grid=grid)
         o, lse = mp.mp3d_attention_forward(q, k, v, softcap=CAP, causal=True)
         h = o.view(t.shape) @ self.wo
-        y, zn, s1 = mp.mp3d_gated_norm_forward(t, h, gate=self.gate.expand(t.shape[0], -1)
-                                               .contiguous(), post_weight=self.post,
+        y, zn, s1 = mp.mp3d_gated_norm_forward(t, h, gate=self.gate, post_weight=self.post,
                                                pre_weight=self.pre)
         return y, zn, (t, z, q, k, v, o, lse, h, s0, s1)
 
@@ -68,8 +67,7 @@ class Block:
         the norms', which come with it)."""
         t, z, q, k, v, o, lse, h, s0, s1 = kept
         dt, dh, dgate, dpost, dpre = mp.mp3d_gated_norm_backward(
-            dy, dz, t, h, s1, gate=self.gate.expand(t.shape[0], -1).contiguous(),
-            post_weight=self.post, pre_weight=self.pre)
+            dy, dz, t, h, s1, gate=self.gate, post_weight=self.post, pre_weight=self.pre)
         do = (dh @ self.wo.t()).view_as(o)
         dq, dk, dv = mp.mp3d_attention_backward(do, q, k, v, o, lse, softcap=CAP, causal=True)
         dq, dk = mp.mp3d_rope_backward(dq, dk, self.inv_freq, PAIRS, grid=grid)
@@ -91,8 +89,7 @@ class Block:
         lengths += 1
         o, _ = mp.mp3d_attention_forward(q, kc, vc, softcap=CAP, causal=True, kv_len=lengths)
         h = o.view(t.shape) @ self.wo
-        return mp.mp3d_gated_norm_forward(t, h, gate=self.gate.expand(t.shape[0], -1)
-                                          .contiguous(), post_weight=self.post,
+        return mp.mp3d_gated_norm_forward(t, h, gate=self.gate, post_weight=self.post,
                                           pre_weight=self.pre)[:2]
 
 
