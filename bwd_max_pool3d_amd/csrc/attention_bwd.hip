@@ -32,12 +32,12 @@
 // us; max |v| by a launch of its own 372).
 //
 // Bound: with 64 channels and a bias the vector unit and the waits between
-// its work and the matrix unit's (vector 42 %, matrix 25 % of the cycles busy
-// in dk, dv; 44 and 29 % in dq), with 128 the waits.  Measured: 8192 packed
+// its work and the matrix unit's (vector 41 %, matrix 25 % of the cycles busy
+// in dk, dv; 43 and 29 % in dq), with 128 the waits.  Measured: 8192 packed
 // bfloat16 tokens in 9 documents, 16 heads of 64, bias on 3 axes: constants
-// 13 us, dk and dv 208, dq 140.  2 x 2047 float16, causal with a prefix, 16
-// heads of 128 on 2: 9.5, 174 and its parts' sum 15.5, 122.  32 x 245 float32,
-// 4 heads of 64, bias on 3 axes: 9, 74, 45.
+// 13 us, dk and dv 208, dq 137.  2 x 2047 float16, causal with a prefix, 16
+// heads of 128 on 2: 12.5, 175 and its parts' sum 15.5, 122.  32 x 245 float32,
+// 4 heads of 64, bias on 3 axes: 8, 76, 47.
 #include <type_traits>
 
 #include "attention.hpp"
@@ -1023,7 +1023,7 @@ int64_t round16(int64_t bytes) { return (bytes + 15) & ~(int64_t)15; }
 }  // namespace
 
 // A key head's query heads are dealt out until two workgroups a CU are there
-// (2 x 2047 with 8 heads a key head: dk, dv 174 us and 15.5 for the sum of the
+// (2 x 2047 with 8 heads a key head: dk, dv 175 us and 15.5 for the sum of the
 // parts, 740 without).  Workspace: tiles, spans, rowd, the blocks' orders, the
 // positions and what is far of them, float16's bounds, then the parts (each
 // at a multiple of 16 bytes).

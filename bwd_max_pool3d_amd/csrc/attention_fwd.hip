@@ -24,8 +24,8 @@
 //
 // Measured: 10935 causal bfloat16 tokens, 16 heads of 128 on 4, cap 50:
 // 605 to 675 us by the card's clock (730 to 810 TFLOP/s of visible pairs; 70 %
-// of the cycles the vector unit is busy, 38 % the matrix unit).  8192 packed
-// tokens in 9 documents, 16 heads of 64, bias on 3 axes: 126 us (of which
+// of the cycles the vector unit is busy, 39 % the matrix unit).  8192 packed
+// tokens in 9 documents, 16 heads of 64, bias on 3 axes: 125 us (of which
 // the bias was 40 on the vector unit alone).  2 x 2047 float16, prefix, 16
 // heads of 128 on 2: 64 us.
 #include "attention.hpp"

@@ -3,7 +3,7 @@
 // would run on an almost idle card.  One small workgroup per sequence ranks
 // the blocks by the keys (queries) they walk; the attention kernels look
 // their block up.  On 8192 tokens in 9 documents of 178 to 1605, 16 heads of
-// 64 with a distance bias, the three kernels take 126, 141 and 210 us with it
+// 64 with a distance bias, the three kernels take 125, 137 and 208 us with it
 // and 168, 184 and 266 without; the ranking takes 4.5 us forward, 13
 // backward.  Up to kOrderMax blocks (one thread each); beyond that there are
 // so many that the last ones no longer count.

@@ -227,7 +227,8 @@ def mp3d_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
     """Attention of q (B, Tq, Hq, D) over k, v (B, Tk, Hk, D): (out, lse),
     out (B, Tq, Hq, D) and lse float32 (B, Hq, Tq).
 
-    ``scale`` None: 1 / sqrt(D).  ``softcap`` c > 0: scores c tanh(s / c).
+    ``scale`` None: 1 / sqrt(D).  ``softcap`` c (1e-30 to 1e30): scores
+    c tanh(s / c).
     ``slopes`` float32 (Hq, axes) with ``pos_q`` (axes, B, Tq) and ``pos_k``
     (axes, B, Tk) int32: minus slope times distance, summed over 1 to 3
     axes.  ``kv_len`` int32 (B): keys in use, the queries the last Tq of

@@ -315,7 +315,10 @@ int mp3d_time_next_call(void *start_event, void *stop_event);
  *
  * Storage types: MP3D_F32, MP3D_F16, MP3D_BF16 (MP3D_F64: MP3D_EDTYPE).
  * Every sum, softmax statistic and norm is held in binary32 and rounded
- * once on its way out.  Strides are in elements, for (batch, token, head),
+ * once on its way out.  Attention's weights, and in its backward their
+ * gradients, are rounded to the storage type on the way, as operands of a
+ * second matrix product (in float16 times powers of two that keep them in its
+ * range).  Strides are in elements, for (batch, token, head),
  * and >= 0; a head's channels are adjacent.  Accesses are 16 bytes wide
  * where every row starts at a multiple of 16 bytes, and element-wise
  * otherwise.  Streams, errors, MP3D_LOG and mp3d_time_next_call are as for
