@@ -115,3 +115,59 @@ def test_norm_sums_of_no_rows():
     assert dx.shape == dh.shape == e.shape
     for t, like in zip(got, (gate, w, w)):
         assert torch.equal(t, torch.zeros_like(like))
+
+
+@pytest.mark.parametrize("dt", tk.TYPES, ids=tk.name_of)
+def test_attention_training_under_graph_capture(dt):
+    """Forward and backward with documents, a bias of near and then of far
+    positions, a cap, and gradients of other sizes, captured once: every replay
+    gives the eager bits."""
+    T, H, D = 300, 4, 64
+    docs = torch.tensor([[0, 90, 170, 300]], dtype=torch.int32, device="cuda")
+    slopes = torch.full((H, 2), 0.05, device="cuda")
+    pos = torch.zeros((2, 1, T), dtype=torch.int32, device="cuda")
+    q, k, v, do = (torch.zeros((1, T, h, D), dtype=dt, device="cuda") for h in (H, 2, 2, H))
+
+    def both():
+        how = dict(causal=True, softcap=30.0, doc_offsets=docs, slopes=slopes, pos_q=pos,
+                   pos_k=pos)
+        out, lse = mp.mp3d_attention_forward(q, k, v, **how)
+        return (out, lse) + mp.mp3d_attention_backward(do, q, k, v, out, lse, **how)
+
+    cells = torch.stack((torch.arange(T) // 20, torch.arange(T) % 20)).int()[:, None].cuda()
+    far = cells.clone()
+    far[:, :, 170:] += 1 << 30
+    inputs = []
+    for n, (p, size) in enumerate(((cells, 1.0), (far, 2.0 ** -12), (cells, 2.0 ** 10))):
+        ten = [t.cuda() for t in make(1, T, T, H, 2, D, dt, 90 + n)]
+        inputs.append((p, ten[:3] + [(ten[3].float() * size).to(dt)]))
+
+    def load(p, ten):
+        pos.copy_(p)
+        for t, new in zip((q, k, v, do), ten):
+            t.copy_(new)
+
+    want = []
+    for p, ten in inputs:
+        load(p, ten)
+        want.append([t.clone() for t in both()])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        both()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both()
+    for rep in range(3):
+        for (p, ten), ref in zip(inputs, want):
+            load(p, ten)
+            for t in got:
+                t.fill_(float("nan"))
+            graph.replay()
+            torch.cuda.synchronize()
+            for a, b in zip(got, ref):
+                assert torch.equal(a, b)
+            both()                                       # eager work between the replays
+            torch.cuda.synchronize()
