@@ -36,7 +36,7 @@
 // in dk, dv; 43 and 29 % in dq), with 128 the waits.  Measured: 8192 packed
 // bfloat16 tokens in 9 documents, 16 heads of 64, bias on 3 axes: constants
 // 13 us, dk and dv 208, dq 137.  2 x 2047 float16, causal with a prefix, 16
-// heads of 128 on 2: 12.5, 175 and its parts' sum 15.5, 122.  32 x 245 float32,
+// heads of 128 on 2: 12, 175 and its parts' sum 15.5, 122.  32 x 245 float32,
 // 4 heads of 64, bias on 3 axes: 8, 76, 47.
 #include <type_traits>
 
@@ -185,6 +185,7 @@ __global__ __launch_bounds__(256, 6) void attn_rows_kernel(AttnArgs a)
     const int qt = (int)(id - bh * nt);
     const int b = (int)(bh / a.Hq), h = (int)(bh - (int64_t)b * a.Hq);
     const int row = threadIdx.x >> 3, sub = threadIdx.x & 7, i = qt * 32 + row;
+    const float l = a.lse[bh * a.Tq + min(i, a.Tq - 1)];
     float s = 0.f, norm = 0.f, value = 0.f;    // norm: |do|_1; value: |v| of a share of the keys
     if constexpr (ranged<T>()) {
         const int hk = h / a.G, shares = nt * a.G, per = (a.Tk + shares - 1) / shares;
@@ -228,8 +229,7 @@ __global__ __launch_bounds__(256, 6) void attn_rows_kernel(AttnArgs a)
     }
     if constexpr (ranged<T>()) {
         // (what is not finite has no bound; a query that sees nothing no say)
-        const bool some = i < a.Tq && norm < kInf &&
-                          a.lse[bh * a.Tq + min(i, a.Tq - 1)] != kNegInf;
+        const bool some = i < a.Tq && norm < kInf && l != kNegInf;
         norm = some ? norm : 0.f;
         if (sub == 0 && i < a.Tq) a.norms[bh * a.Tq + i] = norm;
         __shared__ float most[2][4];
@@ -255,7 +255,6 @@ __global__ __launch_bounds__(256, 6) void attn_rows_kernel(AttnArgs a)
     }
     if (sub == 0 && i < a.Tq) {
         const int64_t at = bh * a.Tq + i;
-        const float l = a.lse[at];
         // a row without weights: its exponents become -inf
         *(float2 *)(a.rowd + 2 * at) = make_float2(
             l == kNegInf ? kInf : fmaf(l, kLog2e, ranged<T>() ? -(float)kWeightBits : 0.f), -s);
