@@ -174,6 +174,20 @@ __device__ __forceinline__ int keys_share(const AttnArgs &a)
     return max((a.Tk + nt - 1) / nt, 1);
 }
 
+// float16: keys whose |v| a workgroup of the constants looks at, and how many
+// of a key head's workgroups do.  (Not fewer than it has rows of threads for:
+// the other kernels read one number for each.)
+__device__ __forceinline__ int value_share(const AttnArgs &a)
+{
+    const int shares = (a.Tq + 31) / 32 * a.G;
+    return max((a.Tk + shares - 1) / shares, 16);
+}
+__device__ __forceinline__ int value_parts(const AttnArgs &a)
+{
+    const int per = value_share(a);
+    return (a.Tk + per - 1) / per;
+}
+
 // One workgroup per 32 queries of one head: 8 threads per row.
 template <typename T>
 __global__ __launch_bounds__(256, 6) void attn_rows_kernel(AttnArgs a)
@@ -188,16 +202,17 @@ __global__ __launch_bounds__(256, 6) void attn_rows_kernel(AttnArgs a)
     const float l = a.lse[bh * a.Tq + min(i, a.Tq - 1)];
     float s = 0.f, norm = 0.f, value = 0.f;    // norm: |do|_1; value: |v| of a share of the keys
     if constexpr (ranged<T>()) {
-        const int hk = h / a.G, shares = nt * a.G, per = (a.Tk + shares - 1) / shares;
+        const int hk = h / a.G, per = value_share(a);
         const int L = a.kv_len ? min(a.kv_len[b], a.Tk) : a.Tk;        // (past it: nobody's)
-        const int first = ((h - hk * a.G) * nt + qt) * per, c = (threadIdx.x & 15) * 8;
+        const int64_t first = ((int64_t)(h - hk * a.G) * nt + qt) * per;
+        const int c = (threadIdx.x & 15) * 8;
         const R *v = (const R *)a.v + b * a.vs[0] + hk * a.vs[2];
 #pragma unroll 2
-        for (int k = first + (threadIdx.x >> 4); k < min(first + per, L); k += 16) {
+        for (int64_t k = first + (threadIdx.x >> 4); k < min(first + per, (int64_t)L); k += 16) {
             struct alignas(16) {
                 R e[8];
             } x = __builtin_bit_cast(decltype(x),
-                                     load8<T>(v + (int64_t)k * a.vs[1], c, a.D, a.vec));
+                                     load8<T>(v + k * a.vs[1], c, a.D, a.vec));
 #pragma unroll
             for (int n = 0; n < 8; ++n) {
                 const float y = fabsf(T::widen(x.e[n]));
@@ -401,11 +416,13 @@ __global__ __launch_bounds__(64 * kBwdWaves, (bwd_occupancy<T, DP>())) void attn
     float lse2 = rd.x, delta = rd.y;       // (delta negated)
     int xq = 0;                            // what e is rounded over, its exponent
     if constexpr (ranged<T>()) {
-        float most = 0.f;
+        const float norm = a.norms[(int64_t)bh * a.Tq + ic];
         const float *v = a.v_most + ((int64_t)b * a.Hq + hk * a.G) * nt;
+        const int parts = value_parts(a);
+        float most = 0.f;
 #pragma unroll 4
-        for (int t = lane; t < nt * a.G; t += 64) most = fmaxf(most, v[t]);
-        xq = range_exponent(a.norms[(int64_t)bh * a.Tq + ic], wave_max(most));
+        for (int t = lane; t < parts; t += 64) most = fmaxf(most, v[t]);
+        xq = range_exponent(norm, wave_max(most));
         lse2 += (float)(kWeightBits + xq);
     }
     arrived(qf);
@@ -626,7 +643,8 @@ void attn_dkv_kernel(AttnArgs a)
         float norm = 0.f, value = 0.f;
         if constexpr (ranged<T>()) {
             const float *v = a.v_most + ((int64_t)b * a.Hq + hk * a.G) * nt;
-            for (int t = tid; t < nt * a.G; t += NT) value = fmaxf(value, v[t]);
+            const int parts = nt > 0 ? value_parts(a) : 0;
+            for (int t = tid; t < parts; t += NT) value = fmaxf(value, v[t]);
         }
         for (int t = tid; t < nt; t += NT) {
             float here = 0.f;

@@ -110,7 +110,7 @@ struct AttnArgs {
     // keys
     int32_t f16;
     float *norms;              // (B, Hq, Tq)
-    float *norm_most, *v_most; // (B, Hq, ceil(Tq / 32)) each
+    float *norm_most, *v_most; // (B, Hq, ceil(Tq / 32)) each (of v a key head's first value_parts)
 };
 // Scores with a cap, a bias or a factor that is not positive: kernels of
 // their own, whose registers the plain ones do not carry.

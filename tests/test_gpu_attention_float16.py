@@ -74,3 +74,14 @@ def test_gradients_of_unequal_size(D, monkeypatch):
     check_f16(got, ten, how, monkeypatch)
     for name in ("dq", "dk", "dv"):
         assert not got[name][1].any()
+
+
+@pytest.mark.parametrize("Tq,Tk,Hq,Hk", [(1, 3000, 8, 2), (33, 17, 4, 1),
+                                         (700, 40, 8, 1), (40, 700, 2, 2)])
+def test_the_largest_value_wherever_it_stands(Tq, Tk, Hq, Hk, monkeypatch):
+    """Shares of the keys of every size, the largest value in the first, the
+    last or the middle key: its gradients do not leave the range."""
+    for n, at in enumerate({0, Tk // 2, Tk - 1}):
+        ten = scaled((2, Tq, Tk, Hq, Hk, 64), 82 + n, 0.05, 0.05, 1.0, 2000.0)
+        ten[2][:, at] *= 64
+        check_f16(run(*ten, {}), ten, {}, monkeypatch)
