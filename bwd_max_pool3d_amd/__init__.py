@@ -32,6 +32,13 @@ Operators over a pooled volume's tokens (bwd_max_pool3d_amd/tokens.py):
   mp3d_gated_norm_backward(dy, dz, x, h, stats, ...) -> (dx, dh, dgate, dpost, dpre)
       norm after a block, gate, residual sum, norm before the next block
 
+Caches of keys and values in 8 or 4 bits (bwd_max_pool3d_amd/caches.py):
+  mp3d_cache_empty(B, T, H, D, format), mp3d_cache_write(k, v, cache, format, ...),
+  mp3d_cache_read(cache, format, D, dtype, ...) -> (k, v)
+  mp3d_attention_cached(q, own, prefix, ...) -> (out, lse)
+      new tokens over such caches or plain ones, behind a prefix that
+      sequences share
+
 The names of the three-call sketch are kept as aliases:
   max_pool3d(x, kernel, stride) = mp3d_forward,
   adaptive_max_pool3d(x, out_size) = amp3d_forward,
@@ -55,7 +62,8 @@ __all__ = ["mp3d_forward", "amp3d_forward", "mp3d_backward", "mp3d_out_size",
            "mp3d_rope_forward", "mp3d_rope_backward", "mp3d_attention_forward",
            "mp3d_attention_backward", "mp3d_attention_workspace_bytes",
            "mp3d_gated_norm_forward", "mp3d_gated_norm_backward",
-           "mp3d_gated_norm_workspace_bytes"]
+           "mp3d_gated_norm_workspace_bytes", "mp3d_cache_empty", "mp3d_cache_write",
+           "mp3d_cache_read", "mp3d_attention_cached", "mp3d_attention_cached_workspace_bytes"]
 
 _IDX = {torch.int32: _lib.MP3D_IDX_I32, torch.int64: _lib.MP3D_IDX_I64}
 
@@ -379,6 +387,8 @@ def max_pool3d_backward(gy: torch.Tensor, idx: torch.Tensor, in_shape, kernel=No
     return mp3d_backward(gy, idx, in_shape, kernel, stride, overlap=overlap_code(overlap), out=out)
 
 
+from .caches import (mp3d_attention_cached, mp3d_attention_cached_workspace_bytes,  # noqa: E402
+                     mp3d_cache_empty, mp3d_cache_read, mp3d_cache_write)
 from .tokens import (mp3d_attention_backward, mp3d_attention_forward,  # noqa: E402
                      mp3d_attention_workspace_bytes, mp3d_gated_norm_backward,
                      mp3d_gated_norm_forward, mp3d_gated_norm_workspace_bytes, mp3d_rope_backward,

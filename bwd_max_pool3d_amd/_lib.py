@@ -24,10 +24,12 @@ EXPORTS = ("mp3d_forward", "amp3d_forward", "mp3d_backward", "mp3d_out_size",
            "mp3d_backward_recompute_static", "mp3d_strerror", "mp3d_last_error",
            "mp3d_rope_forward", "mp3d_rope_backward", "mp3d_attention_workspace_bytes",
            "mp3d_attention_forward", "mp3d_attention_backward", "mp3d_gated_norm_forward",
-           "mp3d_gated_norm_workspace_bytes", "mp3d_gated_norm_backward")
+           "mp3d_gated_norm_workspace_bytes", "mp3d_gated_norm_backward", "mp3d_cache_write",
+           "mp3d_cache_read", "mp3d_attention_cached_workspace_bytes", "mp3d_attention_cached")
 
 MP3D_NORM_RMS, MP3D_NORM_LAYER = 0, 1
 MP3D_NORM_POST, MP3D_NORM_PRE = 1, 2
+MP3D_CACHE_PLAIN, MP3D_CACHE_E4M3, MP3D_CACHE_E2M1 = 0, 1, 2
 
 _i32, _i64, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
 _lib = None
@@ -41,6 +43,22 @@ class Attention(ctypes.Structure):
                 ("causal", ctypes.c_int), ("kv_len", _vp), ("doc_offsets", _vp),
                 ("n_docs", _i32), ("prefix", _vp), ("axes", _i32), ("slopes", _vp),
                 ("pos_q", _vp), ("pos_k", _vp)]
+
+
+class Cache(ctypes.Structure):
+    """struct mp3d_cache (include/mp3d.h)."""
+    _fields_ = [("B", _i64), ("T", _i64), ("k", _vp), ("v", _vp), ("k_scale", _vp),
+                ("v_scale", _vp), ("k_stride", _i64 * 3), ("v_stride", _i64 * 3),
+                ("k_scale_stride", _i64 * 3), ("v_scale_stride", _i64 * 3)]
+
+
+class AttentionCache(ctypes.Structure):
+    """struct mp3d_attention_cache (include/mp3d.h)."""
+    _fields_ = [("dtype", ctypes.c_int), ("format", ctypes.c_int), ("B", _i64), ("Tq", _i64),
+                ("Hq", _i32), ("Hk", _i32), ("D", _i32), ("causal", _i32), ("q_stride", _i64 * 3),
+                ("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("own", Cache),
+                ("prefix", Cache), ("kv_len", _vp), ("prefix_len", _vp), ("axes", _i32),
+                ("slopes", _vp), ("pos_q", _vp), ("pos_k", _vp), ("pos_prefix", _vp)]
 
 
 class Mp3dError(RuntimeError):
@@ -106,6 +124,10 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                                     ctypes.POINTER(_size)]
     lib.mp3d_gated_norm_backward.argtypes = ([_vp] * 13 + [_int, _i64, _i32, _i64, _f32, _int,
                                                           _int, _f32, _vp, _size, _vp])
+    lib.mp3d_cache_write.argtypes = [_vp, _int, _vp, _vp, _int, _i64, _i32, _i32] + [_vp] * 5
+    lib.mp3d_cache_read.argtypes = [_vp, _int, _vp, _vp, _int, _i64, _i32, _i32] + [_vp] * 3
+    lib.mp3d_attention_cached_workspace_bytes.argtypes = [_vp, ctypes.POINTER(_size)]
+    lib.mp3d_attention_cached.argtypes = [_vp] * 5 + [_size, _vp]
     lib.mp3d_strerror.argtypes = [ctypes.c_int]
     lib.mp3d_strerror.restype = ctypes.c_char_p
     lib.mp3d_last_error.argtypes = []
@@ -117,7 +139,9 @@ def load(path: str | None = None) -> ctypes.CDLL:
                  "mp3d_time_next_call", "mp3d_backward_recompute_static", "mp3d_rope_forward",
                  "mp3d_rope_backward", "mp3d_attention_workspace_bytes",
                  "mp3d_attention_forward", "mp3d_attention_backward", "mp3d_gated_norm_forward",
-                 "mp3d_gated_norm_workspace_bytes", "mp3d_gated_norm_backward"):
+                 "mp3d_gated_norm_workspace_bytes", "mp3d_gated_norm_backward",
+                 "mp3d_cache_write", "mp3d_cache_read",
+                 "mp3d_attention_cached_workspace_bytes", "mp3d_attention_cached"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib

@@ -134,4 +134,50 @@ hipError_t launch_attn_forward(const AttnArgs &a, hipStream_t s);
 template <typename T>
 hipError_t launch_attn_split(const AttnArgs &a, hipStream_t s);
 
+// --- caches in 8 or 4 bits (cache.hip), strides in bytes: sequence, token, head
+struct CachePlan {
+    const void *x[2];          // k, v (the read writes them, contiguous (B, T, H, D))
+    int64_t xs[2][3];          // their strides in elements (write)
+    uint8_t *codes[2], *scales[2];
+    int64_t cs[2][3], ss[2][3];
+    const int32_t *start, *count;  // (B) each, or NULL: 0 and T
+    int64_t rows;              // of a sequence's cache
+    int32_t B, T, H, D;
+    int32_t format, vec;
+    int32_t pieces, threads;   // threads of a row, of a workgroup
+    int32_t per, tiles;        // tokens of a workgroup, workgroups of a sequence
+};
+constexpr int kCacheMaxD = 1024;
+void plan_cache(CachePlan *p, int elem_bytes, bool read);
+template <typename T>
+hipError_t launch_cache(const CachePlan &p, bool read, hipStream_t s);
+
+// --- attention over caches (attention_cached.hip): a prefix for every S
+// sequences, and a cache of each sequence's own
+struct CachedPart {
+    const void *k, *v;         // elements, or codes
+    const uint8_t *k_scale, *v_scale;
+    int64_t ks[3], vs[3];      // strides in elements (bytes of codes): cache, token, head
+    int64_t kss[3], vss[3];    // and of the scales, in bytes
+    const int32_t *len;        // tokens in use of each cache, or NULL: T
+    const int32_t *pos;        // (axes, caches, T)
+    int32_t T, caches;
+    int32_t seqs;              // sequences of a cache
+    int32_t width;             // bytes that a load of codes may take: 16, 4 or 1
+    int32_t vec;               // plain: every row starts at a multiple of 16 bytes
+    int32_t rows;              // seqs * Tq * G, of a key head
+    int32_t wr;                // waves with rows of their own (4 / wr share the keys out)
+    int32_t nrb, nsplit, chunk;  // blocks of 32 wr rows, chunks of keys
+    int64_t units, blocks;     // (cache, key head, chunk)s, workgroups
+};
+struct CachedArgs {
+    AttnArgs a;                // q, the scores, out and lse, the parts
+    CachedPart part[2];        // the prefix, the own caches
+    int32_t format;
+};
+size_t plan_attn_cached(CachedArgs *c);
+void place_attn_cached(CachedArgs *c, void *workspace);
+template <typename T>
+hipError_t launch_attn_cached(const CachedArgs &c, hipStream_t s);
+
 }  // namespace mp3d

@@ -415,6 +415,92 @@ int mp3d_attention_backward(const mp3d_attention *a, const void *dout, const int
                             const float *lse, void *dq, void *dk, void *dv, void *workspace,
                             size_t workspace_bytes, void *stream);
 
+/* --- Caches of keys and values, and attention over them ----------------
+ *
+ * A cache holds T rows (tokens) of H heads of D channels for each of B
+ * sequences, keys and values apart: as elements (MP3D_CACHE_PLAIN), or in 8
+ * or 4 bits.  There, 32 adjacent channels x (a head's last group may be
+ * shorter) are held as a scale byte and a code for each channel:
+ *   scale byte s + 127, s the least integer >= -126 with max |x| <= M 2^s
+ *   code       the format's number nearest to x / 2^s, ties to the even last
+ *              bit; but the largest whose value is not past the written type's
+ *              largest number
+ *   value      code 2^s, rounded to the type it is read in
+ * MP3D_CACHE_E4M3: sign, 4 exponent bits (bias 7), 3 fraction bits, M = 448,
+ * code 127 is NaN, a byte each.  MP3D_CACHE_E2M1: sign, 2 exponent bits, 1
+ * fraction bit (0 0.5 1 1.5 2 3 4 6), M = 6, two to a byte, the even channel
+ * in its lower half; a head's row is (D + 1) / 2 bytes.  A group with an
+ * infinity or a NaN has the scale byte 255: it is read as NaN.
+ *
+ * The caller allocates all four parts, and says where they are by strides in
+ * bytes (of a plain cache: in elements), for (sequence, row, head); codes,
+ * scales and channels of a head are adjacent.  Codes are read 16 bytes (e2m1:
+ * 8) at a time where every head's row starts at, and has, a multiple of that;
+ * else 4 or 1.  Parts that are written overlap nothing else.  What was never
+ * written may hold anything: no result depends on a row out of use. */
+enum mp3d_cache_format { MP3D_CACHE_PLAIN = 0, MP3D_CACHE_E4M3 = 1, MP3D_CACHE_E2M1 = 2 };
+typedef struct mp3d_cache {
+    int64_t B, T;
+    void *k, *v;                             /* codes, or elements */
+    void *k_scale, *v_scale;                 /* uint8; NULL in a plain cache */
+    int64_t k_stride[3], v_stride[3];        /* sequence, row, head */
+    int64_t k_scale_stride[3], v_scale_stride[3];
+} mp3d_cache;
+
+/* Quantises T tokens k, v (B, T, H, D), D <= 1024, into a cache of the format
+ * (not plain) of H heads of D channels: token t of sequence b goes to the row
+ * start[b] + t (start NULL: t).  Tokens from count[b] on (a padded batch; NULL:
+ * none) are not written, nor those whose row is not one of the cache's;
+ * every other row keeps its bytes.  start and count: (B) int32, device. */
+int mp3d_cache_write(const mp3d_cache *cache, int format, const void *k, const void *v, int dtype,
+                     int64_t T, int32_t H, int32_t D, const int64_t *k_stride,
+                     const int64_t *v_stride, const int32_t *start, const int32_t *count,
+                     void *stream);
+
+/* Reads T rows of each sequence back: k, v (B, T, H, D), contiguous, 16-byte
+ * aligned, get the values of the rows start[b] + t; zeros from count[b] on, and
+ * where the cache has no such row. */
+int mp3d_cache_read(const mp3d_cache *cache, int format, void *k, void *v, int dtype, int64_t T,
+                    int32_t H, int32_t D, const int32_t *start, const int32_t *count,
+                    void *stream);
+
+/* Attention of new tokens q (B, Tq, Hq, D), D <= 128, over the caches of
+ * their sequences (`own`, of Hk heads; Hq a multiple of Hk) behind a prefix.
+ * `prefix` holds N = prefix.B sequences (0: there is no prefix), each shared by B / N
+ * sequences that follow each other, and is read once for all of them.  Query
+ * i of sequence b sees
+ *   - the first prefix_len[n] rows of the prefix n = b / (B / N) (NULL: all),
+ *   - the first L = kv_len[b] rows of its own cache (NULL: all), if causal up
+ *     to the row i + L - Tq: the new tokens' own rows are the last Tq of L.
+ * Lengths are clamped to the caches.  Scores, softcap, bias by distance, out
+ * and lse are those of mp3d_attention_forward, over all these keys together;
+ * pos_k is (axes, B, own.T), pos_prefix (axes, N, prefix.T).  Keys and values
+ * of 8 or 4 bits are as mp3d_cache_read gives them in q's type.  Both caches
+ * have the same format.  A query that sees no key gets out = 0, lse =
+ * -infinity. */
+typedef struct mp3d_attention_cache {
+    int dtype, format;
+    int64_t B, Tq;
+    int32_t Hq, Hk, D;
+    int32_t causal;
+    int64_t q_stride[3];                     /* batch, token, head */
+    float scale, softcap;
+    mp3d_cache own, prefix;                  /* own.B is B */
+    const int32_t *kv_len, *prefix_len;      /* (B), (N) */
+    int32_t axes;                            /* 0: no bias by distance; at most 3 */
+    const float *slopes;                     /* (Hq, axes) */
+    const int32_t *pos_q;                    /* (axes, B, Tq) */
+    const int32_t *pos_k, *pos_prefix;
+} mp3d_attention_cache;
+
+/* Device workspace of the call, in bytes; as mp3d_attention_workspace_bytes. */
+int mp3d_attention_cached_workspace_bytes(const mp3d_attention_cache *a, size_t *bytes);
+
+/* Writes out (B, Tq, Hq, D), contiguous, 16-byte aligned, and lse
+ * (B, Hq, Tq) float32. */
+int mp3d_attention_cached(const mp3d_attention_cache *a, const void *q, void *out, float *lse,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
 /* Norms of the gated norm, and which of its two are there. */
 enum mp3d_norm { MP3D_NORM_RMS = 0, MP3D_NORM_LAYER = 1 };
 enum mp3d_norm_parts { MP3D_NORM_POST = 1, MP3D_NORM_PRE = 2 };

@@ -1,0 +1,419 @@
+"""Attention over caches against the plain form in float64, at the sizes and
+masks where it can go wrong."""
+import pytest
+import torch
+
+import _caches as oracle
+import _tokens as tk
+import bwd_max_pool3d_amd as mp
+
+pytestmark = pytest.mark.gpu
+
+KINDS = ["", "e4m3", "e2m1"]
+
+
+def make_cache(B, T, H, D, fmt, dt, seed, garbage=True):
+    """(host (k, v) of the values held, device cache)."""
+    parts, host = [], []
+    for i in range(2):
+        x = tk.randn((B, T, H, D), seed + i, dt)
+        if fmt:
+            c, s = oracle.write(x, fmt)
+            host.append(oracle.read(c, s, fmt, D, dt))
+            parts += [c, s]
+        else:
+            host.append(x)
+            parts.append(x)
+    # head by head
+    return host, [p.transpose(1, 2).contiguous().cuda().transpose(1, 2) for p in parts]
+
+
+def spoil(cache, fmt, b, first):
+    """Rows from `first` on hold what was there before: infinities, NaN."""
+    for i, t in enumerate(cache):
+        if fmt:
+            t[b, first:] = 255 if i % 2 else 0x7F
+        else:
+            t[b, first:] = float("inf") if i else float("nan")
+
+
+def run(q, own, prefix, fmt, how):
+    how = {n: v.cuda() if torch.is_tensor(v) else v for n, v in how.items()}
+    out, lse = mp.mp3d_attention_cached(q.cuda(), own, prefix, format=fmt or None, **how)
+    return {"out": out, "lse": lse}
+
+
+def positions(axes, B, N, Tq, Tk, P, Hq, seed):
+    g = torch.Generator().manual_seed(seed)
+    draw = lambda n, T: torch.randint(-40, 40, (axes, n, T), generator=g).int()  # noqa: E731
+    how = dict(slopes=torch.rand((Hq, axes), generator=g) * 0.1, pos_q=draw(B, Tq),
+               pos_k=draw(B, Tk))
+    if N:
+        how["pos_prefix"] = draw(N, P)
+    return how
+
+
+CASES = [
+    # B, N, Tq, Tk, P, Hq, Hk, D
+    (3, 1, 1, 40, 70, 4, 2, 64),           # short, one block of rows
+    (4, 2, 2, 33, 129, 8, 2, 128),
+    (1, 0, 1, 1, 0, 1, 1, 32),             # one key
+    (2, 0, 5, 700, 0, 6, 2, 72),           # no prefix
+    (12, 1, 1, 100, 300, 8, 2, 128),       # 48 rows share the prefix
+    (20, 2, 1, 65, 257, 16, 2, 64),        # 80
+    (6, 1, 7, 31, 500, 12, 3, 80),         # 168, and 28 of an own cache
+    (2, 1, 40, 90, 200, 8, 2, 96),         # 160 rows of an own cache
+    (3, 3, 3, 50, 33, 4, 4, 33),           # a prefix each, an odd width
+    (2, 1, 1, 5, 1, 4, 1, 7),
+]
+
+
+@pytest.mark.parametrize("dt", tk.TYPES, ids=tk.name_of)
+@pytest.mark.parametrize("fmt", KINDS, ids=lambda f: f or "plain")
+@pytest.mark.parametrize("case", CASES, ids=str)
+@pytest.mark.parametrize("more", ["", "cap", "bias"])
+def test_against_float64(more, case, fmt, dt):
+    B, N, Tq, Tk, P, Hq, Hk, D = case
+    q = tk.randn((B, Tq, Hq, D), 1, dt)
+    hk, own = make_cache(B, Tk, Hk, D, fmt, dt, 2)
+    hp, prefix = make_cache(N, P, Hk, D, fmt, dt, 4) if N else (None, None)
+    g = torch.Generator().manual_seed(5)
+    how = dict(kv_len=torch.randint(Tq, Tk + 1, (B,), generator=g).int())
+    for b in range(B):
+        spoil(own, fmt, b, int(how["kv_len"][b]))
+    if N > 1:
+        how["prefix_len"] = torch.randint(0, P + 1, (N,), generator=g).int()
+        for n in range(N):
+            spoil(prefix, fmt, n, int(how["prefix_len"][n]))
+    if more == "cap":
+        how["softcap"] = 3.0
+    if more == "bias":
+        how.update(positions(1 + D % 3, B, N, Tq, Tk, P, Hq, 6))
+    got = run(q, own, prefix, fmt, how)
+    want = oracle.attention(q, hk, hp, **how)
+    for name in ("out", "lse"):
+        tk.close(got[name], *want[name], name)
+
+
+@pytest.mark.parametrize("dt", tk.TYPES, ids=tk.name_of)
+@pytest.mark.parametrize("fmt", KINDS, ids=lambda f: f or "plain")
+def test_lengths_of_zero(fmt, dt):
+    """Empty prefixes, empty caches, both, and caches shorter than the new
+    tokens (whose first see the prefix alone)."""
+    B, N, Tq, Tk, P, Hq, Hk, D = 6, 3, 4, 40, 50, 4, 2, 64
+    q = tk.randn((B, Tq, Hq, D), 11, dt)
+    hk, own = make_cache(B, Tk, Hk, D, fmt, dt, 12)
+    hp, prefix = make_cache(N, P, Hk, D, fmt, dt, 14)
+    how = dict(kv_len=torch.tensor([0, 2, 40, 0, 1, 99]).int(),
+               prefix_len=torch.tensor([0, 7, -3]).int())
+    for b in range(B):
+        spoil(own, fmt, b, int(how["kv_len"][b]))
+    for n in range(N):
+        spoil(prefix, fmt, n, max(0, int(how["prefix_len"][n])))
+    got = run(q, own, prefix, fmt, how)
+    want = oracle.attention(q, hk, hp, **how)
+    for name in ("out", "lse"):
+        tk.close(got[name], *want[name], name)
+    assert torch.equal(got["out"][0], torch.zeros_like(got["out"][0]))
+    assert bool((got["lse"][0] == float("-inf")).all())
+
+
+@pytest.mark.parametrize("fmt", KINDS, ids=lambda f: f or "plain")
+def test_caches_without_rows(fmt):
+    """Own caches of no rows behind a prefix, a prefix of no rows, neither."""
+    dt, B, Hq, Hk, D = torch.bfloat16, 4, 4, 2, 64
+    q = tk.randn((B, 3, Hq, D), 21, dt)
+    none, no_rows = make_cache(B, 0, Hk, D, fmt, dt, 22)
+    hk, own = make_cache(B, 20, Hk, D, fmt, dt, 22)
+    for P in (40, 600):
+        hp, prefix = make_cache(2, P, Hk, D, fmt, dt, 24)
+        for h, o in ((none, no_rows), (hk, own)):
+            got, want = run(q, o, prefix, fmt, {}), oracle.attention(q, h, hp)
+            for name in ("out", "lse"):
+                tk.close(got[name], *want[name], name)
+    _, empty = make_cache(2, 0, Hk, D, fmt, dt, 24)
+    for prefix in (empty, None):
+        got = run(q, own, prefix, fmt, {})
+        want = oracle.attention(q, hk, None)
+        for name in ("out", "lse"):
+            tk.close(got[name], *want[name], name)
+        got = run(q, no_rows, prefix, fmt, {})
+        assert torch.equal(got["out"].cpu(), torch.zeros_like(q))
+        assert bool((got["lse"] == float("-inf")).all())
+    for shape in ((0, 3, Hq, D), (B, 0, Hq, D)):
+        e = torch.empty(shape, dtype=dt, device="cuda")
+        o = own if shape[0] else [t[:0] for t in own]
+        out, lse = mp.mp3d_attention_cached(e, o, format=fmt or None)
+        assert out.shape == e.shape and lse.numel() == 0
+
+
+@pytest.mark.parametrize("dt", tk.TYPES, ids=tk.name_of)
+@pytest.mark.parametrize("fmt", KINDS, ids=lambda f: f or "plain")
+@pytest.mark.parametrize("Tq", [6, 70])
+def test_values_that_are_not_finite(Tq, fmt, dt):
+    """A key's value that is not finite reaches the tokens that see it, in its
+    channels, and no others."""
+    B, Tk, Hq, Hk, D = 2, 130, 4, 2, 64
+    q = tk.randn((B, Tq, Hq, D), 31, dt)
+    hk, own = make_cache(B, Tk, Hk, D, fmt, dt, 32)
+    at = Tk - 3                                            # the last three tokens see it
+    if fmt:
+        own[3][0, at, 1, 1] = 255
+        hk[1][0, at, 1, 32:] = float("nan")
+    else:
+        own[1][0, at, 1, 40] = hk[1][0, at, 1, 40] = float("inf")
+        own[1][0, at, 1, 41] = hk[1][0, at, 1, 41] = float("nan")
+    clean = [t.clone() for t in hk]
+    clean[1][0, at, 1] = 0
+    got = run(q, own, None, fmt, {})
+    want = oracle.attention(q, clean, None)
+    out = got["out"].cpu().double()
+    bad = ~torch.isfinite(hk[1][0, at, 1])
+    assert not torch.isfinite(out[0, -3:, 2:][..., bad]).any()
+    keep = torch.ones_like(out, dtype=torch.bool)
+    keep[0, -3:, 2:] = False
+    value, tol = want["out"]
+    zero = torch.zeros_like(out)
+    tk.close(torch.where(keep, out, zero), torch.where(keep, value, zero), tol, "out")
+    tk.close(got["lse"], *want["lse"], "lse")
+
+
+@pytest.mark.parametrize("fmt", KINDS, ids=lambda f: f or "plain")
+@pytest.mark.parametrize("Tq", [3, 50])
+def test_keys_that_are_not_finite(Tq, fmt):
+    """A NaN key makes the tokens that see it NaN, and no others."""
+    dt, B, Tk, Hq, Hk, D = torch.bfloat16, 1, 200, 4, 2, 128
+    q = tk.randn((B, Tq, Hq, D), 41, dt)
+    hk, own = make_cache(B, Tk, Hk, D, fmt, dt, 42)
+    if fmt:
+        own[1][0, Tk - 2, 0, 3] = 255
+    else:
+        own[0][0, Tk - 2, 0, 5] = float("nan")
+    want = oracle.attention(q, hk, None)
+    got = run(q, own, None, fmt, {})
+    out, lse = got["out"].cpu(), got["lse"].cpu()
+    assert torch.isnan(out[0, -2:, :2]).all() and torch.isnan(lse[0, :2, -2:]).all()
+    out[0, -2:, :2] = want["out"][0][0, -2:, :2].to(dt)
+    lse[0, :2, -2:] = want["lse"][0][0, :2, -2:].float()
+    tk.close(out, *want["out"], "out")
+    tk.close(lse, *want["lse"], "lse")
+
+
+@pytest.mark.parametrize("dt", tk.TYPES, ids=tk.name_of)
+@pytest.mark.parametrize("fmt", KINDS, ids=lambda f: f or "plain")
+def test_without_causal(fmt, dt):
+    B, N, Tq, Tk, P, Hq, Hk, D = 4, 1, 9, 77, 40, 8, 2, 64
+    q = tk.randn((B, Tq, Hq, D), 51, dt)
+    hk, own = make_cache(B, Tk, Hk, D, fmt, dt, 52)
+    hp, prefix = make_cache(N, P, Hk, D, fmt, dt, 54)
+    how = dict(kv_len=torch.tensor([77, 3, 0, 50]).int(), causal=False, scale=0.3)
+    got, want = run(q, own, prefix, fmt, how), oracle.attention(q, hk, hp, **how)
+    for name in ("out", "lse"):
+        tk.close(got[name], *want[name], name)
+
+
+@pytest.mark.parametrize("scale", [-0.2, 0.0])
+def test_scales_that_are_not_positive(scale):
+    dt, B, Tq, Tk, P, Hq, Hk, D = torch.float16, 2, 2, 30, 50, 4, 2, 64
+    q = tk.randn((B, Tq, Hq, D), 61, dt)
+    hk, own = make_cache(B, Tk, Hk, D, "e4m3", dt, 62)
+    hp, prefix = make_cache(1, P, Hk, D, "e4m3", dt, 64)
+    got = run(q, own, prefix, "e4m3", dict(scale=scale))
+    want = oracle.attention(q, hk, hp, scale=scale)
+    for name in ("out", "lse"):
+        tk.close(got[name], *want[name], name)
+
+
+@pytest.mark.parametrize("fmt", KINDS, ids=lambda f: f or "plain")
+@pytest.mark.parametrize("D", [64, 72, 128])
+def test_layouts(D, fmt):
+    """Token by token, heads cut from more, and rows that start anywhere: the
+    same bits as head by head (the sums do not depend on the layout)."""
+    dt, B, N, Tq, Tk, P, Hq, Hk = torch.bfloat16, 4, 2, 2, 90, 150, 8, 2
+    q = tk.randn((B, Tq, Hq + 1, D + 3), 71, dt).cuda()[:, :, :Hq, 1:D + 1]
+    hk, own = make_cache(B, Tk, Hk, D, fmt, dt, 72)
+    hp, prefix = make_cache(N, P, Hk, D, fmt, dt, 74)
+    how = dict(kv_len=torch.tensor([90, 33, 2, 64]).int())
+    first = run(q.contiguous(), own, prefix, fmt, how)
+    want = oracle.attention(q.cpu(), hk, hp, **how)
+    for name in ("out", "lse"):
+        tk.close(first[name], *want[name], name)
+
+    def cut(t, extra):
+        big = torch.empty(t.shape[:2] + (t.shape[2] + 1, t.shape[3] + extra), dtype=t.dtype,
+                          device="cuda")
+        big = big[:, :, 1:, extra:]
+        big.copy_(t)
+        return big
+
+    for extra in (0, 1, 4, 8):
+        a, b = [cut(t, extra) for t in own], [cut(t, extra) for t in prefix]
+        got = run(q, a, b, fmt, how)
+        for name in ("out", "lse"):
+            assert torch.equal(got[name], first[name]), (extra, name)
+
+
+def test_far_positions():
+    """Positions up to 2^31 apart: distances to 24 bits."""
+    dt, B, Hq, Hk, D = torch.float32, 2, 2, 1, 32
+    q = tk.randn((B, 2, Hq, D), 81, dt)
+    hk, own = make_cache(B, 40, Hk, D, "e4m3", dt, 82)
+    hp, prefix = make_cache(1, 60, Hk, D, "e4m3", dt, 84)
+    how = positions(2, B, 1, 2, 40, 60, Hq, 86)
+    how["slopes"] = torch.full((Hq, 2), 2.0 ** -30)
+    for n in ("pos_q", "pos_k", "pos_prefix"):
+        how[n][0] *= 50_000_000
+    how["pos_q"][0, 0] = -2 ** 31
+    how["pos_prefix"][0, 0, :3] = 2 ** 31 - 1
+    got, want = run(q, own, prefix, "e4m3", how), oracle.attention(q, hk, hp, **how)
+    for name in ("out", "lse"):
+        tk.close(got[name], *want[name], name)
+
+
+@pytest.mark.parametrize("fmt", KINDS, ids=lambda f: f or "plain")
+def test_many_sequences_of_a_long_prefix(fmt):
+    """Several blocks of 128 rows, and chunks of many tiles."""
+    dt, B, Tq, Tk, P, Hq, Hk, D = torch.bfloat16, 24, 4, 70, 5000, 8, 2, 128
+    q = tk.randn((B, Tq, Hq, D), 91, dt)
+    hk, own = make_cache(B, Tk, Hk, D, fmt, dt, 92)
+    hp, prefix = make_cache(1, P, Hk, D, fmt, dt, 94)
+    how = dict(kv_len=(torch.arange(B) * 5 % 67 + 4).int(), prefix_len=torch.tensor([4987]).int())
+    for b in range(B):
+        spoil(own, fmt, b, int(how["kv_len"][b]))
+    spoil(prefix, fmt, 0, 4987)
+    got, want = run(q, own, prefix, fmt, how), oracle.attention(q, hk, hp, **how)
+    for name in ("out", "lse"):
+        tk.close(got[name], *want[name], name)
+
+
+def test_rows_past_32_bits():
+    """Caches whose last rows are more than 2^32 bytes from their first."""
+    dt, D, T = torch.float16, 128, (1 << 25) + 4096
+    q = tk.randn((1, 1, 2, D), 101, dt)
+    hk, own = make_cache(1, 100, 1, D, "e4m3", dt, 102)
+    # the same rows as every (T / 100)-th of a long cache's: by its row stride
+    for fmt, small, host in (("e4m3", own, hk),):
+        long = mp.mp3d_cache_empty(1, T, 1, D, fmt)
+        step = (T - 1) // 99
+        far = [t.as_strided((1, 100, 1, t.shape[3]), (t.stride(0), step * t.shape[3], t.stride(2), 1))
+               for t in long]
+        for a, b in zip(far, small):
+            a.copy_(b)
+        got, want = run(q, far, None, fmt, {}), oracle.attention(q, host, None)
+        for name in ("out", "lse"):
+            tk.close(got[name], *want[name], name)
+
+
+def test_the_callers_workspace_and_outputs():
+    dt, B, D = torch.bfloat16, 3, 64
+    q = tk.randn((B, 1, 4, D), 111, dt).cuda()
+    _, own = make_cache(B, 30, 2, D, "e2m1", dt, 112)
+    _, prefix = make_cache(1, 300, 2, D, "e2m1", dt, 114)
+    want = mp.mp3d_attention_cached(q, own, prefix, format="e2m1")
+    n = mp.mp3d_attention_cached_workspace_bytes(q, own, prefix, format="e2m1")
+    assert n > 0
+    ws = torch.full((n + 64,), 255, dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+    mp.mp3d_attention_cached(q, own, prefix, format="e2m1", out=(out, lse), workspace=ws)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert bool((ws[n:] == 255).all())
+    with pytest.raises(mp.Mp3dError):
+        mp.mp3d_attention_cached(q, own, prefix, format="e2m1", workspace=ws[:n - 16])
+
+
+def test_arguments_are_checked():
+    dt, D = torch.float32, 32
+    q = torch.zeros((4, 1, 4, D), device="cuda")
+    _, own = make_cache(4, 8, 2, D, "e4m3", dt, 1)
+    _, plain = make_cache(4, 8, 2, D, "", dt, 1)
+    pre = [t[:2] for t in own]
+    bad = [dict(own=own), dict(own=plain, format="e4m3"), dict(own=plain, format="fp8"),
+           dict(own=[t[:2] for t in own], format="e4m3"),
+           dict(own=own, prefix=[t[:3] for t in own], format="e4m3"),
+           dict(own=own, prefix=[t[:0] for t in own], format="e4m3"),
+           dict(own=own, prefix=[t[:2, :, :1] for t in own], format="e4m3"),
+           dict(own=plain, prefix=pre), dict(own=[t.half() for t in plain]),
+           dict(own=own, format="e4m3", kv_len=torch.zeros(3, dtype=torch.int32, device="cuda")),
+           dict(own=own, format="e4m3", prefix_len=torch.zeros(1, dtype=torch.int32, device="cuda")),
+           dict(own=own, format="e4m3", pos_q=torch.zeros((1, 4, 1), dtype=torch.int32, device="cuda")),
+           dict(own=own, format="e4m3", slopes=torch.zeros((4, 1), device="cuda"))]
+    for how in bad:
+        with pytest.raises(ValueError):
+            mp.mp3d_attention_cached(q, **how)
+    with pytest.raises(mp.Mp3dError):
+        mp.mp3d_attention_cached(q[:, :, :3], own, format="e4m3")      # 3 heads on 2
+
+
+def test_capture():
+    """Captured once with a workspace of its own: every replay gives the eager
+    bits of the lengths that are there then."""
+    dt, B, D, fmt = torch.bfloat16, 6, 128, "e4m3"
+    q = torch.zeros((B, 1, 8, D), dtype=dt, device="cuda")
+    _, own = make_cache(B, 200, 2, D, fmt, dt, 122)
+    _, prefix = make_cache(2, 400, 2, D, fmt, dt, 124)
+    kv, pl = (torch.ones(n, dtype=torch.int32, device="cuda") for n in (B, 2))
+
+    def call():
+        return mp.mp3d_attention_cached(q, own, prefix, format=fmt, kv_len=kv, prefix_len=pl)
+
+    inputs = [(tk.randn((B, 1, 8, D), 130 + n, dt), (torch.arange(B) * 31 * n + 1).int() % 201,
+               torch.tensor([400 - 100 * n, 57 * n]).int()) for n in range(3)]
+
+    def load(x):
+        for t, new in zip((q, kv, pl), x):
+            t.copy_(new)
+
+    want = []
+    for x in inputs:
+        load(x)
+        want.append([t.clone() for t in call()])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = call()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(other, want[-1]))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call()
+    for _ in range(2):
+        for x, ref in zip(inputs, want):
+            load(x)
+            for t in got:
+                t.fill_(float("nan"))
+            graph.replay()
+            torch.cuda.synchronize()
+            for a, b in zip(got, ref):
+                assert torch.equal(a, b)
+            call()                                         # eager work between the replays
+            torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dt", tk.TYPES, ids=tk.name_of)
+@pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
+def test_together(fmt, dt):
+    """A clip's tokens are written once, answers of several sequences follow
+    token by token: the same, within the bounds, as attention over the values
+    read back."""
+    S, P, n, Hq, Hk, D = 5, 150, 6, 8, 2, 64
+    k, v = (tk.randn((1, P, Hk, D), s, dt).cuda() for s in (141, 142))
+    clip = mp.mp3d_cache_empty(1, P, Hk, D, fmt)
+    mp.mp3d_cache_write(k, v, clip, fmt)
+    own = mp.mp3d_cache_empty(S, n, Hk, D, fmt)
+    lengths = torch.zeros(S, dtype=torch.int32, device="cuda")
+    for i in range(n):
+        q, k1, v1 = (tk.randn((S, 1, h, D), 150 + 3 * i + j, dt).cuda()
+                     for j, h in enumerate((Hq, Hk, Hk)))
+        mp.mp3d_cache_write(k1, v1, own, fmt, start=lengths)
+        lengths += 1
+        out, lse = mp.mp3d_attention_cached(q, own, clip, format=fmt, softcap=20.0, kv_len=lengths)
+        kp, vp = mp.mp3d_cache_read(clip, fmt, D, dt)
+        ko, vo = mp.mp3d_cache_read(own, fmt, D, dt, count=lengths)
+        kk, vv = (torch.cat((a.expand(S, -1, -1, -1), b[:, :i + 1]), 1) for a, b in ((kp, ko), (vp, vo)))
+        want = tk.attention(q.cpu(), kk.cpu(), vv.cpu(), causal=True, softcap=20.0)
+        tk.close(out, *want["out"], "out")
+        tk.close(lse, *want["lse"], "lse")
+        ref, lref = mp.mp3d_attention_forward(q, kk, vv, causal=True, softcap=20.0)
+        tk.close(out, ref.cpu().double(), 2 * want["out"][1], "out of mp3d_attention_forward")
+        tk.close(lse, lref.cpu().double(), 2 * want["lse"][1], "lse of mp3d_attention_forward")
