@@ -18,9 +18,11 @@ SOURCES = ["api.hip", "plan.hip", "forward.hip", "forward_fixed.hip", "forward_c
            "api_tokens.hip", "rope.hip", "gated_norm.hip", "attention_fwd.hip",
            "attention_split.hip", "attention_bwd.hip", "attention_order.hip"]
 # caches of 8 or 4 bits and attention over caches
-CACHE_SOURCES = ["api_cache.hip", "cache.hip", "attention_cached.hip",
-                 "attention_cached_plain.hip", "attention_cached_e4m3.hip",
-                 "attention_cached_e2m1.hip"]
+CACHE_SOURCES = ["attention_cached_e4m3_f32.hip", "attention_cached_e2m1_f32.hip",
+                 "attention_cached_e4m3_f16.hip", "attention_cached_e2m1_f16.hip",
+                 "attention_cached_e4m3_bf16.hip", "attention_cached_e2m1_bf16.hip",
+                 "attention_cached_plain.hip", "attention_cached.hip", "api_cache.hip",
+                 "cache.hip"]
 # the pooling kernels, what chooses among them, and what they include
 POOL_KERNELS = ["api.hip", "api_common.hpp", "plan.hip", "forward.hip", "forward_fixed.hip",
                 "forward_col.hip", "backward.hip", "backward_owner.hip", "small.hip",
@@ -38,7 +40,7 @@ HIPCC_FLAGS = [
 
 
 def sources() -> list[str]:
-    return [os.path.join(CSRC, s) for s in SOURCES + CACHE_SOURCES]
+    return [os.path.join(CSRC, s) for s in CACHE_SOURCES + SOURCES]
 
 
 def _jobs() -> int:

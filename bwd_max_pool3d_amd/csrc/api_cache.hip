@@ -171,6 +171,7 @@ int cached_args(const mp3d_attention_cache *d, CachedArgs *c)
     a.axes = d->axes;
     a.causal = d->causal;
     c->format = d->format;
+    c->f32 = d->dtype == MP3D_F32;
     const int es = elem_bytes(d->dtype);
     const int unit = d->format == kE4M3 ? 16 : 8;          // bytes of 16 channels
     const mp3d_cache *src[2] = {&d->prefix, &d->own};
@@ -195,6 +196,13 @@ int cached_args(const mp3d_attention_cache *d, CachedArgs *c)
         p.vec = wide_rows(x.k, p.ks, es) && wide_rows(x.v, p.vs, es);
         const int bytes = row_bytes(d->format, d->D);
         p.width = divides(unit, x, bytes) ? unit : divides(4, x, bytes) ? 4 : 1;
+        if (p.caches == 0 || p.T == 0) continue;
+        // whole units, and a row's offset in a tile within 31 bits
+        const int64_t far = (int64_t)1 << 24;
+        const bool near = p.ks[1] < far && p.vs[1] < far;
+        if (d->format == kPlain ? !(near && p.vec && d->D % 8 == 0)
+                                : !(near && p.width == unit && p.kss[1] < far && p.vss[1] < far))
+            c->any = 1;
     }
     return MP3D_OK;
 }
@@ -255,7 +263,7 @@ int mp3d_attention_cached(const mp3d_attention_cache *d, const void *q, void *ou
     a.q = q;
     a.out = out;
     a.lse = lse;
-    a.vec = wide_rows(q, a.qs, es);
+    a.vec = wide_rows(q, a.qs, es) && a.D % 8 == 0;
     if ((rc = check_workspace(workspace, workspace_bytes, plan_attn_cached(&c)))) return rc;
     if ((rc = check_launch(c.part[0].blocks + c.part[1].blocks))) return rc;
     place_attn_cached(&c, workspace);

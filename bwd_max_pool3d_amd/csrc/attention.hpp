@@ -684,7 +684,8 @@ __device__ __forceinline__ Scores scores(const AttnArgs &a)
 }
 
 // (a branch: as a choice between two results it would be in every tile)
-__device__ __forceinline__ void multiply_scores(f32x16 &s, const Scores &sc)
+template <typename V>
+__device__ __forceinline__ void multiply_scores(V &s, const Scores &sc)
 {
     if (!sc.multiply) return;
     asm volatile("");
@@ -776,7 +777,7 @@ __device__ __forceinline__ void add_bias(f32x16 &s, const u32x2 *rows, int step,
     add_axes<false>(s, rows, step, axes, cols, slopes);
 }
 
-// The 16 scores of a result to c tanh(s / c).  float32: the library's
+// The scores of a result (a vector of them) to c tanh(s / c).  float32: the library's
 // tanhf, for its relative accuracy near 0.  16-bit types, which keep 2^-9 or
 // 2^-12 of a weight: 1 - 2 / (1 + e^2x), within 2e-7; and where no score of the
 // wave passes c / 4, as with a cap well above the scores, the odd Taylor
@@ -784,30 +785,31 @@ __device__ __forceinline__ void add_bias(f32x16 &s, const u32x2 *rows, int step,
 // exponential and the reciprocal) take twice the time or more.  So a query's
 // last bits depend on the scores of the wave's other queries, but not on what
 // it does not see: a tile of which some is masked (`part`) takes the first form.
-template <typename T>
-__device__ __forceinline__ void cap_scores(f32x16 &s, const Scores &sc, bool part)
+template <typename T, typename V>
+__device__ __forceinline__ void cap_scores(V &s, const Scores &sc, bool part)
 {
+    constexpr int N = sizeof(V) / sizeof(float);
     const float f = sc.per_cap;
     if constexpr (T::code == F32::code) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s[r] = sc.cap * tanhf(s[r] * f);
+        for (int r = 0; r < N; ++r) s[r] = sc.cap * tanhf(s[r] * f);
         return;
     }
     float big = fabsf(s[0]);
 #pragma unroll
-    for (int r = 1; r < 16; ++r) big = fmaxf(big, fabsf(s[r]));
+    for (int r = 1; r < N; ++r) big = fmaxf(big, fabsf(s[r]));
     if (!part && !__any(!(big * f < 0.25f))) {
         const float f2 = f * f, c3 = -f2 / 3.f, c5 = f2 * f2 * (2.f / 15.f),
                     c7 = f2 * f2 * f2 * (-17.f / 315.f);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
+        for (int r = 0; r < N; ++r) {
             const float y = s[r] * s[r];
             s[r] = fmaf(fmaf(fmaf(c7, y, c5), y, c3) * y, s[r], s[r]);
         }
     } else {
         const float g = f * (2.f * kLog2e);
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
+        for (int r = 0; r < N; ++r)
             s[r] = fmaf(-2.f * sc.cap,
                         __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(s[r] * g)), sc.cap);
     }

@@ -9,24 +9,27 @@ namespace {
 constexpr int kJoinGroups = 8;
 constexpr int64_t kJoinRow = 1 << 22;       // workgroups of the join in a row of its grid
 
-// Joins the chunks of a row: a workgroup per row, 8 groups of 32 lanes with 4
-// channels a lane.  The groups take the chunks that the row has keys in, in
-// turn, each with a running maximum of its own, and are joined in LDS in a
-// fixed order.
-template <typename T>
+// Joins the chunks of a row: NG groups of 32 lanes a row, with 4 channels a
+// lane.  The groups take the chunks that the row has keys in, in turn, each
+// with a running maximum of its own, and are joined in LDS in a fixed order.
+// Few chunks: a group a row, and nothing to join.
+template <typename T, int NG>
 __global__ __launch_bounds__(32 * kJoinGroups) void cached_join_kernel(CachedArgs c)
 {
     using R = typename T::raw;
-    constexpr int NG = kJoinGroups;
-    __shared__ __align__(16) float jo[NG][kAttnMaxD];
-    __shared__ float jm[NG], jl[NG];
+    __shared__ __align__(16) float jo[kJoinGroups][kAttnMaxD];
+    __shared__ float jm[kJoinGroups], jl[kJoinGroups];
     const AttnArgs &a = c.a;
-    const int tid = threadIdx.x, g = tid >> 5, d0 = (tid & 31) * 4, per = a.Tq * a.G;
-    const int64_t total = (int64_t)a.B * a.Hq * a.Tq, row = blockIdx.y * (int64_t)gridDim.x + blockIdx.x;
-    if (row >= total) return;
-    const int64_t bh = row / per;
-    const int r = (int)(row - bh * per), t = r / a.G;
-    const int b = (int)(bh / a.Hk), h = (int)(bh % a.Hk) * a.G + (r - t * a.G);
+    const int tid = threadIdx.x, group = tid >> 5, g = group % NG, d0 = (tid & 31) * 4,
+              per = a.Tq * a.G;
+    const int64_t total = (int64_t)a.B * a.Hq * a.Tq;
+    const int64_t row = (blockIdx.y * (int64_t)gridDim.x + blockIdx.x) * (kJoinGroups / NG) + group / NG;
+    if (row >= total) return;              // (with NG groups of kJoinGroups, all of them)
+    const uint32_t in_b = (uint32_t)a.Hk * per;                    // rows of a sequence
+    const int b = (int)(row / in_b);
+    const uint32_t in = (uint32_t)(row - (int64_t)b * in_b), hk = in / (uint32_t)per, r = in - hk * per,
+                   t = r / (uint32_t)a.G;
+    const int h = hk * a.G + (r - t * a.G);
     const int ds = cached_stride(a.D);
     // its chunks of the prefix, then of the own cache
     const CachedPart &pre = c.part[0], &own = c.part[1];
@@ -53,29 +56,34 @@ __global__ __launch_bounds__(32 * kJoinGroups) void cached_join_kernel(CachedArg
         for (int e = 0; e < 4; ++e) o[e] = o[e] * fo + fn * x[e];
         m = mn;
     }
-    *(f32x4 *)&jo[g][d0] = o;
-    if (d0 == 0) {
-        jm[g] = m;
-        jl[g] = l;
-    }
-    __syncthreads();
-    if (tid >= kAttnMaxD) return;
-    float mt = kNegInf, lt = 0.f, ot = 0.f;
+    R *const out = (R *)a.out + (((int64_t)b * a.Tq + t) * a.Hq + h) * a.D;
+    float *const lse = a.lse + ((int64_t)b * a.Hq + h) * a.Tq + t;
+    if constexpr (NG == 1) {
 #pragma unroll
-    for (int x = 0; x < NG; ++x) mt = fmaxf(mt, jm[x]);
-    const float ms = mt == kNegInf ? 0.f : mt;
+        for (int e = 0; e < 4; ++e)
+            if (d0 + e < a.D) out[d0 + e] = T::narrow(l == 0.f ? 0.f : o[e] / l);
+        if (d0 == 0) *lse = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
+    } else {
+        *(f32x4 *)&jo[g][d0] = o;
+        if (d0 == 0) {
+            jm[g] = m;
+            jl[g] = l;
+        }
+        __syncthreads();
+        if (tid >= kAttnMaxD) return;
+        float mt = kNegInf, lt = 0.f, ot = 0.f;
 #pragma unroll
-    for (int x = 0; x < NG; ++x) {
-        const float f = __builtin_amdgcn_exp2f(jm[x] - ms);
-        lt = fmaf(f, jl[x], lt);
-        ot = fmaf(f, jo[x][tid], ot);
+        for (int x = 0; x < NG; ++x) mt = fmaxf(mt, jm[x]);
+        const float ms = mt == kNegInf ? 0.f : mt;
+#pragma unroll
+        for (int x = 0; x < NG; ++x) {
+            const float f = __builtin_amdgcn_exp2f(jm[x] - ms);
+            lt = fmaf(f, jl[x], lt);
+            ot = fmaf(f, jo[x][tid], ot);
+        }
+        if (tid < a.D) out[tid] = T::narrow(lt == 0.f ? 0.f : ot / lt);
+        if (tid == 0) *lse = lt == 0.f ? kNegInf : (mt + log2f(lt)) * kLn2;
     }
-    if (tid < a.D)
-        ((R *)a.out)[(((int64_t)b * a.Tq + t) * a.Hq + h) * a.D + tid] =
-            T::narrow(lt == 0.f ? 0.f : ot / lt);
-    if (tid == 0)
-        a.lse[((int64_t)b * a.Hq + h) * a.Tq + t] =
-            lt == 0.f ? kNegInf : (mt + log2f(lt)) * kLn2;
 }
 
 }  // namespace
@@ -85,37 +93,47 @@ __global__ __launch_bounds__(32 * kJoinGroups) void cached_join_kernel(CachedArg
 size_t plan_attn_cached(CachedArgs *c)
 {
     AttnArgs &a = c->a;
+    constexpr int64_t kStep = kCachedKeys * kCachedWaves;  // keys that a workgroup takes at a time
+    // (a step of 128 rows takes three times one of 16)
+    auto kWeight = [](const CachedPart &p) -> int64_t { return p.mb == 16 ? 1 : 3; };
+    auto blocks = [&](CachedPart &p) {
+        p.units = (int64_t)a.Hk * p.caches * p.nsplit;
+        p.blocks = p.nrb > 1 ? (p.units + 7) / 8 * 8 * p.nrb : p.units;
+    };
+    int64_t cost = 0;                      // steps of 16 rows, over all workgroups
+    bool wide = false;
     for (CachedPart &p : c->part) {
         p.nsplit = 0;
         p.units = p.blocks = 0;
         p.chunk = 1;
-        p.wr = 1;
-        p.nrb = 1;
-        if (p.caches == 0 || p.T == 0) continue;
         p.rows = (int32_t)((int64_t)p.seqs * a.Tq * a.G);
-        if (c->format != kPlain) p.wr = p.rows <= 32 ? 1 : p.rows <= 64 ? 2 : 4;
-        p.nrb = (p.rows + 32 * p.wr - 1) / (32 * p.wr);
-        // tiles that a workgroup takes in one step
-        const int64_t unit = (int64_t)kCachedKeys * (kCachedWaves / p.wr);
-        const int64_t most = (p.T + unit - 1) / unit;
-        const int64_t base = (int64_t)p.nrb * a.Hk * p.caches;
-        const int64_t want = (p.wr > 1 ? 2 : 8) * device_cus();
-        int64_t n = (want + base - 1) / base;
-        n = n > most ? most : n;
-        const int64_t chunk = (most + n - 1) / n * unit;
-        p.chunk = (int32_t)chunk;
-        p.nsplit = (int32_t)((p.T + chunk - 1) / chunk);
-        p.units = (int64_t)a.Hk * p.caches * p.nsplit;
-        p.blocks = p.nrb > 1 ? (p.units + 7) / 8 * 8 * p.nrb : p.units;
+        p.mb = p.rows <= 64 || c->f32 || (c->format == kPlain && c->any) ? 16 : 32;
+        p.wr = p.mb == 16 ? 1 : 4;
+        p.nrb = (p.rows + p.mb * p.wr - 1) / (p.mb * p.wr);
+        if (p.caches == 0 || p.T == 0) continue;
+        wide |= p.mb == 32;
+        cost += (int64_t)p.nrb * a.Hk * p.caches * ((p.T + kStep - 1) / kStep) * kWeight(p);
+    }
+    // One round of workgroups: as many as run at once; of 16 rows a third more
+    // where lengths are given, which leave some without keys (16 caches of 9728
+    // to 32768, e4m3: 145 us for one round, 134 so, 150 to 164 for two to four).
+    const int64_t once = device_cus() * (wide || c->format == kPlain || attn_general(a) ? 2 : 3);
+    const bool ragged = !wide && c->part[1].len;
+    const int64_t want = ragged ? once * 4 / 3 : once;
+    const int64_t per = (cost + want - 1) / want;
+    for (CachedPart &p : c->part) {
+        if (p.caches == 0 || p.T == 0) continue;
+        const int64_t steps = (p.T + kStep - 1) / kStep;
+        int64_t n = (per + kWeight(p) - 1) / kWeight(p);
+        n = n > steps ? steps : n;
+        p.nsplit = (int32_t)((steps + n - 1) / n);
+        p.chunk = (int32_t)((steps + p.nsplit - 1) / p.nsplit * kStep);
+        blocks(p);
     }
     CachedPart &own = c->part[1];
     if (c->part[0].nsplit + own.nsplit == 0) {
-        // no key anywhere: one workgroup a row block writes the zeros
-        own.rows = a.Tq * a.G;
-        own.nrb = (own.rows + 31) / 32;
-        own.nsplit = 1;
-        own.units = (int64_t)a.Hk * a.B;
-        own.blocks = own.nrb > 1 ? (own.units + 7) / 8 * 8 * own.nrb : own.units;
+        own.nsplit = 1;                    // no key anywhere: the zeros are written all the same
+        blocks(own);
     }
     const int64_t slots = c->part[0].nsplit + own.nsplit;
     if (slots == 1) return 0;
@@ -133,15 +151,20 @@ void place_attn_cached(CachedArgs *c, void *workspace)
 template <typename T>
 hipError_t launch_attn_cached(const CachedArgs &c, hipStream_t s)
 {
-    const hipError_t e = c.format == kPlain  ? launch_cached_plain<T>(c, s)
-                         : c.format == kE4M3 ? launch_cached_e4m3<T>(c, s)
-                                             : launch_cached_e2m1<T>(c, s);
+    const hipError_t e = c.format == kPlain  ? launch_cached<T, kPlain>(c, s)
+                         : c.format == kE4M3 ? launch_cached<T, kE4M3>(c, s)
+                                             : launch_cached<T, kE2M1>(c, s);
     if (e != hipSuccess) return e;         // the join would read what was not written
-    if (c.part[0].nsplit + c.part[1].nsplit > 1) {
+    const int slots = c.part[0].nsplit + c.part[1].nsplit;
+    if (slots > 1) {
+        const bool one = slots <= 8;
+        const int64_t rows = (int64_t)c.a.B * c.a.Hq * c.a.Tq;
+        const int64_t n = one ? (rows + kJoinGroups - 1) / kJoinGroups : rows;
         // (a launch's first dimension takes 2^24 workgroups of 256)
-        const int64_t rows = (int64_t)c.a.B * c.a.Hq * c.a.Tq, x = rows < kJoinRow ? rows : kJoinRow;
-        launch_kernel((cached_join_kernel<T>), dim3((uint32_t)x, (uint32_t)((rows + x - 1) / x)),
-                      dim3(32 * kJoinGroups), 0, s, c);
+        const int64_t x = n < kJoinRow ? n : kJoinRow;
+        const dim3 grid((uint32_t)x, (uint32_t)((n + x - 1) / x)), block(32 * kJoinGroups);
+        if (one) launch_kernel((cached_join_kernel<T, 1>), grid, block, 0, s, c);
+        else launch_kernel((cached_join_kernel<T, kJoinGroups>), grid, block, 0, s, c);
     }
     return hipGetLastError();
 }

@@ -17,11 +17,11 @@
 // fragments instead would need a value's scale per key inside a lane's eight
 // keys.)  Elements go to LDS directly.
 //
-// wr of a workgroup's four waves have rows of their own, 32 each, and share
-// tiles; the other waves have other tiles.  wr = 1 (up to 32 rows): no wave
-// waits for another.  wr = 2, 4: codes are read and widened once for 64 or 128
-// rows, each wave a part of the tile, with two or four tiles of LDS in turn and
-// a barrier a tile.
+// Up to 32 rows go in blocks of 16 (MB = 16): each wave has all 16 and tiles of
+// its own, no wave waits for another.  More rows go in blocks of 128 (MB = 32):
+// the waves have 32 each, and share two tiles that they bring in turn, a
+// quarter each; codes are read and widened once for 128 rows, into the one half
+// of LDS while the products run from the other.
 #pragma once
 
 #include "attention.hpp"
@@ -36,18 +36,141 @@ constexpr int kCachedPad = 4;              // floats between the rows of the joi
 // floats between the rows of a chunk's sums, for loads of 4
 __host__ __device__ inline int cached_stride(int D) { return (D + 3) & ~3; }
 
-template <typename T, int DP>
+// Tiles of LDS a wave: elements straight from memory need one for keys and one
+// for values; codes of up to 16 rows take turns in one, so that three
+// workgroups fit on a CU.
+template <int FMT, int MB>
+constexpr int cached_slots() { return FMT == kPlain || MB == 32 ? 2 : 1; }
+template <typename T, int FMT, int DP, int MB>
 constexpr uint32_t cached_tiles()
 {
-    const uint32_t tiles = kCachedWaves * 2 * kCachedKeys * DP * sizeof(typename T::raw);
-    const uint32_t join = kCachedWaves * 32 * (DP + kCachedPad) * sizeof(float);
+    const uint32_t tiles = kCachedWaves * cached_slots<FMT, MB>() * kCachedKeys * DP *
+                           sizeof(typename T::raw);
+    const uint32_t join = kCachedWaves * MB * (DP + kCachedPad) * sizeof(float);
     return tiles > join ? tiles : join;
 }
-template <typename T, int DP>
+template <typename T, int FMT, int DP, int MB>
 constexpr uint32_t cached_lds()
 {
-    return cached_tiles<T, DP>() +
-           (kCachedWaves * (2 * 3 * kCachedKeys + 64) + 4) * (uint32_t)sizeof(float);
+    return cached_tiles<T, FMT, DP, MB>() +
+           (kCachedWaves * (2 * 3 * kCachedKeys + 2 * MB) + 4) * (uint32_t)sizeof(float);
+}
+
+// Workgroups on a CU.
+template <typename T, int FMT, int DP, bool GEN, int MP>
+constexpr int cached_occupancy()
+{
+    if (sizeof(typename T::raw) * DP > 256) return FMT == kPlain ? 1 : 2;
+    return FMT != kPlain && MP == 16 && !GEN ? 3 : 2;
+}
+
+// --- products with MB columns (rows of the call, in lanes l % MB).  A lane's
+// 8 elements of an operand are 8 deep at 8 (l / MB); register e of a result is
+// its row group(e) + 4 (l / MB) + e % 4: with 16 columns a result has 16 rows,
+// and a tile's keys are two results.  As with 32, registers 8c .. 8c + 7 of the
+// scores are the next product's operand, 16 or 32 keys deep.
+template <int MB>
+struct Cols {
+    static constexpr int PARTS = 64 / MB, DEPTH = 8 * PARTS, SCORES = kCachedKeys / PARTS;
+    static constexpr int PER = MB == 32 ? 16 : 4;          // registers of a result
+    typedef float acc __attribute__((ext_vector_type(MB == 32 ? 16 : 4)));
+    typedef float scores __attribute__((ext_vector_type(MB == 32 ? 16 : 8)));
+    // a key's place in the tile, or a channel's in its block, without 4 (l / MB)
+    __device__ static constexpr int group(int e) { return (MB == 32 ? 8 : 16) * (e / 4) + e % 4; }
+    __device__ static __forceinline__ float over_parts_max(float v)
+    {
+        if constexpr (MB == 16) {
+            const auto x = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v),
+                                                            __builtin_bit_cast(uint32_t, v), false,
+                                                            false);
+            const uint32_t a = x[0], b = x[1];
+            v = fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
+        }
+        return halves_max(v);
+    }
+    __device__ static __forceinline__ float over_parts_sum(float v)
+    {
+        if constexpr (MB == 16) {
+            const auto x = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v),
+                                                            __builtin_bit_cast(uint32_t, v), false,
+                                                            false);
+            const uint32_t a = x[0], b = x[1];
+            v = __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b);
+        }
+        return halves_sum(v);
+    }
+};
+
+template <typename T, int MB>
+__device__ __forceinline__ typename Cols<MB>::acc mma_cols(const Frag<T> &a, const Frag<T> &b,
+                                                           typename Cols<MB>::acc c)
+{
+    if constexpr (MB == 32) {
+        return mma<T>(a, b, c);
+    } else if constexpr (T::code == BF16::code) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a.w[0]),
+                                                       __builtin_bit_cast(bf16x8, b.w[0]), c, 0, 0,
+                                                       0);
+    } else if constexpr (T::code == F16::code) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a.w[0]),
+                                                      __builtin_bit_cast(f16x8, b.w[0]), c, 0, 0,
+                                                      0);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const u32x4 x = a.w[i / 4], y = b.w[i / 4];
+            const uint32_t xe[4] = {x.x, x.y, x.z, x.w}, ye[4] = {y.x, y.y, y.z, y.w};
+            c = __builtin_amdgcn_mfma_f32_16x16x4f32(__builtin_bit_cast(float, xe[i % 4]),
+                                                     __builtin_bit_cast(float, ye[i % 4]), c, 0, 0,
+                                                     0);
+        }
+        return c;
+    }
+}
+
+// Channel d0 + l % MB of the keys that registers 8c .. 8c + 7 are of.
+template <typename T, int DP, int MB>
+__device__ __forceinline__ Frag<T> value_frag(const typename T::raw *tile, int c, int d0, int l)
+{
+    using R = typename T::raw;
+    if constexpr (MB == 32) {
+        return col_frag<T, DP>(tile, c, d0, l);
+    } else if constexpr (sizeof(R) == 2) {
+        const int col = d0 + (l & 3) * 4, row = 4 * (l >> 4) + ((l & 15) >> 2);
+        typedef __attribute__((address_space(3))) s16x4 lds_t;
+        struct alignas(16) {
+            s16x4 v[2];
+        } o;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const R *p = tile + tile_at<R, DP>(row + 16 * k, col >> 3) + (col & 7);
+            o.v[k] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t *)p);
+        }
+        return __builtin_bit_cast(Frag<T>, o);
+    } else {
+        const int col = d0 + (l & 15);
+        struct alignas(16) {
+            float e[8];
+        } o;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = 4 * (l >> 4) + Cols<16>::group(i);
+            o.e[i] = tile[tile_at<R, DP>(row, col >> 3) + (col & 7)];
+        }
+        return __builtin_bit_cast(Frag<T>, o);
+    }
+}
+
+// Scores 8c .. 8c + 7, rounded, as an operand.
+template <typename T, typename V>
+__device__ __forceinline__ Frag<T> pack_scores(const V &s, int c)
+{
+    struct alignas(16) {
+        typename T::raw e[8];
+    } o;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o.e[i] = T::narrow(s[8 * c + i]);
+    return __builtin_bit_cast(Frag<T>, o);
 }
 
 // The keys [0, end) of its own cache that new token t of sequence b sees, or
@@ -63,76 +186,82 @@ __device__ __forceinline__ int cached_end(const CachedArgs &c, bool own, int len
 }
 
 // A tile of codes on its way from memory to LDS.  A wave's lanes take its
-// rows in rounds, 16 channels each; with wr waves to a tile each takes every
-// wr-th round.
-template <typename T, int FMT, int DP>
+// rows in rounds, 16 channels each.
+template <typename T, int FMT, int DP, int KEYS>
 struct CodeTile {
     using R = typename T::raw;
-    static constexpr int UNITS = DP / 16, ROWS = 64 / UNITS, N = kCachedKeys / ROWS;
+    static constexpr int UNITS = DP / 16, ROWS = 64 / UNITS, N = KEYS / ROWS;
     static constexpr int BYTES = code_bytes<FMT>(16), WORDS = BYTES / 4;
     uint32_t c[N][WORDS], s[N];
 
     static __device__ __forceinline__ int row(int lane) { return lane / UNITS; }
     static __device__ __forceinline__ int unit(int lane) { return lane % UNITS; }
 
-    // Tile whose rows are all there, the first at p (scales at ps), of
-    // strides under 2^24; `off`, `soff` the lane's places in a round.
-    static __device__ __forceinline__ uint32_t offset(int lane, int64_t stride, int D)
+    // The lane's place in a round, of strides under 2^24; `rows`: those of the
+    // tile that are there (the others are read from the last, and set to zero
+    // when they are placed).
+    static __device__ __forceinline__ uint32_t offset(int lane, uint32_t stride, int D)
     {
-        return (uint32_t)(row(lane) * stride) + min(unit(lane), (D - 1) / 16) * BYTES;
+        return row(lane) * stride + min(unit(lane), (D - 1) / 16) * BYTES;
     }
-    static __device__ __forceinline__ uint32_t scale_offset(int lane, int64_t stride, int D)
+    static __device__ __forceinline__ uint32_t scale_offset(int lane, uint32_t stride, int D)
     {
-        return (uint32_t)(row(lane) * stride) + min(unit(lane), (D - 1) / 16) / 2;
+        return row(lane) * stride + min(unit(lane), (D - 1) / 16) / 2;
     }
-    __device__ __forceinline__ void load(const uint8_t *p, const uint8_t *ps, int64_t stride,
-                                         int64_t sstride, uint32_t off, uint32_t soff, int rw,
-                                         int wr)
+    // A tile at p, its scales at ps.
+    __device__ __forceinline__ void load(const uint8_t *p, const uint8_t *ps, uint32_t stride,
+                                         uint32_t sstride, uint32_t off, uint32_t soff, int rows,
+                                         int lane)
     {
+        if (__builtin_expect(rows >= KEYS, 1)) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            if ((j & (wr - 1)) != rw) continue;
-            const uint8_t *q = p + j * ROWS * stride + off;
-            if constexpr (WORDS == 4) {
-                const u32x4 x = *(const u32x4 *)q;
-                c[j][0] = x.x;
-                c[j][1] = x.y;
-                c[j][2] = x.z;
-                c[j][3] = x.w;
-            } else {
-                const u32x2 x = *(const u32x2 *)q;
-                c[j][0] = x.x;
-                c[j][1] = x.y;
+            for (int j = 0; j < N; ++j) {
+                word(j, p + j * ROWS * stride + off);
+                s[j] = (ps + j * ROWS * sstride)[soff];
             }
-            s[j] = (ps + j * ROWS * sstride)[soff];
+        } else {
+            const int r = row(opaque(lane));
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const uint32_t at = min(j * ROWS + r, rows - 1) - r;       // (may be under 0: wraps)
+                word(j, p + (uint32_t)(at * stride + off));
+                s[j] = ps[(uint32_t)(at * sstride + soff)];
+            }
         }
     }
-    // Any tile, from row k0 of base; rows from `end` on are read from the last
-    // before it, and set to zero when they are placed.
+    __device__ __forceinline__ void word(int j, const uint8_t *q)
+    {
+        if constexpr (WORDS == 4) {
+            const u32x4 x = *(const u32x4 *)q;
+            c[j][0] = x.x;
+            c[j][1] = x.y;
+            c[j][2] = x.z;
+            c[j][3] = x.w;
+        } else {
+            const u32x2 x = *(const u32x2 *)q;
+            c[j][0] = x.x;
+            c[j][1] = x.y;
+        }
+    }
+    // Any tile, from row k0 of base (up to row end - 1), 4 bytes or 1 at a time.
     __device__ __forceinline__ void load_any(const uint8_t *base, const uint8_t *sbase,
                                              int64_t stride, int64_t sstride, int k0, int end,
-                                             int width, int D, int lane, int rw, int wr)
+                                             int width, int D, int lane)
     {
-        const int l = opaque(lane), bytes = code_bytes<FMT>(D);
-        const int u = min(unit(l), (D - 1) / 16);
+        const int bytes = code_bytes<FMT>(D), u = min(unit(lane), (D - 1) / 16);
+        const int left = bytes - u * BYTES;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            if ((j & (wr - 1)) != rw) continue;
-            const int64_t r = min(k0 + j * ROWS + row(l), end - 1);
+            const int64_t r = min(k0 + j * ROWS + row(lane), end - 1);
             const uint8_t *q = base + r * stride + u * BYTES;
-            const int left = bytes - u * BYTES;
             s[j] = sbase[r * sstride + u / 2];
-            if (width == BYTES) {
-                const uint32_t *w = (const uint32_t *)__builtin_assume_aligned(q, BYTES);
 #pragma unroll
-                for (int i = 0; i < WORDS; ++i) c[j][i] = w[i];
-            } else if (width == 4) {
+            for (int i = 0; i < WORDS; ++i) c[j][i] = 0u;
+            if (width >= 4) {
 #pragma unroll
                 for (int i = 0; i < WORDS; ++i)
-                    c[j][i] = 4 * i < left ? ((const uint32_t *)q)[i] : 0u;
+                    if (4 * i < left) c[j][i] = ((const uint32_t *)q)[i];
             } else {
-#pragma unroll
-                for (int i = 0; i < WORDS; ++i) c[j][i] = 0u;
 #pragma unroll
                 for (int i = 0; i < BYTES; ++i)
                     if (i < left) c[j][i / 4] |= (uint32_t)q[i] << (8 * (i % 4));
@@ -142,14 +271,13 @@ struct CodeTile {
     // Into LDS, widened.  clear: rows from `end` on, and units past D, are
     // zero; drop: infinities and NaN too (true if there was one).
     __device__ __forceinline__ bool place(R *tile, int k0, int end, int D, bool clear, bool drop,
-                                          int lane, int rw, int wr)
+                                          int lane)
     {
         bool bad = false;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            if ((j & (wr - 1)) != rw) continue;
             const int r = j * ROWS + row(lane), u = unit(lane);
-            if (clear) {
+            if (__builtin_expect(clear, 0)) {
                 const bool there = k0 + r < end && u * 16 < D;
                 s[j] = there ? s[j] : 127u;
 #pragma unroll
@@ -161,7 +289,7 @@ struct CodeTile {
                 Frag<T> x;
                 if constexpr (FMT == kE4M3) widen8<T, FMT>(c[j][2 * h], c[j][2 * h + 1], f, x.w);
                 else widen8<T, FMT>(c[j][h], 0u, f, x.w);
-                if (drop) bad |= drop_nonfinite<T>(x);
+                if (__builtin_expect(drop, 0)) bad |= drop_nonfinite<T>(x);
                 u32x4 *q = (u32x4 *)(tile + tile_at<R, DP>(r, 2 * u + h));
 #pragma unroll
                 for (int i = 0; i < Frag<T>::NV; ++i) q[i] = x.w[i];
@@ -171,55 +299,73 @@ struct CodeTile {
     }
 };
 
-template <typename T, int FMT, int DP, int DU, bool GEN>
-__global__ __launch_bounds__(64 * kCachedWaves, (sizeof(typename T::raw) * DP > 256 ? 1 : 2))
-void attn_cached_kernel(CachedArgs c)
+template <int N>
+struct Half {
+    static constexpr int value = N;
+};
+
+// The kernel's arguments, read no earlier than here.
+__device__ __forceinline__ auto late_args()
+{
+    typedef const __attribute__((address_space(4))) CachedArgs args_t;
+    const args_t *p = (const args_t *)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return p;
+}
+
+// A workgroup's chunk: `id` of its part of the launch.  ANY: codes of any
+// alignment and strides.
+template <typename T, int FMT, int DP, int DU, bool GEN, bool ANY, int MB>
+__device__ __forceinline__ void cached_chunk(const CachedArgs &c, bool own, uint32_t id,
+                                             unsigned char *smem)
 {
     using R = typename T::raw;
+    using C = Cols<MB>;
     constexpr bool PLAIN = FMT == kPlain;
-    constexpr int KB = kCachedKeys, NC = DU / 16, ND = DU / 32, NW = kCachedWaves;
+    constexpr int KB = kCachedKeys, NW = kCachedWaves, SLOTS = cached_slots<FMT, MB>();
+    constexpr int WR = MB == 16 ? 1 : NW, WK = NW / WR;    // waves that share the rows, the keys out
+    constexpr int NC = DU / C::DEPTH, ND = DU / MB, NS = C::SCORES;
+    // keys that a wave brings, and goes through, at a time
+    constexpr int BRING = WR == 1 ? KB : 2 * KB / NW, TILES = WR == 1 ? 1 : 2;
     constexpr bool ALL = DU == DP;         // whole tiles with all their channels
     constexpr float kRaise = 8.f;
-    extern __shared__ __align__(16) unsigned char smem[];
     const AttnArgs &a = c.a;
+    const CachedPart &p = c.part[own];
     const int axes = GEN ? a.axes : 0;
-    const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63, col = lane & 31,
-              half = lane >> 5;
-    int *const pos_lds = (int *)(smem + cached_tiles<T, DP>());        // [NW][2][3][KB]
-    float *const ml = (float *)pos_lds + NW * 2 * 3 * KB;              // [NW][32][2]
-    int *const flag = (int *)(ml + NW * 64);                           // something was dropped
+    const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63, col = lane & (MB - 1),
+              part4 = lane / MB * 4;
+    int *const pos_lds = (int *)(smem + cached_tiles<T, FMT, DP, MB>());   // [NW][2][3][KB]
+    float *const ml = (float *)pos_lds + NW * 2 * 3 * KB;              // [NW][MB][2]
+    int *const flag = (int *)(ml + NW * 2 * MB);                       // something was dropped
 
     // Which cache, head, chunk and rows.  Blocks of rows that read the same
     // chunk go to the same XCD, one after another.
-    const bool own = blockIdx.x >= c.part[0].blocks;
-    const CachedPart &p = c.part[own];
-    int64_t id = blockIdx.x - (own ? c.part[0].blocks : 0);
     int rb = 0;
     if (p.nrb > 1) {
-        const int64_t i = id >> 3;
-        rb = (int)(i % p.nrb);
-        id = (i / p.nrb) * 8 + (id & 7);
-        if (id >= p.units) return;
+        const uint32_t i = id >> 3, group = i / (uint32_t)p.nrb;
+        rb = (int)(i - group * p.nrb);
+        id = group * 8 + (id & 7);
+        if (id >= (uint32_t)p.units) return;
     }
-    const int hk = (int)(id % a.Hk);
-    id /= a.Hk;
-    const int cache = (int)(id % p.caches), sp_no = (int)(id / p.caches);
-    const int wr = PLAIN ? 1 : p.wr, wk = NW / wr, rw = wave & (wr - 1), kw = wave / wr;
+    const uint32_t rest_id = id / (uint32_t)a.Hk, sp_no = rest_id / (uint32_t)p.caches;
+    const int hk = (int)(id - rest_id * a.Hk), cache = (int)(rest_id - sp_no * p.caches);
+    const int rw = WR == 1 ? 0 : wave;
 
     // the rows: new token t and query head of a sequence
-    const int per = a.Tq * a.G, row0 = rb * 32 * wr, r = row0 + rw * 32 + col;
-    const int rc = min(r, p.rows - 1), seq = rc / per, t = (rc - seq * per) / a.G;
-    const int b = cache * p.seqs + seq, h = hk * a.G + (rc - seq * per) % a.G;
+    const int per = a.Tq * a.G, row0 = rb * MB * WR, r = row0 + rw * MB + col;
+    const int rc = min(r, p.rows - 1), seq = (uint32_t)rc / (uint32_t)per,
+              in_seq = rc - seq * per, t = (uint32_t)in_seq / (uint32_t)a.G;
+    const int b = cache * p.seqs + seq, h = hk * a.G + in_seq - t * a.G;
     const int len = cached_len(p, cache);
     const int end = cached_end(c, own, len, t);            // the row's keys
     // the workgroup's chunk, and the keys that all its rows see: the last row
     // of a block sees the most of an own cache, the first the least
-    const int last = min(row0 + 32 * wr, p.rows) - 1;
+    const int last = min(row0 + MB * WR, p.rows) - 1;
     const int most = cached_end(c, own, len, own ? last / a.G : 0);
     const int all = cached_end(c, own, len, own ? row0 / a.G : 0);
-    const int c0 = sp_no * p.chunk, c1 = (int)min((int64_t)c0 + p.chunk, (int64_t)most);
-    const int slots = c.part[0].nsplit + c.part[1].nsplit;
-    if (c0 >= c1 && slots > 1) return;     // (the join does not read this chunk)
+    const int c0 = (int)sp_no * p.chunk, c1 = (int)min((int64_t)c0 + p.chunk, (int64_t)most);
+    // (the join does not read this chunk)
+    if (c0 >= c1 && c.part[0].nsplit + c.part[1].nsplit > 1) return;
     if (tid == 0) *flag = 0;
 
     const auto *kp = (const R *)p.k, *vp = (const R *)p.v;             // plain
@@ -234,49 +380,84 @@ void attn_cached_kernel(CachedArgs c)
         ksc += cache * p.kss[0] + hk * p.kss[2];
         vsc += cache * p.vss[0] + hk * p.vss[2];
     }
-    f32x16 o[ND];
+    typename C::acc o[ND];
 #pragma unroll
-    for (int d = 0; d < ND; ++d) o[d] = f32x16(0.f);
+    for (int d = 0; d < ND; ++d) o[d] = typename C::acc(0.f);
     float m = kNegInf, l = 0.f;
     bool dropped = false;
     __syncthreads();                       // (the flag)
 
     if (c0 < c1) {
-        R *const tiles = (R *)smem;
-        int *const pk = pos_lds + wave * 2 * 3 * KB;
         const int32_t *pos = p.pos + (int64_t)cache * p.T;
         const int64_t pos_axis = (int64_t)p.caches * p.T;
-        const int steps = ((c1 - c0 + KB - 1) / KB + wk - 1) / wk;
+        // wr = 1: the wave's tiles of keys and values, one or two places.
+        // wr = 4: the wave's part of two tiles of keys; those of values behind
+        // them; the second half of LDS behind all that.
+        constexpr int kHalf = 4 * KB * DP;
+        R *const kt = (R *)smem + (WR == 1 ? wave * SLOTS * KB * DP : wave * BRING * DP);
+        R *const vt = kt + (WR == 1 ? (SLOTS - 1) * KB * DP : 2 * KB * DP);
+        // positions: [2][3][keys of a step]
+        constexpr int kPos = WR == 1 ? KB : 2 * KB;
+        int *const pk = pos_lds + (WR == 1 ? wave * 2 * 3 * KB : 0);
+
+        // (a wave alone with its tile: its operations on LDS keep their order)
+        auto in_order = [] { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); };
+
+        // the wave's queries: element by element by way of LDS, or (below, with
+        // the first keys on their way) 16 bytes at a time
+        const R *qp = (const R *)a.q + b * a.qs[0] + h * a.qs[2] + (int64_t)t * a.qs[1];
+        Frag<T> qf[NC];
+        if (__builtin_expect(!a.vec, 0)) {
+            R *const x = (R *)smem + wave * MB * DP;
+            for (int i = 0; i < MB; ++i) {
+                const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)(uintptr_t)qp, i),
+                               hi = __builtin_amdgcn_readlane((uint32_t)((uintptr_t)qp >> 32), i);
+                const R *row = (const R *)(((uintptr_t)hi << 32) | lo);
+                for (int ch = lane; ch < DP; ch += 64)
+                    x[tile_at<R, DP>(i, ch >> 3) + (ch & 7)] = ch < a.D ? row[ch] : R(0);
+            }
+            wait_all();
+            in_order();
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+                qf[i] = row_frag<T, DP>(x, col, i * C::DEPTH + part4 * 2);
+            reads_done();
+            __syncthreads();
+        }
 
         // plain: straight to LDS
-        TileDirect<T, DP, KB, 64> kd, vd;
-        R *const kt = tiles + wave * 2 * KB * DP, *const vt = kt + KB * DP;
+        using Direct = TileDirect<T, DP, BRING, 64>;
+        Direct kd, vd;
         bool usable = false, whole = false;
         uint32_t lds_k = 0, lds_v = 0, lds_p = 0;
         if constexpr (PLAIN) {
             kd.init(lane, p.ks[1], a.D);
             vd.init(lane, p.vs[1], a.D);
-            usable = kd.usable(p.vec, p.ks[1], a.D) && vd.usable(p.vec, p.vs[1], a.D);
+            usable = MB == 32 || !c.any;   // (or blocks of 16)
             whole = usable && (!ALL || a.D == DP);
             lds_k = lds_address(kt);
             lds_v = lds_address(vt);
             lds_p = lds_address(pk);
             if (a.D < DP) {                // channels that no direct load writes
-                for (int x = lane; x < 2 * KB * DP * (int)sizeof(R) / 16; x += 64)
-                    ((u32x4 *)kt)[x] = u32x4{0u, 0u, 0u, 0u};
-                reads_done();              // (these writes are)
+                for (int x = tid; x < NW * 2 * KB * DP * (int)sizeof(R) / 16; x += 64 * NW)
+                    ((u32x4 *)smem)[x] = u32x4{0u, 0u, 0u, 0u};
+                __syncthreads();
             }
         }
-        auto direct = [&](const TileDirect<T, DP, KB, 64> &d, const R *x, int64_t stride, int k0,
-                          uint32_t lds) {
-            if (whole && k0 + KB <= c1) d.template load<ALL>(x + k0 * stride, lds);
+        auto direct = [&](const Direct &d, const R *x, int64_t stride, int k0, uint32_t lds) {
+            if (whole && k0 + BRING <= c1) d.template load<ALL>(x + k0 * stride, lds);
             else if (usable) d.load_edge(x, stride, k0, c0, c1, lds);
         };
-        auto by_registers = [&](const R *x, int64_t stride, int k0, R *tile) {
-            TileRegs<T, DP, KB, 64> g;
-            g.load(x, stride, k0, c0, c1, a.D, p.vec, lane);
-            g.store(tile, lane);
+        // element by element (rows of any alignment)
+        auto one_by_one = [&](const R *x, int64_t stride, int k0, R *tile) {
+#pragma unroll 4
+            for (int i = lane; i < KB * DP; i += 64) {
+                const int row = i / DP, ch = i % DP;
+                tile[tile_at<R, DP>(row, ch >> 3) + (ch & 7)] =
+                    k0 + row < c1 && ch < a.D ? x[(int64_t)(k0 + row) * stride + ch] : R(0);
+            }
             wait_all();
+            in_order();
         };
         // three axes or none, so that what is in flight can be counted
         auto direct_pos = [&](int k0, int buf) {
@@ -288,47 +469,78 @@ void attn_cached_kernel(CachedArgs c)
         };
 
         // codes: by way of registers
-        using Codes = CodeTile<T, PLAIN ? kE4M3 : FMT, DP>;
+        using Codes = CodeTile<T, PLAIN ? kE4M3 : FMT, DP, BRING>;
         Codes kc, vc;
-        const bool fast = !PLAIN && p.width == Codes::BYTES &&
-                          max(max(p.ks[1], p.vs[1]), max(p.kss[1], p.vss[1])) < (1 << 24);
-        const uint32_t koff = Codes::offset(lane, p.ks[1], a.D),
-                       voff = Codes::offset(lane, p.vs[1], a.D),
-                       ksoff = Codes::scale_offset(lane, p.kss[1], a.D),
-                       vsoff = Codes::scale_offset(lane, p.vss[1], a.D);
+        const uint32_t kst = (uint32_t)p.ks[1], vst = (uint32_t)p.vs[1], ksst = (uint32_t)p.kss[1],
+                       vsst = (uint32_t)p.vss[1];
+        const uint32_t koff = Codes::offset(lane, kst, a.D), voff = Codes::offset(lane, vst, a.D),
+                       ksoff = Codes::scale_offset(lane, ksst, a.D),
+                       vsoff = Codes::scale_offset(lane, vsst, a.D);
         int pr[3] = {0, 0, 0};
-        auto fetch = [&](int k0) {
-            if (fast && k0 + KB <= c1) {
-                kc.load(kq + k0 * p.ks[1], ksc + k0 * p.kss[1], p.ks[1], p.kss[1], koff, ksoff, rw,
-                        wr);
-                vc.load(vq + k0 * p.vs[1], vsc + k0 * p.vss[1], p.vs[1], p.vss[1], voff, vsoff, rw,
-                        wr);
-            } else {
-                kc.load_any(kq, ksc, p.ks[1], p.kss[1], k0, c1, p.width, a.D, lane, rw, wr);
-                vc.load_any(vq, vsc, p.vs[1], p.vss[1], k0, c1, p.width, a.D, lane, rw, wr);
-            }
+        auto fetch_pos = [&](int k0) {
 #pragma unroll
             for (int x = 0; x < 3; ++x) {
                 if (x >= axes) break;
-                pr[x] = pos[x * pos_axis + min(k0 + col, p.T - 1)];
+                pr[x] = pos[x * pos_axis + min(k0 + (lane & (BRING - 1)), p.T - 1)];
             }
         };
-
-        const int kbeg = c0 + kw * KB;
-        if constexpr (PLAIN) {
-            if (kbeg < c1) {
-                direct_pos(kbeg, 0);
+        auto fetch_keys = [&](int k0) {
+            if constexpr (ANY)
+                kc.load_any(kq, ksc, p.ks[1], p.kss[1], k0, c1, p.width, a.D, lane);
+            else
+                kc.load(kq + (int64_t)k0 * kst, ksc + (int64_t)k0 * ksst, kst, ksst, koff, ksoff,
+                        c1 - k0, lane);
+            fetch_pos(k0);
+        };
+        auto fetch_values = [&](int k0) {
+            if constexpr (ANY)
+                vc.load_any(vq, vsc, p.vs[1], p.vss[1], k0, c1, p.width, a.D, lane);
+            else
+                vc.load(vq + (int64_t)k0 * vst, vsc + (int64_t)k0 * vsst, vst, vsst, voff, vsoff,
+                        c1 - k0, lane);
+        };
+        // some of these keys are not there, or some rows do not see them
+        auto partly = [&](int k0, int keys) { return k0 + keys > min(all, c1); };
+        auto place_pos = [&](int buf) {
+#pragma unroll
+            for (int x = 0; x < 3; ++x) {
+                if (x >= axes) break;
+                if (lane < BRING)
+                    pk[(buf * 3 + x) * kPos + (WR == 1 ? 0 : wave * BRING) + lane] = pr[x];
+            }
+        };
+        auto place_keys = [&](int k0, int buf) {
+            kc.place(kt + buf * kHalf, k0, c1, a.D, k0 + BRING > c1 || a.D < DP, false, lane);
+            place_pos(buf);
+        };
+        auto place_values = [&](int k0, int buf) {
+            dropped |= vc.place(vt + buf * kHalf, k0, c1, a.D, k0 + BRING > c1 || a.D < DP,
+                                partly(k0, BRING), lane);
+        };
+        const int kbeg = c0 + wave * BRING;
+        if (kbeg < c1) {
+            if constexpr (PLAIN) {
+                if (WR == 1) direct_pos(kbeg, 0);
+                else fetch_pos(kbeg);
                 direct(kd, kp, p.ks[1], kbeg, lds_k);
                 direct(vd, vp, p.vs[1], kbeg, lds_v);
+            } else {
+                fetch_keys(kbeg);
+                fetch_values(kbeg);
             }
-        } else {
-            if (kbeg < c1) fetch(kbeg);
         }
 
-        const R *qp = (const R *)a.q + b * a.qs[0] + h * a.qs[2] + (int64_t)t * a.qs[1];
-        Frag<T> qf[NC];
+        if (a.vec) {
 #pragma unroll
-        for (int i = 0; i < NC; ++i) qf[i] = load8<T>(qp, i * 16 + half * 8, a.D, a.vec);
+            for (int i = 0; i < NC; ++i) {
+                const int d0 = i * C::DEPTH + part4 * 2;
+                qf[i].zero();
+                if (ALL || d0 < a.D)
+#pragma unroll
+                    for (int j = 0; j < Frag<T>::NV; ++j) qf[i].w[j] = ((const u32x4 *)(qp + min(d0, a.D - 8)))[j];
+                if (ALL && d0 >= a.D) qf[i].zero();
+            }
+        }
         const Scores sc = scores(a);
         int pq[3];
         float sl[3];
@@ -341,95 +553,48 @@ void attn_cached_kernel(CachedArgs c)
             arrived(sl[x]);
         }
         arrived(qf);
-        constexpr int kTile = TileDirect<T, DP, KB, 64>::LOADS;
-        int buf = 0;
-        for (int i = 0; i < steps; ++i, buf ^= 1) {
-            const int k0 = kbeg + i * wk * KB;
-            const bool live = k0 < c1, more = k0 + wk * KB < c1, part = k0 + KB > min(all, c1);
-            const R *kx = kt, *vx = vt;
-            const int *px = pk + buf * 3 * KB;
-            Frag<T> kf[NC], vf[ND][2];
-            f32x16 s = f32x16(0.f);
-            if constexpr (PLAIN) {
-                if (!live) break;
-                // keys: in flight after them are this tile's values.  (A wave's
-                // LDS operations keep their order: no barrier)
-                wait_loads<kTile>(usable);
-                if (!usable) by_registers(kp, p.ks[1], k0, kt);
-            } else {
-                R *const slot = tiles + (kw * wr + (i & (wr - 1))) * 2 * KB * DP;
-                kx = slot;
-                vx = slot + KB * DP;
-                px = pk;
-                if (live) {
-                    // (a wave alone with its tile: its reads of the last one
-                    // come before these writes)
-                    const bool edge = k0 + KB > c1 || a.D < DP;
-                    kc.place(slot, k0, c1, a.D, edge, false, lane, rw, wr);
-                    dropped |= vc.place(slot + KB * DP, k0, c1, a.D, edge, part, lane, rw, wr);
-#pragma unroll
-                    for (int x = 0; x < 3; ++x) {
-                        if (x >= axes) break;
-                        if (half == 0) pk[x * KB + col] = pr[x];
-                    }
-                }
-                if (wr > 1) hand_over();
-                else __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-                if (more) fetch(k0 + wk * KB);
-                if (!live) continue;
-            }
-#pragma unroll
-            for (int d = 0; d < NC; ++d) kf[d] = row_frag<T, DP>(kx, col, d * 16 + half * 8);
-            if constexpr (PLAIN) {
-                reads_done();
-                if (more) {
-                    direct_pos(k0 + wk * KB, buf ^ 1);
-                    direct(kd, kp, p.ks[1], k0 + wk * KB, lds_k);
-                }
-            }
-#pragma unroll
-            for (int d = 0; d < NC; ++d) s = mma<T>(kf[d], qf[d], s);
-            if constexpr (PLAIN) {
-                // values: in flight after them are the next tile's keys
-                if (axes > 0) wait_loads<kTile + 3>(more && usable);
-                else wait_loads<kTile>(more && usable);
-                if (!usable) by_registers(vp, p.vs[1], k0, vt);
-                if (part) {
-                    dropped |= vd.scrub(vt, k0, c0, c1, true, nullptr, 0);
-                    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-                }
-            }
-#pragma unroll
-            for (int d = 0; d < ND; ++d)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) vf[d][e] = col_frag<T, DP>(vx, e, d * 32, lane);
-            if constexpr (PLAIN) {
-                reads_done();
-                if (more) direct(vd, vp, p.vs[1], k0 + wk * KB, lds_v);
-            }
+        constexpr int kTile = Direct::LOADS;
 
-            if (GEN) multiply_scores(s, sc);
-            if (GEN && a.cap > 0.f) cap_scores<T>(s, sc, part);
+        // The scores' factor, cap, bias and mask; keys from k0 on.
+        auto finish = [&](typename C::scores (&s)[TILES], int k0, const int *px, bool part) {
+            if (GEN) {
+#pragma unroll
+                for (int u = 0; u < TILES; ++u) multiply_scores(s[u], sc);
+            }
+            if (GEN && a.cap > 0.f) {
+#pragma unroll
+                for (int u = 0; u < TILES; ++u) cap_scores<T>(s[u], sc, part);
+            }
 #pragma unroll
             for (int x = 0; x < 3; ++x) {
                 if (x >= axes) break;
-                const int *q = px + x * KB + 4 * half;
+                const int *q = px + x * kPos + part4;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int k = q[acc_row(e, 0)];        // (up to 2^32 apart)
-                    s[e] = fmaf(-sl[x], (float)((uint32_t)max(k, pq[x]) - (uint32_t)min(k, pq[x])),
-                                s[e]);
-                }
+                for (int u = 0; u < TILES; ++u)
+#pragma unroll
+                    for (int e = 0; e < NS; ++e) {
+                        const int k = q[u * KB + C::group(e)];     // (up to 2^32 apart)
+                        const uint32_t far = (uint32_t)max(k, pq[x]) - (uint32_t)min(k, pq[x]);
+                        s[u][e] = fmaf(-sl[x], (float)far, s[u][e]);
+                    }
             }
             if (part) {
-                const int left = end - k0 - 4 * half;
+                const int left = end - k0 - part4;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) s[e] = acc_row(e, 0) < left ? s[e] : kNegInf;
+                for (int u = 0; u < TILES; ++u)
+#pragma unroll
+                    for (int e = 0; e < NS; ++e)
+                        s[u][e] = u * KB + C::group(e) < left ? s[u][e] : kNegInf;
             }
-            float mx = s[0];
+        };
+        // The maximum raised to these scores, and the sums so far with it.
+        auto raise = [&](const typename C::scores (&s)[TILES]) {
+            float mx = s[0][0];
 #pragma unroll
-            for (int e = 1; e < 16; ++e) mx = fmaxf(mx, s[e]);
-            mx = halves_max(mx) * sc.mul;
+            for (int u = 0; u < TILES; ++u)
+#pragma unroll
+                for (int e = 0; e < NS; ++e) mx = fmaxf(mx, s[u][e]);
+            mx = C::over_parts_max(mx) * sc.mul;
             if (__any(mx > m + kRaise)) {
                 // (each query by itself: its sums do not depend on its neighbours')
                 const float mn = mx > m + kRaise ? mx : m;
@@ -438,131 +603,363 @@ void attn_cached_kernel(CachedArgs c)
 #pragma unroll
                 for (int d = 0; d < ND; ++d)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) o[d][e] *= al;
+                    for (int e = 0; e < C::PER; ++e) o[d][e] *= al;
                 m = mn;
             }
+        };
+        auto weights = [&](typename C::scores &s) {
             const float ms = m == kNegInf ? 0.f : m;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
+            for (int e = 0; e < NS; ++e) {
                 s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], sc.mul, -ms));
                 l += s[e];
             }
-            const Frag<T> p0 = pack8<T>(s, 0), p1 = pack8<T>(s, 1);
+        };
+
+        if constexpr (WR == 1) {
+            typename C::scores s[1];
+            auto products = [&] {
+                Frag<T> kf[KB / MB][NC];
+                typename C::acc x[KB / MB];
 #pragma unroll
-            for (int d = 0; d < ND; ++d) {
-                o[d] = mma<T>(vf[d][0], p0, o[d]);
-                o[d] = mma<T>(vf[d][1], p1, o[d]);
+                for (int u = 0; u < KB / MB; ++u) {
+                    x[u] = typename C::acc(0.f);
+#pragma unroll
+                    for (int d = 0; d < NC; ++d)
+                        kf[u][d] = row_frag<T, DP>(kt, u * MB + col, d * C::DEPTH + part4 * 2);
+                }
+#pragma unroll
+                for (int d = 0; d < NC; ++d)
+#pragma unroll
+                    for (int u = 0; u < KB / MB; ++u)
+                        x[u] = mma_cols<T, MB>(kf[u][d], qf[d], x[u]);
+#pragma unroll
+                for (int u = 0; u < KB / MB; ++u)
+#pragma unroll
+                    for (int e = 0; e < C::PER; ++e) s[0][u * C::PER + e] = x[u][e];
+            };
+            int buf = 0;
+            for (int k0 = kbeg; k0 < c1; k0 += NW * KB, buf ^= PLAIN) {
+                const int next = k0 + NW * KB;
+                const bool more = next < c1, part = partly(k0, KB);
+                if constexpr (PLAIN) {
+                    // keys: in flight after them are this tile's values
+                    wait_loads<kTile>(usable);
+                    if (!usable) one_by_one(kp, p.ks[1], k0, kt);
+                    products();
+                    reads_done();
+                    if (more) {
+                        direct_pos(next, buf ^ 1);
+                        direct(kd, kp, p.ks[1], next, lds_k);
+                    }
+                    // values: in flight after them are the next tile's keys
+                    if (axes > 0) wait_loads<kTile + 3>(more && usable);
+                    else wait_loads<kTile>(more && usable);
+                    if (!usable) one_by_one(vp, p.vs[1], k0, vt);
+                    if (part) {
+                        dropped |= vd.scrub(vt, k0, c0, c1, true, nullptr, 0);
+                        in_order();
+                    }
+                } else {
+                    in_order();
+                    place_keys(k0, 0);
+                    if (more) fetch_keys(next);
+                    in_order();
+                    products();
+                    in_order();
+                    place_values(k0, 0);
+                    if (more) fetch_values(next);
+                    in_order();
+                }
+                Frag<T> vf[ND][NS / 8], w[NS / 8];
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int e = 0; e < NS / 8; ++e)
+                        vf[d][e] = value_frag<T, DP, MB>(vt, e, d * MB, lane);
+                if constexpr (PLAIN) {
+                    reads_done();
+                    if (more) direct(vd, vp, p.vs[1], next, lds_v);
+                }
+                finish(s, k0, pk + buf * 3 * KB, part);
+                raise(s);
+                weights(s[0]);
+#pragma unroll
+                for (int e = 0; e < NS / 8; ++e) w[e] = pack_scores<T>(s[0], e);
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int e = 0; e < NS / 8; ++e) o[d] = mma_cols<T, MB>(vf[d][e], w[e], o[d]);
+            }
+        } else {
+            // this wave's part of two tiles, into the half `buf`
+            auto place = [&](int k0, int buf) {
+                if constexpr (PLAIN) {
+                    wait_loads<0>(false);
+                    if (k0 < c1) {
+                        if (partly(k0, BRING))
+                            dropped |= vd.scrub(vt + buf * kHalf, k0, c0, c1, true, nullptr, 0);
+                        place_pos(buf);
+                    }
+                } else if (k0 < c1) {
+                    place_keys(k0, buf);
+                    place_values(k0, buf);
+                }
+                if (k0 >= c1 && k0 - wave * BRING < c1) {
+                    // (behind the last key, in a step that has some)
+                    for (int x = lane; x < BRING * DP * (int)sizeof(R) / 16; x += 64)
+                        ((u32x4 *)(vt + buf * kHalf))[x] = u32x4{0u, 0u, 0u, 0u};
+                }
+                hand_over();
+            };
+            place(kbeg, 0);
+            // blocks of channels whose values are read ahead of the weights
+            constexpr int AHEAD = GEN ? 1 : ND / 2;
+            auto step = [&](int first, auto half) {
+                constexpr int buf = decltype(half)::value;
+                const int next = first + 2 * KB + wave * BRING;
+                const bool part = partly(first, 2 * KB);
+                if (next < c1) {
+                    if constexpr (PLAIN) {
+                        constexpr uint32_t off = (buf ^ 1) * kHalf * (uint32_t)sizeof(R);
+                        fetch_pos(next);
+                        direct(kd, kp, p.ks[1], next, lds_k + off);
+                        direct(vd, vp, p.vs[1], next, lds_v + off);
+                    } else {
+                        fetch_keys(next);
+                        fetch_values(next);
+                    }
+                }
+                const R *kb = (const R *)smem + buf * kHalf, *vb = kb + 2 * KB * DP;
+                Frag<T> kf[NC][2], vf[ND][4], w[4];
+                typename C::scores s[TILES] = {};
+                auto read_values = [&](int d) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) vf[d][e] = col_frag<T, DP>(vb, e, d * 32, lane);
+                };
+#pragma unroll
+                for (int d = 0; d < NC; ++d)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        kf[d][u] = row_frag<T, DP>(kb, u * 32 + col, d * 16 + part4 * 2);
+#pragma unroll
+                for (int d = 0; d < NC; ++d)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) s[u] = mma<T>(kf[d][u], qf[d], s[u]);
+#pragma unroll
+                for (int d = 0; d < AHEAD; ++d) read_values(d);
+                reads_ahead<T, NC>();
+                products_and_reads<T, NC, 1>();
+                products_and_reads<T, AHEAD * 4, 2>();
+                products_and_reads<T, NC - AHEAD * 4, 0>();
+                issued<T>();
+                finish(s, first, pk + buf * 3 * kPos, part);
+                raise(s);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    weights(s[u]);
+                    w[2 * u] = pack_scores<T>(s[u], 0);
+                    w[2 * u + 1] = pack_scores<T>(s[u], 1);
+                }
+                // (a block's reads go out under the products of the AHEAD before)
+#pragma unroll
+                for (int x = 0; x < ND; x += AHEAD) {
+#pragma unroll
+                    for (int d = x + AHEAD; d < x + 2 * AHEAD && d < ND; ++d) read_values(d);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int d = x; d < x + AHEAD && d < ND; ++d)
+                            o[d] = mma<T>(vf[d][e], w[e], o[d]);
+                }
+                products_and_reads<T, (ND - AHEAD) * 4, 2>();
+                products_and_reads<T, AHEAD * 4, 0>();
+                issued<T>();
+                if (first + 2 * KB < c1) place(next, buf ^ 1);
+            };
+            for (int first = c0; first < c1; first += 4 * KB) {
+                step(first, Half<0>{});
+                if (first + 2 * KB < c1) step(first + 2 * KB, Half<1>{});
             }
         }
         if (__any(dropped) && lane == 0) *flag = 1;
     }
-    l = halves_sum(l);
+    l = C::over_parts_sum(l);
 
     __syncthreads();
-    if (*flag) {
-        // the wave's tiles again: infinities and NaN to the rows that see them
-        for (int k0 = c0 + kw * KB; k0 < c1; k0 += wk * KB) {
-            if (k0 + KB <= min(all, c1)) continue;
-            for (int key = k0; key < min(k0 + KB, c1); ++key) {
-                if (key >= end) continue;
+
+    if (WR > 1 && !*flag) {
+        // every row is one wave's: straight from its registers
+        const auto *late = late_args();
+        const int64_t total = (int64_t)late->a.B * late->a.Hq * late->a.Tq;
+        const int D = late->a.D, first_slot = late->part[0].nsplit,
+                  slots = first_slot + late->part[1].nsplit,
+                  slot = (int)sp_no + (own ? first_slot : 0);
+        if (r >= late->part[own].rows) return;
+        if (slots > 1) {
+            const int64_t at = slot * total + ((int64_t)b * late->a.Hk + hk) * per + in_seq;
+            float *out = late->a.part_o + at * cached_stride(D);
 #pragma unroll
-                for (int d = 0; d < ND; ++d)
+            for (int d = 0; d < ND; ++d)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int x = d * 32 + acc_row(e, half);
-                        float v = 0.f;
-                        if (x < a.D) {
-                            if constexpr (PLAIN) v = T::widen(vp[(int64_t)key * p.vs[1] + x]);
-                            else
-                                v = value_at<T, FMT>(vq + key * p.vs[1], vsc + key * p.vss[1], x);
-                        }
-                        if (!(fabsf(v) < __builtin_huge_valf())) o[d][e] += v;
-                    }
-            }
+                for (int e = 0; e < C::PER; e += 4) {
+                    const int x = d * MB + C::group(e) + part4;
+                    if (x < D) *(f32x4 *)(out + x) = f32x4{o[d][e], o[d][e + 1], o[d][e + 2], o[d][e + 3]};
+                }
+            if (part4 == 0) *(float2 *)(late->a.part_ml + 2 * at) = make_float2(m, l);
+        } else {
+            const int64_t at = ((int64_t)b * late->a.Tq + t) * late->a.Hq + h;
+            if constexpr (MB == 32)
+                store_cols<T, ND>((R *)late->a.out + at * D, o, l == 0.f ? 0.f : 1.f / l, D, part4 / 4);
+            if (part4 == 0)
+                late->a.lse[((int64_t)b * late->a.Hq + h) * late->a.Tq + t] =
+                    l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
         }
+        return;
     }
 
     // join the waves that have the same rows
-    float *const jo = (float *)smem;                       // [NW][32][DP + pad]
+    float *const jo = (float *)smem;                       // [NW][MB][DP + pad]
     constexpr int JW = DP + kCachedPad;
-    if (half == 0) {
-        ml[(wave * 32 + col) * 2] = m;
-        ml[(wave * 32 + col) * 2 + 1] = l;
+    if (part4 == 0) {
+        ml[(wave * MB + col) * 2] = m;
+        ml[(wave * MB + col) * 2 + 1] = l;
     }
 #pragma unroll
     for (int d = 0; d < ND; ++d)
 #pragma unroll
-        for (int e = 0; e < 16; e += 4)
-            *(f32x4 *)(jo + (wave * 32 + col) * JW + d * 32 + acc_row(e, half)) =
+        for (int e = 0; e < C::PER; e += 4)
+            *(f32x4 *)(jo + (wave * MB + col) * JW + d * MB + C::group(e) + part4) =
                 f32x4{o[d][e], o[d][e + 1], o[d][e + 2], o[d][e + 3]};
     __syncthreads();
-    const int64_t total = (int64_t)a.B * a.Hq * a.Tq;
-    const int slot = sp_no + (own ? c.part[0].nsplit : 0), stride = cached_stride(a.D);
-    for (int x = tid; x < 32 * wr * (DP / 4); x += 64 * NW) {
+    // (the call's arguments are read again here: kept through the loops they
+    // would fill the scalar registers)
+    const auto *late = late_args();
+    const int64_t total = (int64_t)late->a.B * late->a.Hq * late->a.Tq;
+    const int D = late->a.D, G = late->a.G, rows = late->part[own].rows;
+    const int first_slot = late->part[0].nsplit, slots = first_slot + late->part[1].nsplit;
+    const int slot = (int)sp_no + (own ? first_slot : 0), stride = cached_stride(D);
+    const bool some = *flag;               // an infinity or a NaN was dropped
+    for (int x = tid; x < MB * WR * (DP / 4); x += 64 * NW) {
         const int rr = x / (DP / 4), d = (x - rr * (DP / 4)) * 4;
-        if (row0 + rr >= p.rows) break;
-        if (d >= a.D) continue;
-        const int first = (rr >> 5) * 32 + (rr & 31);      // row of the first such wave
+        if (row0 + rr >= rows) break;
+        if (d >= D) continue;
         float mt = kNegInf;
-        for (int w = 0; w < wk; ++w) mt = fmaxf(mt, ml[(w * wr * 32 + first) * 2]);
+#pragma unroll
+        for (int w = 0; w < WK; ++w) mt = fmaxf(mt, ml[(w * MB + rr) * 2]);
         const float ms = mt == kNegInf ? 0.f : mt;
         float lt = 0.f;
         f32x4 ot = f32x4(0.f);
-        for (int w = 0; w < wk; ++w) {
-            const int at = w * wr * 32 + first;
+#pragma unroll
+        for (int w = 0; w < WK; ++w) {
+            const int at = w * MB + rr;
             const float f = __builtin_amdgcn_exp2f(ml[at * 2] - ms);
             lt = fmaf(f, ml[at * 2 + 1], lt);
             const f32x4 v = *(const f32x4 *)(jo + at * JW + d);
 #pragma unroll
             for (int e = 0; e < 4; ++e) ot[e] = fmaf(f, v[e], ot[e]);
         }
-        const int rg = row0 + rr, sq = rg / per, rest = rg - sq * per;
-        const int64_t bb = cache * (int64_t)p.seqs + sq;
+        const int rg = row0 + rr, sq = rg / per, rest = rg - sq * per, tt = rest / G;
+        if (some) {
+            // the keys that some rows do not see again: what was dropped, to
+            // the rows that do see it
+            const int row_end = min(cached_end(c, own, len, tt), c1), whole = min(all, c1);
+            for (int key = max(c0, whole - 2 * KB + 1); key < row_end; ++key) {
+                if (key / BRING * BRING + BRING <= whole) continue;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (d + e >= D) break;
+                    float v;
+                    if constexpr (PLAIN) v = T::widen(vp[(int64_t)key * p.vs[1] + d + e]);
+                    else v = value_at<T, FMT>(vq + key * p.vs[1], vsc + key * p.vss[1], d + e);
+                    if (!(fabsf(v) < __builtin_huge_valf())) ot[e] += v;
+                }
+            }
+        }
+        const int64_t bb = cache * (int64_t)late->part[own].seqs + sq;
         if (slots > 1) {
-            const int64_t at = slot * total + (bb * a.Hk + hk) * per + rest;
-            *(f32x4 *)(a.part_o + at * stride + d) = ot;
-            if (d == 0) *(float2 *)(a.part_ml + 2 * at) = make_float2(mt, lt);
+            const int64_t at = slot * total + (bb * late->a.Hk + hk) * per + rest;
+            *(f32x4 *)(late->a.part_o + at * stride + d) = ot;
+            if (d == 0) *(float2 *)(late->a.part_ml + 2 * at) = make_float2(mt, lt);
         } else {
-            const int tt = rest / a.G, hh = hk * a.G + rest - tt * a.G;
-            R *out = (R *)a.out + ((bb * a.Tq + tt) * a.Hq + hh) * a.D + d;
+            const int hh = hk * G + rest - tt * G;
+            const int64_t at = (bb * late->a.Tq + tt) * late->a.Hq + hh;
+            R *out = (R *)late->a.out + at * D + d;
             const float inv = lt == 0.f ? 0.f : 1.f / lt;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (d + e < a.D) out[e] = T::narrow(lt == 0.f ? 0.f : ot[e] * inv);
+                if (d + e < D) out[e] = T::narrow(lt == 0.f ? 0.f : ot[e] * inv);
             if (d == 0)
-                a.lse[(bb * a.Hq + hh) * a.Tq + tt] =
+                late->a.lse[(bb * late->a.Hq + hh) * late->a.Tq + tt] =
                     lt == 0.f ? kNegInf : (mt + log2f(lt)) * kLn2;
         }
     }
 }
 
-template <typename T, int FMT, int DP, int DU>
+// MP, MO: columns of the prefix' and of the own caches' workgroups.
+template <typename T, int FMT, int DP, int DU, bool GEN, bool ANY, int MP, int MO>
+__global__ __launch_bounds__(64 * kCachedWaves, (cached_occupancy<T, FMT, DP, GEN, MP>()))
+void attn_cached_kernel(CachedArgs c)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    const uint32_t first = (uint32_t)c.part[0].blocks;
+    if constexpr (MP == MO) {
+        const bool own = blockIdx.x >= first;
+        cached_chunk<T, FMT, DP, DU, GEN, ANY, MP>(c, own, blockIdx.x - (own ? first : 0), smem);
+    } else if (blockIdx.x < first) {
+        cached_chunk<T, FMT, DP, DU, GEN, ANY, MP>(c, false, blockIdx.x, smem);
+    } else {
+        cached_chunk<T, FMT, DP, DU, GEN, ANY, MO>(c, true, blockIdx.x - first, smem);
+    }
+}
+
+template <typename T, int FMT, int DP, int DU, bool GEN, bool ANY, int MP, int MO>
 hipError_t run_cached(const CachedArgs &c, hipStream_t s)
 {
-    const dim3 grid((uint32_t)(c.part[0].blocks + c.part[1].blocks)), block(64 * kCachedWaves);
-    if (attn_general(c.a))
-        launch_kernel((attn_cached_kernel<T, FMT, DP, DU, true>), grid, block,
-                      (cached_lds<T, DP>()), s, c);
-    else
-        launch_kernel((attn_cached_kernel<T, FMT, DP, DU, false>), grid, block,
-                      (cached_lds<T, DP>()), s, c);
+    constexpr uint32_t p = cached_lds<T, FMT, DP, MP>(), o = cached_lds<T, FMT, DP, MO>();
+    launch_kernel((attn_cached_kernel<T, FMT, DP, DU, GEN, ANY, MP, MO>),
+                  dim3((uint32_t)(c.part[0].blocks + c.part[1].blocks)), dim3(64 * kCachedWaves),
+                  p > o ? p : o, s, c);
     return hipGetLastError();
+}
+
+template <typename T, int FMT, int DP, int DU, bool GEN, bool ANY = false>
+hipError_t run_cached_rows(const CachedArgs &c, hipStream_t s)
+{
+    // (a prefix has at least the rows of an own cache; a part without
+    // workgroups takes the other's)
+    if constexpr (T::code == F32::code) {
+        return run_cached<T, FMT, DP, DU, GEN, ANY, 16, 16>(c, s);
+    } else {
+        const int mo = c.part[1].blocks ? c.part[1].mb : c.part[0].mb;
+        const int mp = c.part[0].blocks ? c.part[0].mb : mo;
+        if (mp == 16) return run_cached<T, FMT, DP, DU, GEN, ANY, 16, 16>(c, s);
+        if (mo == 16) return run_cached<T, FMT, DP, DU, GEN, ANY, 32, 16>(c, s);
+        return run_cached<T, FMT, DP, DU, GEN, ANY, 32, 32>(c, s);
+    }
+}
+
+template <typename T, int FMT, int DP, int DU>
+hipError_t run_cached_scores(const CachedArgs &c, hipStream_t s)
+{
+    return attn_general(c.a) ? run_cached_rows<T, FMT, DP, DU, true>(c, s)
+                             : run_cached_rows<T, FMT, DP, DU, false>(c, s);
 }
 
 template <typename T, int FMT>
 hipError_t run_cached_width(const CachedArgs &c, hipStream_t s)
 {
-    if (c.a.D <= 64) return run_cached<T, FMT, 64, 64>(c, s);
-    if (c.a.D <= 96) return run_cached<T, FMT, 128, 96>(c, s);
-    return run_cached<T, FMT, 128, 128>(c, s);
+    if constexpr (FMT != kPlain)
+        if (c.any)
+            return c.a.D <= 64 ? run_cached_rows<T, FMT, 64, 64, true, true>(c, s)
+                               : run_cached_rows<T, FMT, 128, 128, true, true>(c, s);
+    if (c.a.D <= 64) return run_cached_scores<T, FMT, 64, 64>(c, s);
+    if (c.a.D <= 96) return run_cached_scores<T, FMT, 128, 96>(c, s);
+    return run_cached_scores<T, FMT, 128, 128>(c, s);
 }
 
-// one translation unit a format
-template <typename T>
-hipError_t launch_cached_plain(const CachedArgs &c, hipStream_t s);
-template <typename T>
-hipError_t launch_cached_e4m3(const CachedArgs &c, hipStream_t s);
-template <typename T>
-hipError_t launch_cached_e2m1(const CachedArgs &c, hipStream_t s);
+// (in translation units by format and type)
+template <typename T, int FMT>
+hipError_t launch_cached(const CachedArgs &c, hipStream_t s);
 
 }  // namespace mp3d

@@ -21,48 +21,167 @@ namespace {
 
 constexpr int kRowsAhead = 4;              // rows of a thread whose loads are in flight together
 
-// A workgroup's rows of (tokens x heads), a thread's place among them.
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+// A workgroup's rows of (tokens x heads), and a thread's places among them: of
+// the row that it is at, from the workgroup's first token, in each of the
+// tensors that it walks.
 struct Walk {
     int piece, t, h, dt, dh;
     bool idle;
     __device__ __forceinline__ Walk(int pieces, int H)
     {
-        const int rows = blockDim.x / pieces, r = threadIdx.x / pieces;
+        const uint32_t rows = blockDim.x / (uint32_t)pieces, r = threadIdx.x / (uint32_t)pieces;
         piece = threadIdx.x - r * pieces;
         idle = r >= rows;
-        t = r / H;
+        t = r / (uint32_t)H;
         h = r - t * H;
-        dt = rows / H;
+        dt = rows / (uint32_t)H;
         dh = rows - dt * H;
     }
-    __device__ __forceinline__ void next(int H)
+    // true: the head went past the last, and back
+    __device__ __forceinline__ bool next(int H)
     {
         t += dt;
         h += dh;
-        if (h >= H) {
-            h -= H;
-            ++t;
+        const bool over = h >= H;
+        h -= over ? H : 0;
+        t += over;
+        return over;
+    }
+};
+struct Place {
+    int64_t at, step, over;
+    __device__ __forceinline__ Place(const Walk &w, int H, int64_t token, int64_t head)
+        : at(w.t * token + w.h * head), step(w.dt * token + w.dh * head), over(step + token - H * head)
+    {
+    }
+    __device__ __forceinline__ void next(bool past) { at += past ? over : step; }
+};
+
+// 8 elements of a row, as they are stored.
+template <typename T>
+struct Eight {
+    using R = typename T::raw;
+    static constexpr int N = sizeof(R) * 8 / 16;
+    u32x4 w[N];
+
+    // from d0 on, zero past D
+    template <bool VEC>
+    __device__ __forceinline__ void load(const R *p, int d0, int D)
+    {
+        if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                w[i] = d0 < D ? ((const u32x4 *)(p + d0))[i] : u32x4{0u, 0u, 0u, 0u};
+        } else {
+            struct alignas(16) {
+                R e[8];
+            } o;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o.e[i] = d0 + i < D ? p[d0 + i] : R(0);
+            __builtin_memcpy(w, &o, sizeof(o));
+        }
+    }
+    // The largest magnitude's bits, as binary32: patterns without their signs
+    // are in the order of what they stand for, infinities and NaN last.
+    __device__ __forceinline__ uint32_t largest() const
+    {
+        if constexpr (T::code == F32::code) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) m = max(m, w[i][j] & 0x7fffffffu);
+            return m;
+        } else {
+            typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+            u16x2 m = {0, 0};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t x = w[0][j] & 0x7fff7fffu;
+                m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, x));
+            }
+            const uint16_t most = m[0] > m[1] ? m[0] : m[1];
+            return __builtin_bit_cast(uint32_t, T::widen(most));
+        }
+    }
+    // Codes under a scale.
+    template <int FMT>
+    __device__ __forceinline__ u32x2 codes(float scale) const
+    {
+        u32x2 q = {0u, 0u};
+        if constexpr (T::code == F32::code) {
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < N; ++i) T::unpack(w[i], f + 4 * i);
+            return codes_of<FMT>(f, scale);
+        } else if constexpr (FMT == kE4M3) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                s16x2 c = {0, 0};
+                const uint32_t a = w[0][2 * i], b = w[0][2 * i + 1];
+                if constexpr (T::code == F16::code) {
+                    c = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(c, __builtin_bit_cast(f16x2, a), scale, false);
+                    c = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(c, __builtin_bit_cast(f16x2, b), scale, true);
+                } else {
+                    c = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(c, __builtin_bit_cast(bf16x2, a), scale, false);
+                    c = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(c, __builtin_bit_cast(bf16x2, b), scale, true);
+                }
+                q[i] = __builtin_bit_cast(uint32_t, c);
+            }
+        } else {
+            const uint32_t x[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+            uint32_t c = 0;
+            if constexpr (T::code == F16::code) {
+                c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(f16x2, x[0]), scale, 0);
+                c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(f16x2, x[1]), scale, 1);
+                c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(f16x2, x[2]), scale, 2);
+                c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(f16x2, x[3]), scale, 3);
+            } else {
+                c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, x[0]), scale, 0);
+                c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, x[1]), scale, 1);
+                c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, x[2]), scale, 2);
+                c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, x[3]), scale, 3);
+            }
+            q.x = c;
+        }
+        return q;
+    }
+    // The same, no magnitude past lim.
+    template <int FMT>
+    __device__ __forceinline__ u32x2 codes_within(float scale, float lim) const
+    {
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < N; ++i) T::unpack(w[i], f + 8 / N * i);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = fminf(fmaxf(f[i], -lim), lim);
+        return codes_of<FMT>(f, scale);
+    }
+    template <int FMT>
+    static __device__ __forceinline__ u32x2 codes_of(const float *f, float scale)
+    {
+        if constexpr (FMT == kE4M3) {
+            s16x2 c[2] = {{0, 0}, {0, 0}};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                c[i] = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(c[i], f[4 * i], f[4 * i + 1], scale, false);
+                c[i] = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(c[i], f[4 * i + 2], f[4 * i + 3], scale, true);
+            }
+            return u32x2{__builtin_bit_cast(uint32_t, c[0]), __builtin_bit_cast(uint32_t, c[1])};
+        } else {
+            uint32_t c = 0;
+            c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[0], f[1], scale, 0);
+            c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[2], f[3], scale, 1);
+            c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[4], f[5], scale, 2);
+            c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[6], f[7], scale, 3);
+            return u32x2{c, 0u};
         }
     }
 };
-
-// Elements d0 .. d0 + 7 of a row, zero past D.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load_row8(const typename T::raw *p, int d0, int D, float *x)
-{
-    if constexpr (VEC) {
-        constexpr int PER = 16 / sizeof(typename T::raw);
-        u32x4 w[8 / PER];
-#pragma unroll
-        for (int i = 0; i < 8 / PER; ++i)
-            w[i] = d0 < D ? ((const u32x4 *)(p + d0))[i] : u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-        for (int i = 0; i < 8 / PER; ++i) T::unpack(w[i], x + i * PER);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = d0 + i < D ? T::widen(p[d0 + i]) : 0.f;
-    }
-}
 
 // A group's scale byte, from the bits of its largest magnitude.
 template <int FMT>
@@ -76,81 +195,90 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax)
     return (uint32_t)max(s, 1);
 }
 
+// The largest of four adjacent lanes.
+__device__ __forceinline__ uint32_t quad_max(uint32_t v)
+{
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xb1, 0xf, 0xf, true));
+    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4e, 0xf, 0xf, true));
+}
+
+// What a workgroup has: `which` of k and v, a sequence's tokens [T0, T0 + Tn),
+// and of these [from, to) those that are in use and have a row in the cache.
+struct Tile {
+    int v, T0, Tn, from, to;
+    int64_t b, row;                        // row: of the first token
+    __device__ __forceinline__ explicit Tile(const CachePlan &p)
+    {
+        const uint32_t id = blockIdx.x / (uint32_t)p.tiles, tile = blockIdx.x - id * p.tiles;
+        v = id & 1;
+        b = id >> 1;
+        T0 = (int)tile * p.per;
+        Tn = min(p.per, p.T - T0);
+        row = (p.start ? p.start[b] : 0) + (int64_t)T0;
+        const int used = (p.count ? p.count[b] : p.T) - min(T0, p.count ? p.count[b] : p.T);
+        from = (int)min(max(-row, (int64_t)0), (int64_t)Tn);
+        to = (int)min((int64_t)min(used, Tn), max(p.rows - row, (int64_t)0));
+    }
+};
+
 template <typename T, int FMT, bool VEC>
 __global__ __launch_bounds__(256) void cache_write_kernel(CachePlan p)
 {
     using R = typename T::raw;
-    constexpr float kTop = FMT == kE4M3 ? 448.f : 6.f, kLast = FMT == kE4M3 ? 240.f : 3.f;
+    constexpr float kLast = FMT == kE4M3 ? 240.f : 3.f;
     // the scale under which the code of a group's binade is past the type
     constexpr uint32_t kPast = T::code == F16::code ? (FMT == kE4M3 ? 135u : 141u)
                                                     : (FMT == kE4M3 ? 247u : 253u);
-    const int64_t id = blockIdx.x / p.tiles;
-    const int tile = (int)(blockIdx.x - id * p.tiles), v = (int)(id & 1);
-    const int64_t b = id >> 1;
-    const int T0 = tile * p.per, Tn = min(p.per, p.T - T0);
-    const int64_t first = p.start ? p.start[b] : 0;
-    const int used = p.count ? p.count[b] : p.T;
-    const R *src = (const R *)p.x[v] + b * p.xs[v][0] + T0 * p.xs[v][1];
-    uint8_t *codes = p.codes[v] + b * p.cs[v][0], *scales = p.scales[v] + b * p.ss[v][0];
     Walk w(p.pieces, p.H);
-    if (w.idle) return;
+    const Tile tile(p);
+    if (w.idle || tile.from >= tile.to) return;
+    const int v = tile.v;
+    const R *src = (const R *)p.x[v] + tile.b * p.xs[v][0] + tile.T0 * p.xs[v][1];
+    uint8_t *codes = p.codes[v] + tile.b * p.cs[v][0] + tile.row * p.cs[v][1];
+    uint8_t *scales = p.scales[v] + tile.b * p.ss[v][0] + tile.row * p.ss[v][1] + w.piece / 4;
+    Place x(w, p.H, p.xs[v][1], p.xs[v][2]), c(w, p.H, p.cs[v][1], p.cs[v][2]),
+        s(w, p.H, p.ss[v][1], p.ss[v][2]);
     const int d0 = w.piece * 8;
-    while (w.t < Tn) {
-        float x[kRowsAhead][8];
-        int t[kRowsAhead], h[kRowsAhead];
+    while (w.t < tile.to) {
+        Eight<T> e[kRowsAhead];
+        int64_t at[kRowsAhead], scale_at[kRowsAhead];
+        bool there[kRowsAhead];
 #pragma unroll
         for (int i = 0; i < kRowsAhead; ++i) {
-            t[i] = w.t;
-            h[i] = w.h;
             // (the four threads of a group have the same row)
-            if (t[i] < Tn) load_row8<T, VEC>(src + t[i] * p.xs[v][1] + h[i] * p.xs[v][2], d0, p.D, x[i]);
-            w.next(p.H);
+            there[i] = w.t >= tile.from && w.t < tile.to;
+            at[i] = c.at;
+            scale_at[i] = s.at;
+            if (there[i]) e[i].template load<VEC>(src + x.at, d0, p.D);
+            const bool past = w.next(p.H);
+            x.next(past);
+            c.next(past);
+            s.next(past);
         }
 #pragma unroll
         for (int i = 0; i < kRowsAhead; ++i) {
-            if (t[i] >= Tn) break;
-            const int64_t row = first + T0 + t[i];
-            uint32_t amax = 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                amax = max(amax, __builtin_bit_cast(uint32_t, x[i][e]) & 0x7fffffffu);
-            amax = max(amax, (uint32_t)__shfl_xor((int)amax, 1));
-            amax = max(amax, (uint32_t)__shfl_xor((int)amax, 2));
-            if (T0 + t[i] >= used || row < 0 || row >= p.rows) continue;
-            const uint32_t s = scale_byte<FMT>(amax);
-            // (a group with an infinity or a NaN: codes of 0)
-            const float f = s == 255u ? 0.f : __builtin_bit_cast(float, (254u - s) << 23);
-            const float lim = s == kPast ? kLast : kTop;
-            float y[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                y[e] = s == 255u ? 0.f : fminf(fmaxf(x[i][e] * f, -lim), lim);
-            uint8_t *c = codes + row * p.cs[v][1] + h[i] * p.cs[v][2];
-            uint32_t q[2] = {0u, 0u};
-            if constexpr (FMT == kE4M3) {
-                q[0] = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
-                q[0] = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], q[0], true);
-                q[1] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4], y[5], 0, false);
-                q[1] = __builtin_amdgcn_cvt_pk_fp8_f32(y[6], y[7], q[1], true);
-            } else {
-                q[0] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, y[0], y[1], 1.f, 0);
-                q[0] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q[0], y[2], y[3], 1.f, 1);
-                q[0] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q[0], y[4], y[5], 1.f, 2);
-                q[0] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q[0], y[6], y[7], 1.f, 3);
+            if (!there[i]) continue;
+            const uint32_t byte = scale_byte<FMT>(quad_max(e[i].largest()));
+            const float scale = scale_of(byte);
+            u32x2 q = e[i].template codes<FMT>(scale);
+            if (__builtin_expect(byte >= kPast, 0)) {
+                if (byte == kPast) q = e[i].template codes_within<FMT>(scale, kLast * scale);
+                else q = u32x2{0u, 0u};    // an infinity or a NaN
             }
+            uint8_t *const out = codes + at[i];
             if constexpr (VEC) {
                 if (d0 < p.D) {
-                    if constexpr (FMT == kE4M3) *(u32x2 *)(c + d0) = u32x2{q[0], q[1]};
-                    else *(uint32_t *)(c + d0 / 2) = q[0];
+                    if constexpr (FMT == kE4M3) *(u32x2 *)(out + d0) = q;
+                    else *(uint32_t *)(out + d0 / 2) = q.x;
                 }
             } else {
-                const int at = code_bytes<FMT>(d0), end = code_bytes<FMT>(p.D);
+                const int first = code_bytes<FMT>(d0), end = code_bytes<FMT>(p.D);
+                const uint32_t word[2] = {q.x, q.y};
 #pragma unroll
-                for (int e = 0; e < code_bytes<FMT>(8); ++e)
-                    if (at + e < end) c[at + e] = (uint8_t)(q[e / 4] >> (8 * (e % 4)));
+                for (int j = 0; j < code_bytes<FMT>(8); ++j)
+                    if (first + j < end) out[first + j] = (uint8_t)(word[j / 4] >> (8 * (j % 4)));
             }
-            if ((w.piece & 3) == 0)
-                scales[row * p.ss[v][1] + h[i] * p.ss[v][2] + w.piece / 4] = (uint8_t)s;
+            if ((w.piece & 3) == 0) scales[scale_at[i]] = (uint8_t)byte;
         }
     }
 }
@@ -161,61 +289,62 @@ __global__ __launch_bounds__(256) void cache_read_kernel(CachePlan p)
 {
     using R = typename T::raw;
     constexpr int N = 16 / sizeof(R);
-    const int64_t id = blockIdx.x / p.tiles;
-    const int tile = (int)(blockIdx.x - id * p.tiles), v = (int)(id & 1);
-    const int64_t b = id >> 1;
-    const int T0 = tile * p.per, Tn = min(p.per, p.T - T0);
-    const int64_t first = p.start ? p.start[b] : 0;
-    const int used = p.count ? p.count[b] : p.T;
-    const uint8_t *codes = p.codes[v] + b * p.cs[v][0], *scales = p.scales[v] + b * p.ss[v][0];
-    R *dst = (R *)p.x[v] + (b * p.T + T0) * p.H * (int64_t)p.D;
     Walk w(p.pieces, p.H);
+    const Tile tile(p);
     if (w.idle) return;
-    const int d0 = w.piece * N;
-    while (w.t < Tn) {
-        uint32_t q[kRowsAhead][2], s[kRowsAhead];
-        int t[kRowsAhead], h[kRowsAhead];
+    const int v = tile.v, d0 = w.piece * N;
+    const uint8_t *codes = p.codes[v] + tile.b * p.cs[v][0] + tile.row * p.cs[v][1];
+    const uint8_t *scales = p.scales[v] + tile.b * p.ss[v][0] + tile.row * p.ss[v][1] + d0 / kGroup;
+    R *dst = (R *)p.x[v] + (tile.b * p.T + tile.T0) * p.H * (int64_t)p.D + d0;
+    Place x(w, p.H, (int64_t)p.H * p.D, p.D), c(w, p.H, p.cs[v][1], p.cs[v][2]),
+        s(w, p.H, p.ss[v][1], p.ss[v][2]);
+    while (w.t < tile.Tn) {
+        uint32_t q[kRowsAhead][2], byte[kRowsAhead];
+        int64_t at[kRowsAhead];
+        bool there[kRowsAhead];
 #pragma unroll
         for (int i = 0; i < kRowsAhead; ++i) {
-            t[i] = w.t;
-            h[i] = w.h;
+            there[i] = w.t < tile.Tn;
+            at[i] = x.at;
             q[i][0] = q[i][1] = 0u;
-            s[i] = 127u;
-            const int64_t row = first + T0 + t[i];
-            if (t[i] < Tn && T0 + t[i] < used && row >= 0 && row < p.rows) {
-                const uint8_t *c = codes + row * p.cs[v][1] + h[i] * p.cs[v][2];
-                s[i] = scales[row * p.ss[v][1] + h[i] * p.ss[v][2] + d0 / kGroup];
+            byte[i] = 127u;
+            if (w.t >= tile.from && w.t < tile.to) {
+                const uint8_t *in = codes + c.at;
+                byte[i] = scales[s.at];
                 if constexpr (VEC) {
                     if constexpr (FMT == kE4M3) {
                         if constexpr (N == 8) {
-                            const u32x2 x = *(const u32x2 *)(c + d0);
-                            q[i][0] = x.x;
-                            q[i][1] = x.y;
+                            const u32x2 y = *(const u32x2 *)(in + d0);
+                            q[i][0] = y.x;
+                            q[i][1] = y.y;
                         } else {
-                            q[i][0] = *(const uint32_t *)(c + d0);
+                            q[i][0] = *(const uint32_t *)(in + d0);
                         }
                     } else if constexpr (N == 8) {
-                        q[i][0] = *(const uint32_t *)(c + d0 / 2);
+                        q[i][0] = *(const uint32_t *)(in + d0 / 2);
                     } else {
-                        q[i][0] = *(const uint16_t *)(c + d0 / 2);
+                        q[i][0] = *(const uint16_t *)(in + d0 / 2);
                     }
                 } else {
-                    const int at = code_bytes<FMT>(d0), end = code_bytes<FMT>(p.D);
+                    const int first = code_bytes<FMT>(d0), end = code_bytes<FMT>(p.D);
 #pragma unroll
-                    for (int e = 0; e < code_bytes<FMT>(N); ++e)
-                        if (at + e < end) q[i][e / 4] |= (uint32_t)c[at + e] << (8 * (e % 4));
+                    for (int j = 0; j < code_bytes<FMT>(N); ++j)
+                        if (first + j < end) q[i][j / 4] |= (uint32_t)in[first + j] << (8 * (j % 4));
                 }
             }
-            w.next(p.H);
+            const bool past = w.next(p.H);
+            x.next(past);
+            c.next(past);
+            s.next(past);
         }
 #pragma unroll
         for (int i = 0; i < kRowsAhead; ++i) {
-            if (t[i] >= Tn) break;
+            if (!there[i]) break;
             struct alignas(16) {
                 u32x4 v[sizeof(R) * 8 / 16];
             } o;
-            widen8<T, FMT>(q[i][0], q[i][1], scale_of(s[i]), o.v);
-            R *out = dst + ((int64_t)t[i] * p.H + h[i]) * p.D + d0;
+            widen8<T, FMT>(q[i][0], q[i][1], scale_of(byte[i]), o.v);
+            R *const out = dst + at[i];
             if constexpr (VEC) {
                 *(u32x4 *)out = o.v[0];
             } else {
@@ -249,12 +378,13 @@ void plan_cache(CachePlan *p, int elem_bytes, bool read)
     const int per = read ? 16 / elem_bytes : 8;
     p->pieces = read ? (p->D + per - 1) / per : (p->D + kGroup - 1) / kGroup * (kGroup / per);
     p->threads = 256;
-    const int64_t rows = 256 / p->pieces;
-    // kRowsAhead rows a thread where that still fills the card, else one
-    const int64_t all = (int64_t)p->B * 2 * p->T * p->H;
+    // kRowsAhead rows a thread where that leaves two workgroups for a CU, else
+    // one; whole tokens, so that no thread goes round again for the last few
+    // (5 x 1330 tokens of 8 heads of 72, which did: 12.9 us)
+    const int64_t rows = 256 / p->pieces, all = (int64_t)p->B * 2 * p->T * p->H;
     int64_t want = rows * kRowsAhead;
-    if (all / want < 8 * device_cus()) want = rows;
-    int64_t tokens = (want + p->H - 1) / p->H;
+    if (all / want < 2 * device_cus()) want = rows;
+    const int64_t tokens = want > p->H ? want / p->H : 1;
     p->per = (int32_t)(tokens < p->T ? tokens : p->T);
     p->tiles = (p->T + p->per - 1) / p->per;
 }
