@@ -30,14 +30,20 @@ _FORMAT = {None: _lib.MP3D_CACHE_PLAIN, "e4m3": _lib.MP3D_CACHE_E4M3,
 _cache_struct = struct.Struct("@qqPPPP12q").pack
 _attention_struct = struct.Struct("@iiqqiiii3qff" + 2 * "qqPPPP12q" + "PPiPPPP").pack
 _NONE = (0,) * 18
+_u8, _i32, _f32 = torch.uint8, torch.int32, torch.float32
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _on(device, call, *args):
-    """The call's result, with the tensors' device as the current one."""
-    if device.index == torch.cuda.current_device():
-        return call(*args)
-    with torch.cuda.device(device):
-        return call(*args)
+def _run(index, name, *args):
+    """Calls the library with the tensors' device as the current one."""
+    call = getattr(_lib._lib or _lib.load(), name)
+    if index == _current_device():
+        code = call(*args)
+    else:
+        with torch.cuda.device(index):
+            code = call(*args)
+    if code:
+        _lib.check(code)
 
 
 def _quantised(format):
@@ -51,32 +57,41 @@ def _widths(code, D):
     return D if code == _lib.MP3D_CACHE_E4M3 else (D + 1) // 2, (D + 31) // 32
 
 
-def _bytes(t, name, device):
-    """(shape, first three strides) of a part of a cache."""
-    shape, strides = t.shape, t.stride()
-    if t.dtype != torch.uint8 or len(shape) != 4 or t.device != device:
-        raise ValueError("%s must be a uint8 tensor (B, T, H, bytes) on %s" % (name, device))
-    if strides[3] != 1 and shape[3] > 1:
-        raise ValueError("%s: a head's bytes must be adjacent (stride 1)" % name)
-    return shape, strides[:3]
-
-
-def _parts(cache, code, D, device, name):
+def _parts(cache, code, D, index, name):
     """The fields of struct mp3d_cache, and H."""
-    if len(cache) != 4:
-        raise ValueError("%s must be (k_codes, k_scales, v_codes, v_scales)" % name)
-    kc, ks, vc, vs = cache
-    shape, s0 = _bytes(kc, name, device)
-    scale, s1 = _bytes(ks, name, device)
-    vshape, s2 = _bytes(vc, name, device)
-    vscale, s3 = _bytes(vs, name, device)
-    B, T, H, width = shape
-    if (vshape != shape or vscale != scale or scale[:3] != shape[:3]
-            or (width, scale[3]) != _widths(code, D)):
-        raise ValueError("%s must have codes (B, T, H, %d) and scales (B, T, H, %d)"
-                         % ((name,) + _widths(code, D)))
-    return (B, T, kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), *s0, *s2, *s1,
-            *s3), H
+    # (for one new token the calls are bound by the host: nothing here is a
+    # call that can be done without)
+    if len(cache) == 4:
+        kc, ks, vc, vs = cache
+        shape, scale = kc.shape, ks.shape
+        if len(shape) == 4 and len(scale) == 4 and vc.shape == shape and vs.shape == scale:
+            B, T, H, width = shape
+            a0, a1, a2, a3 = kc.stride()
+            b0, b1, b2, b3 = ks.stride()
+            c0, c1, c2, c3 = vc.stride()
+            d0, d1, d2, d3 = vs.stride()
+            groups = (D + 31) // 32
+            if (scale == (B, T, H, groups)
+                    and width == (D if code == _lib.MP3D_CACHE_E4M3 else (D + 1) // 2)
+                    and kc.dtype is ks.dtype is vc.dtype is vs.dtype is _u8
+                    and index == kc.get_device() == ks.get_device() == vc.get_device()
+                    == vs.get_device()
+                    and (a3 == c3 == 1 or width == 1) and (b3 == d3 == 1 or groups == 1)):
+                return (B, T, kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), a0, a1,
+                        a2, c0, c1, c2, b0, b1, b2, d0, d1, d2), H
+    raise ValueError("%s must be (k_codes, k_scales, v_codes, v_scales), uint8 on device %d: codes "
+                     "(B, T, H, %d), scales (B, T, H, %d), a head's bytes adjacent"
+                     % ((name, index) + _widths(code, D)))
+
+
+def _per_sequence(t, name, B, index):
+    """The address of a (B) int32 tensor, or None."""
+    if t is None:
+        return None
+    if t.shape != (B,) or t.dtype is not _i32 or t.get_device() != index or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 tensor of shape (%d,) on device %d"
+                         % (name, B, index))
+    return t.data_ptr()
 
 
 def mp3d_cache_empty(B: int, T: int, H: int, D: int, format: str, device="cuda"):
@@ -95,23 +110,19 @@ def mp3d_cache_write(k: torch.Tensor, v: torch.Tensor, cache, format: str, *,
     token t of sequence b to the row start[b] + t.  ``start`` int32 (B) (None:
     0).  ``count`` int32 (B): tokens in use (None: all); those after them,
     and those whose row the cache does not have, are not written."""
-    lib = _lib.load()
     shape, sk = _heads(k, "k")
     vshape, sv = _heads(v, "v", k)
     if vshape != shape:
         raise ValueError("k and v must have the same shape")
     B, T, H, D = shape
-    code, dev = _quantised(format), k.device
-    c, heads = _parts(cache, code, D, dev, "cache")
+    code, index = _quantised(format), k.get_device()
+    c, heads = _parts(cache, code, D, index, "cache")
     if c[0] != B or heads != H:
         raise ValueError("the cache must have k's B and H")
-    if start is not None:
-        _same(start, "start", (B,), torch.int32, dev)
-    if count is not None:
-        _same(count, "count", (B,), torch.int32, dev)
-    _lib.check(_on(dev, lib.mp3d_cache_write, _cache_struct(*c), code, k.data_ptr(), v.data_ptr(),
-                   _code(k, "k"), T, H, D, _i64x3(*sk), _i64x3(*sv), _ptr(start), _ptr(count),
-                   _stream(k)))
+    _run(index, "mp3d_cache_write", _cache_struct(*c), code, k.data_ptr(), v.data_ptr(),
+         _code(k, "k"), T, H, D, _i64x3(*sk), _i64x3(*sv),
+         _per_sequence(start, "start", B, index), _per_sequence(count, "count", B, index),
+         _stream(k))
 
 
 def mp3d_cache_read(cache, format: str, D: int, dtype: torch.dtype, *, rows: int | None = None,
@@ -121,27 +132,23 @@ def mp3d_cache_read(cache, format: str, D: int, dtype: torch.dtype, *, rows: int
     (``rows`` None: as many as it has; ``start`` None: from 0), zeros from
     count[b] on and where the cache has no such row.  ``out``: preallocated
     contiguous (k, v)."""
-    lib = _lib.load()
-    code = _quantised(format)
-    if not cache[0].is_cuda:
+    code, first = _quantised(format), cache[0]
+    if not first.is_cuda:
         raise ValueError("cache must be device tensors")
-    dev = cache[0].device
-    c, H = _parts(cache, code, D, dev, "cache")
+    index = first.get_device()
+    c, H = _parts(cache, code, D, index, "cache")
     B = c[0]
     T = c[1] if rows is None else rows
     if out is None:
-        k = torch.empty((B, T, H, D), dtype=dtype, device=dev)
+        k = first.new_empty((B, T, H, D), dtype=dtype)
         v = torch.empty_like(k)
     else:
         k, v = out
-        _same(k, "out for k", (B, T, H, D), dtype, dev)
-        _same(v, "out for v", (B, T, H, D), dtype, dev)
-    if start is not None:
-        _same(start, "start", (B,), torch.int32, dev)
-    if count is not None:
-        _same(count, "count", (B,), torch.int32, dev)
-    _lib.check(_on(dev, lib.mp3d_cache_read, _cache_struct(*c), code, k.data_ptr(), v.data_ptr(),
-                   _code(k, "out"), T, H, D, _ptr(start), _ptr(count), _stream(k)))
+        _same(k, "out for k", (B, T, H, D), dtype, first.device)
+        _same(v, "out for v", (B, T, H, D), dtype, first.device)
+    _run(index, "mp3d_cache_read", _cache_struct(*c), code, k.data_ptr(), v.data_ptr(),
+         _code(k, "out"), T, H, D, _per_sequence(start, "start", B, index),
+         _per_sequence(count, "count", B, index), _stream(k))
     return k, v
 
 
@@ -149,7 +156,7 @@ def _fields(cache, code, q, name):
     """The fields of struct mp3d_cache of any format, and H."""
     D = q.shape[3]
     if code:
-        return _parts(cache, code, D, q.device, name)
+        return _parts(cache, code, D, q.get_device(), name)
     if len(cache) != 2:
         raise ValueError("%s must be (k, v)" % name)
     k, v = cache
@@ -166,7 +173,7 @@ def _descriptor(q, own, prefix, format, scale, softcap, causal, kv_len, prefix_l
     (B, Tq, Hq, D), qs = _heads(q, "q")
     if format not in _FORMAT:
         raise ValueError("format must be 'e4m3', 'e2m1' or None")
-    code, dev = _FORMAT[format], q.device
+    code, dev, index = _FORMAT[format], q.device, q.get_device()
     o, Hk = _fields(own, code, q, "own")
     if o[0] != B:
         raise ValueError("the own cache must have q's B")
@@ -178,13 +185,11 @@ def _descriptor(q, own, prefix, format, scale, softcap, causal, kv_len, prefix_l
             raise ValueError("own and prefix must have the same heads")
         if N < 1 or B % N:
             raise ValueError("%d sequences do not divide among %d prefixes" % (B, N))
-    kv = pl = axes = psl = ppq = ppk = ppp = 0
-    if kv_len is not None:
-        kv = _same(kv_len, "kv_len", (B,), torch.int32, dev).data_ptr()
-    if prefix_len is not None:
-        if prefix is None:
-            raise ValueError("prefix_len goes with prefix")
-        pl = _same(prefix_len, "prefix_len", (N,), torch.int32, dev).data_ptr()
+    axes = psl = ppq = ppk = ppp = 0
+    if prefix_len is not None and prefix is None:
+        raise ValueError("prefix_len goes with prefix")
+    kv = _per_sequence(kv_len, "kv_len", B, index) or 0
+    pl = _per_sequence(prefix_len, "prefix_len", N, index) or 0
     if slopes is not None:
         if slopes.dim() != 2 or pos_q is None or pos_k is None or (
                 (pos_prefix is None) != (prefix is None)):
@@ -213,8 +218,7 @@ def mp3d_attention_cached_workspace_bytes(q, own, prefix=None, *, format=None, s
     a = _descriptor(q, own, prefix, format, scale, softcap, causal, kv_len, prefix_len, slopes,
                     pos_q, pos_k, pos_prefix)
     nbytes = ctypes.c_size_t()
-    _lib.check(_on(q.device, _lib.load().mp3d_attention_cached_workspace_bytes, a,
-                   ctypes.byref(nbytes)))
+    _run(q.get_device(), "mp3d_attention_cached_workspace_bytes", a, ctypes.byref(nbytes))
     return nbytes.value
 
 
@@ -240,21 +244,20 @@ def mp3d_attention_cached(q: torch.Tensor, own, prefix=None, *, format: str | No
     (axes, N, P) int32.  ``out``: preallocated (out, lse); ``workspace``: a
     uint8 tensor of mp3d_attention_cached_workspace_bytes(...) (None:
     allocated)."""
-    lib = _lib.load()
     a = _descriptor(q, own, prefix, format, scale, softcap, causal, kv_len, prefix_len, slopes,
                     pos_q, pos_k, pos_prefix)
-    B, Tq, Hq, _ = q.shape
-    dev = q.device
+    B, Tq, Hq, _ = shape = q.shape
+    index = q.get_device()
     if out is None:
         o = torch.empty_like(q, memory_format=_contiguous)
-        lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=dev)
+        lse = q.new_empty((B, Hq, Tq), dtype=_f32)
     else:
         o, lse = out
-        _same(o, "out", q.shape, q.dtype, dev)
-        _same(lse, "lse", (B, Hq, Tq), torch.float32, dev)
+        _same(o, "out", shape, q.dtype, q.device)
+        _same(lse, "lse", (B, Hq, Tq), _f32, q.device)
     nbytes = ctypes.c_size_t()
-    _lib.check(_on(dev, lib.mp3d_attention_cached_workspace_bytes, a, ctypes.byref(nbytes)))
-    ws, n = _lend(nbytes.value, workspace, dev)
-    _lib.check(_on(dev, lib.mp3d_attention_cached, a, q.data_ptr(), o.data_ptr(), lse.data_ptr(),
-                   _ptr(ws), n, _stream(q)))
+    _run(index, "mp3d_attention_cached_workspace_bytes", a, ctypes.byref(nbytes))
+    ws, n = _lend(nbytes.value, workspace, q.device)
+    _run(index, "mp3d_attention_cached", a, q.data_ptr(), o.data_ptr(), lse.data_ptr(), _ptr(ws), n,
+         _stream(q))
     return o, lse

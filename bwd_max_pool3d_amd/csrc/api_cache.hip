@@ -15,12 +15,12 @@ namespace {
 
 int row_bytes(int format, int D) { return format == kE4M3 ? code_bytes<kE4M3>(D) : code_bytes<kE2M1>(D); }
 
-// Bases, strides and a row's bytes are multiples of n.
-bool divides(int n, const mp3d_cache &c, int bytes)
+// Bases, strides (in units of es bytes) and a row's bytes are multiples of n.
+bool divides(int n, const mp3d_cache &c, int es, int bytes)
 {
     if (!aligned(c.k, n) || !aligned(c.v, n) || bytes % n) return false;
     for (int i = 0; i < 3; ++i)
-        if (c.k_stride[i] % n || c.v_stride[i] % n) return false;
+        if (c.k_stride[i] * es % n || c.v_stride[i] * es % n) return false;
     return true;
 }
 
@@ -106,7 +106,7 @@ int cache_call(const mp3d_cache *c, int format, void *k, void *v, int dtype, int
     const int per = read && es == 4 ? 4 : 8;
     const bool elements = read || (wide_rows(k, k_stride, es) && wide_rows(v, v_stride, es));
     p.vec = D % per == 0 && elements &&
-            (c->T == 0 || divides(per * (format == kE4M3 ? 2 : 1) / 2, *c, row_bytes(format, D)));
+            (c->T == 0 || divides(per * (format == kE4M3 ? 2 : 1) / 2, *c, 1, row_bytes(format, D)));
     plan_cache(&p, es, read);
     if ((rc = check_launch((int64_t)p.tiles * p.B * 2))) return rc;
     if (log_enabled())
@@ -193,15 +193,17 @@ int cached_args(const mp3d_attention_cache *d, CachedArgs *c)
         p.T = (int32_t)x.T;
         p.caches = (int32_t)x.B;
         p.seqs = i ? 1 : (int32_t)S;
-        p.vec = wide_rows(x.k, p.ks, es) && wide_rows(x.v, p.vs, es);
-        const int bytes = row_bytes(d->format, d->D);
-        p.width = divides(unit, x, bytes) ? unit : divides(4, x, bytes) ? 4 : 1;
+        // whole units, or what there is
+        const bool plain = d->format == kPlain;
+        const int size = plain ? es : 1, bytes = plain ? d->D * es : row_bytes(d->format, d->D);
+        p.width = size;
+        for (int w : {plain ? 16 : unit, 8, 4})
+            if (p.width == size && w <= (plain ? 16 : unit) && divides(w, x, size, bytes)) p.width = w;
         if (p.caches == 0 || p.T == 0) continue;
-        // whole units, and a row's offset in a tile within 31 bits
+        // (a row's offset in a tile has to be within 31 bits)
         const int64_t far = (int64_t)1 << 24;
-        const bool near = p.ks[1] < far && p.vs[1] < far;
-        if (d->format == kPlain ? !(near && p.vec && d->D % 8 == 0)
-                                : !(near && p.width == unit && p.kss[1] < far && p.vss[1] < far))
+        if (p.width != (plain ? 16 : unit) || (plain && d->D % 8) || p.ks[1] >= far || p.vs[1] >= far ||
+            (!plain && (p.kss[1] >= far || p.vss[1] >= far)))
             c->any = 1;
     }
     return MP3D_OK;

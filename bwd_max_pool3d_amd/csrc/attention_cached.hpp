@@ -24,6 +24,8 @@
 // of LDS while the products run from the other.
 #pragma once
 
+#include <type_traits>
+
 #include "attention.hpp"
 #include "cache.hpp"
 
@@ -299,6 +301,66 @@ struct CodeTile {
     }
 };
 
+// A tile of elements whose rows start anywhere, by way of registers: 8
+// channels a lane, `width` bytes (8, 4, or an element) at a time.
+template <typename T, int DP, int KEYS>
+struct NarrowTile {
+    using R = typename T::raw;
+    static constexpr int UNITS = DP / 8, ROWS = 64 / UNITS, N = KEYS / ROWS;
+    static constexpr int WORDS = 2 * sizeof(R), PER = 4 / sizeof(R);   // words of 8 channels,
+                                                                       // channels of a word
+    uint32_t c[N][WORDS];
+
+    __device__ __forceinline__ void load_any(const R *base, const uint8_t *, int64_t stride, int64_t,
+                                             int k0, int end, int width, int D, int lane)
+    {
+        const int d0 = min(lane % UNITS, (D - 1) / 8) * 8, left = D - d0;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int64_t r = min(k0 + j * ROWS + lane / UNITS, end - 1);
+            const R *p = base + r * stride + d0;
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) c[j][i] = 0u;
+            if (width >= 8) {
+#pragma unroll
+                for (int i = 0; i < WORDS; i += 2)
+                    if (i * PER < left) {
+                        const u32x2 x = ((const u32x2 *)p)[i / 2];
+                        c[j][i] = x.x;
+                        c[j][i + 1] = x.y;
+                    }
+            } else if (width == 4) {
+#pragma unroll
+                for (int i = 0; i < WORDS; ++i)
+                    if (i * PER < left) c[j][i] = ((const uint32_t *)p)[i];
+            } else if constexpr (PER == 2) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < left) c[j][i / 2] |= (uint32_t)p[i] << (16 * (i % 2));
+            }
+        }
+    }
+    __device__ __forceinline__ bool place(R *tile, int k0, int end, int D, bool, bool drop, int lane)
+    {
+        bool bad = false;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int r = j * ROWS + lane / UNITS, u = lane % UNITS;
+            const bool there = k0 + r < end && u * 8 < D;
+            Frag<T> x;
+#pragma unroll
+            for (int i = 0; i < Frag<T>::NV; ++i)
+                x.w[i] = there ? u32x4{c[j][4 * i], c[j][4 * i + 1], c[j][4 * i + 2], c[j][4 * i + 3]}
+                               : u32x4{0u, 0u, 0u, 0u};
+            if (drop) bad |= drop_nonfinite<T>(x);
+            u32x4 *q = (u32x4 *)(tile + tile_at<R, DP>(r, u));
+#pragma unroll
+            for (int i = 0; i < Frag<T>::NV; ++i) q[i] = x.w[i];
+        }
+        return bad;
+    }
+};
+
 template <int N>
 struct Half {
     static constexpr int value = N;
@@ -321,7 +383,7 @@ __device__ __forceinline__ void cached_chunk(const CachedArgs &c, bool own, uint
 {
     using R = typename T::raw;
     using C = Cols<MB>;
-    constexpr bool PLAIN = FMT == kPlain;
+    constexpr bool PLAIN = FMT == kPlain, DIRECT = PLAIN && !ANY;
     constexpr int KB = kCachedKeys, NW = kCachedWaves, SLOTS = cached_slots<FMT, MB>();
     constexpr int WR = MB == 16 ? 1 : NW, WK = NW / WR;    // waves that share the rows, the keys out
     constexpr int NC = DU / C::DEPTH, ND = DU / MB, NS = C::SCORES;
@@ -425,16 +487,15 @@ __device__ __forceinline__ void cached_chunk(const CachedArgs &c, bool own, uint
             __syncthreads();
         }
 
-        // plain: straight to LDS
+        // whole rows of elements: straight to LDS
         using Direct = TileDirect<T, DP, BRING, 64>;
         Direct kd, vd;
-        bool usable = false, whole = false;
+        bool whole = false;
         uint32_t lds_k = 0, lds_v = 0, lds_p = 0;
-        if constexpr (PLAIN) {
+        if constexpr (DIRECT) {
             kd.init(lane, p.ks[1], a.D);
             vd.init(lane, p.vs[1], a.D);
-            usable = MB == 32 || !c.any;   // (or blocks of 16)
-            whole = usable && (!ALL || a.D == DP);
+            whole = !ALL || a.D == DP;
             lds_k = lds_address(kt);
             lds_v = lds_address(vt);
             lds_p = lds_address(pk);
@@ -446,18 +507,7 @@ __device__ __forceinline__ void cached_chunk(const CachedArgs &c, bool own, uint
         }
         auto direct = [&](const Direct &d, const R *x, int64_t stride, int k0, uint32_t lds) {
             if (whole && k0 + BRING <= c1) d.template load<ALL>(x + k0 * stride, lds);
-            else if (usable) d.load_edge(x, stride, k0, c0, c1, lds);
-        };
-        // element by element (rows of any alignment)
-        auto one_by_one = [&](const R *x, int64_t stride, int k0, R *tile) {
-#pragma unroll 4
-            for (int i = lane; i < KB * DP; i += 64) {
-                const int row = i / DP, ch = i % DP;
-                tile[tile_at<R, DP>(row, ch >> 3) + (ch & 7)] =
-                    k0 + row < c1 && ch < a.D ? x[(int64_t)(k0 + row) * stride + ch] : R(0);
-            }
-            wait_all();
-            in_order();
+            else d.load_edge(x, stride, k0, c0, c1, lds);
         };
         // three axes or none, so that what is in flight can be counted
         auto direct_pos = [&](int k0, int buf) {
@@ -468,9 +518,9 @@ __device__ __forceinline__ void cached_chunk(const CachedArgs &c, bool own, uint
                             (uint32_t)min(lane, p.T - 1 - k0) * 4, lds_p + (buf * 3 + x) * KB * 4);
         };
 
-        // codes: by way of registers
+        // all others: by way of registers
         using Codes = CodeTile<T, PLAIN ? kE4M3 : FMT, DP, BRING>;
-        Codes kc, vc;
+        std::conditional_t<PLAIN, NarrowTile<T, DP, BRING>, Codes> kc, vc;
         const uint32_t kst = (uint32_t)p.ks[1], vst = (uint32_t)p.vs[1], ksst = (uint32_t)p.kss[1],
                        vsst = (uint32_t)p.vss[1];
         const uint32_t koff = Codes::offset(lane, kst, a.D), voff = Codes::offset(lane, vst, a.D),
@@ -485,7 +535,9 @@ __device__ __forceinline__ void cached_chunk(const CachedArgs &c, bool own, uint
             }
         };
         auto fetch_keys = [&](int k0) {
-            if constexpr (ANY)
+            if constexpr (PLAIN)
+                kc.load_any(kp, nullptr, p.ks[1], 0, k0, c1, p.width, a.D, lane);
+            else if constexpr (ANY)
                 kc.load_any(kq, ksc, p.ks[1], p.kss[1], k0, c1, p.width, a.D, lane);
             else
                 kc.load(kq + (int64_t)k0 * kst, ksc + (int64_t)k0 * ksst, kst, ksst, koff, ksoff,
@@ -493,7 +545,9 @@ __device__ __forceinline__ void cached_chunk(const CachedArgs &c, bool own, uint
             fetch_pos(k0);
         };
         auto fetch_values = [&](int k0) {
-            if constexpr (ANY)
+            if constexpr (PLAIN)
+                vc.load_any(vp, nullptr, p.vs[1], 0, k0, c1, p.width, a.D, lane);
+            else if constexpr (ANY)
                 vc.load_any(vq, vsc, p.vs[1], p.vss[1], k0, c1, p.width, a.D, lane);
             else
                 vc.load(vq + (int64_t)k0 * vst, vsc + (int64_t)k0 * vsst, vst, vsst, voff, vsoff,
@@ -519,7 +573,7 @@ __device__ __forceinline__ void cached_chunk(const CachedArgs &c, bool own, uint
         };
         const int kbeg = c0 + wave * BRING;
         if (kbeg < c1) {
-            if constexpr (PLAIN) {
+            if constexpr (DIRECT) {
                 if (WR == 1) direct_pos(kbeg, 0);
                 else fetch_pos(kbeg);
                 direct(kd, kp, p.ks[1], kbeg, lds_k);
@@ -639,13 +693,12 @@ __device__ __forceinline__ void cached_chunk(const CachedArgs &c, bool own, uint
                     for (int e = 0; e < C::PER; ++e) s[0][u * C::PER + e] = x[u][e];
             };
             int buf = 0;
-            for (int k0 = kbeg; k0 < c1; k0 += NW * KB, buf ^= PLAIN) {
+            for (int k0 = kbeg; k0 < c1; k0 += NW * KB, buf ^= DIRECT) {
                 const int next = k0 + NW * KB;
                 const bool more = next < c1, part = partly(k0, KB);
-                if constexpr (PLAIN) {
+                if constexpr (DIRECT) {
                     // keys: in flight after them are this tile's values
-                    wait_loads<kTile>(usable);
-                    if (!usable) one_by_one(kp, p.ks[1], k0, kt);
+                    wait_loads<kTile>(true);
                     products();
                     reads_done();
                     if (more) {
@@ -653,9 +706,8 @@ __device__ __forceinline__ void cached_chunk(const CachedArgs &c, bool own, uint
                         direct(kd, kp, p.ks[1], next, lds_k);
                     }
                     // values: in flight after them are the next tile's keys
-                    if (axes > 0) wait_loads<kTile + 3>(more && usable);
-                    else wait_loads<kTile>(more && usable);
-                    if (!usable) one_by_one(vp, p.vs[1], k0, vt);
+                    if (axes > 0) wait_loads<kTile + 3>(more);
+                    else wait_loads<kTile>(more);
                     if (part) {
                         dropped |= vd.scrub(vt, k0, c0, c1, true, nullptr, 0);
                         in_order();
@@ -677,7 +729,7 @@ __device__ __forceinline__ void cached_chunk(const CachedArgs &c, bool own, uint
 #pragma unroll
                     for (int e = 0; e < NS / 8; ++e)
                         vf[d][e] = value_frag<T, DP, MB>(vt, e, d * MB, lane);
-                if constexpr (PLAIN) {
+                if constexpr (DIRECT) {
                     reads_done();
                     if (more) direct(vd, vp, p.vs[1], next, lds_v);
                 }
@@ -694,7 +746,7 @@ __device__ __forceinline__ void cached_chunk(const CachedArgs &c, bool own, uint
         } else {
             // this wave's part of two tiles, into the half `buf`
             auto place = [&](int k0, int buf) {
-                if constexpr (PLAIN) {
+                if constexpr (DIRECT) {
                     wait_loads<0>(false);
                     if (k0 < c1) {
                         if (partly(k0, BRING))
@@ -720,7 +772,7 @@ __device__ __forceinline__ void cached_chunk(const CachedArgs &c, bool own, uint
                 const int next = first + 2 * KB + wave * BRING;
                 const bool part = partly(first, 2 * KB);
                 if (next < c1) {
-                    if constexpr (PLAIN) {
+                    if constexpr (DIRECT) {
                         constexpr uint32_t off = (buf ^ 1) * kHalf * (uint32_t)sizeof(R);
                         fetch_pos(next);
                         direct(kd, kp, p.ks[1], next, lds_k + off);
@@ -928,7 +980,7 @@ hipError_t run_cached_rows(const CachedArgs &c, hipStream_t s)
 {
     // (a prefix has at least the rows of an own cache; a part without
     // workgroups takes the other's)
-    if constexpr (T::code == F32::code) {
+    if constexpr (T::code == F32::code || (FMT == kPlain && ANY)) {
         return run_cached<T, FMT, DP, DU, GEN, ANY, 16, 16>(c, s);
     } else {
         const int mo = c.part[1].blocks ? c.part[1].mb : c.part[0].mb;
@@ -949,10 +1001,9 @@ hipError_t run_cached_scores(const CachedArgs &c, hipStream_t s)
 template <typename T, int FMT>
 hipError_t run_cached_width(const CachedArgs &c, hipStream_t s)
 {
-    if constexpr (FMT != kPlain)
-        if (c.any)
-            return c.a.D <= 64 ? run_cached_rows<T, FMT, 64, 64, true, true>(c, s)
-                               : run_cached_rows<T, FMT, 128, 128, true, true>(c, s);
+    if (c.any)
+        return c.a.D <= 64 ? run_cached_rows<T, FMT, 64, 64, true, true>(c, s)
+                           : run_cached_rows<T, FMT, 128, 128, true, true>(c, s);
     if (c.a.D <= 64) return run_cached_scores<T, FMT, 64, 64>(c, s);
     if (c.a.D <= 96) return run_cached_scores<T, FMT, 128, 96>(c, s);
     return run_cached_scores<T, FMT, 128, 128>(c, s);

@@ -163,8 +163,7 @@ struct CachedPart {
     const int32_t *pos;        // (axes, caches, T)
     int32_t T, caches;
     int32_t seqs;              // sequences of a cache
-    int32_t width;             // bytes that a load of codes may take: 16, 4 or 1
-    int32_t vec;               // plain: every row starts at a multiple of 16 bytes
+    int32_t width;             // bytes that a load may take: 16, 8, 4, 2 or 1
     int32_t rows;              // seqs * Tq * G, of a key head
     int32_t mb;                // rows of a wave: 16 or 32
     int32_t wr;                // waves with rows of their own (4 / wr share the keys out)
@@ -175,8 +174,7 @@ struct CachedArgs {
     AttnArgs a;                // q, the scores, out and lse, the parts
     CachedPart part[2];        // the prefix, the own caches
     int32_t format, f32;
-    int32_t any;               // rows of any alignment and strides: codes have kernels of their
-                               // own, plain caches go in blocks of 16 rows
+    int32_t any;               // rows of any alignment and strides: kernels of their own
 };
 size_t plan_attn_cached(CachedArgs *c);
 void place_attn_cached(CachedArgs *c, void *workspace);

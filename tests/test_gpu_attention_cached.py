@@ -65,6 +65,8 @@ CASES = [
     (2, 1, 40, 90, 200, 8, 2, 96),         # 160 rows of an own cache
     (3, 3, 3, 50, 33, 4, 4, 33),           # a prefix each, an odd width
     (2, 1, 1, 5, 1, 4, 1, 7),
+    (3, 1, 2, 140, 90, 4, 2, 100),         # rows at multiples of 8 bytes
+    (10, 1, 2, 50, 700, 8, 2, 46),         # of 4
 ]
 
 
