@@ -346,7 +346,7 @@ __global__ __launch_bounds__(256) void cache_read_kernel(CachePlan p)
             widen8<T, FMT>(q[i][0], q[i][1], scale_of(byte[i]), o.v);
             R *const out = dst + at[i];
             if constexpr (VEC) {
-                *(u32x4 *)out = o.v[0];
+                st_stream((u32x4 *)out, o.v[0]);
             } else {
                 R e[8];
                 __builtin_memcpy(e, &o, sizeof(e));
