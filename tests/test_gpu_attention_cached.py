@@ -419,3 +419,40 @@ def test_together(fmt, dt):
         ref, lref = mp.mp3d_attention_forward(q, kk, vv, causal=True, softcap=20.0)
         tk.close(out, ref.cpu().double(), 2 * want["out"][1], "out of mp3d_attention_forward")
         tk.close(lse, lref.cpu().double(), 2 * want["lse"][1], "lse of mp3d_attention_forward")
+
+
+@pytest.mark.parametrize("fmt", KINDS, ids=lambda f: f or "plain")
+@pytest.mark.parametrize("lengths", [[8192, 0, 1, 129], [0, 3, 0, 8192], [0] * 4], ids=str)
+def test_long_caches_of_different_lengths(lengths, fmt):
+    """Chunks of several steps, many of them without keys."""
+    dt, B, Tq, Tk, Hq, Hk, D = torch.bfloat16, 4, 2, 8192, 8, 8, 32
+    q = tk.randn((B, Tq, Hq, D), 161, dt)
+    hk, own = make_cache(B, Tk, Hk, D, fmt, dt, 162)
+    hp, prefix = make_cache(1, 70, Hk, D, fmt, dt, 164)
+    how = dict(kv_len=torch.tensor(lengths).int())
+    for b in range(B):
+        spoil(own, fmt, b, lengths[b])
+    for pre, host in ((None, None), (prefix, hp)):
+        got, want = run(q, own, pre, fmt, how), oracle.attention(q, hk, host, **how)
+        for name in ("out", "lse"):
+            tk.close(got[name], *want[name], name)
+
+
+@pytest.mark.parametrize("fmt", KINDS, ids=lambda f: f or "plain")
+@pytest.mark.parametrize("lengths", [[3000, 2048, 100, 1000], [0, 3000, 1, 0]], ids=str)
+def test_long_prefixes_of_different_lengths(lengths, fmt):
+    """1200 rows share a prefix, the last block of 128 not full."""
+    dt, B, N, Tq, Tk, P, Hq, Hk, D = torch.bfloat16, 40, 4, 15, 40, 3000, 16, 2, 32
+    q = tk.randn((B, Tq, Hq, D), 171, dt)
+    hk, own = make_cache(B, Tk, Hk, D, fmt, dt, 172)
+    hp, prefix = make_cache(N, P, Hk, D, fmt, dt, 174)
+    how = dict(prefix_len=torch.tensor(lengths).int(), kv_len=(torch.arange(B) % 26 + 15).int())
+    for n in range(N):
+        spoil(prefix, fmt, n, lengths[n])
+    got = run(q, own, prefix, fmt, how)
+    some = [0, 9, 10, 19, 20, 39]                          # sequences of all prefixes
+    how = dict(kv_len=how["kv_len"][some], prefix_len=torch.tensor([lengths[b // 10] for b in some]))
+    want = oracle.attention(q[some], [t[some] for t in hk], [t[[b // 10 for b in some]] for t in hp],
+                            **how)
+    for name in ("out", "lse"):
+        tk.close(got[name][some], *want[name], name)
