@@ -2,6 +2,8 @@
 // join of its parts (the kernel that walks the caches: attention_cached.hpp).
 #include "attention_cached.hpp"
 
+#include <algorithm>
+
 namespace mp3d {
 
 namespace {
@@ -95,8 +97,9 @@ size_t plan_attn_cached(CachedArgs *c)
 {
     AttnArgs &a = c->a;
     constexpr int64_t kStep = kCachedKeys * kCachedWaves;  // keys that a workgroup takes at a time
-    // (a step of 128 rows takes twice as long as one of 16)
-    auto kWeight = [](const CachedPart &p) -> int64_t { return p.mb == 16 ? 1 : 2; };
+    // (a step of 128 rows takes three times one of 16; as twice it measured 4 %
+    // more, as four times up to 30 %)
+    auto kWeight = [](const CachedPart &p) -> int64_t { return p.mb == 16 ? 1 : 3; };
     auto blocks = [&](CachedPart &p) {
         p.units = (int64_t)a.Hk * p.caches * p.nsplit;
         p.blocks = p.nrb > 1 ? (p.units + 7) / 8 * 8 * p.nrb : p.units;
@@ -108,20 +111,39 @@ size_t plan_attn_cached(CachedArgs *c)
         p.units = p.blocks = 0;
         p.chunk = 1;
         p.rows = (int32_t)((int64_t)p.seqs * a.Tq * a.G);
-        p.mb = p.rows <= 64 || c->f32 || (c->format == kPlain && c->any) ? 16 : 32;
+        // Blocks of 16 rows or of 128.  Over a prefix, 16 heads on 4 of 128,
+        // bfloat16, 48 / 64 / 96 / 256 rows: 10935 e4m3 keys 19.6 / 20.7 / 24.9 /
+        // 39.1 us by 16, 20.5 / 22.8 / 24.9 / 31.3 by 128; 32768: 28.8 / 35.5 /
+        // 41.7 / 74.8 and 28.8 / 30.2 / 32.1 / 43.9; plain, 10935: 21.6 / 20.4 /
+        // 23.7 / 33.8 and 18.8 / 19.9 / 21.2 / 28.6.  (float32 is bound by its
+        // matrix instructions either way, and 128 rows leave waves idle: 15
+        // sequences of 7 tokens on three prefixes of 245 32 us by 128, 16 by 16.)
+        const bool plain = c->format == kPlain;
+        const int few = plain || p.T >= 16384 ? 32 : 64;
+        p.mb = p.rows <= few || c->f32 || (plain && c->any) ? 16 : 32;
         p.wr = p.mb == 16 ? 1 : 4;
         p.nrb = (p.rows + p.mb * p.wr - 1) / (p.mb * p.wr);
         if (p.caches == 0 || p.T == 0) continue;
         wide |= p.mb == 32;
         cost += (int64_t)p.nrb * a.Hk * p.caches * ((p.T + kStep - 1) / kStep) * kWeight(p);
     }
-    // One round of workgroups: as many as run at once; of 16 rows a third more
-    // where lengths are given, which leave some without keys (16 caches of 9728
-    // to 32768, e4m3: 145 us for one round, 134 so, 150 to 164 for two to four).
+    // One round of workgroups: as many as run at once, two a CU, or of 16 rows
+    // over codes three.  Of 16 rows four where lengths are given, which leave
+    // some without keys (16 caches of 9728 to 32768, e4m3: 145 us for three a
+    // CU, 134 for four, 150 to 164 for six to twelve; plain 275 and 254).
     const int64_t once = device_cus() * (wide || c->format == kPlain || attn_general(a) ? 2 : 3);
-    const bool ragged = !wide && c->part[1].len;
-    const int64_t want = ragged ? once * 4 / 3 : once;
-    const int64_t per = (cost + want - 1) / want;
+    const int64_t want = !wide && c->part[1].len ? 4 * device_cus() : once;
+    // Short calls: a workgroup's start takes as long as five steps and each
+    // writes a chunk to join, so a workgroup takes up to three steps before a
+    // CU gets a second one, of float32, whose steps are long, a third.  8
+    // sequences of 200 on 4000, 32 heads on 8, at least one step and by this
+    // rule: plain 18.5 and 12.5 us, e4m3 16.8 and 13.5, float32 29.0 and 26.8; 4 x
+    // 2048 plain 10.6 and 9.6; one sequence of 2048, which keeps one step, 9.1,
+    // with two 9.5.  (float32 as the others: that case 22.7, but 15 sequences of 7
+    // tokens on three prefixes of 245 18.5 us for 16.1.)
+    const int64_t spread = device_cus() * (c->f32 ? 2 : 1);
+    const int64_t per = std::max((cost + want - 1) / want,
+                                 std::min<int64_t>(3, (cost + spread - 1) / spread));
     for (CachedPart &p : c->part) {
         if (p.caches == 0 || p.T == 0) continue;
         const int64_t steps = (p.T + kStep - 1) / kStep;
@@ -132,13 +154,20 @@ size_t plan_attn_cached(CachedArgs *c)
         blocks(p);
     }
     CachedPart &own = c->part[1];
-    // Few keys and nothing to join with: a step more takes 1.2 us, a join 5.
-    for (int i = 0; i < 2; ++i)
-        if (c->part[1 - i].nsplit == 0 && c->part[i].T <= kAlone) {
-            c->part[i].nsplit = c->part[i].T > 0;
-            c->part[i].chunk = kAlone;
-            blocks(c->part[i]);
+    // Few keys and nothing to join with: not split, which saves the join (one
+    // sequence, 16 heads on 4, plain, 256 / 512 / 768 / 1024 keys: 6.4 / 7.9 / 9.4
+    // / 10.9 us, split 8.7 / 8.5 / 9.4 / 9.3; e4m3 7.3 / 9.6 / 11.8 / 14.3 and 9.3 /
+    // 9.1 / 10.0 / 9.8; 32 sequences, e4m3, 9.1 / 11.4 / 13.7 / 16.2 and 10.8 / 13.1 /
+    // 14.6 / 16.8), and a launch.
+    for (int i = 0; i < 2; ++i) {
+        CachedPart &p = c->part[i];
+        const bool many = (int64_t)p.nrb * a.Hk * p.caches >= 128;
+        if (c->part[1 - i].nsplit == 0 && p.T <= (many ? 2 : 1) * kAlone) {
+            p.nsplit = p.T > 0;
+            p.chunk = 2 * kAlone;
+            blocks(p);
         }
+    }
     if (c->part[0].nsplit + own.nsplit == 0) {
         own.nsplit = 1;                    // no key anywhere: the zeros are written all the same
         blocks(own);
@@ -165,8 +194,10 @@ hipError_t launch_attn_cached(const CachedArgs &c, hipStream_t s)
     if (e != hipSuccess) return e;         // the join would read what was not written
     const int slots = c.part[0].nsplit + c.part[1].nsplit;
     if (slots > 1) {
-        const bool one = slots <= 8;
+        // A group a row where rows are many and chunks few (8192 rows of 8: 9.8
+        // us, 17 by eight groups; 512 rows of 8: 5.8 and 5.2).
         const int64_t rows = (int64_t)c.a.B * c.a.Hq * c.a.Tq;
+        const bool one = rows >= 4096 && slots <= 16;
         const int64_t n = one ? (rows + kJoinGroups - 1) / kJoinGroups : rows;
         // (a launch's first dimension takes 2^24 workgroups of 256)
         const int64_t x = n < kJoinRow ? n : kJoinRow;
