@@ -6,7 +6,7 @@
 // the sequences' own caches; a chunk of keys of one cache and key head each.
 // The rows of a block are the query heads that share the key head, of all
 // new tokens, and over a prefix of all sequences that share it: so a prefix
-// is read once for all of them (for each 32 wr rows, see below), not once a
+// is read once for all of them (for each block of rows, see below), not once a
 // sequence.  The chunks' sums are joined by a second kernel, which does not
 // care which cache they came from.
 //
@@ -17,11 +17,21 @@
 // fragments instead would need a value's scale per key inside a lane's eight
 // keys.)  Elements go to LDS directly.
 //
-// Up to 32 rows go in blocks of 16 (MB = 16): each wave has all 16 and tiles of
-// its own, no wave waits for another.  More rows go in blocks of 128 (MB = 32):
-// the waves have 32 each, and share two tiles that they bring in turn, a
-// quarter each; codes are read and widened once for 128 rows, into the one half
-// of LDS while the products run from the other.
+// Few rows go in blocks of 16 (MB = 16): each wave has all 16 and tiles of its
+// own, no wave waits for another.  More rows go in blocks of 128 (MB = 32): the
+// waves have 32 each, and share two tiles that they bring in turn, a quarter
+// each; codes are read and widened once for 128 rows, into the one half of LDS
+// while the products run from the other.
+//
+// Bound, and what the kernel takes (the join's 4 to 10 us apart):
+//   blocks of 16, long caches: HBM.  16 caches of 9728 to 32768, 32 heads on 8
+//     of 128, e4m3: 135 us, 5.3 TB/s; every byte is fetched once.
+//   blocks of 128, long prefixes: the matrix and the vector unit in turn, as a
+//     wave's softmax waits for its scores.  4096 sequences on 8192 keys, 32 heads
+//     on 8 of 128: plain 910 to 960 TFLOP/s, e4m3 790, e2m1 820; 64 sequences
+//     on 32768 keys, e4m3, 69 us; a workgroup's start and end (6 to 8 us) weigh
+//     the more the shorter the chunks are.
+//   a few hundred keys: the launch and one step's latency.  777 keys, e2m1: 9 us.
 #pragma once
 
 #include <type_traits>
@@ -40,7 +50,8 @@ __host__ __device__ inline int cached_stride(int D) { return (D + 3) & ~3; }
 
 // Tiles of LDS a wave: elements straight from memory need one for keys and one
 // for values; codes of up to 16 rows take turns in one, so that three
-// workgroups fit on a CU.
+// workgroups fit on a CU (16 caches of 9728 to 32768, e4m3: 137 us; the same
+// with two workgroups that read two tiles ahead, for twice the registers).
 template <int FMT, int MB>
 constexpr int cached_slots() { return FMT == kPlain || MB == 32 ? 2 : 1; }
 template <typename T, int FMT, int DP, int MB>

@@ -12,7 +12,10 @@
 //
 // Bound: HBM; for new tokens of a few sequences, the launch.  A thread has 8
 // adjacent channels (4 or 8 to read, 16 bytes of them), four threads share a
-// group; k and v go in one launch.
+// group; k and v go in one launch.  A write of 4 x 10935 tokens of 4 heads of
+// 128, bfloat16 to e4m3: 26.4 us, 5.1 TB/s; a read of 2 x 32768 of 8 heads: 64
+// us, 6.3 TB/s, by stores that stay out of the caches (75 with plain ones); one
+// token of 32 sequences: 4 us.
 #include "cache.hpp"
 
 namespace mp3d {
