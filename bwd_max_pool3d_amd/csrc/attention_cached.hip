@@ -104,6 +104,8 @@ size_t plan_attn_cached(CachedArgs *c)
         p.units = (int64_t)a.Hk * p.caches * p.nsplit;
         p.blocks = p.nrb > 1 ? (p.units + 7) / 8 * 8 * p.nrb : p.units;
     };
+    const bool plain = c->format == kPlain;
+    const int few = plain || std::max(c->part[0].T, c->part[1].T) >= 16384 ? 32 : 64;
     int64_t cost = 0;                      // steps of 16 rows, over all workgroups
     bool wide = false;
     for (CachedPart &p : c->part) {
@@ -118,8 +120,8 @@ size_t plan_attn_cached(CachedArgs *c)
         // 23.7 / 33.8 and 18.8 / 19.9 / 21.2 / 28.6.  (float32 is bound by its
         // matrix instructions either way, and 128 rows leave waves idle: 15
         // sequences of 7 tokens on three prefixes of 245 32 us by 128, 16 by 16.)
-        const bool plain = c->format == kPlain;
-        const int few = plain || p.T >= 16384 ? 32 : 64;
+        // One bound for both parts: a prefix, which has at least an own cache's
+        // rows, then never has the smaller blocks (run_cached_rows).
         p.mb = p.rows <= few || c->f32 || (plain && c->any) ? 16 : 32;
         p.wr = p.mb == 16 ? 1 : 4;
         p.nrb = (p.rows + p.mb * p.wr - 1) / (p.mb * p.wr);

@@ -456,3 +456,21 @@ def test_long_prefixes_of_different_lengths(lengths, fmt):
                             **how)
     for name in ("out", "lse"):
         tk.close(got[name][some], *want[name], name)
+
+
+@pytest.mark.parametrize("fmt", KINDS, ids=lambda f: f or "plain")
+@pytest.mark.parametrize("Tk, P", [(16500, 70), (70, 16500)])
+def test_a_short_part_beside_a_long_one(Tk, P, fmt):
+    """40 rows, which go in blocks of 16 over short codes, in one of 128 over
+    long ones: in the same over both parts of a call."""
+    dt, B, Tq, Hq, Hk, D = torch.bfloat16, 2, 10, 8, 2, 32
+    q = tk.randn((B, Tq, Hq, D), 181, dt)
+    hk, own = make_cache(B, Tk, Hk, D, fmt, dt, 182)
+    hp, prefix = make_cache(B, P, Hk, D, fmt, dt, 184)
+    how = dict(kv_len=torch.tensor([Tk, Tk // 2]).int(), prefix_len=torch.tensor([P - 1, P]).int())
+    for b in range(B):
+        spoil(own, fmt, b, int(how["kv_len"][b]))
+        spoil(prefix, fmt, b, int(how["prefix_len"][b]))
+    got, want = run(q, own, prefix, fmt, how), oracle.attention(q, hk, hp, **how)
+    for name in ("out", "lse"):
+        tk.close(got[name], *want[name], name)
