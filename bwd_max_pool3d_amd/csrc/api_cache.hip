@@ -190,8 +190,8 @@ int cached_args(const mp3d_attention_cache *d, CachedArgs *c)
         }
         p.len = i ? d->kv_len : d->prefix_len;
         p.pos = i ? d->pos_k : d->pos_prefix;
-        p.T = (int32_t)x.T;
         p.caches = (int32_t)x.B;
+        p.T = p.caches ? (int32_t)x.T : 0;                 // (no prefix has no rows)
         p.seqs = i ? 1 : (int32_t)S;
         // whole units, or what there is
         const bool plain = d->format == kPlain;
