@@ -3,6 +3,8 @@
 // first launch.
 #include <stdio.h>
 
+#include <algorithm>
+
 #include "api_tokens.hpp"
 #include "cache.hpp"
 
@@ -193,20 +195,42 @@ int cached_args(const mp3d_attention_cache *d, CachedArgs *c)
         p.caches = (int32_t)x.B;
         p.T = p.caches ? (int32_t)x.T : 0;                 // (no prefix has no rows)
         p.seqs = i ? 1 : (int32_t)S;
-        // whole units, or what there is
+        // whole units, or what there is: of the strides, and with the addresses
         const bool plain = d->format == kPlain;
-        const int size = plain ? es : 1, bytes = plain ? d->D * es : row_bytes(d->format, d->D);
-        p.width = size;
-        for (int w : {plain ? 16 : unit, 8, 4})
-            if (p.width == size && w <= (plain ? 16 : unit) && divides(w, x, size, bytes)) p.width = w;
+        const int size = plain ? es : 1, most = plain ? 16 : unit;
+        uint64_t bits = plain ? d->D * es : row_bytes(d->format, d->D);
+        for (int j = 0; j < 3; ++j) bits |= (uint64_t)(p.ks[j] * size) | (uint64_t)(p.vs[j] * size);
+        auto width = [&](uint64_t x) {
+            const int w = (int)std::min<uint64_t>(most, x & -x);
+            return w >= 4 ? w : size;
+        };
+        p.width = width(bits | (uintptr_t)x.k | (uintptr_t)x.v);
         if (p.caches == 0 || p.T == 0) continue;
         // (a row's offset in a tile has to be within 31 bits)
         const int64_t far = (int64_t)1 << 24;
-        if (p.width != (plain ? 16 : unit) || (plain && d->D % 8) || p.ks[1] >= far || p.vs[1] >= far ||
+        if (width(bits) != most || (plain && d->D % 8) || p.ks[1] >= far || p.vs[1] >= far ||
             (!plain && (p.kss[1] >= far || p.vss[1] >= far)))
-            c->any = 1;
+            c->any_strides = 1;
+        if (c->any_strides || p.width != most) c->any = 1;
     }
     return MP3D_OK;
+}
+
+// The workspace of a call.  Its plan depends on whether kv_len is given and on
+// the caches' addresses, which a caller may not have yet: the most that the call
+// takes with any of them.
+size_t cached_workspace(const CachedArgs &c, int cus)
+{
+    size_t most = 0;
+    const int32_t lengths = 0;             // (its address is looked at, no more)
+    for (int any = c.any_strides; any <= 1; ++any)
+        for (const int32_t *len : {(const int32_t *)nullptr, &lengths}) {
+            CachedArgs x = c;
+            x.any = any;
+            x.part[1].len = len;
+            most = std::max(most, plan_attn_cached(&x, cus));
+        }
+    return most;
 }
 
 }  // namespace
@@ -237,9 +261,9 @@ int mp3d_attention_cached_workspace_bytes(const mp3d_attention_cache *d, size_t 
 {
     if (!bytes) return fail(MP3D_EINVAL, "bytes is NULL");
     CachedArgs c;
-    int rc = cached_args(d, &c);
+    const int rc = cached_args(d, &c);
     if (rc) return rc;
-    *bytes = c.a.B == 0 || c.a.Tq == 0 ? 0 : plan_attn_cached(&c);
+    *bytes = c.a.B == 0 || c.a.Tq == 0 ? 0 : cached_workspace(c, device_cus());
     return MP3D_OK;
 }
 
@@ -266,7 +290,9 @@ int mp3d_attention_cached(const mp3d_attention_cache *d, const void *q, void *ou
     a.out = out;
     a.lse = lse;
     a.vec = wide_rows(q, a.qs, es) && a.D % 8 == 0;
-    if ((rc = check_workspace(workspace, workspace_bytes, plan_attn_cached(&c)))) return rc;
+    const int cus = device_cus();
+    if ((rc = check_workspace(workspace, workspace_bytes, cached_workspace(c, cus)))) return rc;
+    plan_attn_cached(&c, cus);
     if ((rc = check_launch(c.part[0].blocks + c.part[1].blocks))) return rc;
     place_attn_cached(&c, workspace);
     if (log_enabled())

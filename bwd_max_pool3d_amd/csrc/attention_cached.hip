@@ -91,9 +91,9 @@ __global__ __launch_bounds__(32 * kJoinGroups) void cached_join_kernel(CachedArg
 
 }  // namespace
 
-// Rows a workgroup, chunks and workgroups of both parts; returns the
-// workspace's bytes.
-size_t plan_attn_cached(CachedArgs *c)
+// Rows a workgroup, chunks and workgroups of both parts on a device of `cus`
+// CUs; returns the workspace's bytes.
+size_t plan_attn_cached(CachedArgs *c, int cus)
 {
     AttnArgs &a = c->a;
     constexpr int64_t kStep = kCachedKeys * kCachedWaves;  // keys that a workgroup takes at a time
@@ -133,8 +133,8 @@ size_t plan_attn_cached(CachedArgs *c)
     // over codes three.  Of 16 rows four where lengths are given, which leave
     // some without keys (16 caches of 9728 to 32768, e4m3: 145 us for three a
     // CU, 134 for four, 150 to 164 for six to twelve; plain 275 and 254).
-    const int64_t once = device_cus() * (wide || c->format == kPlain || attn_general(a) ? 2 : 3);
-    const int64_t want = !wide && c->part[1].len ? 4 * device_cus() : once;
+    const int64_t once = cus * (wide || c->format == kPlain || attn_general(a) ? 2 : 3);
+    const int64_t want = !wide && c->part[1].len ? 4 * (int64_t)cus : once;
     // Short calls: a workgroup's start takes as long as five steps and each
     // writes a chunk to join, so a workgroup takes up to three steps before a
     // CU gets a second one, of float32, whose steps are long, a third.  8
@@ -143,7 +143,7 @@ size_t plan_attn_cached(CachedArgs *c)
     // 2048 plain 10.6 and 9.6; one sequence of 2048, which keeps one step, 9.1,
     // with two 9.5.  (float32 as the others: that case 22.7, but 15 sequences of 7
     // tokens on three prefixes of 245 18.5 us for 16.1.)
-    const int64_t spread = device_cus() * (c->f32 ? 2 : 1);
+    const int64_t spread = cus * (c->f32 ? 2 : 1);
     const int64_t per = std::max((cost + want - 1) / want,
                                  std::min<int64_t>(3, (cost + spread - 1) / spread));
     for (CachedPart &p : c->part) {

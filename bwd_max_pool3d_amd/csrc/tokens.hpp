@@ -175,8 +175,9 @@ struct CachedArgs {
     CachedPart part[2];        // the prefix, the own caches
     int32_t format, f32;
     int32_t any;               // rows of any alignment and strides: kernels of their own
+    int32_t any_strides;       // the same, whatever the rows' addresses
 };
-size_t plan_attn_cached(CachedArgs *c);
+size_t plan_attn_cached(CachedArgs *c, int cus);
 void place_attn_cached(CachedArgs *c, void *workspace);
 template <typename T>
 hipError_t launch_attn_cached(const CachedArgs &c, hipStream_t s);

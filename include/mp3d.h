@@ -493,7 +493,9 @@ typedef struct mp3d_attention_cache {
     const int32_t *pos_k, *pos_prefix;
 } mp3d_attention_cache;
 
-/* Device workspace of the call, in bytes; as mp3d_attention_workspace_bytes. */
+/* Device workspace of the call, in bytes; as mp3d_attention_workspace_bytes.
+ * Depends on none of the caches' addresses, nor on whether kv_len is given: a
+ * caller may size it before these exist. */
 int mp3d_attention_cached_workspace_bytes(const mp3d_attention_cache *a, size_t *bytes);
 
 /* Writes out (B, Tq, Hq, D), contiguous, 16-byte aligned, and lse

@@ -42,3 +42,25 @@ def test_no_prefix_has_no_rows(T):
     without = size(desc(2, 10, T, 8, 2, 32))
     for P in (1, 70, 16500):
         assert size(desc(2, 10, T, 8, 2, 32, P=P)) == without
+
+
+@pytest.mark.parametrize("shape", [
+    dict(B=16, Tq=1, T=8000, Hq=32, Hk=8, D=128, format=0),
+    dict(B=16, Tq=1, T=8000, Hq=32, Hk=8, D=128, format=1),
+    dict(B=32, Tq=16, T=777, Hq=16, Hk=2, D=128, N=4, P=6272, format=0),
+    dict(B=32, Tq=16, T=777, Hq=16, Hk=2, D=128, N=4, P=6272, format=1),
+    dict(B=4, Tq=3, T=900, Hq=8, Hk=2, D=100, N=1, P=5000, format=0),     # no 16-byte rows at all
+], ids=str)
+def test_a_workspace_is_sized_before_the_caches_exist(shape):
+    """Caches given or not, at addresses of any alignment, lengths given or not:
+    one size, and a call takes no more (16 sequences of 8000 plain keys were
+    2129920 bytes without kv_len and 2795520 with it)."""
+    first = size(desc(at=None, **shape))
+    assert first > 0
+    for at in (None, FAKE, FAKE + 4):
+        for kv_len in (None, FAKE):
+            a = desc(at=at, kv_len=kv_len, **shape)
+            assert size(a) == first, (at, kv_len)
+            if at is not None:
+                assert _lib.load().mp3d_attention_cached(
+                    ctypes.byref(a), FAKE, FAKE, FAKE, FAKE, first - 16, None) == _lib.MP3D_EWORKSPACE
