@@ -208,7 +208,8 @@ int cached_args(const mp3d_attention_cache *d, CachedArgs *c)
         if (p.caches == 0 || p.T == 0) continue;
         // (a row's offset in a tile has to be within 31 bits)
         const int64_t far = (int64_t)1 << 24;
-        if (width(bits) != most || (plain && d->D % 8) || p.ks[1] >= far || p.vs[1] >= far ||
+        if (width(bits) != most || (plain && d->D % 8) || (d->format == kE2M1 && d->D % 2) ||
+            p.ks[1] >= far || p.vs[1] >= far ||
             (!plain && (p.kss[1] >= far || p.vss[1] >= far)))
             c->any_strides = 1;
         if (c->any_strides || p.width != most) c->any = 1;

@@ -263,6 +263,9 @@ struct CodeTile {
     {
         const int bytes = code_bytes<FMT>(D), u = min(unit(lane), (D - 1) / 16);
         const int left = bytes - u * BYTES;
+        // (half of an odd row's last byte is no channel's: what it holds could be
+        // past the type, and times the query's 0 there NaN)
+        const int odd = FMT == kE2M1 && D & 1 ? D - u * 16 : 16;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const int64_t r = min(k0 + j * ROWS + row(lane), end - 1);
@@ -278,6 +281,11 @@ struct CodeTile {
 #pragma unroll
                 for (int i = 0; i < BYTES; ++i)
                     if (i < left) c[j][i / 4] |= (uint32_t)q[i] << (8 * (i % 4));
+            }
+            if constexpr (FMT == kE2M1) {
+#pragma unroll
+                for (int i = 0; i < WORDS; ++i)
+                    if (odd / 8 == i) c[j][i] &= ~(15u << (4 * (odd % 8)));
             }
         }
     }

@@ -429,8 +429,9 @@ int mp3d_attention_backward(const mp3d_attention *a, const void *dout, const int
  * MP3D_CACHE_E4M3: sign, 4 exponent bits (bias 7), 3 fraction bits, M = 448,
  * code 127 is NaN, a byte each.  MP3D_CACHE_E2M1: sign, 2 exponent bits, 1
  * fraction bit (0 0.5 1 1.5 2 3 4 6), M = 6, two to a byte, the even channel
- * in its lower half; a head's row is (D + 1) / 2 bytes.  A group with an
- * infinity or a NaN has the scale byte 255: it is read as NaN.
+ * in its lower half; a head's row is (D + 1) / 2 bytes (the last half of an odd
+ * one is written as 0 and may hold anything).  A group with an infinity or a
+ * NaN has the scale byte 255: it is read as NaN.
  *
  * The caller allocates all four parts, and says where they are by strides in
  * bytes (of a plain cache: in elements), for (sequence, row, head); codes,

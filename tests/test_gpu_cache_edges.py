@@ -4,7 +4,9 @@ import ctypes
 import pytest
 import torch
 
+import _caches as oracle
 import _tokens as tk
+import bwd_max_pool3d_amd as mp
 from bwd_max_pool3d_amd import _lib
 
 pytestmark = pytest.mark.gpu
@@ -34,3 +36,31 @@ def test_no_prefix_and_no_own_rows(P, dt):
                                          lse.data_ptr(), ws.data_ptr(), n.value, stream))
     assert torch.equal(out, torch.zeros_like(out))
     assert bool((lse == float("-inf")).all())
+
+
+@pytest.mark.parametrize("dt", tk.TYPES, ids=tk.name_of)
+@pytest.mark.parametrize("Tq", [1, 40])
+@pytest.mark.parametrize("D", [7, 15, 47, 63, 101, 127])
+def test_half_a_byte_that_is_no_channels(D, Tq, dt):
+    """Heads of an odd width in 4 bits: the upper half of a row's last byte may
+    hold anything (6 there, under the scale of a last group near the type's
+    largest number, was an infinity, and the scores NaN)."""
+    B, T, Hq, Hk, fmt = 2, 70, 4, 2, "e2m1"
+    q = tk.randn((B, Tq, Hq, D), 1, dt)
+    host, cache = [], []
+    for i in range(2):
+        x = tk.randn((B, T, Hk, D), 2 + i, dt)
+        last = (D - 1) // 32 * 32
+        x[..., last:] = 0                                  # codes 0, so that no score is large
+        codes, scales = oracle.write(x, fmt)
+        codes[..., -1] = 0x70
+        scales[..., -1] = 142 if dt == torch.float16 else 254
+        host.append(oracle.read(codes, scales, fmt, D, dt))
+        assert torch.isfinite(host[i]).all()
+        cache += [t.transpose(1, 2).contiguous().cuda().transpose(1, 2) for t in (codes, scales)]
+    for got, want in zip(mp.mp3d_cache_read(cache, fmt, D, dt), host):
+        assert torch.equal(got.cpu(), want)
+    out, lse = mp.mp3d_attention_cached(q.cuda(), cache, format=fmt)
+    want = oracle.attention(q, host)
+    tk.close(out, *want["out"], "out")
+    tk.close(lse, *want["lse"], "lse")
