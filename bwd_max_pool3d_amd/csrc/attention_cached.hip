@@ -129,11 +129,17 @@ size_t plan_attn_cached(CachedArgs *c, int cus)
         wide |= p.mb == 32;
         cost += (int64_t)p.nrb * a.Hk * p.caches * ((p.T + kStep - 1) / kStep) * kWeight(p);
     }
-    // One round of workgroups: as many as run at once, two a CU, or of 16 rows
-    // over codes three.  Of 16 rows four where lengths are given, which leave
-    // some without keys (16 caches of 9728 to 32768, e4m3: 145 us for three a
-    // CU, 134 for four, 150 to 164 for six to twelve; plain 275 and 254).
-    const int64_t once = cus * (wide || c->format == kPlain || attn_general(a) ? 2 : 3);
+    // One round of workgroups: as many as run at once.  (e4m3 by three a CU where
+    // the kernels leave room for two, and by two: 16 caches of 16384, 32 heads on 8
+    // of 128 in float32 257 and 238 us, of 100 in bfloat16, which cannot go by 16
+    // bytes, 316 and 240; plain float32 over 64 channels, which has room for one, by
+    // two and by one 362 and 369, one cache of 32768 41 and 35, 8 of 1500 48 and
+    // 54.)  Of 16 rows four where lengths are given, which leave some without keys
+    // (16 caches of 9728 to 32768, e4m3: 145 us for three a CU, 134 for four, 150 to
+    // 164 for six to twelve; plain 275 and 254).
+    const int at_once = cached_occupancy(c->f32 ? 4 : 2, c->format, a.D <= 64 ? 64 : 128,
+                                         c->any || attn_general(a), wide ? 32 : 16);
+    const int64_t once = (int64_t)cus * std::max(2, at_once);
     const int64_t want = !wide && c->part[1].len ? 4 * (int64_t)cus : once;
     // Short calls: a workgroup's start takes as long as five steps and each
     // writes a chunk to join, so a workgroup takes up to three steps before a

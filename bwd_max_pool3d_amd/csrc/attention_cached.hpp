@@ -69,12 +69,12 @@ constexpr uint32_t cached_lds()
            (kCachedWaves * (2 * 3 * kCachedKeys + 2 * MB) + 4) * (uint32_t)sizeof(float);
 }
 
-// Workgroups on a CU.
-template <typename T, int FMT, int DP, bool GEN, int MP>
-constexpr int cached_occupancy()
+// Workgroups on a CU: of tiles DP wide, of elements of `size` bytes; `general`: the
+// kernels with GEN; mb: the most rows of a wave.
+constexpr int cached_occupancy(int size, int format, int DP, bool general, int mb)
 {
-    if (sizeof(typename T::raw) * DP > 256) return FMT == kPlain ? 1 : 2;
-    return FMT != kPlain && MP == 16 && !GEN ? 3 : 2;
+    if (size * DP > 256) return format == kPlain ? 1 : 2;
+    return format != kPlain && mb == 16 && !general ? 3 : 2;
 }
 
 // --- products with MB columns (rows of the call, in lanes l % MB).  A lane's
@@ -976,7 +976,8 @@ __device__ __forceinline__ void cached_chunk(const CachedArgs &c, bool own, uint
 
 // MP, MO: columns of the prefix' and of the own caches' workgroups.
 template <typename T, int FMT, int DP, int DU, bool GEN, bool ANY, int MP, int MO>
-__global__ __launch_bounds__(64 * kCachedWaves, (cached_occupancy<T, FMT, DP, GEN, MP>()))
+__global__ __launch_bounds__(64 * kCachedWaves,
+                             (cached_occupancy(sizeof(typename T::raw), FMT, DP, GEN, MP)))
 void attn_cached_kernel(CachedArgs c)
 {
     extern __shared__ __align__(16) unsigned char smem[];
