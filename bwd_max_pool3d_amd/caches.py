@@ -243,7 +243,11 @@ def mp3d_attention_cached(q: torch.Tensor, own, prefix=None, *, format: str | No
     ``pos_q`` (axes, B, Tq), ``pos_k`` (axes, B, T) and ``pos_prefix``
     (axes, N, P) int32.  ``out``: preallocated (out, lse); ``workspace``: a
     uint8 tensor of mp3d_attention_cached_workspace_bytes(...) (None:
-    allocated)."""
+    allocated).
+
+    Over plain caches without a prefix mp3d_attention_forward(kv_len=...)
+    gives the same, and has a backward; this is the faster of the two for new
+    tokens."""
     a = _descriptor(q, own, prefix, format, scale, softcap, causal, kv_len, prefix_len, slopes,
                     pos_q, pos_k, pos_prefix)
     B, Tq, Hq, _ = shape = q.shape

@@ -92,7 +92,9 @@ __global__ __launch_bounds__(32 * kJoinGroups) void cached_join_kernel(CachedArg
 }  // namespace
 
 // Rows a workgroup, chunks and workgroups of both parts on a device of `cus`
-// CUs; returns the workspace's bytes.
+// CUs; returns the workspace's bytes.  By the caches' rows, T: the lengths in use
+// are on the device, and chunks behind them have nothing to do (one of 1000 keys,
+// 32 heads on 8, e4m3: 11.4 us in a cache of 1024, 19.5 in one of 131072).
 size_t plan_attn_cached(CachedArgs *c, int cus)
 {
     AttnArgs &a = c->a;
@@ -120,6 +122,11 @@ size_t plan_attn_cached(CachedArgs *c, int cus)
         // 23.7 / 33.8 and 18.8 / 19.9 / 21.2 / 28.6.  (float32 is bound by its
         // matrix instructions either way, and 128 rows leave waves idle: 15
         // sequences of 7 tokens on three prefixes of 245 32 us by 128, 16 by 16.)
+        // The same bound is taken with other widths and a cap, where 16 stay ahead
+        // longer (48 / 64 / 96 / 256 rows: 64 channels, e4m3, 10935 12.7 / 13.1 /
+        // 15.4 / 22.2 and 14.9 / 15.7 / 17.8 / 21.6; 128 and a cap, e4m3, 32768 26.9 /
+        // 30.5 / 38.2 / 71.6 and 38.1 / 38.9 / 41.6 / 58.8; 32 channels, e4m3, 32768
+        // 18.2 / 19.3 / 23.5 / 40.7 and 19.7 / 20.1 / 21.3 / 28.8).
         // One bound for both parts: a prefix, which has at least an own cache's
         // rows, then never has the smaller blocks (run_cached_rows).
         p.mb = p.rows <= few || c->f32 || (plain && c->any) ? 16 : 32;
@@ -166,7 +173,10 @@ size_t plan_attn_cached(CachedArgs *c, int cus)
     // sequence, 16 heads on 4, plain, 256 / 512 / 768 / 1024 keys: 6.4 / 7.9 / 9.4
     // / 10.9 us, split 8.7 / 8.5 / 9.4 / 9.3; e4m3 7.3 / 9.6 / 11.8 / 14.3 and 9.3 /
     // 9.1 / 10.0 / 9.8; 32 sequences, e4m3, 9.1 / 11.4 / 13.7 / 16.2 and 10.8 / 13.1 /
-    // 14.6 / 16.8), and a launch.
+    // 14.6 / 16.8), and a launch.  (float32 takes the same bound, though its steps
+    // are longer: one sequence, e4m3, 256 / 512 / 1024 keys 14.8 / 22.6 / 38.2 whole
+    // and 13.6 / 13.6 / 13.8 split; 32 sequences 15.4 / 24.2 / 41.7 and 14.5 / 20.4 /
+    // 28.3, plain 15.8 / 23.5 / 36.5 and 14.9 / 29.2 / 39.1.)
     for (int i = 0; i < 2; ++i) {
         CachedPart &p = c->part[i];
         const bool many = (int64_t)p.nrb * a.Hk * p.caches >= 128;

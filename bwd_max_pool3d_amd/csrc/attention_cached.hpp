@@ -28,9 +28,14 @@
 //     of 128, e4m3: 135 us, 5.3 TB/s; every byte is fetched once.
 //   blocks of 128, long prefixes: the matrix and the vector unit in turn, as a
 //     wave's softmax waits for its scores.  4096 sequences on 8192 keys, 32 heads
-//     on 8 of 128: plain 910 to 960 TFLOP/s, e4m3 790, e2m1 820; 64 sequences
-//     on 32768 keys, e4m3, 69 us; a workgroup's start and end (6 to 8 us) weigh
-//     the more the shorter the chunks are.
+//     on 8 of 128, no own keys: plain 591 us, 930 TFLOP/s, e4m3 646 us, 850, e2m1
+//     591 us, 930 (with an own cache of one key each, 32768 workgroups more, 862,
+//     950 and 893 us); 64 sequences on 32768 keys, e4m3, 69 us; a workgroup's
+//     start and end (6 to 8 us) weigh the more the shorter the chunks are.
+//   the same over 128 channels with a cap, a bias or a factor: registers too.
+//     The compiler spills 63 of them (e2m1) or 73 (e4m3; plain 15, and without
+//     these 2, 14 and none), and a reload in the loop waits behind the codes in
+//     flight.  128 drafted rows on 6272 keys, e2m1, cap: 66 us.
 //   a few hundred keys: the launch and one step's latency.  777 keys, e2m1: 9 us.
 #pragma once
 
@@ -174,7 +179,11 @@ __device__ __forceinline__ Frag<T> value_frag(const typename T::raw *tile, int c
     }
 }
 
-// Scores 8c .. 8c + 7, rounded, as an operand.
+// Weights 8c .. 8c + 7 as an operand of the second product, which has operands
+// of the queries' type alone: each is off by up to half a step (2^-8 of it in
+// bfloat16, 2^-11 in float16), as in mp3d_attention_forward.  Float32 weights would
+// take the float32 instructions, at an eighth of the rate.  Out is off by 0.0023 with it where one rounding of the output is 0.0017
+// (bfloat16; float16 0.00024 and 0.0002); the sums of weights are not rounded.
 template <typename T, typename V>
 __device__ __forceinline__ Frag<T> pack_scores(const V &s, int c)
 {

@@ -374,8 +374,8 @@ hipError_t run(const CachePlan &p, bool read, hipStream_t s)
 
 }  // namespace
 
-// Threads that walk a row, tokens of a workgroup.  Rows of up to 256 pieces
-// share a workgroup; longer ones (heads over 2048 channels) are refused.
+// Threads that walk a row, tokens of a workgroup.  A row has at most 256 pieces:
+// a head of kCacheMaxD = 1024 channels of float32, read 4 a thread.
 void plan_cache(CachePlan *p, int elem_bytes, bool read)
 {
     const int per = read ? 16 / elem_bytes : 8;

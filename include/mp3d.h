@@ -478,7 +478,11 @@ int mp3d_cache_read(const mp3d_cache *cache, int format, void *k, void *v, int d
  * pos_k is (axes, B, own.T), pos_prefix (axes, N, prefix.T).  Keys and values
  * of 8 or 4 bits are as mp3d_cache_read gives them in q's type.  Both caches
  * have the same format.  A query that sees no key gets out = 0, lse =
- * -infinity. */
+ * -infinity.
+ * Over plain caches without a prefix mp3d_attention_forward with kv_len forms
+ * the same, and has the masks and the backward that training takes; new tokens
+ * over a cache are faster here.  A cache costs by its T, not by its lengths
+ * alone: one of as many rows as will be in use is the fastest. */
 typedef struct mp3d_attention_cache {
     int dtype, format;
     int64_t B, Tq;
