@@ -182,8 +182,9 @@ __device__ __forceinline__ Frag<T> value_frag(const typename T::raw *tile, int c
 // Weights 8c .. 8c + 7 as an operand of the second product, which has operands
 // of the queries' type alone: each is off by up to half a step (2^-8 of it in
 // bfloat16, 2^-11 in float16), as in mp3d_attention_forward.  Float32 weights would
-// take the float32 instructions, at an eighth of the rate.  Out is off by 0.0023 with it where one rounding of the output is 0.0017
-// (bfloat16; float16 0.00022 and 0.0002); the sums of weights are not rounded.
+// take the float32 instructions, at an eighth of the rate.  Out is off by 0.0023
+// with it where one rounding of the output is 0.0017 (bfloat16; float16 0.00022 and
+// 0.0002); the sums of weights are not rounded.
 template <typename T, typename V>
 __device__ __forceinline__ Frag<T> pack_scores(const V &s, int c)
 {
